@@ -1,7 +1,9 @@
 /*
  * pagedkv.h -- C ABI of libpagedkv: decode-step and chunked-prefill attention
- * over a paged KV cache, the cache writes of a step (slot write, copy-on-write
- * copy, swap copy to and from host memory), and the host-side block manager
+ * over a paged KV cache, decode attention over selected blocks of it (with the
+ * score that selects them), the cache writes of a step (slot write, with or
+ * without the position rotation, copy-on-write copy, swap copy to and from host
+ * memory), and the host-side block manager
  * (with prefix caching, beam-search reshuffles and swapping).
  *
  * Sources, by page title and section:
@@ -425,6 +427,153 @@ PKV_API int paged_attention_decode_noalloc(void* out, const void* q,
                                    int num_heads, int num_kv_heads, int head_dim,
                                    int block_size, float scale, int q_dtype, int kv_dtype,
                                    float k_scale, float v_scale, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Long contexts: the rotated append, and decode attention over a few selected
+ * blocks of each sequence. The pages have no counterpart of these; the cache
+ * they work on is the pages' paged cache, unchanged, and a step may use
+ * them in place of reshape_and_cache and paged_attention_decode:
+ *     copy_blocks -> rotary_and_cache -> update_key_bounds -> select_blocks
+ *                 -> paged_attention_decode_sparse.
+ * All four are asynchronous on `stream`, allocate nothing and are launched with
+ * programmatic stream serialisation, as paged_attention_decode is.
+ *
+ * rotary_and_cache -- rotate every token's query and key heads by the token's
+ * positions, write the queries to q_out and the keys and values into the cache.
+ *
+ * For each token t < num_tokens with s = slot_mapping[t] >= 0, every head and
+ * every pair i < rotary_dim / 2 of axis a(i), p = positions[a(i)][t]:
+ *     c = cos_sin[p][0][i],  n = cos_sin[p][1][i]
+ *     (x1, x2) -> (x1*c - x2*n, x2*c + x1*n)
+ * where the pair is dims (i, i + rotary_dim/2), or (2i, 2i+1) if interleaved;
+ * dims >= rotary_dim pass unchanged. Products and sums are rounded to float32
+ * one by one; the result is rounded once to the type of q_out or of the cache
+ * (E4M3 as in reshape_and_cache, from the rotated float32 value). Keys and
+ * values go to slot s of the pools as in reshape_and_cache.
+ *     s < 0: padding, the token is skipped (its row of q_out is left as it was).
+ *     s >= num_blocks*block_size, or a position outside [0, num_positions): the
+ *     token is skipped and PKV_ERR_OUT_OF_RANGE is set in the device error word.
+ *
+ *   q_out, q     device, num_heads*head_dim elements per token, dtype src_dtype;
+ *                tokens q_out_stride / q_stride elements apart (at least a row, a
+ *                multiple of 16 bytes), so q, k and v may be views of one fused
+ *                projection. q_out may be q itself (same stride); any other
+ *                overlap is not allowed
+ *   k, v         device, num_kv_heads*head_dim elements per token, k_stride /
+ *                v_stride elements apart
+ *   slot_mapping device int64 [num_tokens]; distinct where >= 0
+ *   positions    device int32 [num_axes][num_tokens]
+ *   cos_sin      device float32 [num_positions][2][rotary_dim/2], 16-byte aligned
+ *   sections     HOST int32 [num_axes], read by the call: the pairs of each axis,
+ *                in order, adding up to rotary_dim/2 (one axis: {rotary_dim/2};
+ *                time, height, width of image tokens: three)
+ * Supported: 1 to 4 axes; head_dim (at most 1024) and rotary_dim multiples of
+ * 16; block_size a multiple of 16; the (src, cache) types of reshape_and_cache.
+ * ---------------------------------------------------------------------- */
+PKV_API int rotary_and_cache(void* q_out, const void* q, const void* k, const void* v,
+                             void* k_pool, void* v_pool, const int64_t* slot_mapping,
+                             const int32_t* positions, const float* cos_sin,
+                             const int32_t* sections, int num_axes, int64_t q_out_stride,
+                             int64_t q_stride, int64_t k_stride, int64_t v_stride, int num_tokens,
+                             int num_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                             int interleaved, int block_size, int num_blocks, int num_positions,
+                             int src_dtype, int cache_dtype, float k_scale, float v_scale,
+                             void* stream);
+
+/* ------------------------------------------------------------------------
+ * update_key_bounds -- the smallest and largest value of every key dim over the
+ * filled slots of a block, for the blocks that hold the positions
+ * first_changed[b] .. seq_lens[b]-1 of each sequence b (the positions written
+ * since the bounds were last updated; first_changed[b] >= seq_lens[b]: none; 0
+ * after a block moved: swapping, copies outside the step's own copy-on-write):
+ *     key_bounds[blk][h][0][d] = min over t of K[blk][h][t][d]
+ *     key_bounds[blk][h][1][d] = max over t of K[blk][h][t][d]
+ * over the slots t of the block that the sequence has filled; a NaN key gives a
+ * NaN bound. E4M3 caches: of the codes' values, without the scale. Every other
+ * row is left as it was. Sequences sharing a block must have filled it alike
+ * (the block manager copies a shared block before a write into it).
+ *
+ *   k_pool         device pool, dtype kv_dtype
+ *   key_bounds     device [num_blocks][num_kv_heads][2][head_dim], 16-byte
+ *                  aligned: float32 for a float32 cache, bfloat16 (exact) for
+ *                  bfloat16 and E4M3 caches
+ *   block_tables, seq_lens  as for paged_attention_decode
+ *   first_changed  device int32 [num_seqs]
+ *   max_new_tokens the most positions that changed in one sequence: sizes the
+ *                  launch, no more (0: unknown; the result does not depend on it)
+ * Supported: head_dim and block_size multiples of 16; F32, BF16, E4M3. A length
+ * the table cannot hold, a negative first_changed or a table entry outside the
+ * pool sets PKV_ERR_OUT_OF_RANGE (clamped; the entry is skipped).
+ * ---------------------------------------------------------------------- */
+PKV_API int update_key_bounds(const void* k_pool, void* key_bounds, const int32_t* block_tables,
+                              const int32_t* seq_lens, const int32_t* first_changed, int num_seqs,
+                              int max_blocks_per_seq, int num_blocks, int num_kv_heads,
+                              int head_dim, int block_size, int max_new_tokens, int kv_dtype,
+                              void* stream);
+
+/* ------------------------------------------------------------------------
+ * select_blocks -- the blocks of each sequence that a decode query attends over,
+ * chosen for each kv head by the bound that the key bounds put on its logits.
+ *
+ * With n = ceil(seq_lens[b]/block_size), G = num_heads/num_kv_heads, lo and hi
+ * the bounds of block j = block_tables[b][j]:
+ *     score(b, h, j) = max_{g<G} sum_d max(q[b][h*G+g][d] lo[d], q[..][d] hi[d])
+ * selected[b][h] lists, in ascending order and -1 padded to num_selected: every
+ * block if n <= num_selected; else blocks 0 .. first_blocks-1, n-last_blocks ..
+ * n-1 and the num_selected - first_blocks - last_blocks others of the highest
+ * score, equal scores by the lower index. The choice is that of the exact
+ * scores: it does not depend on float32 rounding. (Computed as q+ hi + q- lo; a
+ * score that is not finite, from bounds or queries that are not, ranks above
+ * every finite one.)
+ *
+ *   selected     device int32 [num_seqs][num_kv_heads][num_selected], written
+ *   q            device [num_seqs][num_heads][head_dim], dtype q_dtype, 16-byte
+ *                aligned: the rotated query
+ *   key_bounds   as update_key_bounds keeps them, in q_dtype
+ *   num_blocks   rows of key_bounds (bounds for table entries)
+ *   workspace    device scratch of select_blocks_workspace_size bytes, 16-byte
+ *                aligned (NULL if no sequence can have more than num_selected
+ *                blocks, or nothing is left to score). Needs no clearing; calls
+ *                that overlap on the GPU need one each.
+ * Supported: head_dim in {64,128}; G <= 8; F32 (float32 cache), BF16 (bfloat16
+ * and E4M3 caches); at most 524288 blocks per sequence. A length the table
+ * cannot hold is clamped and sets PKV_ERR_OUT_OF_RANGE, as does a table entry
+ * outside the pool (its block ranks last).
+ * ---------------------------------------------------------------------- */
+PKV_API int select_blocks(int32_t* selected, const void* q, const void* key_bounds,
+                          const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                          int max_blocks_per_seq, int num_blocks, int num_heads, int num_kv_heads,
+                          int head_dim, int block_size, int num_selected, int first_blocks,
+                          int last_blocks, int q_dtype, void* workspace, size_t workspace_bytes,
+                          void* stream);
+PKV_API size_t select_blocks_workspace_size(int num_seqs, int num_kv_heads, int max_blocks_per_seq);
+
+/* ------------------------------------------------------------------------
+ * paged_attention_decode_sparse -- paged_attention_decode over the tokens of
+ * selected blocks alone: query head h of sequence b attends over the positions
+ * t < seq_lens[b] whose block t/block_size is listed in selected[b][h/G]:
+ *     out[b][h] = v_scale * sum_t softmax(scale * k_scale * <q[b][h], K[t]>)_t * V[t]
+ * No listed token (an empty sequence, a list of padding) gives a zero row. With
+ * every block listed it is paged_attention_decode's result up to rounding.
+ *
+ *   selected      device int32 [num_seqs][num_kv_heads][num_selected]: logical
+ *                 blocks, strictly ascending, the rest -1 (select_blocks' output
+ *                 or the caller's own choice). An entry that is past the
+ *                 sequence, not above the entry before it, or directly behind
+ *                 padding sets PKV_ERR_OUT_OF_RANGE and is skipped; entries past
+ *                 the sequence's number of blocks are not read
+ *   the rest      as paged_attention_decode (same supported sizes and types)
+ * One launch, no workspace: the CTAs that share a (sequence, kv head) are a
+ * thread-block cluster and merge their partial results in shared memory.
+ * ---------------------------------------------------------------------- */
+PKV_API int paged_attention_decode_sparse(void* out, const void* q, const void* k_pool,
+                                          const void* v_pool, const int32_t* block_tables,
+                                          const int32_t* seq_lens, const int32_t* selected,
+                                          int num_seqs, int max_blocks_per_seq, int num_blocks,
+                                          int num_selected, int num_heads, int num_kv_heads,
+                                          int head_dim, int block_size, float scale, int q_dtype,
+                                          int kv_dtype, float k_scale, float v_scale,
+                                          void* stream);
 
 /* ------------------------------------------------------------------------
  * Stream plumbing of a pipelined step (no counterpart in the pages: it is how

@@ -41,6 +41,8 @@ Modules:
 * ``block_manager``-- free list, block tables, reference counts, fork, CoW, free,
                       beam-search reshuffles, swapping to a host pool, and the
                       script replayer.
+* ``long_context`` -- position rotation, key bounds, block choice and attention
+                      over chosen blocks, as their definitions.
 * ``prefix_cache`` -- the block manager with full blocks shared across requests
                       by their exact prefix (evictable when unused).
 """

@@ -11,6 +11,9 @@ Entry points (same names as the C ABI):
 * ``paged_attention_decode`` -- decode attention through block tables.
 * ``reshape_and_cache``      -- slot-mapped write of new K/V (optionally E4M3).
 * ``copy_blocks``            -- whole-block copies for copy-on-write.
+* ``rotary_and_cache``       -- slot-mapped write with the position rotation of q and k.
+* ``update_key_bounds``, ``select_blocks``, ``paged_attention_decode_sparse`` --
+  decode attention over the blocks a bound on their logits selects.
 * ``paged_attention_workspace_size``, ``get_device_error``.
 * ``BlockManager``           -- the host block manager (free list, tables,
                                 reference counts, fork, copy-on-write).
@@ -28,7 +31,10 @@ __all__ = [
     "reshape_and_cache", "copy_blocks", "get_device_error", "check_wait_timeout",
     "BoundCall", "bind_paged_attention_decode", "bind_paged_attention_decode_grouped",
     "bind_reshape_and_cache", "bind_copy_blocks", "paged_decode_step", "bind_paged_decode_step", "paged_prefill_step",
-    "kernel_launches", "BlockManager",
+    "rotary_and_cache", "bind_rotary_and_cache", "rotary_table", "key_bounds_shape",
+    "key_bounds_dtype", "update_key_bounds", "bind_update_key_bounds", "select_blocks",
+    "bind_select_blocks", "select_blocks_workspace_size", "paged_attention_decode_sparse",
+    "bind_paged_attention_decode_sparse", "kernel_launches", "BlockManager",
     "library_path", "load_library", "pool_shapes", "pool_views", "pools_from_views", "PKV_F32",
     "PKV_BF16", "PKV_E4M3", "PKV_ERR_POOL_EXHAUSTED",
 ]
@@ -123,6 +129,18 @@ def load_library():
         "reshape_and_cache": (c_int, [vp, vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int,
                                       c_int, c_int, c_float, c_float, vp]),
         "copy_blocks": (c_int, [vp, vp, vp, c_int, c_int, c_size, vp]),
+        "rotary_and_cache": (c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32p, c_int,
+                                     ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                     ctypes.c_int64, c_int, c_int, c_int, c_int, c_int, c_int,
+                                     c_int, c_int, c_int, c_int, c_int, c_float, c_float, vp]),
+        "update_key_bounds": (c_int, [vp, vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int,
+                                      c_int, c_int, c_int, vp]),
+        "select_blocks": (c_int, [vp, vp, vp, vp, vp, c_int, c_int, c_int, c_int, c_int, c_int,
+                                  c_int, c_int, c_int, c_int, c_int, vp, c_size, vp]),
+        "select_blocks_workspace_size": (c_size, [c_int, c_int, c_int]),
+        "paged_attention_decode_sparse": (c_int, [vp, vp, vp, vp, vp, vp, vp, c_int, c_int, c_int,
+                                                  c_int, c_int, c_int, c_int, c_int, c_float,
+                                                  c_int, c_int, c_float, c_float, vp]),
         "pkv_get_device_error": (c_int, [ip, vp]),
         "pkv_check_wait_timeout": (c_int, [vp]),
         "pkv_stage_upload": (c_int, [vp, vp, c_size, vp, vp, vp, vp, vp]),
@@ -625,6 +643,226 @@ def bind_reshape_and_cache(k, v, k_pool, v_pool, slot_mapping, k_scale=1.0, v_sc
     args += _c_args([T, Hkv, D, bs, NB, _dt(k, "k"), _dt(k_pool, "k_pool"), float(k_scale),
                      float(v_scale)])
     return BoundCall(lib.reshape_and_cache, args, "reshape_and_cache", dev)
+
+
+def rotary_table(num_positions, rotary_dim, base=10000.0, stretch=1.0, device=None):
+    """Cosines and sines ``[num_positions, 2, rotary_dim // 2]`` float32 for
+    ``rotary_and_cache``: pair i of position p turns by ``p / stretch *
+    base**(-2 i / rotary_dim)``. Angles are formed in float64: a float32 angle
+    of position 10**6 would be off by up to 0.03."""
+    if num_positions <= 0 or rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("num_positions must be positive and rotary_dim positive and even")
+    if not base > 0 or not stretch > 0:
+        raise ValueError("base and stretch must be positive")
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    p = torch.arange(num_positions, dtype=torch.float64, device=device) / stretch
+    angle = p[:, None] * torch.pow(torch.tensor(base, dtype=torch.float64, device=device),
+                                   -2.0 * i / rotary_dim)
+    return torch.stack([angle.cos(), angle.sin()], 1).to(torch.float32)
+
+
+def rotary_and_cache(q_out, q, k, v, k_pool, v_pool, slot_mapping, positions, cos_sin,
+                     sections=None, interleaved=False, k_scale=1.0, v_scale=1.0, stream=None):
+    """Rotate q ``[T, Hq, D]`` and k ``[T, Hkv, D]`` by the tokens' positions;
+    q goes to ``q_out`` (which may be ``q``), k and v into the pools at
+    ``slot_mapping`` (int64 ``[T]``, < 0: padding, skipped).
+
+    ``positions``: int32 ``[T]``, or ``[A, T]`` for A axes (e.g. time, height,
+    width); ``cos_sin``: float32 ``[P, 2, R / 2]`` (``rotary_table``), R <= D
+    dims are rotated; ``sections``: the pairs each axis turns, in order, adding
+    up to R / 2 (None: one axis turns all); ``interleaved``: pairs are dims (2i,
+    2i + 1) instead of (i, i + R / 2). q_out, q, k and v may have any token
+    stride that is a multiple of 16 bytes (views of a fused projection)."""
+    bind_rotary_and_cache(q_out, q, k, v, k_pool, v_pool, slot_mapping, positions, cos_sin,
+                          sections, interleaved, k_scale, v_scale)(stream)
+    return q_out
+
+
+def _token_rows(t, name):
+    """The token stride of ``[T, H, D]`` rows whose heads are contiguous."""
+    T, H, D = t.shape
+    if (H > 1 and t.stride(1) != D) or (D > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if T > 1 else H * D
+
+
+def bind_rotary_and_cache(q_out, q, k, v, k_pool, v_pool, slot_mapping, positions, cos_sin,
+                          sections=None, interleaved=False, k_scale=1.0, v_scale=1.0):
+    """``rotary_and_cache`` checked once and bound to these tensors (``BoundCall``)."""
+    lib = load_library()
+    rows = ((q_out, "q_out"), (q, "q"), (k, "k"), (v, "v"))
+    rest = ((k_pool, "k_pool"), (v_pool, "v_pool"), (slot_mapping, "slot_mapping"),
+            (positions, "positions"), (cos_sin, "cos_sin"))
+    _tensors(rows + rest)
+    if q.dim() != 3 or q_out.shape != q.shape or q_out.dtype != q.dtype:
+        raise ValueError("q and q_out must be [T, Hq, D] of the same dtype")
+    T, Hq, D = q.shape
+    NB, Hkv, bs, D2 = _pool_dims(k_pool, v_pool)
+    if D2 != D or tuple(k.shape) != (T, Hkv, D) or v.shape != k.shape or k.dtype != q.dtype or \
+            v.dtype != q.dtype:
+        raise ValueError("k and v must be [T, Hkv, D] in the dtype of q, with the pools' Hkv and D")
+    if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int32:
+        raise TypeError("slot_mapping must be int64 and positions int32")
+    if tuple(slot_mapping.shape) != (T,) or positions.dim() not in (1, 2) or \
+            positions.shape[-1] != T:
+        raise ValueError("slot_mapping must be [T], positions [T] or [axes, T]")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if cos_sin.dtype != torch.float32:
+        raise TypeError("cos_sin must be float32")
+    if cos_sin.dim() != 3 or cos_sin.shape[1] != 2:
+        raise ValueError("cos_sin must be [P, 2, R / 2]")
+    half = cos_sin.shape[2]
+    sections = [half] if sections is None else [int(s) for s in sections]
+    if len(sections) != axes or sum(sections) != half or min(sections, default=-1) < 0:
+        raise ValueError("sections must give the pairs of each axis of positions, adding up to R / 2")
+    strides = [_token_rows(t, n) for t, n in rows]
+    if q_out.numel() and T > 1 and strides[0] < Hq * D:
+        raise ValueError("q_out: tokens overlap")
+    dev = _on_gpu(rest)
+    for t, n in rows:
+        if _cuda(t, n, contiguous=False).device != dev:
+            raise ValueError(f"{n} is on {t.device}, the other tensors on {dev}")
+    args = [_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool), _ptr(slot_mapping),
+            _ptr(positions), _ptr(cos_sin), (ctypes.c_int32 * axes)(*sections), ctypes.c_int(axes)]
+    args += [ctypes.c_int64(s) for s in strides]
+    args += _c_args([T, Hq, Hkv, D, 2 * half, bool(interleaved), bs, NB, cos_sin.shape[0], _dt(q, "q"),
+                     _dt(k_pool, "k_pool"), float(k_scale), float(v_scale)])
+    return BoundCall(lib.rotary_and_cache, args, "rotary_and_cache", dev)
+
+
+def key_bounds_shape(num_blocks, num_kv_heads, head_dim):
+    """Shape of the key bounds of a pool: (block, kv head, smallest / largest, dim)."""
+    return (num_blocks, num_kv_heads, 2, head_dim)
+
+
+def key_bounds_dtype(kv_dtype):
+    """dtype of the key bounds of a cache: float32 for float32, else bfloat16 (which
+    holds every E4M3 value)."""
+    return torch.float32 if kv_dtype == torch.float32 else torch.bfloat16
+
+
+def _check_bounds(key_bounds, NB, Hkv, D, dtype):
+    if tuple(key_bounds.shape) != key_bounds_shape(NB, Hkv, D):
+        raise ValueError("key_bounds must be [NB, Hkv, 2, D] (see key_bounds_shape)")
+    if key_bounds.dtype != dtype:
+        raise TypeError(f"key_bounds must be {dtype} here (see key_bounds_dtype)")
+
+
+def update_key_bounds(k_pool, key_bounds, block_tables, seq_lens, first_changed, max_new_tokens=0,
+                      stream=None):
+    """Per-dim smallest and largest key of every block that holds a position
+    ``first_changed[b] .. seq_lens[b] - 1`` (int32 ``[B]``) of a sequence, into
+    ``key_bounds`` (``key_bounds_shape``, ``key_bounds_dtype``); call it after a
+    step's keys are written. ``max_new_tokens``: the most positions that changed
+    in one sequence, sizing the launch (0: unknown)."""
+    bind_update_key_bounds(k_pool, key_bounds, block_tables, seq_lens, first_changed,
+                           max_new_tokens)(stream)
+    return key_bounds
+
+
+def bind_update_key_bounds(k_pool, key_bounds, block_tables, seq_lens, first_changed,
+                           max_new_tokens=0):
+    """``update_key_bounds`` checked once and bound to these tensors (``BoundCall``)."""
+    lib = load_library()
+    named = ((k_pool, "k_pool"), (key_bounds, "key_bounds"), (block_tables, "block_tables"),
+             (seq_lens, "seq_lens"), (first_changed, "first_changed"))
+    _tensors(named)
+    if k_pool.dim() != 6 or k_pool.shape[4] != 8 or k_pool.shape[5] * k_pool.element_size() != 16:
+        raise ValueError("k_pool must be [NB, Hkv, bs/8, D/X, 8, X] (see pool_shapes)")
+    NB, Hkv, bs, D = k_pool.shape[0], k_pool.shape[1], k_pool.shape[2] * 8, \
+        k_pool.shape[3] * k_pool.shape[5]
+    _check_bounds(key_bounds, NB, Hkv, D, key_bounds_dtype(k_pool.dtype))
+    for t in (block_tables, seq_lens, first_changed):
+        if t.dtype != torch.int32:
+            raise TypeError("block_tables, seq_lens and first_changed must be int32")
+    if seq_lens.dim() != 1 or block_tables.dim() != 2 or \
+            block_tables.shape[0] != seq_lens.shape[0] or first_changed.shape != seq_lens.shape:
+        raise ValueError("inconsistent shapes: block_tables [B, max_blocks], seq_lens and "
+                         "first_changed [B]")
+    dev = _on_gpu(named)
+    args = [_ptr(t) for t, _ in named]
+    args += _c_args([seq_lens.shape[0], block_tables.shape[1], NB, Hkv, D, bs, int(max_new_tokens),
+                     _dt(k_pool, "k_pool")])
+    return BoundCall(lib.update_key_bounds, args, "update_key_bounds", dev)
+
+
+def select_blocks_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq):
+    """Bytes of scratch that ``select_blocks`` needs for these sizes."""
+    return int(load_library().select_blocks_workspace_size(num_seqs, num_kv_heads,
+                                                           max_blocks_per_seq))
+
+
+def select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_size, first_blocks=1,
+                  last_blocks=1, workspace=None, stream=None):
+    """The blocks each sequence's decode query attends over, per kv head, into
+    ``selected`` (int32 ``[B, Hkv, K]``: logical blocks, ascending, -1 padded):
+    the first and last blocks and those whose ``key_bounds`` allow the largest
+    logits under q ``[B, Hq, D]`` (exact; equal scores by the lower index); every
+    block of a sequence that has at most K. ``workspace``: a CUDA tensor of
+    ``select_blocks_workspace_size`` bytes (not needed when no sequence can have
+    more than K blocks)."""
+    bind_select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_size, first_blocks,
+                       last_blocks, workspace)(stream)
+    return selected
+
+
+def bind_select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_size,
+                       first_blocks=1, last_blocks=1, workspace=None):
+    """``select_blocks`` checked once and bound to these tensors (``BoundCall``)."""
+    lib = load_library()
+    named = ((selected, "selected"), (q, "q"), (key_bounds, "key_bounds"),
+             (block_tables, "block_tables"), (seq_lens, "seq_lens"))
+    _tensors(named)
+    for t in (selected, block_tables, seq_lens):
+        if t.dtype != torch.int32:
+            raise TypeError("selected, block_tables and seq_lens must be int32")
+    if q.dim() != 3 or selected.dim() != 3 or key_bounds.dim() != 4:
+        raise ValueError("q must be [B, Hq, D], selected [B, Hkv, K], key_bounds [NB, Hkv, 2, D]")
+    B, Hq, D = q.shape
+    Hkv, K = selected.shape[1:]
+    _check_bounds(key_bounds, key_bounds.shape[0], Hkv, D, key_bounds_dtype(q.dtype))
+    if selected.shape[0] != B or tuple(seq_lens.shape) != (B,) or block_tables.dim() != 2 or \
+            block_tables.shape[0] != B:
+        raise ValueError("inconsistent shapes: selected [B, Hkv, K], block_tables [B, max_blocks], "
+                         "seq_lens [B]")
+    dev = _on_gpu(named)
+    ws_ptr, ws_bytes = _workspace(workspace, dev)
+    args = [_ptr(t) for t, _ in named]
+    args += _c_args([B, block_tables.shape[1], key_bounds.shape[0], Hq, Hkv, D, int(block_size), K,
+                     int(first_blocks), int(last_blocks), _dt(q, "q")])
+    args += [ctypes.c_void_p(ws_ptr), ctypes.c_size_t(ws_bytes)]
+    return BoundCall(lib.select_blocks, args, "select_blocks", dev)
+
+
+def paged_attention_decode_sparse(out, q, k_pool, v_pool, block_tables, seq_lens, selected, scale,
+                                  k_scale=1.0, v_scale=1.0, stream=None):
+    """``paged_attention_decode`` over the tokens of the blocks listed in
+    ``selected`` (int32 ``[B, Hkv, K]``: logical blocks of the sequence, strictly
+    ascending, -1 padded; ``select_blocks``' output or the caller's own list).
+    Needs no workspace."""
+    bind_paged_attention_decode_sparse(out, q, k_pool, v_pool, block_tables, seq_lens, selected,
+                                       scale, k_scale, v_scale)(stream)
+    return out
+
+
+def bind_paged_attention_decode_sparse(out, q, k_pool, v_pool, block_tables, seq_lens, selected,
+                                       scale, k_scale=1.0, v_scale=1.0):
+    """``paged_attention_decode_sparse`` checked once and bound to these tensors
+    (``BoundCall``)."""
+    lib = load_library()
+    B, Hq, D, NB, Hkv, bs = _decode_shapes(out, q, k_pool, v_pool, block_tables, seq_lens)
+    _tensors(((selected, "selected"),))
+    if selected.dtype != torch.int32:
+        raise TypeError("selected must be int32")
+    if selected.dim() != 3 or tuple(selected.shape[:2]) != (B, Hkv):
+        raise ValueError("selected must be [B, Hkv, K]")
+    named = ((out, "out"), (q, "q"), (k_pool, "k_pool"), (v_pool, "v_pool"),
+             (block_tables, "block_tables"), (seq_lens, "seq_lens"), (selected, "selected"))
+    dev = _on_gpu(named)
+    args = [_ptr(t) for t, _ in named]
+    args += _c_args([B, block_tables.shape[1], NB, selected.shape[2], Hq, Hkv, D, bs, float(scale),
+                     _dt(q, "q"), _dt(k_pool, "k_pool"), float(k_scale), float(v_scale)])
+    return BoundCall(lib.paged_attention_decode_sparse, args, "paged_attention_decode_sparse", dev)
 
 
 class BoundCall:

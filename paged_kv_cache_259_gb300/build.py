@@ -24,6 +24,12 @@ CUDA_SOURCES = [
     "pkv_decode_noalloc.cu",
     "pkv_prefill.cu",
     "pkv_pipeline.cu",
+    "pkv_rotary.cu",
+    "pkv_select.cu",
+    "pkv_sparse.cu",
+    "pkv_sparse_f32.cu",
+    "pkv_sparse_bf16.cu",
+    "pkv_sparse_e4m3.cu",
 ]
 CXX_SOURCES = ["block_manager.cpp"]
 

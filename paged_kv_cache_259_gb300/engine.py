@@ -22,9 +22,11 @@ import numpy as np
 import torch
 
 from . import (PKV_ERR_POOL_EXHAUSTED, BlockManager, DecodePipelineStepArgs, PagedKVError, _check,
-               _decode_shapes, _dt, _workspace, bind_paged_decode_step, copy_blocks, paged_attention_decode, paged_prefill_step,
-               paged_attention_decode_grouped, load_library, paged_attention_workspace_size, pool_shapes, pool_views,
-               reshape_and_cache, swap_blocks)
+               _decode_shapes, _dt, _workspace, bind_paged_decode_step, copy_blocks, key_bounds_dtype,
+               key_bounds_shape, paged_attention_decode, paged_attention_decode_sparse, paged_attention_prefill,
+               paged_prefill_step, paged_attention_decode_grouped, load_library, paged_attention_workspace_size,
+               pool_shapes, pool_views, reshape_and_cache, rotary_and_cache, select_blocks,
+               select_blocks_workspace_size, swap_blocks, update_key_bounds)
 
 
 @dataclass
@@ -438,12 +440,87 @@ class PagedKVCache:
             call(stream, **counts)
         return run
 
+    def enable_key_bounds(self):
+        """Keep the key bounds of every block (``update_key_bounds``), which sparse
+        decode steps choose their blocks by."""
+        if getattr(self, "key_bounds", None) is None:
+            self.key_bounds = torch.zeros(
+                key_bounds_shape(self.num_blocks, self.num_kv_heads, self.head_dim),
+                dtype=key_bounds_dtype(self.k_pool.dtype), device=self.device)
+        return self.key_bounds
+
+    def refresh_key_bounds(self, tables, lens, stream=None):
+        """Bounds of every block of these sequences (device tables and lengths),
+        e.g. after ``load`` or ``swap_in``."""
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
+            first = torch.zeros_like(lens)
+        first.record_stream(stream or torch.cuda.current_stream(self.device))
+        update_key_bounds(self.k_pool, self.enable_key_bounds(), tables, lens, first, stream=stream)
+
+    def select_workspace(self, batch, max_blocks):
+        """Scratch of a sparse step's block choice."""
+        n = select_blocks_workspace_size(batch, self.num_kv_heads, max_blocks)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
+
+    def _rotated_append(self, q, k_new, v_new, dev_plan, positions, first, rotary, max_new,
+                        k_scale, v_scale, stream):
+        if dev_plan["pairs"].shape[0]:
+            copy_blocks(self.k_pool, self.v_pool, dev_plan["pairs"], stream)
+        rotary_and_cache(q, q, k_new, v_new, self.k_pool, self.v_pool, dev_plan["slots"], positions,
+                         rotary.cos_sin, rotary.sections, rotary.interleaved, k_scale, v_scale, stream)
+        if getattr(self, "key_bounds", None) is not None:
+            update_key_bounds(self.k_pool, self.key_bounds, dev_plan["tables"], dev_plan["lens"], first,
+                              max_new, stream)
+
+    def rotary_prefill_step(self, q, k_new, v_new, dev_plan, positions, first, rotary, out, scale,
+                            max_query_len, stream=None):
+        """Device half of a chunked-prefill step on keys and queries as the
+        projection left them: CoW copies, rotation (q in place) and append, key
+        bounds (when kept), causal attention. ``positions``: int32 ``[T]`` or
+        ``[axes, T]``; ``first``: ``first_changed(plan)`` on the device."""
+        self._rotated_append(q, k_new, v_new, dev_plan, positions, first, rotary, max_query_len,
+                             1.0, 1.0, stream)
+        return paged_attention_prefill(out, q, self.k_pool, self.v_pool, dev_plan["tables"],
+                                       dev_plan["lens"], dev_plan["query_start"], scale,
+                                       max_query_len, stream)
+
+    def sparse_step(self, q, k_new, v_new, dev_plan, positions, first, rotary, selected, out, scale,
+                    first_blocks=1, last_blocks=1, k_scale=1.0, v_scale=1.0, workspace=None,
+                    stream=None):
+        """Device half of a decode step that attends over ``selected.shape[2]``
+        blocks of each sequence: CoW copies, rotation (q in place) and append, key
+        bounds, block choice into ``selected`` (int32 ``[B, Hkv, K]``), attention
+        over the chosen blocks. ``workspace``: ``select_workspace``."""
+        self.enable_key_bounds()
+        self._rotated_append(q, k_new, v_new, dev_plan, positions, first, rotary, 1, k_scale, v_scale,
+                             stream)
+        select_blocks(selected, q, self.key_bounds, dev_plan["tables"], dev_plan["lens"],
+                      self.block_size, first_blocks, last_blocks, workspace, stream)
+        return paged_attention_decode_sparse(out, q, self.k_pool, self.v_pool, dev_plan["tables"],
+                                             dev_plan["lens"], selected, scale, k_scale, v_scale, stream)
+
     def step(self, q, k_new, v_new, dev_plan, out, scale, k_scale=1.0, v_scale=1.0,
              workspace=None, stream=None):
         """The device half of a decode step: copies, slot writes, attention (one
         ``paged_decode_step`` call)."""
         self.bind_step(q, k_new, v_new, dev_plan, out, scale, k_scale, v_scale, workspace)(stream)
         return out
+
+
+@dataclass
+class Rotary:
+    """How a model turns its heads: the table (``rotary_table``), the pairs each
+    position axis turns (None: one axis) and which dims form a pair."""
+    cos_sin: torch.Tensor
+    sections: list = None
+    interleaved: bool = False
+
+
+def first_changed(plan):
+    """int32 ``[B]``: the first position each sequence of a decode or prefill plan
+    writes, for ``update_key_bounds``."""
+    new = plan.chunks if isinstance(plan, PrefillPlan) else 1
+    return (plan.lens - new).astype(np.int32)
 
 
 def slab_layout(templates, align=256):
