@@ -215,7 +215,7 @@ struct SelectParams {
     float* tile_max;                   // [B][Hkv][stride / 16]: largest |bound| of 16 blocks
     unsigned long long* exact;         // [B][Hkv][stride]
     int max_blocks, num_blocks, hq, hkv, d, bs, k, first, last;
-    int stride, cached;                // cached: scores a row keeps in shared memory
+    int stride, scored;                // scored: behind a scoring launch of the same call
     int* err;
 };
 
@@ -243,58 +243,110 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t x) {
     return r;
 }
 
-// Scores of 16 blocks per warp. The k order of the product is free as long as
-// both operands agree on it, so lane (r, c) loads 16 bytes of blocks r and r+8
-// at dims 32i + 8c .. +7 straight into the A fragments of k-steps 2i and 2i+1
-// (no shared memory), and the same dims of query head r into the B fragments.
-// Four accumulator chains (by i) shorten the dependency and the rounding.
-// Bound: HBM bytes of the bounds.
+// Scores of 16 blocks per warp at a time. The k order of the product is free as
+// long as both operands agree on it, so lane (r, c) loads 16 bytes of blocks r
+// and r+8 at dims 32i + 8c .. +7 straight into the A fragments of k-steps 2i and
+// 2i+1 (no shared memory), and the same dims of query head r into the B
+// fragments. Four accumulator chains (by i) shorten the dependency and the
+// rounding. The lower and the upper bounds of a tile are two halves of a software
+// pipeline: the next tile's half is loaded into the registers that the product
+// has just read, so a warp always has 4 to 8 KB on the way.
+// Bound: HBM bytes of the bounds. The 4 warps of a CTA take neighbouring kv heads
+// of the same blocks (as many as there are), so a block's rows are read together.
 template <int D>
-__global__ void __launch_bounds__(128) score_blocks_bf16(const SelectParams p, int tiles_per_warp) {
+struct ScoreTile {
+    static constexpr int I = D / 32;                       // 16-byte chunks a lane holds per bound
+    uint4 x0[I], x1[I];                                    // blocks r and r+8
+
+    __device__ __forceinline__ void load(const uint4* p0, const uint4* p1, bool ok0, bool ok1) {
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            x0[i] = ok0 ? __ldg(p0 + 4 * i) : make_uint4(0, 0, 0, 0);
+            x1[i] = ok1 ? __ldg(p1 + 4 * i) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    template <int CHAIN>                                   // I chains from CHAIN on (mod 4)
+    __device__ __forceinline__ void multiply(float (&acc)[4][4], uint32_t& m, const uint32_t (&q)[I][4]) const {
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            mma_bf16(acc[(CHAIN + i) & 3], x0[i].x, x1[i].x, x0[i].y, x1[i].y, q[i][0], q[i][1]);
+            mma_bf16(acc[(CHAIN + i) & 3], x0[i].z, x1[i].z, x0[i].w, x1[i].w, q[i][2], q[i][3]);
+            m = abs_max2(abs_max2(m, x0[i].x), x0[i].y);
+            m = abs_max2(abs_max2(m, x0[i].z), x0[i].w);
+            m = abs_max2(abs_max2(m, x1[i].x), x1[i].y);
+            m = abs_max2(abs_max2(m, x1[i].z), x1[i].w);
+        }
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(128, 4) score_blocks_bf16(const SelectParams p, int tiles_per_warp,
+                                                            int heads_per_cta) {
     pdl_enter();                                           // launched with launch_pdl
-    const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
-    const int n = row_blocks(p, b, false);
-    if (n <= p.k) return;                                  // every block is selected
-    const int lo = p.first, hi = n - p.last;               // blocks with a score: [lo, hi)
-    const int tile0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * tiles_per_warp;
-    if (tile0 * 16 >= hi) return;
+    using Tile = ScoreTile<D>;
+    constexpr int I = Tile::I;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.z;
     const int r = lane >> 2, c = lane & 3, G = p.hq / p.hkv;
-    constexpr int I = D / 32;                              // 16-byte chunks a lane holds per bound
+    const int h = blockIdx.y * heads_per_cta + w % heads_per_cta;
+    const int tile0 = (blockIdx.x * (4 / heads_per_cta) + w / heads_per_cta) * tiles_per_warp;
+    // the table and the query are read beside the length: entries past it are in
+    // the table, and unused
+    auto table_at = [&](int tile) {
+        const int j = tile * 16 + (lane & 15);
+        return j < p.max_blocks ? p.tables[(size_t)b * p.max_blocks + j] : -1;
+    };
+    int id_next = table_at(tile0);
     uint32_t qn[I][4], qp[I][4];                           // min(q, 0), max(q, 0)
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-        uint4 w = make_uint4(0, 0, 0, 0);
+        uint4 x = make_uint4(0, 0, 0, 0);
         if (r < G)
-            w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                ((size_t)b * p.hq + h * G + r) * D + 32 * i + 8 * c);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                     ((size_t)b * p.hq + h * G + r) * D + 32 * i + 8 * c));
+        qp[i][0] = x.x, qp[i][1] = x.y, qp[i][2] = x.z, qp[i][3] = x.w;
+    }
+    const int n = row_blocks(p, b, false);
+    if (n <= p.k) return;                                  // every block is selected
+    const int lo = p.first, hi = n - p.last;               // blocks with a score: [lo, hi)
+    const int first = max(tile0, lo / 16), end = min(tile0 + tiles_per_warp, (hi + 15) / 16);
+    if (first >= end) return;
+    if (first > tile0) id_next = table_at(first);
+#pragma unroll
+    for (int i = 0; i < I; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            qn[i][j] = min2(x[j], 0u, __nv_bfloat16{});
-            qp[i][j] = max2(x[j], 0u, __nv_bfloat16{});
+            qn[i][j] = min2(qp[i][j], 0u, __nv_bfloat16{});
+            qp[i][j] = max2(qp[i][j], 0u, __nv_bfloat16{});
         }
-    }
     const size_t row = (size_t)b * p.hkv + h;
-    for (int tile = tile0; tile < tile0 + tiles_per_warp && tile * 16 < hi; ++tile) {
-        if (tile * 16 + 15 < lo) continue;
+    const uint4* base = reinterpret_cast<const uint4*>(p.bounds) + (size_t)h * (D / 4) + c;
+    const size_t pitch = (size_t)p.hkv * (D / 4);          // 16-byte units of a block
+    // the ids of a tile's blocks r and r+8 (-1: no score), from the lanes' entries
+    auto blocks_of = [&](int tile, int id, int* id0, int* id1) {
         const int j = tile * 16 + (lane & 15);
-        int id = -1;
-        if (j >= lo && j < hi) {
-            id = p.tables[(size_t)b * p.max_blocks + j];
-            if (id < 0 || id >= p.num_blocks) {
-                flag_error(p.err, kErrOutOfRange);
-                id = -1;
-            }
+        if (j < lo || j >= hi) {
+            id = -1;
+        } else if (id < 0 || id >= p.num_blocks) {
+            flag_error(p.err, kErrOutOfRange);
+            id = -1;
         }
-        const int id0 = __shfl_sync(kFull, id, r), id1 = __shfl_sync(kFull, id, r + 8);
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.bounds);
-        const uint4* p0 = reinterpret_cast<const uint4*>(src + ((size_t)max(id0, 0) * p.hkv + h) * 2 * D) + c;
-        const uint4* p1 = reinterpret_cast<const uint4*>(src + ((size_t)max(id1, 0) * p.hkv + h) * 2 * D) + c;
-        uint4 x0[2 * I], x1[2 * I];
-#pragma unroll
-        for (int i = 0; i < 2 * I; ++i) {
-            x0[i] = id0 >= 0 ? __ldg(p0 + 4 * i) : make_uint4(0, 0, 0, 0);
-            x1[i] = id1 >= 0 ? __ldg(p1 + 4 * i) : make_uint4(0, 0, 0, 0);
+        *id0 = __shfl_sync(kFull, id, r);
+        *id1 = __shfl_sync(kFull, id, r + 8);
+    };
+    Tile lower, upper;
+    int id0, id1;
+    blocks_of(first, id_next, &id0, &id1);
+    id_next = first + 1 < end ? table_at(first + 1) : -1;
+    const uint4 *p0 = base + max(id0, 0) * pitch, *p1 = base + max(id1, 0) * pitch;
+    lower.load(p0, p1, id0 >= 0, id1 >= 0);
+    upper.load(p0 + D / 8, p1 + D / 8, id0 >= 0, id1 >= 0);
+    for (int tile = first; tile < end; ++tile) {
+        const bool ok0 = id0 >= 0, ok1 = id1 >= 0, more = tile + 1 < end;
+        if (more) {
+            blocks_of(tile + 1, id_next, &id0, &id1);
+            id_next = tile + 2 < end ? table_at(tile + 2) : -1;
+            p0 = base + max(id0, 0) * pitch;
+            p1 = base + max(id1, 0) * pitch;
         }
         float acc[4][4];
 #pragma unroll
@@ -302,16 +354,10 @@ __global__ void __launch_bounds__(128) score_blocks_bf16(const SelectParams p, i
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[a][e] = 0.f;
         uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 2 * I; ++i) {
-            const uint32_t(&qq)[4] = i < I ? qn[i < I ? i : 0] : qp[i < I ? 0 : i - I];
-            mma_bf16(acc[i & 3], x0[i].x, x1[i].x, x0[i].y, x1[i].y, qq[0], qq[1]);
-            mma_bf16(acc[i & 3], x0[i].z, x1[i].z, x0[i].w, x1[i].w, qq[2], qq[3]);
-            m = abs_max2(abs_max2(m, x0[i].x), x0[i].y);
-            m = abs_max2(abs_max2(m, x0[i].z), x0[i].w);
-            m = abs_max2(abs_max2(m, x1[i].x), x1[i].y);
-            m = abs_max2(abs_max2(m, x1[i].z), x1[i].w);
-        }
+        lower.template multiply<0>(acc, m, qn);
+        if (more) lower.load(p0, p1, id0 >= 0, id1 >= 0);
+        upper.template multiply<I>(acc, m, qp);
+        if (more) upper.load(p0 + D / 8, p1 + D / 8, id0 >= 0, id1 >= 0);
         // heads 2c, 2c+1 of blocks r (s0) and r+8 (s1); columns past G are no heads
         float s0 = -INFINITY, s1 = -INFINITY;
 #pragma unroll
@@ -327,14 +373,12 @@ __global__ void __launch_bounds__(128) score_blocks_bf16(const SelectParams p, i
         }
         float* out = p.scores + row * p.stride + tile * 16;
         if (c == 0) {
-            out[r] = id0 >= 0 ? s0 + 0.f : -INFINITY;      // + 0: no negative zero
-            out[r + 8] = id1 >= 0 ? s1 + 0.f : -INFINITY;
+            out[r] = ok0 ? s0 + 0.f : -INFINITY;           // + 0: no negative zero
+            out[r + 8] = ok1 ? s1 + 0.f : -INFINITY;
         }
-        m &= 0x7fff7fffu;
-        float mf = max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) mf = max_nan(mf, __shfl_xor_sync(kFull, mf, o));
-        if (lane == 0) p.tile_max[row * (p.stride / 16) + tile] = mf;
+        m &= 0x7fff7fffu;                                  // bf16 order is its bits' order; NaN above
+        const uint32_t mm = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
+        if (lane == 0) p.tile_max[row * (p.stride / 16) + tile] = __uint_as_float(mm << 16);
     }
 }
 
@@ -342,7 +386,8 @@ __global__ void __launch_bounds__(128) score_blocks_bf16(const SelectParams p, i
 // block at a time, lane l the dims l, l + 32, ..., and the heads' sums are
 // reduced across the lanes.
 template <int D>
-__global__ void __launch_bounds__(128) score_blocks_f32(const SelectParams p, int tiles_per_warp) {
+__global__ void __launch_bounds__(128) score_blocks_f32(const SelectParams p, int tiles_per_warp,
+                                                        int) {
     pdl_enter();                                           // launched with launch_pdl
     const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
     const int n = row_blocks(p, b, false);
@@ -414,64 +459,144 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
     return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
 }
 
-constexpr int kBins = 2048;            // 11 bits a pass
-constexpr int kListMax = 1024;         // candidates ranked in shared memory
+// 2^(127 - e) for the biased exponent e of a finite float: brings it into [1, 2)
+// (below 1 if it is subnormal).
+__device__ __forceinline__ float unit_scale(float x) {
+    const int e = max((int)(__float_as_uint(x) >> 23), 1);
+    return __uint_as_float(e < 254 ? (uint32_t)(254 - e) << 23 : 0x00400000u);
+}
 
-// One CTA per (kv head, sequence) over the row's scores: threshold by radix
-// passes over the score's range (the range cut into 2,048 bins, then the bin,
-// ...; three passes at most), the 64-bit tie break when the rounding window is
-// crowded, then the selected blocks' bits written out in ascending order.
-// Bound: latency (a row is at most a few hundred KB of scores, from L2).
-template <typename T, int NT>
+// What a term leaves of itself in three exact float32 sums: x is cut at 2^-19, the
+// rest at 2^-35, the rest of that at 2^-51 (adding and subtracting 1.5 x 2^23 units
+// rounds to the unit). With sums of magnitudes below 4 every sum is a whole number
+// of its unit below 2^24, so it is exact in any order.
+__device__ __forceinline__ void add_exact(float (&s)[3], float x) {
+    const float a = __fadd_rn(__fadd_rn(x, 24.f), -24.f);
+    s[0] = __fadd_rn(s[0], a);
+    x = __fadd_rn(x, -a);
+    const float b = __fadd_rn(__fadd_rn(x, 0x1.8p-12f), -0x1.8p-12f);
+    s[1] = __fadd_rn(s[1], b);
+    x = __fadd_rn(x, -b);
+    s[2] = __fadd_rn(s[2], __fadd_rn(__fadd_rn(x, 0x1.8p-28f), -0x1.8p-28f));
+}
+
+// The score of a block (row `id_row` of the bounds) under heads g0 .. g1-1 (rows
+// of `qs`, float32 in shared memory) in 64 bits, as an ordered key above 0 (the
+// whole warp). The query times scale_q and the bounds times scale_b make a score's
+// magnitudes sum to less than 4; its terms, exact products (float32 inputs: with
+// the rest of the product), are summed exactly down to 2^-51. (In float64, at two
+// multiply-adds a clock per SM, a block with 8 heads took 3 us.)
+template <typename T>
+__device__ __forceinline__ unsigned long long exact_key(const T* bounds, size_t id_row, int d, const float* qs,
+                                                        int g0, int g1, int lane, float scale_q, float scale_b) {
+    const T* bl = bounds + id_row * 2 * d + lane;
+    float lo[4], hi[4];                                     // d is 64 or 128
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo[i] = 32 * i < d ? (float)bl[32 * i] * scale_b : 0.f;
+        hi[i] = 32 * i < d ? (float)bl[d + 32 * i] * scale_b : 0.f;
+    }
+    unsigned long long best = 0;
+    for (int g = g0; g < g1; ++g) {
+        float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (32 * i >= d) break;
+            const float q = qs[g * d + lane + 32 * i] * scale_q;
+            const float x = q < 0.f ? lo[i] : hi[i];
+            const float t = __fmul_rn(q, x);
+            add_exact(s, t);
+            if constexpr (std::is_same<T, float>::value) add_exact(s, __fmaf_rn(q, x, -t));
+        }
+        const long long i0 = __reduce_add_sync(kFull, (int)(s[0] * 0x1p19f));
+        const long long i1 = __reduce_add_sync(kFull, (int)(s[1] * 0x1p35f));
+        const long long i2 = __reduce_add_sync(kFull, (int)(s[2] * 0x1p51f));
+        const long long sum = i0 * (1ll << 32) + i1 * (1ll << 16) + i2;
+        best = max(best, (unsigned long long)sum ^ (1ull << 63));
+    }
+    return best;
+}
+// The same in float64, for rows with values that are not finite: a block that no
+// finite score describes comes first.
+template <typename T>
+__device__ unsigned long long exact_key_f64(const SelectParams& p, int b, int h, int id, int lane) {
+    const int G = p.hq / p.hkv, d = p.d;
+    const T* bl = static_cast<const T*>(p.bounds) + ((size_t)id * p.hkv + h) * 2 * d;
+    double best = -INFINITY;
+    bool nan = false;
+    for (int g = 0; g < G; ++g) {
+        const T* qr = static_cast<const T*>(p.q) + ((size_t)b * p.hq + h * G + g) * d;
+        double s = 0.0;
+        for (int i = lane; i < d; i += 32) {
+            const double q = (double)(float)qr[i];
+            const double neg = q > 0.0 ? 0.0 : q, pos = q < 0.0 ? 0.0 : q;   // NaN stays
+            s = fma(neg, (double)(float)bl[i], s);
+            s = fma(pos, (double)(float)bl[d + i], s);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+        nan |= s != s;
+        best = s > best ? s : best;
+    }
+    if (nan || !(fabs(best) < INFINITY)) best = INFINITY;
+    return ordered64(best + 0.0);
+}
+
+constexpr int kBins = 1024;
+constexpr int kListMax = 1024;         // blocks ranked in shared memory
+
+// One CTA per (kv head, sequence) over the row's scores. A thread owns chunks of
+// 8 blocks (KEEP: one chunk, in registers). The score range is cut into 1,024
+// equal bins; the bin of the last place and its neighbours within the rounding
+// window hold the few blocks that are undecided (the range is cut again when they
+// are too many), which are ranked among themselves: by their float32 scores, and
+// those within the window of the last place by their 64-bit scores if there are
+// more of them than places. A bin of a score is a monotone function of it, so
+// bins decide soundly whatever the rounding of their edges.
+// Bound: latency (a row's scores are at most a few hundred KB, from L2).
+template <typename T, int NT, bool KEEP>
 __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
-    pdl_enter();                                           // launched with launch_pdl
     constexpr int NW = NT / 32;
+    // Launched behind this call's scoring kernel: lengths, tables and queries were
+    // written before that launch began, its scores only when it has completed.
+    if (p.scored) launch_dependents();
+    else pdl_enter();
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const size_t row = (size_t)b * p.hkv + h;
     int32_t* out = p.selected + row * p.k;
     const int n = row_blocks(p, b, h == 0 && tid == 0);
     if (n <= p.k) {                                        // all of them
+        if (p.scored) wait_prerequisites();
         for (int i = tid; i < p.k; i += NT) out[i] = i < n ? i : -1;
         return;
     }
     extern __shared__ __align__(16) unsigned char smem[];
-    const int words = (n + 31) / 32;
     const int words_max = (p.max_blocks + 31) / 32;
     unsigned long long* list_key = reinterpret_cast<unsigned long long*>(smem);    // [kListMax]
-    int* list_id = reinterpret_cast<int*>(list_key + kListMax);                    // [kListMax]
-    uint32_t* hist = reinterpret_cast<uint32_t*>(list_id + kListMax);              // [kBins]
+    float* list_s = reinterpret_cast<float*>(list_key + kListMax);                 // [kListMax]
+    int* list_id = reinterpret_cast<int*>(list_s + kListMax);                      // [kListMax]
+    int* list_row = list_id + kListMax;                                            // [kListMax]
+    float* qf = reinterpret_cast<float*>(list_row + kListMax);                     // [8][128]
+    uint32_t* hist = reinterpret_cast<uint32_t*>(qf + 8 * 128);                    // [kBins]
     uint32_t* sel = hist + kBins;                                                  // selected blocks
-    uint32_t* cand = sel + words_max;                                              // undecided blocks
-    float* cache = reinterpret_cast<float*>(cand + words_max);                     // [cached]
-    __shared__ uint32_t warp_a[NW], warp_b[NW];
-    __shared__ uint32_t sh_bin, sh_left;
+    uint32_t* cand = sel + words_max;                                              // a crowd
+    unsigned char* sel8 = reinterpret_cast<unsigned char*>(sel);
+    unsigned char* cand8 = reinterpret_cast<unsigned char*>(cand);
+    __shared__ uint32_t sh_a[NW], sh_b[NW], sh_q[NW], sh_m[NW];
+    __shared__ int sh_bin, sh_cnt, sh_win[2];
+    __shared__ float sh_thr;
 
     const int lo = p.first, hi = n - p.last;               // scored blocks
-    const int nmid = hi - lo, need = p.k - p.first - p.last;   // 0 <= need < nmid
-    const float* scores = p.scores + row * p.stride + lo;
-    const bool in_smem = nmid <= p.cached;
-    for (int i = tid; i < words; i += NT) {
-        // the forced blocks' bits: [0, first) and [n - last, n)
-        uint32_t bits = 0;
-        for (int j = 0; j < 32; ++j) {
-            const int blk = 32 * i + j;
-            if (blk < lo || (blk >= hi && blk < n)) bits |= 1u << j;
-        }
-        sel[i] = bits;
-        cand[i] = 0;
-    }
-
-    auto block_sum = [&](uint32_t a, uint32_t bb, uint32_t* suma, uint32_t* sumb) {
-        a = __reduce_add_sync(kFull, a);
-        bb = __reduce_add_sync(kFull, bb);
-        __syncthreads();                                   // earlier readers of warp_a / warp_b
-        if (lane == 0) warp_a[w] = a, warp_b[w] = bb;
-        __syncthreads();
-        uint32_t x = lane < NW ? warp_a[lane] : 0, y = lane < NW ? warp_b[lane] : 0;
-        *suma = __reduce_add_sync(kFull, x);
-        *sumb = __reduce_add_sync(kFull, y);
+    const int need = p.k - p.first - p.last;               // 0 <= need < hi - lo
+    const int chunks = (n + 7) / 8;
+    // a chunk's blocks below n, and those of them that are scored
+    auto below = [](int c, int end) -> uint32_t {
+        const int m = end - 8 * c;
+        return m >= 8 ? 0xffu : m <= 0 ? 0u : (1u << m) - 1u;
     };
-    // exclusive prefix over the threads
+    auto scored_of = [&](int c) { return below(c, hi) & ~below(c, lo); };
+    auto forced_of = [&](int c) { return below(c, n) & ~scored_of(c); };
+    // exclusive prefix over the threads, and the total
     auto block_scan = [&](uint32_t v, uint32_t* total) -> uint32_t {
         uint32_t incl = v;
 #pragma unroll
@@ -479,20 +604,14 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
             const uint32_t t = __shfl_up_sync(kFull, incl, o);
             if (lane >= o) incl += t;
         }
+        __syncthreads();                                   // earlier readers of sh_a
+        if (lane == 31) sh_a[w] = incl;
         __syncthreads();
-        if (lane == 31) warp_a[w] = incl;
-        __syncthreads();
-        uint32_t x = lane < NW ? warp_a[lane] : 0, xi = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t t = __shfl_up_sync(kFull, xi, o);
-            if (lane >= o) xi += t;
-        }
-        *total = __shfl_sync(kFull, xi, 31);
-        return __shfl_sync(kFull, xi - x, w) + incl - v;
+        const uint32_t x = lane < NW ? sh_a[lane] : 0;
+        const uint32_t under = __reduce_add_sync(kFull, lane < w ? x : 0u);
+        *total = __reduce_add_sync(kFull, x);
+        return under + incl - v;
     };
-    const int per = (words + NT - 1) / NT;                 // bitmap words of a thread, in order
-    const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
 
     if (need > 0) {
         // ---- how far a score can be off. A = max_g sum_d |q_gd| times the largest
@@ -506,67 +625,105 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
         float qsum = 0.f;
         if (w < G) {
             const T* qr = static_cast<const T*>(p.q) + ((size_t)b * p.hq + h * G + w) * d;
-            for (int i = lane; i < d; i += 32) qsum += fabsf((float)qr[i]);
+            for (int i = lane; i < d; i += 32) {
+                const float q = (float)qr[i];
+                qf[w * d + i] = q;
+                qsum += fabsf(q);
+            }
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) qsum += __shfl_xor_sync(kFull, qsum, o);
         }
-        float mx = 0.f;
-        const float* tm = p.tile_max + row * (p.stride / 16);
-        for (int i = lo / 16 + tid; i * 16 < hi; i += NT) mx = max_nan(mx, tm[i]);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(kFull, mx, o));
-        if (lane == 0) {
-            warp_a[w] = __float_as_uint(qsum);             // 0 for warps past G
-            warp_b[w] = __float_as_uint(mx);
-        }
-        // ---- the row's scores, their range
-        uint32_t kmin = 0xffffffffu, kmax = 0;
-        for (int i = tid; i < nmid; i += NT) {
-            const float s = scores[i];
-            if (in_smem) cache[i] = s;
-            const uint32_t k = ordered(s);
-            kmin = min(kmin, k);
-            kmax = max(kmax, k);
-        }
-        kmin = __reduce_min_sync(kFull, kmin);
-        kmax = __reduce_max_sync(kFull, kmax);
-        if (lane == 0) list_id[w] = (int)kmin, list_id[32 + w] = (int)kmax;
-        __syncthreads();
-        const float qs = lane < NW ? __uint_as_float(warp_a[lane]) : 0.f;
-        const float ms = lane < NW ? __uint_as_float(warp_b[lane]) : 0.f;
-        kmin = __reduce_min_sync(kFull, lane < NW ? (uint32_t)list_id[lane] : 0xffffffffu);
-        kmax = __reduce_max_sync(kFull, lane < NW ? (uint32_t)list_id[32 + lane] : 0u);
-        float qm = qs, mm = ms;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            qm = max_nan(qm, __shfl_xor_sync(kFull, qm, o));
-            mm = max_nan(mm, __shfl_xor_sync(kFull, mm, o));
-        }
-        const float A = qm * mm;
-        // (1e-35: products too small for float32; a zero side makes every score 0)
-        const bool zero = qm == 0.f || mm == 0.f;
-        const float E = zero ? 0.f : A * (std::is_same<T, float>::value ? 0x1p-19f : 0x1p-16f) + 1e-35f;
-        const bool sane = A < 1e37f;                       // false for NaN too
-        const float* src = in_smem ? cache : scores;
+        for (int i = tid; i < kBins; i += NT) hist[i] = 0;
+        if (tid == 0) sh_cnt = 0, sh_win[0] = 0, sh_win[1] = 0;
+        if (p.scored) wait_prerequisites();
 
-        uint32_t left = need;                              // places among the undecided blocks
-        uint32_t undecided = nmid;
-        if (sane) {
-            // ---- T: the need-th largest score
-            uint32_t base = kmin, range = kmax - kmin;
-            uint32_t want = need;
-            while (range > 0) {
-                const int bits = 32 - __clz(range);
-                const int shift = bits > 11 ? bits - 11 : 0;
-                for (int i = tid; i < kBins; i += NT) hist[i] = 0;
-                __syncthreads();
-                for (int i = tid; i < nmid; i += NT) {
-                    const uint32_t off = ordered(src[i]) - base;
-                    if (ordered(src[i]) >= base && off <= range) atomicAdd(&hist[off >> shift], 1u);
+        const T* bounds = static_cast<const T*>(p.bounds);
+        const float* scores = p.scores + row * p.stride;   // 64-byte aligned rows
+        // a chunk's scores, -inf for blocks that have none
+        auto load_chunk = [&](int c, float (&s)[8]) {
+            const float4 x = *reinterpret_cast<const float4*>(scores + 8 * c);
+            const float4 y = *reinterpret_cast<const float4*>(scores + 8 * c + 4);
+            s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
+            s[4] = y.x, s[5] = y.y, s[6] = y.z, s[7] = y.w;
+            const uint32_t m = scored_of(c);
+            if (m != 0xffu) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] = (m >> j) & 1 ? s[j] : -INFINITY;
+            }
+        };
+        float kept[8];
+        // f(chunk, its scores) for every chunk of this thread
+        auto for_chunks = [&](auto f) {
+            if constexpr (KEEP) {
+                if (tid < chunks) f(tid, kept);
+            } else {
+                for (int c = tid; c < chunks; c += NT) {
+                    float s[8];
+                    load_chunk(c, s);
+                    f(c, s);
                 }
+            }
+        };
+        uint32_t mx = 0;                                   // |bounds|: their bits' order, NaN on top
+        const float* tm = p.tile_max + row * (p.stride / 16);
+        for (int i = lo / 16 + tid; i * 16 < hi; i += NT) mx = max(mx, __float_as_uint(__ldcg(tm + i)));
+        if (KEEP && tid < chunks) load_chunk(tid, kept);
+        float smin = INFINITY, smax = -INFINITY;
+        for_chunks([&](int, const float (&s)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                smin = fminf(smin, s[j] == -INFINITY ? INFINITY : s[j]);
+                smax = fmaxf(smax, s[j]);
+            }
+        });
+        const uint32_t kmin = __reduce_min_sync(kFull, ordered(smin));
+        const uint32_t kmax = __reduce_max_sync(kFull, ordered(smax));
+        mx = __reduce_max_sync(kFull, mx);
+        const uint32_t qx = __reduce_max_sync(kFull, __float_as_uint(qsum));
+        if (lane == 0) sh_a[w] = kmin, sh_b[w] = kmax, sh_q[w] = qx, sh_m[w] = mx;
+        __syncthreads();
+        float rlo = unordered(__reduce_min_sync(kFull, lane < NW ? sh_a[lane] : 0xffffffffu));
+        float rhi = unordered(__reduce_max_sync(kFull, lane < NW ? sh_b[lane] : 0u));
+        const float qm = __uint_as_float(__reduce_max_sync(kFull, lane < NW ? sh_q[lane] : 0u));
+        const float mm = __uint_as_float(__reduce_max_sync(kFull, lane < NW ? sh_m[lane] : 0u));
+        const float A = qm * mm;
+        // 1e-35: products too small for float32
+        const float E = A * (std::is_same<T, float>::value ? 0x1p-19f : 0x1p-16f) + 1e-35f;
+        const float win = 2.02f * E;                       // 2E, and the rounding of what it is added to
+        const bool sane = A < 1e37f;                       // false for NaN too
+        const bool finite = qm < INFINITY && mm < INFINITY;
+        const float scale_q = unit_scale(qm), scale_b = unit_scale(mm);   // for exact_key
+
+        bool crowd = false;                                // the undecided blocks are in `cand`
+        bool all = !sane;                                  // and are all that have a score
+        int left = need;                                   // places among the undecided blocks
+        if (sane && (qm == 0.f || mm == 0.f)) {
+            // every score is zero: the lowest blocks
+            for_chunks([&](int c, const float (&)[8]) {
+                sel8[c] = (unsigned char)(forced_of(c) | (below(c, lo + need) & ~below(c, lo)));
+            });
+        } else if (sane) {
+            // ---- bins over [rlo, rhi]; scores above it are in, scores below out
+            int bin0 = 0, bin1 = 0;                        // undecided bins
+            float inv = 0.f;
+            auto bin_of = [&](float s) -> int {            // -1: below the range
+                if (s > rhi) return kBins - 1;
+                return s < rlo ? -1 : min(kBins - 2, (int)((s - rlo) * inv));
+            };
+            int bins[8];                                   // KEEP: of the scores this thread holds
+            for (int round = 0;; ++round) {
+                const float width = (rhi - rlo) * (1.f / (kBins - 2));
+                inv = width > 1e-30f && width < 1e30f ? 1.f / width : 0.f;
+                for_chunks([&](int, const float (&s)[8]) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int bin = bin_of(s[j]);
+                        if (KEEP) bins[j] = bin;
+                        if (bin >= 0) atomicAdd(&hist[bin], 1u);
+                    }
+                });
                 __syncthreads();
-                // the bin that holds the want-th from the top: thread t sums the
-                // bins kBins-1 - t*BPT downwards
+                // the bin of the last place: thread t sums bins from the top down
                 constexpr int BPT = kBins / NT;
                 uint32_t cnt[BPT], sum = 0;
 #pragma unroll
@@ -574,211 +731,265 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
                     cnt[i] = hist[kBins - 1 - (tid * BPT + i)];
                     sum += cnt[i];
                 }
+                const float reach = win * inv;             // the window in bins
+                const int span = reach < (float)kBins ? (int)reach + 2 : kBins;
                 uint32_t total;
                 uint32_t above = block_scan(sum, &total);
+                if ((int)total < need) {                   // blocks with a bad id must fill up
+                    all = true;
+                    break;
+                }
 #pragma unroll
                 for (int i = 0; i < BPT; ++i) {
-                    if (above < want && want <= above + cnt[i]) {
-                        sh_bin = kBins - 1 - (tid * BPT + i);
-                        sh_left = want - above;
+                    if (above < (uint32_t)need && (uint32_t)need <= above + cnt[i]) {
+                        // this thread: the bin, what lies above its window, what in it
+                        const int bin = kBins - 1 - (tid * BPT + i);
+                        int over = above, in = cnt[i];
+                        for (int x = bin + 1; x <= min(kBins - 2, bin + span); ++x) over -= hist[x], in += hist[x];
+                        for (int x = max(0, bin - span); x < bin; ++x) in += hist[x];
+                        sh_bin = bin;
+                        sh_win[0] = over;
+                        sh_win[1] = in;
                     }
                     above += cnt[i];
                 }
                 __syncthreads();
-                base += sh_bin << shift;
-                want = sh_left;
-                // what is left of the range inside that bin
-                const uint32_t top = kmax - base;
-                range = shift == 0 ? 0u : min((1u << shift) - 1u, top);
-                __syncthreads();                           // sh_bin, hist are rewritten
+                const int bin = sh_bin;
+                bin0 = max(0, bin - span);
+                bin1 = min(kBins - 2, bin + span);
+                left = need - sh_win[0];
+                crowd = sh_win[1] > kListMax;
+                if (!crowd || round == 3 || inv == 0.f || bin1 - bin0 > kBins / 4) break;
+                // too many to rank: cut the undecided bins (and one more on each side) again
+                const float a = rlo + (float)(bin0 - 1) * width, z = rlo + (float)(bin1 + 2) * width;
+                rlo = fmaxf(rlo, a);
+                rhi = fminf(rhi, z);
+                __syncthreads();                           // hist, sh_bin, sh_win are read
+                for (int i = tid; i < kBins; i += NT) hist[i] = 0;
+                __syncthreads();
             }
-            const float thr = unordered(base);
-            // ---- the window 2E around it (2.02: the rounding of these two sums)
-            const float win = 2.02f * E, up = thr + win, dn = thr - win;
-            uint32_t in = 0, near = 0;
-            for (int i = tid; i < nmid; i += NT) {
-                const float s = src[i];
-                in += s > up;
-                near += s >= dn && s <= up;
-            }
-            uint32_t n_in, n_near;
-            block_sum(in, near, &n_in, &n_near);
-            left = need - n_in;
-            undecided = n_near;
-            for (int i0 = tid - lane; i0 < nmid; i0 += NT) {
-                const int i = i0 + lane;
-                const float s = i < nmid ? src[i] : 0.f;
-                const bool is_in = i < nmid && s > up, is_near = i < nmid && s >= dn && s <= up;
-                // block lo + i: bit (lo + i) & 31 of its word; a warp's 32 blocks
-                // reach over two words at most
-                if (is_in) atomicOr(&sel[(lo + i) >> 5], 1u << ((lo + i) & 31));
-                if (is_near) atomicOr(&cand[(lo + i) >> 5], 1u << ((lo + i) & 31));
-            }
-        } else {
-            for (int i = tid; i < nmid; i += NT)
-                atomicOr(&cand[(lo + i) >> 5], 1u << ((lo + i) & 31));
-        }
-        __syncthreads();
-
-        if (undecided > left && !(sane && zero)) {
-            // ---- score the undecided blocks in 64 bits (products of two float32 or
-            // bf16 values are exact there; one order of summation for all blocks)
-            auto exact_key = [&](int blk) -> unsigned long long {   // the whole warp
-                const int id = p.tables[(size_t)b * p.max_blocks + blk];
-                if (id < 0 || id >= p.num_blocks) return 0ull;      // flagged when it was scored
-                const T* bl = static_cast<const T*>(p.bounds) + ((size_t)id * p.hkv + h) * 2 * d;
-                double best = -INFINITY;
-                bool nan = false;
-                for (int g = 0; g < G; ++g) {
-                    const T* qr = static_cast<const T*>(p.q) + ((size_t)b * p.hq + h * G + g) * d;
-                    double s = 0.0;
-                    for (int i = lane; i < d; i += 32) {
-                        const double q = (double)(float)qr[i];
-                        const double neg = q > 0.0 ? 0.0 : q, pos = q < 0.0 ? 0.0 : q;   // NaN stays
-                        s = fma(neg, (double)(float)bl[i], s);
-                        s = fma(pos, (double)(float)bl[d + i], s);
-                    }
+            if (!all) {
+                for_chunks([&](int c, const float (&s)[8]) {
+                    uint32_t in = forced_of(c), un = 0;
 #pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-                    nan |= s != s;
-                    best = s > best ? s : best;
-                }
-                // a block that no finite score describes comes first
-                if (nan || !(fabs(best) < INFINITY)) best = INFINITY;
-                return ordered64(best + 0.0);
-            };
-            uint32_t mine = 0;
-            for (int i = w0; i < w1; ++i) mine += __popc(cand[i]);
-            uint32_t total;
-            uint32_t at = block_scan(mine, &total);
-            if (total <= kListMax) {
-                for (int i = w0; i < w1; ++i)
-                    for (uint32_t m = cand[i]; m; m &= m - 1) list_id[at++] = 32 * i + __ffs(m) - 1;
-                __syncthreads();
-                for (int i = w; i < (int)total; i += NW) {
-                    const unsigned long long k = exact_key(list_id[i]);
-                    if (lane == 0) list_key[i] = k;
-                }
-                __syncthreads();
-                for (int i = tid; i < (int)total; i += NT) {
-                    const unsigned long long k = list_key[i];
-                    uint32_t before = 0;
-                    for (int j = 0; j < (int)total; ++j)
-                        before += list_key[j] > k || (list_key[j] == k && j < i);
-                    if (before < left) atomicOr(&sel[list_id[i] >> 5], 1u << (list_id[i] & 31));
-                }
-                undecided = left = 0;                      // decided
-            } else {
-                // a crowd (degenerate scores): keys to the workspace, threshold by
-                // bisection of the 64-bit keys
-                unsigned long long* key = p.exact + row * p.stride;
-                for (int blk = lo + w; blk < hi; blk += NW)
-                    if ((cand[blk >> 5] >> (blk & 31)) & 1) {
-                        const unsigned long long k = exact_key(blk);
-                        if (lane == 0) key[blk] = k;
+                    for (int j = 0; j < 8; ++j) {
+                        const int bin = KEEP ? bins[j] : bin_of(s[j]);
+                        in |= bin > bin1 ? 1u << j : 0u;
+                        un |= bin >= bin0 && bin <= bin1 ? 1u << j : 0u;
                     }
-                __syncthreads();
-                unsigned long long thr = 0;                // largest t with >= left keys >= t
-                for (int bit = 63; bit >= 0; --bit) {
-                    const unsigned long long t = thr | (1ull << bit);
-                    uint32_t c = 0;
-                    for (int blk = lo + tid; blk < hi; blk += NT)
-                        c += ((cand[blk >> 5] >> (blk & 31)) & 1) && key[blk] >= t;
-                    uint32_t all, none;
-                    block_sum(c, 0, &all, &none);
-                    if (all >= left) thr = t;
-                }
-                uint32_t c = 0;
-                for (int blk = lo + tid; blk < hi; blk += NT) {
-                    const uint32_t bit = 1u << (blk & 31);
-                    if (!(cand[blk >> 5] & bit)) continue;
-                    if (key[blk] > thr) {
-                        atomicOr(&sel[blk >> 5], bit);
-                        ++c;
+                    sel8[c] = (unsigned char)in;
+                    if (crowd) {
+                        cand8[c] = (unsigned char)un;
+                    } else if (un) {
+                        int at = atomicAdd(&sh_cnt, __popc(un));
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if ((un >> j) & 1) {
+                                list_s[at] = s[j];
+                                list_key[at] = 0;
+                                list_row[at] = p.tables[(size_t)b * p.max_blocks + 8 * c + j];   // a good id
+                                list_id[at++] = 8 * c + j;
+                            }
                     }
-                    if (key[blk] != thr) atomicAnd(&cand[blk >> 5], ~bit);
-                }
-                uint32_t above, none;
-                block_sum(c, 0, &above, &none);
-                left -= above;
-                undecided = left + 1;                      // equal keys: by index
+                });
             }
+        }
+        if (all) {
+            for_chunks([&](int c, const float (&)[8]) {
+                sel8[c] = (unsigned char)forced_of(c);
+                cand8[c] = (unsigned char)scored_of(c);
+            });
+            crowd = true;
+            left = need;
         }
         __syncthreads();
-        if (left > 0) {
-            // ---- the `left` lowest-indexed undecided blocks (all of them, or equals)
-            uint32_t mine = 0;
-            for (int i = w0; i < w1; ++i) mine += __popc(cand[i]);
-            uint32_t total;
-            uint32_t at = block_scan(mine, &total);
-            for (int i = w0; i < w1; ++i) {
-                uint32_t m = cand[i], take = 0;
-                for (; m && at < left; m &= m - 1, ++at) take |= m & (~m + 1);
-                sel[i] |= take;
+        const int listed = sh_cnt;
+        if (listed > 0) {
+            // ---- the list: `left` of its blocks are selected
+            float up = INFINITY, dn = -INFINITY;           // undecided: dn <= score <= up
+            int certain = 0;
+            bool crowded = listed > left;
+            if (listed > 4 && crowded) {
+                // only those within the window of T, the left-th largest, are scored again
+                for (int i = w; i < listed; i += NW) {
+                    const float s = list_s[i];
+                    const int id = list_id[i];
+                    int before = 0;
+                    for (int j0 = 0; j0 < listed; j0 += 32) {
+                        const int j = min(j0 + lane, listed - 1);
+                        const float o = list_s[j];
+                        before += __popc(__ballot_sync(
+                            kFull, j0 + lane < listed && (o > s || (o == s && list_id[j] < id))));
+                    }
+                    if (before == left - 1 && lane == 0) sh_thr = s;
+                }
+                if (tid == 0) sh_win[0] = sh_win[1] = 0;
+                __syncthreads();
+                up = sh_thr + win;
+                dn = sh_thr - win;
+                for (int i = tid; i < listed; i += NT) {
+                    const float s = list_s[i];
+                    if (s > up) atomicAdd(&sh_win[0], 1);
+                    else if (s >= dn) atomicAdd(&sh_win[1], 1);
+                }
+                __syncthreads();
+                certain = sh_win[0];
+                crowded = certain + sh_win[1] > left;      // more than places
+            }
+            if (crowded) {
+                // a warp takes a block and as few heads as there are warps for
+                int parts = 1;
+                while (2 * parts <= G && 2 * parts * listed <= NW) parts *= 2;
+                const int heads = (G + parts - 1) / parts;
+                for (int i = w; i < listed * parts; i += NW) {
+                    const int e = i / parts, g0 = (i % parts) * heads;
+                    const float s = list_s[e];
+                    if (s <= up && s >= dn && g0 < G) {
+                        const unsigned long long k = exact_key(bounds, (size_t)list_row[e] * p.hkv + h, d, qf, g0,
+                                                               min(G, g0 + heads), lane, scale_q, scale_b);
+                        if (lane == 0) atomicMax(&list_key[e], k);
+                    }
+                }
+                __syncthreads();
+            }
+            // a warp ranks a block, a lane compares it with one other at a time
+            for (int i = w; i < listed; i += NW) {
+                const float s = list_s[i];
+                const int id = list_id[i];
+                bool take = s >= dn;
+                if (crowded && take && s <= up) {
+                    const unsigned long long k = list_key[i];
+                    int before = certain;
+                    for (int j0 = 0; j0 < listed; j0 += 32) {
+                        const int j = min(j0 + lane, listed - 1);
+                        const float o = list_s[j];
+                        const unsigned long long x = list_key[j];
+                        const bool ahead = j0 + lane < listed && o <= up && o >= dn &&
+                                           (x > k || (x == k && list_id[j] < id));
+                        before += __popc(__ballot_sync(kFull, ahead));
+                    }
+                    take = before < left;
+                }
+                if (take && lane == 0) atomicOr(&sel[id >> 5], 1u << (id & 31));
+            }
+        } else if (crowd) {
+            // ---- a crowd (many equal scores, or none finite): 64-bit keys to the
+            // workspace, their threshold by bisection, equal keys by index
+            unsigned long long* key = p.exact + row * p.stride;
+            auto is_cand = [&](int blk) { return (cand8[blk >> 3] >> (blk & 7)) & 1; };
+            auto block_count = [&](uint32_t c) -> int {
+                c = __reduce_add_sync(kFull, c);
+                __syncthreads();
+                if (lane == 0) sh_a[w] = c;
+                __syncthreads();
+                return (int)__reduce_add_sync(kFull, lane < NW ? sh_a[lane] : 0u);
+            };
+            for (int blk = lo + w; blk < hi; blk += NW)
+                if (is_cand(blk)) {
+                    const int id = p.tables[(size_t)b * p.max_blocks + blk];
+                    unsigned long long k = 0;              // a bad id (flagged when it was scored)
+                    if (id >= 0 && id < p.num_blocks)
+                        k = finite ? exact_key(bounds, (size_t)id * p.hkv + h, d, qf, 0, G, lane, scale_q, scale_b)
+                                   : exact_key_f64<T>(p, b, h, id, lane);
+                    if (lane == 0) key[blk] = k;
+                }
+            __syncthreads();
+            unsigned long long thr = 0;                    // the left-th largest key
+            for (int bit = 63; bit >= 0; --bit) {
+                const unsigned long long t = thr | (1ull << bit);
+                uint32_t c = 0;
+                for (int blk = lo + tid; blk < hi; blk += NT) c += is_cand(blk) && key[blk] >= t;
+                if (block_count(c) >= left) thr = t;
+            }
+            uint32_t c = 0;
+            for (int blk = lo + tid; blk < hi; blk += NT)
+                if (is_cand(blk) && key[blk] > thr) {
+                    atomicOr(&sel[blk >> 5], 1u << (blk & 31));
+                    ++c;
+                }
+            int places = left - block_count(c);
+            for (int base = 0; base < chunks && places > 0; base += NT) {
+                const int ch = base + tid;
+                uint32_t eq = 0;
+                if (ch < chunks)
+                    for (uint32_t m = cand8[ch]; m; m &= m - 1) {
+                        const int j = __ffs(m) - 1;
+                        if (key[8 * ch + j] == thr) eq |= 1u << j;
+                    }
+                uint32_t total;
+                int at = (int)block_scan(__popc(eq), &total);
+                for (; eq && at < places; eq &= eq - 1, ++at) {
+                    const int blk = 8 * ch + __ffs(eq) - 1;
+                    atomicOr(&sel[blk >> 5], 1u << (blk & 31));
+                }
+                places -= min(places, (int)total);
             }
         }
+    } else {
+        for (int c = tid; c < chunks; c += NT) sel8[c] = (unsigned char)forced_of(c);
     }
     __syncthreads();
     // ---- the selected blocks, ascending
-    uint32_t mine = 0;
-    for (int i = w0; i < w1; ++i) mine += __popc(sel[i]);
-    uint32_t total;
-    uint32_t at = block_scan(mine, &total);
-    for (int i = w0; i < w1; ++i)
-        for (uint32_t m = sel[i]; m && at < (uint32_t)p.k; m &= m - 1) out[at++] = 32 * i + __ffs(m) - 1;
+    uint32_t done = 0;
+    for (int base = 0; base < chunks; base += NT) {
+        const int c = base + tid;
+        uint32_t m = c < chunks ? sel8[c] : 0, total;
+        uint32_t at = done + block_scan(__popc(m), &total);
+        for (; m && at < (uint32_t)p.k; m &= m - 1) out[at++] = 8 * c + __ffs(m) - 1;
+        done += total;
+    }
 }
 
-constexpr size_t kSelectFixed = kListMax * 12 + kBins * 4;
-constexpr int kSmemMax = 200 * 1024;
+constexpr size_t kSelectFixed = kListMax * 20 + 8 * 128 * 4 + kBins * 4;
 constexpr int kMaxBlocks = 1 << 19;    // 128 KB of bitmaps
 
 inline int padded(int max_blocks) { return (max_blocks + 15) / 16 * 16; }
 
-template <typename T, int NT>
-int launch_select(SelectParams p, int num_seqs, cudaStream_t stream) {
-    const int words = (p.max_blocks + 31) / 32;
-    const size_t fixed = kSelectFixed + (size_t)words * 8;
-    // the row's scores in shared memory when they fit (read once from L2, then
-    // three to five times)
-    p.cached = fixed + (size_t)padded(p.max_blocks) * 4 <= kSmemMax ? padded(p.max_blocks) : 0;
-    const size_t smem = fixed + (size_t)p.cached * 4;
-    auto kern = select_rows<T, NT>;
+template <typename T, int NT, bool KEEP>
+int launch_select(const SelectParams& p, int num_seqs, cudaStream_t stream) {
+    const size_t words = (p.max_blocks + 31) / 32, most = KEEP ? NT / 4 : kMaxBlocks / 32;
+    auto kern = select_rows<T, NT, KEEP>;
     int occ = 0;
-    const int st = kernel_setup(reinterpret_cast<const void*>(kern), kSmemMax, NT, &occ);
+    const int st = kernel_setup(reinterpret_cast<const void*>(kern), (int)(kSelectFixed + most * 8), NT, &occ);
     if (st != PKV_OK) return st;
     note_launch();
-    const cudaError_t e = launch_pdl(kern, dim3(p.hkv, num_seqs), dim3(NT), smem, stream, p);
+    const cudaError_t e = launch_pdl(kern, dim3(p.hkv, num_seqs), dim3(NT), kSelectFixed + words * 8, stream, p);
     return e == cudaSuccess ? PKV_OK : cuda_fail("select_blocks: selection launch", e);
 }
 
 template <typename T>
 int launch_scores(const SelectParams& p, int num_seqs, cudaStream_t stream) {
     const int tiles = padded(p.max_blocks) / 16;
-    // 16-block tiles a warp walks: more once the warps fill the GPU's 16 resident
-    // warps per SM several times over
+    // 16-block tiles a warp walks: more once the warps fill the GPU (20 resident
+    // per SM) twice over
     int per = 1;
-    const long long rows = (long long)num_seqs * p.hkv, fill = 64LL * num_sms();
-    while (per < 8 && rows * tiles / (2 * per) >= fill) per *= 2;
-    dim3 grid((tiles + 4 * per - 1) / (4 * per), p.hkv, num_seqs);
+    const long long rows = (long long)num_seqs * p.hkv, fill = 40LL * num_sms();
+    while (per < 16 && rows * tiles / (2 * per) >= fill) per *= 2;
+    // kv heads side by side in a CTA (bf16): the power of two up to 4 that divides them
+    const int side = std::is_same<T, float>::value ? 1 : p.hkv % 4 == 0 ? 4 : p.hkv % 2 == 0 ? 2 : 1;
+    const int span = (4 / side) * per;
+    dim3 grid((tiles + span - 1) / span, p.hkv / side, num_seqs);
     note_launch();
     cudaError_t e;
     if constexpr (std::is_same<T, float>::value)
-        e = p.d == 64 ? launch_pdl(score_blocks_f32<64>, grid, dim3(128), 0, stream, p, per)
-                      : launch_pdl(score_blocks_f32<128>, grid, dim3(128), 0, stream, p, per);
+        e = p.d == 64 ? launch_pdl(score_blocks_f32<64>, grid, dim3(128), 0, stream, p, per, side)
+                      : launch_pdl(score_blocks_f32<128>, grid, dim3(128), 0, stream, p, per, side);
     else
-        e = p.d == 64 ? launch_pdl(score_blocks_bf16<64>, grid, dim3(128), 0, stream, p, per)
-                      : launch_pdl(score_blocks_bf16<128>, grid, dim3(128), 0, stream, p, per);
+        e = p.d == 64 ? launch_pdl(score_blocks_bf16<64>, grid, dim3(128), 0, stream, p, per, side)
+                      : launch_pdl(score_blocks_bf16<128>, grid, dim3(128), 0, stream, p, per, side);
     return e == cudaSuccess ? PKV_OK : cuda_fail("select_blocks: scoring launch", e);
 }
 
 template <typename T>
 int select_all(const SelectParams& p, int num_seqs, cudaStream_t stream) {
-    if (p.max_blocks > p.k && p.k > p.first + p.last) {
+    if (p.scored) {
         const int st = launch_scores<T>(p, num_seqs, stream);
         if (st != PKV_OK) return st;
     }
-    if (p.max_blocks > 4096) return launch_select<T, 1024>(p, num_seqs, stream);
-    return launch_select<T, 256>(p, num_seqs, stream);
+    // a thread keeps 8 scores: the smallest CTA that holds the longest row
+    if (p.max_blocks <= 4096) return launch_select<T, 512, true>(p, num_seqs, stream);
+    if (p.max_blocks <= 8192) return launch_select<T, 1024, true>(p, num_seqs, stream);
+    return launch_select<T, 1024, false>(p, num_seqs, stream);
 }
 
 }  // namespace
@@ -868,6 +1079,7 @@ int select_blocks(int32_t* selected, const void* q, const void* key_bounds,
     p.first = first_blocks;
     p.last = last_blocks;
     p.stride = padded(max_blocks_per_seq);
+    p.scored = scored;
     const size_t rows = (size_t)num_seqs * num_kv_heads;
     if (scored) {
         p.exact = static_cast<unsigned long long*>(workspace);

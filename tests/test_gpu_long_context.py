@@ -228,6 +228,40 @@ def test_rotary_far_slots_pass_32_bits():
     assert pkv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("scale", [0.037, 1.0, 3.0, 1e-35, 3e-39, 2e33, 0.7 * 2.0 ** -40])
+@pytest.mark.parametrize("src", [BF, F32])
+def test_rotary_e4m3_codes_at_rounding_borders(scale, src):
+    """Values whose quotient by the scale lies on or next to the midpoints between
+    E4M3 codes, in the subnormal range, at saturation and zero: the codes are those of
+    the IEEE quotient."""
+    s = np.float32(scale)
+    mags = ofp8._MAGNITUDES
+    mid = np.concatenate([(mags[1:] + mags[:-1]) / 2, mags, [448.0, 463.9, 464.0, 480.0, 1e6, 0.0]]).astype(np.float32)
+    with np.errstate(over="ignore", under="ignore"):
+        x = (mid * s).astype(np.float32)
+        x = np.concatenate([np.nextafter(np.nextafter(x, np.float32(-np.inf)), np.float32(-np.inf))] +
+                           [np.nextafter(x, np.float32(-np.inf)), x, np.nextafter(x, np.float32(np.inf))])
+    x = x[torch.isfinite(torch.from_numpy(x).to(src)).numpy()]     # an infinity turns its partner into NaN
+    x = np.concatenate([x, -x])
+    x = np.resize(x, -(-len(x) // 64) * 64).reshape(-1, 1, 64)
+    t = torch.from_numpy(x).to(src)
+    T = t.shape[0]
+    NB = -(-T // 16)
+    ks, vs = pkv.pool_shapes(NB, 1, 16, 64, U8)
+    kp, vp = torch.zeros(ks, dtype=U8, device="cuda"), torch.zeros(vs, dtype=U8, device="cuda")
+    table = torch.zeros(1, 2, 8, device="cuda")
+    table[:, 0] = 1.0                                      # no turn
+    q = t.cuda()
+    pkv.rotary_and_cache(torch.empty_like(q), q, q, q, kp, vp, torch.arange(T, dtype=I64, device="cuda"),
+                         torch.zeros(T, dtype=I32, device="cuda"), table, k_scale=float(s), v_scale=float(s))
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy(ofp8.e4m3_encode(np.clip(t.float().numpy() / s, -1e30, 1e30)))
+    zero = want & 0x7f == 0                                # 0 x 1 - 0 x 0: the sign of a zero is the sum's
+    for pool in pkv.pool_views(kp, vp):
+        got = pool.cpu().permute(0, 2, 1, 3).reshape(-1, 1, 64)[:T]
+        assert torch.equal(torch.where(zero, got & 0x7f, got), torch.where(zero, want & 0x7f, want))
+
+
 def test_rotary_no_tokens():
     c = rotary_case("bf16", 4, 2, 1, 64, 16, 64, 1, False, "chunk", seed=1)
     kp, vp = pkv.pools_from_views(c["kv"].cuda(), c["vv"].cuda())
@@ -423,7 +457,7 @@ def test_select_rounding_window_random():
     check_select(q, b, rng.permutation(n).astype(np.int32)[None], [n * 16], 16, 1, 100, 1, 1)
 
 
-@pytest.mark.parametrize("what", ["zero q", "zero bounds", "nan block", "inf blocks", "nan q", "huge", "tiny"])
+@pytest.mark.parametrize("what", ["zero q", "zero bounds", "nan block", "inf blocks", "nan q", "huge", "tiny", "zero q, inf block", "outlier"])
 @pytest.mark.parametrize("n", [500, 5000])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_select_degenerate_values(what, n, dt):
@@ -440,6 +474,12 @@ def test_select_degenerate_values(what, n, dt):
         b[41, 0, 1, 9], b[17, 1, 0, 3], b[n - 9, 0, :, 2] = math.inf, -math.inf, math.inf
     elif what == "nan q":
         q[0, 1, 5] = math.nan
+    elif what == "zero q, inf block":                      # 0 x inf: that block first
+        q.zero_()
+        b[60, 0, 0, 1] = math.inf
+    elif what == "outlier":                                # one score stretches the range
+        b[90, 0, 1] = 3e5
+        b[91, 0, 1] = 1e3
     elif what == "huge":                                   # float32 sums overflow, exact ones do not
         q, b = (q.float() * 1e19).to(dt), (b.float() * 1e19).to(dt)
     else:                                                  # float32 products vanish
@@ -466,6 +506,10 @@ def test_select_flags_bad_entries_and_lengths():
     s = olc.block_scores(q[0].double().numpy(), b[np.array(ok), 0].double().numpy())
     want = sorted([0, 39] + [ok[i] for i in np.argsort(-s, kind="stable")[:18]])
     assert got[0, 0].tolist() == want
+    t[0, 3:38] = 99                                        # fewer good blocks than places
+    got = select_gpu(q, b, t, [40 * 16], 16, 1, 20, 1, 1)
+    assert pkv.get_device_error() == -4
+    assert got[0, 0].tolist() == [0, 1, 2] + list(range(3, 18)) + [38, 39]
     got = select_gpu(q, b, np.arange(40, dtype=np.int32)[None], [40 * 16 + 1], 16, 1, 40, 0, 0)
     assert pkv.get_device_error() == -4 and got[0, 0].tolist() == list(range(40))
     got = select_gpu(q, b, np.arange(40, dtype=np.int32)[None], [-1], 16, 1, 4, 0, 0)
