@@ -45,6 +45,8 @@ _LIB = None
 
 PKV_F32, PKV_BF16, PKV_E4M3 = 0, 1, 2
 PKV_ERR_POOL_EXHAUSTED = -5
+(PKV_CALL_ROTARY_AND_CACHE, PKV_CALL_UPDATE_KEY_BOUNDS, PKV_CALL_SELECT_BLOCKS,
+ PKV_CALL_DECODE_SPARSE) = range(4)
 _STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported configuration",
            -3: "CUDA runtime error", -4: "index out of range", -5: "block pool exhausted",
            -6: "device wait timed out"}
@@ -141,6 +143,7 @@ def load_library():
         "paged_attention_decode_sparse": (c_int, [vp, vp, vp, vp, vp, vp, vp, c_int, c_int, c_int,
                                                   c_int, c_int, c_int, c_int, c_int, c_float,
                                                   c_int, c_int, c_float, c_float, vp]),
+        "pkv_bound_call": (c_int, [c_int, vp, c_int, vp]),
         "pkv_get_device_error": (c_int, [ip, vp]),
         "pkv_check_wait_timeout": (c_int, [vp]),
         "pkv_stage_upload": (c_int, [vp, vp, c_size, vp, vp, vp, vp, vp]),
@@ -727,7 +730,7 @@ def bind_rotary_and_cache(q_out, q, k, v, k_pool, v_pool, slot_mapping, position
     args += [ctypes.c_int64(s) for s in strides]
     args += _c_args([T, Hq, Hkv, D, 2 * half, bool(interleaved), bs, NB, cos_sin.shape[0], _dt(q, "q"),
                      _dt(k_pool, "k_pool"), float(k_scale), float(v_scale)])
-    return BoundCall(lib.rotary_and_cache, args, "rotary_and_cache", dev)
+    return PackedCall(lib, PKV_CALL_ROTARY_AND_CACHE, args, "rotary_and_cache", dev)
 
 
 def key_bounds_shape(num_blocks, num_kv_heads, head_dim):
@@ -783,7 +786,7 @@ def bind_update_key_bounds(k_pool, key_bounds, block_tables, seq_lens, first_cha
     args = [_ptr(t) for t, _ in named]
     args += _c_args([seq_lens.shape[0], block_tables.shape[1], NB, Hkv, D, bs, int(max_new_tokens),
                      _dt(k_pool, "k_pool")])
-    return BoundCall(lib.update_key_bounds, args, "update_key_bounds", dev)
+    return PackedCall(lib, PKV_CALL_UPDATE_KEY_BOUNDS, args, "update_key_bounds", dev)
 
 
 def select_blocks_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq):
@@ -831,7 +834,7 @@ def bind_select_blocks(selected, q, key_bounds, block_tables, seq_lens, block_si
     args += _c_args([B, block_tables.shape[1], key_bounds.shape[0], Hq, Hkv, D, int(block_size), K,
                      int(first_blocks), int(last_blocks), _dt(q, "q")])
     args += [ctypes.c_void_p(ws_ptr), ctypes.c_size_t(ws_bytes)]
-    return BoundCall(lib.select_blocks, args, "select_blocks", dev)
+    return PackedCall(lib, PKV_CALL_SELECT_BLOCKS, args, "select_blocks", dev)
 
 
 def paged_attention_decode_sparse(out, q, k_pool, v_pool, block_tables, seq_lens, selected, scale,
@@ -862,7 +865,7 @@ def bind_paged_attention_decode_sparse(out, q, k_pool, v_pool, block_tables, seq
     args = [_ptr(t) for t, _ in named]
     args += _c_args([B, block_tables.shape[1], NB, selected.shape[2], Hq, Hkv, D, bs, float(scale),
                      _dt(q, "q"), _dt(k_pool, "k_pool"), float(k_scale), float(v_scale)])
-    return BoundCall(lib.paged_attention_decode_sparse, args, "paged_attention_decode_sparse", dev)
+    return PackedCall(lib, PKV_CALL_DECODE_SPARSE, args, "paged_attention_decode_sparse", dev)
 
 
 class BoundCall:
@@ -904,6 +907,48 @@ class BoundCall:
         else:
             st = self._fn(*args, self._sptr)
         _check(st, self._what)
+
+
+class PackedCall(BoundCall):
+    """A ``BoundCall`` whose arguments lie packed for ``pkv_bound_call``: the
+    library unpacks them, so a call passes four arguments instead of twenty-odd
+    (1.6 us of host time on a Grace core for the 29 of ``rotary_and_cache``)."""
+
+    __slots__ = ("_call", "_packed", "_addr", "_n", "_keep")
+
+    def __init__(self, lib, call, args, what, device):
+        super().__init__(lib.pkv_bound_call, args, what, device)
+        self._call, self._n = call, len(args)
+        self._packed = (ctypes.c_uint64 * self._n)()
+        self._keep = args                                  # host arrays the slots point to
+        for i, a in enumerate(args):
+            if isinstance(a, ctypes.Array):
+                self._packed[i] = ctypes.addressof(a)
+            elif isinstance(a, ctypes.c_float):
+                self._packed[i] = ctypes.c_uint32.from_buffer_copy(a).value
+            else:
+                self._packed[i] = (a.value or 0) & 0xffffffffffffffff
+        self._addr = ctypes.addressof(self._packed)
+
+    def __call__(self, stream=None):
+        idx = self._idx
+        sptr = _raw_stream(idx) if stream is None else stream.cuda_stream
+        if torch.cuda.current_device() != idx:
+            with _on_device(torch.device("cuda", idx)):
+                st = self._fn(self._call, self._addr, self._n, sptr)
+        else:
+            st = self._fn(self._call, self._addr, self._n, sptr)
+        if st:
+            _check(st, self._what)
+
+
+def _raw_stream(idx):
+    """The address of the current stream of a device."""
+    return torch.cuda.current_stream(idx).cuda_stream
+
+
+# the same without building a Stream object, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _c_args(values):

@@ -30,6 +30,7 @@ CUDA_SOURCES = [
     "pkv_sparse_f32.cu",
     "pkv_sparse_bf16.cu",
     "pkv_sparse_e4m3.cu",
+    "pkv_bound.cu",
 ]
 CXX_SOURCES = ["block_manager.cpp"]
 

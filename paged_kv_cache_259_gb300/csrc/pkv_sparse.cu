@@ -1,5 +1,8 @@
 // C ABI entry point of sparse decode attention: argument checks and dispatch.
 #include <cmath>
+#include <map>
+#include <mutex>
+#include <tuple>
 
 #include "pkv_sparse_impl.cuh"
 
@@ -8,6 +11,36 @@ namespace sparse {
 int dispatch_f32(const Args& a);
 int dispatch_bf16(const Args& a);
 int dispatch_e4m3(const Args& a);
+
+int resident_clusters(const void* kern, int smem, int threads, int size, int* out) {
+    static std::mutex mu;
+    // (device, kernel, shared memory, threads, size) -> clusters
+    static std::map<std::tuple<int, const void*, int, int, int>, int> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail("sparse decode: current device", e);
+    std::lock_guard<std::mutex> lock(mu);
+    auto it = known.find({dev, kern, smem, threads, size});
+    if (it == known.end()) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = size;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (e != cudaSuccess) return cuda_fail("sparse decode: cluster occupancy", e);
+        it = known.insert({{dev, kern, smem, threads, size}, n}).first;
+    }
+    *out = it->second;
+    return PKV_OK;
+}
 }  // namespace sparse
 }  // namespace pkv
 

@@ -2,15 +2,16 @@
 //
 // The mathematics is the decode kernel's (online softmax over a sequence's
 // cached tokens, tile by tile) over the tokens of the blocks that a list names
-// for each (sequence, kv head), and the tile math is that kernel's (SimtMath,
-// MmaMath). What differs is the walk and the merge:
-//   - an entry of the list is a logical block, so a tile's address takes two
-//     dependent reads (list, block table); a warp makes them for 32 entries at
-//     once, before its first copy;
-//   - a list is short (tens to hundreds of blocks), so a row is split over the
-//     CTAs of one thread-block cluster and its partial results are merged
-//     through distributed shared memory: one launch, no workspace. The split is
-//     taken from the row's own number of entries, so short rows stay balanced.
+// for each row (sequence, kv head), and the tile math is that kernel's (SimtMath,
+// MmaMath). What differs is the walk and the merge. A thread-block cluster takes
+// some rows, lays their listed blocks end to end and gives every warp of its CTAs an
+// equal run of them: a warp streams its run through a ring of its own, across the
+// borders of rows, and keeps no state but the current row's. A row that lies within
+// one warp's run is written at once; the parts of the others meet in shared memory
+// and are merged at the end (a warp has at most two: the row its run begins in and
+// the one it ends in). So one launch does it without a workspace, few rows are spread
+// over many warps, and many rows make one wave of equal shares, whatever their
+// lengths, where a CTA a row left a ragged second wave.
 // Bound: HBM bytes of the selected tiles when there are many rows; a chain of
 // loads (length, list, table, tile, partner's partials) when there are few.
 #pragma once
@@ -33,6 +34,9 @@ struct Params {
     const int32_t* selected;           // [B][Hkv][K] logical blocks, ascending, -1 padded
     int* err;
     int max_blocks, num_blocks, num_heads, num_kv_heads, k;
+    int num_rows;                      // (sequence, kv head), kv heads fastest
+    int cluster_rows;                  // rows of a cluster, at most kMaxRows
+    int stages;                        // of a warp's ring
     float qscale, v_scale;
 };
 
@@ -43,11 +47,24 @@ struct Args {
     cudaStream_t stream;
 };
 
-constexpr int kNumWarps = 4;
-constexpr int kMaxParts = 8;           // the portable cluster size
+constexpr int kNumWarps = 4;           // of a CTA; twice as many when there are few rows
+constexpr int kMaxCluster = 8;         // the portable size
+constexpr int kMaxRows = 32;           // rows of a cluster: one per lane
+constexpr int kMaxStages = 8;          // of a warp's ring
+constexpr int kSmemSm = 227 * 1024;    // shared memory of an SM for CTAs, 1 KB of each reserved
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
 }
 // The address of a shared-memory location in the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
@@ -61,80 +78,212 @@ __device__ __forceinline__ float cluster_ld(uint32_t addr) {
     return v;
 }
 
-// CTA (part, kv head, sequence); the parts of a row are one cluster. PAIR = 2:
-// a pipeline stage holds two list entries of BS / 2 tokens side by side (see the
-// decode kernel); BS is then the stage's token count.
-template <class Math, typename QT, int D, int BS, int G, int NW, int PAIR>
-__global__ void __launch_bounds__(NW * 32, 3) sparse_decode_kernel(const Params p) {
-    using P = decode::Pipe<Math, D, BS, G, NW>;
-    constexpr int TILE = P::kTile, ST = P::kStages;
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Shared memory: mbarriers | tokens per stage | row borders and lengths per warp |
+// first parts | (CUDA-core math) the warps' query rows and scratch | rings, for a CTA
+// of `nw` warps with rings of `stages`, both chosen at launch. A warp's last part goes
+// into its own ring, which is drained by then, a CTA's parts into the second halves of
+// warp 0's and 1's.
+template <class Math, int D, int BS, int G>
+struct Smem {
+    static constexpr bool kSimt = Math::kWarpSmemFloats > 0;
+    static constexpr int kStage = 2 * Math::Lay::kTile;    // bytes of a K and a V tile
+    static constexpr int kPartFloats = G * (D + 4);        // m [G], l [G], (pad), o [G][D]
+    static constexpr int kO = 4 * G;                       // of o within a part
+    __host__ __device__ static constexpr int tok_off(int nw) { return nw * kMaxStages * 8; }
+    __host__ __device__ static constexpr int row_off(int nw) { return tok_off(nw) + nw * kMaxStages * 4; }
+    __host__ __device__ static constexpr int part_off(int nw) {
+        return (row_off(nw) + nw * (2 * kMaxRows + 1) * 4 + 15) / 16 * 16;
+    }
+    __host__ __device__ static constexpr int q_off(int nw) { return part_off(nw) + nw * kPartFloats * 4; }
+    __host__ __device__ static constexpr int warp_off(int nw) { return q_off(nw) + (kSimt ? nw * G * D * 4 : 0); }
+    __host__ __device__ static constexpr int ring_off(int nw) {
+        return (warp_off(nw) + nw * Math::kWarpSmemFloats * 4 + 127) / 128 * 128;
+    }
+    // a warp's part and a CTA's part fit in a ring
+    static constexpr int kMinStages = (2 * kPartFloats * 4 + kStage - 1) / kStage;
+    // stages of a warp's ring within `bytes` of shared memory per CTA
+    static constexpr int stages(int nw, int bytes) {
+        const int n = (bytes - ring_off(nw)) / (nw * kStage);
+        return n < kMinStages ? kMinStages : n > kMaxStages ? kMaxStages : n;
+    }
+    static constexpr int bytes(int nw, int stages) { return ring_off(nw) + nw * stages * kStage; }
+    static_assert(kStage % 32 == 0, "halves of a ring are 16-byte aligned");
+    static_assert(kMinStages <= kMaxStages && bytes(kNumWarps, kMinStages) <= kSmemSm, "shared memory per CTA");
+    // eight warps a CTA where their rings fit (not: float32, 8 heads, 32-token blocks)
+    static constexpr bool kWide = bytes(2 * kNumWarps, kMinStages) <= kSmemSm;
+};
+
+// The query rows of one (sequence, kv head) into a warp's state. Tensor-core math:
+// straight into the operand fragments (the layouts of MmaMath::init); CUDA-core
+// math: through the warp's shared-memory rows, scaled.
+template <class Math, typename QT, int D, int G>
+__device__ __forceinline__ void begin_row(typename Math::State& st, const QT* q, float qscale, float* qs, int lane) {
+    if constexpr (Math::kWarpSmemFloats > 0) {
+        __syncwarp();
+        for (int i = lane; i < G * D; i += 32) qs[i] = decode::to_f(q[i]) * qscale;
+        __syncwarp();
+        Math::init(st, qs, lane);
+    } else {
+        const int r = lane >> 2, c = lane & 3;
+        const bool live = r < G;
+#pragma unroll
+        for (int s = 0; s < Math::KS; ++s) {
+            uint32_t a = 0, b = 0;
+            if constexpr (Math::F8) {
+                if (live) {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(q + r * D + 16 * s + 4 * c));
+                    a = decode::pack_f16(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u));
+                    b = decode::pack_f16(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+                }
+            } else {
+                if (live) {
+                    a = __ldg(reinterpret_cast<const uint32_t*>(q + r * D + 16 * s + 2 * c));
+                    b = __ldg(reinterpret_cast<const uint32_t*>(q + r * D + 16 * s + 8 + 2 * c));
+                }
+            }
+            st.qa[s][0] = a;
+            st.qa[s][1] = b;
+        }
+#pragma unroll
+        for (int nt = 0; nt < Math::NT; ++nt) st.o[nt][0] = st.o[nt][1] = 0.f;
+        st.m = -INFINITY;
+        st.l = 0.f;
+    }
+}
+
+// A row that one warp has seen whole, to the output.
+template <class Math, typename QT, int D, int G>
+__device__ __forceinline__ void write_row(typename Math::State& st, QT* out, float v_scale, int lane) {
+    if constexpr (Math::kWarpSmemFloats > 0) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float l = st.l[g];
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+            const float inv = l > 0.f ? v_scale / l : 0.f;
+#pragma unroll
+            for (int k = 0; k < Math::DPL; ++k) decode::store_out(out + g * D + lane + 32 * k, st.acc[g][k] * inv);
+        }
+    } else {
+        const int r = lane >> 2, c = lane & 3;
+        float l = st.l;
+        l += __shfl_xor_sync(kFull, l, 1);
+        l += __shfl_xor_sync(kFull, l, 2);
+        const float inv = l > 0.f ? v_scale / l : 0.f;
+        if (r < G) {
+#pragma unroll
+            for (int nt = 0; nt < Math::NT; ++nt) {
+                decode::store_out(out + r * D + 8 * nt + 2 * c, st.o[nt][0] * inv);
+                decode::store_out(out + r * D + 8 * nt + 2 * c + 1, st.o[nt][1] * inv);
+            }
+        }
+    }
+}
+
+// PAIR = 2: a pipeline stage holds two list entries of BS / 2 tokens side by side
+// (see the decode kernel); BS is then the stage's token count.
+// 168 registers: three CTAs of 4 warps an SM.
+template <class Math, typename QT, int D, int BS, int G, int PAIR>
+__global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
+    using S = Smem<Math, D, BS, G>;
+    constexpr int TILE = Math::Lay::kTile;
     constexpr int PBS = BS / PAIR, PTILE = TILE / PAIR;
     static_assert(PAIR == 1 || PAIR == 2, "entries per stage");
     pdl_enter();                                           // launched with programmatic serialisation
     extern __shared__ __align__(128) unsigned char smem[];
-    unsigned char* ring = smem;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBarOff);
-    int32_t* stage_tok = reinterpret_cast<int32_t*>(smem + P::kIdOff);   // tokens of the stage
-    float* qs = reinterpret_cast<float*>(smem + P::kQOff);
-    float* wsm = reinterpret_cast<float*>(smem + P::kWarpOff);
-
-    const int part = blockIdx.x, parts = gridDim.x, hk = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    int L = p.seq_lens[b];
-    if (L < 0 || L > p.max_blocks * PBS) {                  // length the table cannot hold
-        if (part == 0 && hk == 0 && tid == 0) flag_error(p.err, kErrOutOfRange);
-        L = L < 0 ? 0 : p.max_blocks * PBS;
-    }
-    const int nblk = (L + PBS - 1) / PBS;
-    // distinct entries below nblk: no more than nblk of them
-    const int total = min(p.k, nblk);
-    const int stages = (total + PAIR - 1) / PAIR;
-    const int per = (stages + parts - 1) / parts;
-    const int first = part * per;                           // first stage of this CTA
-    const int count = max(0, min(per, stages - first));
-    const int32_t* list = p.selected + ((size_t)b * p.num_kv_heads + hk) * p.k;
+    const int NW = blockDim.x >> 5, ST = p.stages, warp_ring = ST * S::kStage;
+    unsigned char* const rings = smem + S::ring_off(NW);
+    unsigned char* const ring = rings + w * warp_ring;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem) + w * kMaxStages;
+    int32_t* stage_tok = reinterpret_cast<int32_t*>(smem + S::tok_off(NW)) + w * kMaxStages;
+    int32_t* border = reinterpret_cast<int32_t*>(smem + S::row_off(NW)) + w * (2 * kMaxRows + 1);
+    int32_t* length = border + kMaxRows + 1;
+    float* part0 = reinterpret_cast<float*>(smem + S::part_off(NW));
+    float* qs = reinterpret_cast<float*>(smem + S::q_off(NW)) + w * G * D;
+    float* pb = reinterpret_cast<float*>(smem + S::warp_off(NW)) + w * Math::kWarpSmemFloats;
 
-    if (lane == 0) {
-#pragma unroll
-        for (int s = 0; s < ST; ++s) mbar_init(smem_addr(&bars[w * ST + s]), 1);
-        fence_mbar_init();
+    // ---- the cluster's rows: stages (every warp works them out for itself)
+    const int rank = (int)cluster_rank(), csize = (int)cluster_size();
+    const int row0 = (int)(blockIdx.x / csize) * p.cluster_rows;
+    const int nrows = min(p.cluster_rows, p.num_rows - row0);
+    int L = 0;
+    if (lane < nrows) {
+        const int b = (row0 + lane) / p.num_kv_heads;
+        L = p.seq_lens[b];
+        if (L < 0 || L > p.max_blocks * PBS) {              // length the table cannot hold
+            flag_error(p.err, kErrOutOfRange);
+            L = L < 0 ? 0 : p.max_blocks * PBS;
+        }
     }
+    // distinct entries below the row's blocks: no more than there are blocks
+    const int entries = min(p.k, (L + PBS - 1) / PBS);
+    int end = (entries + PAIR - 1) / PAIR;                  // inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, end, o);
+        if (lane >= o) end += x;
+    }
+    const int total = __shfl_sync(kFull, end, 31);
+    if (lane == 0) border[0] = 0;
+    border[lane + 1] = end;                                 // rows past nrows: empty
+    length[lane] = L;
+    // ---- this warp's run of them
+    const int share = (total + csize * NW - 1) / (csize * NW);
+    const int begin = min(total, (rank * NW + w) * share), stop = min(total, begin + share);
+    const int nk = stop - begin;
+
+    if (lane < ST) mbar_init(smem_addr(&bars[lane]), 1);
+    fence_mbar_init();
     __syncwarp();
-    const int nk = count > w ? (count - w + NW - 1) / NW : 0;   // this warp's stages
     const uint64_t pol = l2_evict_first();
 
-    // the block id of list entry e (-1: none) and its tokens
-    auto block_of = [&](int e, int* ntok) -> int {
+    // the tile of entry e of row r (-1: none) and its tokens; j, before: the entry and
+    // the one in front of it
+    auto tile_of = [&](int r, int e, int j, int before, int* ntok) -> int {
         *ntok = 0;
-        if (e >= total) return -1;
-        const int j = list[e], before = e > 0 ? list[e - 1] : -1;
-        if (j < 0) return -1;                               // padding
+        const int len = length[r], nblk = (len + PBS - 1) / PBS;
+        if (e >= min(p.k, nblk) || j < 0) return -1;        // past the list, padding
         // past the sequence, repeated or out of order, or behind padding
         if (j >= nblk || j <= before || (e > 0 && before < 0)) {
             flag_error(p.err, kErrOutOfRange);
             return -1;
         }
+        const unsigned b = (unsigned)(row0 + r) / (unsigned)p.num_kv_heads;
         const int id = p.block_tables[(size_t)b * p.max_blocks + j];
         if (id < 0 || id >= p.num_blocks) {
             flag_error(p.err, kErrOutOfRange);
             return -1;
         }
-        *ntok = min(PBS, L - j * PBS);
-        return id;
+        *ntok = min(PBS, len - j * PBS);
+        return id * p.num_kv_heads + (row0 + r - (int)b * p.num_kv_heads);
     };
-    // 32 stages per warp-wide read
+    // 32 stages per warp-wide read: tiles and tokens
     int id_a = -1, id_b = -1, tok_a = 0, tok_b = 0, chunk = -1;
-    auto issue = [&](int kk) {                              // the whole converged warp
+    auto issue = [&](int kk, int s) {                       // stage kk into slot s: the whole converged warp
         if ((kk >> 5) != chunk) {
             chunk = kk >> 5;
-            const int mine = (chunk << 5) + lane;
+            const int at = begin + (chunk << 5) + lane;
             id_a = id_b = -1;
             tok_a = tok_b = 0;
-            if (mine < nk) {
-                const int e = (first + w + mine * NW) * PAIR;
-                id_a = block_of(e, &tok_a);
+            if (at < stop) {
+                int r = 0;
+                while (border[r + 1] <= at) ++r;
+                const int e = (at - border[r]) * PAIR;
+                const int32_t* list = p.selected + (size_t)(row0 + r) * p.k + e;
+                const int before = e > 0 ? list[-1] : -1, j0 = list[0], j1 = PAIR == 2 && e + 1 < p.k ? list[1] : -1;
+                id_a = tile_of(r, e, j0, before, &tok_a);
                 if constexpr (PAIR == 2) {
-                    id_b = block_of(e + 1, &tok_b);
+                    id_b = tile_of(r, e + 1, j1, j0, &tok_b);
                     if (id_a < 0) {                         // a lone second entry moves up
                         id_a = id_b;
                         tok_a = tok_b;
@@ -145,21 +294,20 @@ __global__ void __launch_bounds__(NW * 32, 3) sparse_decode_kernel(const Params 
             }
             __syncwarp();
         }
-        const int s = kk % ST;
-        const uint32_t bar = smem_addr(&bars[w * ST + s]);
+        const uint32_t bar = smem_addr(&bars[s]);
         const int ia = __shfl_sync(kFull, id_a, kk & 31), ta = __shfl_sync(kFull, tok_a, kk & 31);
         const int ib = PAIR == 2 ? __shfl_sync(kFull, id_b, kk & 31) : -1;
         const int tb = PAIR == 2 ? __shfl_sync(kFull, tok_b, kk & 31) : 0;
-        if (lane == 0) stage_tok[w * ST + s] = ta + tb;
+        if (lane == 0) stage_tok[s] = ta + tb;
         __syncwarp();
         if (ia >= 0) {
-            const uint32_t dst = smem_addr(ring + (size_t)((w * ST + s) * 2) * TILE);
-            const size_t off = ((size_t)ia * p.num_kv_heads + hk) * PTILE;
+            const uint32_t dst = smem_addr(ring + (size_t)s * 2 * TILE);
+            const size_t off = (size_t)ia * PTILE;
             mbar_arrive_expect_tx_elect(bar, (ib >= 0 ? 4 : 2) * PTILE);
             bulk_g2s_elect(dst, p.k_pool + off, PTILE, bar, pol);
             bulk_g2s_elect(dst + TILE, p.v_pool + off, PTILE, bar, pol);
             if (ib >= 0) {
-                const size_t off2 = ((size_t)ib * p.num_kv_heads + hk) * PTILE;
+                const size_t off2 = (size_t)ib * PTILE;
                 bulk_g2s_elect(dst + PTILE, p.k_pool + off2, PTILE, bar, pol);
                 bulk_g2s_elect(dst + TILE + PTILE, p.v_pool + off2, PTILE, bar, pol);
             }
@@ -167,29 +315,41 @@ __global__ void __launch_bounds__(NW * 32, 3) sparse_decode_kernel(const Params 
             mbar_arrive_elect(bar);
         }
     };
-    for (int kk = 0; kk < nk && kk < ST; ++kk) issue(kk);
+    for (int kk = 0; kk < nk && kk < ST; ++kk) issue(kk, kk);
 
-    for (int i = tid; i < G * D; i += NW * 32) {            // query rows of this CTA
-        const float qv = decode::to_f(static_cast<const QT*>(p.q)[((size_t)b * p.num_heads + hk * G) * D + i]);
-        qs[i] = Math::kPrescaledQ ? qv * p.qscale : qv;
-    }
-    __syncthreads();
     typename Math::State st;
-    Math::init(st, qs, lane);
-    float* pb = wsm + w * Math::kWarpSmemFloats;
-
+    int row = -1, row_end = begin;                          // the current row ends before stage row_end
+    // the current row's result: whole, or this warp's part of it
+    auto finish_row = [&](bool dead) {
+        if (row < 0) return;
+        const bool first_here = border[row] >= begin, last_here = border[row + 1] <= stop;
+        if (first_here && last_here) {
+            if (!dead)
+                write_row<Math, QT, D, G>(st, static_cast<QT*>(p.out) + (size_t)(row0 + row) * G * D, p.v_scale, lane);
+        } else {
+            float* part = first_here ? reinterpret_cast<float*>(ring) : part0 + w * S::kPartFloats;
+            Math::finish(st, part, part + G, part + S::kO, 0, lane, dead);
+        }
+    };
     bool aborted = false;
-    int k = 0;
+    int k = 0, s = 0;                                       // stage, its slot
+    uint32_t phase = 0;                                     // how often the ring has gone round, mod 2
     for (; k < nk; ++k) {
-        const int s = k % ST;
-        const bool ok = mbar_wait_bounded(smem_addr(&bars[w * ST + s]), (k / ST) & 1, p.err);
+        if (begin + k >= row_end) {                         // the next row
+            finish_row(false);
+            do ++row;
+            while (border[row + 1] <= begin + k);
+            row_end = border[row + 1];
+            begin_row<Math, QT, D, G>(st, static_cast<const QT*>(p.q) + (size_t)(row0 + row) * G * D, p.qscale, qs, lane);
+        }
+        const bool ok = mbar_wait_bounded(smem_addr(&bars[s]), phase, p.err);
         if (__any_sync(kFull, !ok)) {
             aborted = true;
             break;
         }
-        const int ntok = stage_tok[w * ST + s];
+        const int ntok = stage_tok[s];
         if (ntok > 0) {
-            const unsigned char* kt = ring + (size_t)((w * ST + s) * 2) * TILE;
+            const unsigned char* kt = ring + (size_t)s * 2 * TILE;
             if constexpr (Math::kWarpSmemFloats > 0)
                 Math::tile(st, kt, kt + TILE, ntok, lane, qs, pb);
             else
@@ -198,107 +358,222 @@ __global__ void __launch_bounds__(NW * 32, 3) sparse_decode_kernel(const Params 
         __syncwarp();
         if (k + ST < nk) {
             fence_proxy_async_smem();
-            issue(k + ST);
+            issue(k + ST, s);
+        }
+        if (++s == ST) {
+            s = 0;
+            phase ^= 1;
         }
     }
     if (aborted) {
-        // as in the decode kernel: record it and let the copies in flight land
+        // as in the decode kernel: record it and let the copies in flight land; the
+        // parts that the partners will read are marked empty
         if (lane == 0) flag_error(p.err, kErrTimeout);
-        const int last = min(nk, k + ST);
-        for (int kk = k; kk < last; ++kk)
-            (void)mbar_wait_bounded(smem_addr(&bars[w * ST + (kk % ST)]), (kk / ST) & 1, nullptr);
+        for (int kk = k; kk < min(nk, k + ST); ++kk) {
+            (void)mbar_wait_bounded(smem_addr(&bars[s]), phase, nullptr);
+            if (++s == ST) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+        for (int i = lane; i < 2 * G; i += 32) {              // m, l
+            reinterpret_cast<float*>(ring)[i] = i < G ? -INFINITY : 0.f;
+            part0[w * S::kPartFloats + i] = i < G ? -INFINITY : 0.f;
+        }
+        __syncwarp();
     }
+    finish_row(aborted);
 
-    __syncthreads();                                        // every warp is done with its ring
-    float* cm = reinterpret_cast<float*>(ring);             // [NW][G]
-    float* cl = cm + NW * G;                                // [NW][G]
-    float* cacc = cl + NW * G;                              // [NW][G][D]
-    float* pm = cacc + NW * G * D;                          // [G]     this part's maxima,
-    float* pl = pm + G;                                     // [G]     sums
-    float* po = pl + G;                                     // [G][D]  and weighted sums
-    static_assert((NW * G * (D + 2) + G * (D + 2)) * 4 <= P::kRingBytes, "merge area");
-    Math::finish(st, cm, cl, cacc, w, lane, aborted);
+    // ---- the rows that several warps of this CTA share: to the output, or (a row
+    // that reaches into other CTAs of the cluster) to the CTA's part of it. Rolled
+    // loops: this runs once, and fetching straight-line code costs more than it saves.
     __syncthreads();
-    // ---- merge the warps, then (through the cluster) the parts
-    QT* out = static_cast<QT*>(p.out) + ((size_t)b * p.num_heads + hk * G) * D;
-    for (int idx = tid; idx < G * D; idx += NW * 32) {
-        const int g = idx / D, dd = idx % D;
-        float M = -INFINITY;
-#pragma unroll
-        for (int ww = 0; ww < NW; ++ww) M = fmaxf(M, cm[ww * G + g]);
-        float S = 0.f, O = 0.f;
-        if (M != -INFINITY) {
-#pragma unroll
-            for (int ww = 0; ww < NW; ++ww) {
-                const float e = exp2f(cm[ww * G + g] - M);
-                S += e * cl[ww * G + g];
-                O += e * cacc[(ww * G + g) * D + dd];
-            }
-        }
-        if (parts == 1) {
-            decode::store_out(out + idx, (S > 0.f ? O / S : 0.f) * p.v_scale);
-        } else {
-            po[idx] = O;
-            if (dd == 0) {
-                pm[g] = M;
-                pl[g] = S;
+    const int cta_run = NW * share, cta_begin = min(total, rank * cta_run), cta_stop = min(total, cta_begin + cta_run);
+    float* const cta_part = reinterpret_cast<float*>(rings + warp_ring / 2);
+    const int cta_part1 = warp_ring / 4;                    // floats from the first to the last
+    constexpr int kQuads = G * D / 4;                       // a thread's share: four elements
+    QT* const out = static_cast<QT*>(p.out) + (size_t)row0 * G * D;
+    auto store4 = [&](int r, int i, float4 v, float by) {
+        QT* dst = out + (size_t)r * G * D + 4 * i;
+        if constexpr (std::is_same<QT, float>::value)
+            *reinterpret_cast<float4*>(dst) = make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
+        else
+            *reinterpret_cast<uint2*>(dst) = make_uint2(decode::pack_bf16(v.x * by, v.y * by), decode::pack_bf16(v.z * by, v.w * by));
+    };
+    auto add4 = [](float4& v, float e, float4 o) {
+        v.x += e * o.x;
+        v.y += e * o.y;
+        v.z += e * o.z;
+        v.w += e * o.w;
+    };
+    if (cta_begin < cta_stop) {
+        int r = 0;
+        while (border[r + 1] <= cta_begin) ++r;
+#pragma unroll 1
+        for (; border[r] < cta_stop; ++r) {
+            const int a = border[r], z = border[r + 1];
+            if (a == z) continue;
+            const int x0 = max(a - cta_begin, 0) / share, x1 = (min(z, cta_stop) - 1 - cta_begin) / share;
+            const bool whole = a >= cta_begin && z <= cta_stop;
+            if (whole && x0 == x1) continue;                // written by its warp
+            float* const to = cta_part + (a < cta_begin ? 0 : cta_part1);
+            // warp x's part: its first where the row began before its run, else its last
+            auto part_of = [&](int x) -> const float* {
+                return a < cta_begin + x * share ? part0 + x * S::kPartFloats
+                                                 : reinterpret_cast<const float*>(rings + x * warp_ring);
+            };
+#pragma unroll 1
+            for (int i = tid; i < kQuads; i += NW * 32) {
+                const int g = 4 * i / D;
+                float M = -INFINITY, sum = 0.f;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int x = x0; x <= x1; ++x) M = fmaxf(M, part_of(x)[g]);
+                if (M != -INFINITY) {
+#pragma unroll 4
+                    for (int x = x0; x <= x1; ++x) {
+                        const float* part = part_of(x);
+                        const float e = exp2f(part[g] - M);
+                        sum += e * part[G + g];
+                        add4(v, e, *reinterpret_cast<const float4*>(part + S::kO + 4 * i));
+                    }
+                }
+                if (whole) {
+                    store4(r, i, v, sum > 0.f ? p.v_scale / sum : 0.f);
+                } else {
+                    *reinterpret_cast<float4*>(to + S::kO + 4 * i) = v;
+                    if (4 * i % D == 0) {
+                        to[g] = M;
+                        to[G + g] = sum;
+                    }
+                }
             }
         }
     }
-    if (parts == 1) return;
+#pragma unroll 1
+    for (int r = rank; r < nrows; r += csize)               // rows with nothing listed
+        if (border[r] == border[r + 1])
+            for (int i = tid; i < kQuads; i += NW * 32) store4(r, i, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+    if (csize == 1) return;
+    // ---- the rows that several CTAs share (at most the first and the last of this
+    // one's): each CTA takes a slice of a row's elements
     cluster_sync();
-    const int share = (G * D + parts - 1) / parts;
-    const int i1 = min(G * D, (part + 1) * share);
-    for (int idx = part * share + tid; idx < i1; idx += NW * 32) {
-        const int g = idx / D;
-        float m[kMaxParts], M = -INFINITY;
+    if (cta_begin < cta_stop) {
+        int r = 0;
+        while (border[r + 1] <= cta_begin) ++r;
+#pragma unroll 1
+        for (; border[r] < cta_stop; ++r) {
+            const int a = border[r], z = border[r + 1];
+            if (a >= cta_begin && z <= cta_stop) continue;
+            const int y0 = a / cta_run, n = (z - 1) / cta_run - y0 + 1;      // its CTAs
+            const int slice = (kQuads + n - 1) / n, from = (rank - y0) * slice;
+            auto part_of = [&](int y) {
+                return cluster_map(smem_addr(cta_part + (a < (y0 + y) * cta_run ? 0 : cta_part1)), y0 + y);
+            };
+#pragma unroll 1
+            for (int i = from + tid; i < min(kQuads, from + slice); i += NW * 32) {
+                const int g = 4 * i / D;
+                // every CTA's part read at once: one trip through the cluster
+                float m[kMaxCluster], l[kMaxCluster], M = -INFINITY, sum = 0.f;
+                float4 o[kMaxCluster], v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int r = 0; r < kMaxParts; ++r) {
-            m[r] = r < parts ? cluster_ld(cluster_map(smem_addr(pm + g), r)) : -INFINITY;
-            M = fmaxf(M, m[r]);
-        }
-        float S = 0.f, O = 0.f;
-        if (M != -INFINITY) {
-#pragma unroll
-            for (int r = 0; r < kMaxParts; ++r)
-                if (r < parts) {
-                    const float e = exp2f(m[r] - M);
-                    S += e * cluster_ld(cluster_map(smem_addr(pl + g), r));
-                    O += e * cluster_ld(cluster_map(smem_addr(po + idx), r));
+                for (int y = 0; y < kMaxCluster; ++y) {
+                    const uint32_t at = part_of(min(y, n - 1));
+                    m[y] = cluster_ld(at + g * 4);
+                    l[y] = cluster_ld(at + (G + g) * 4);
+                    o[y] = cluster_ld4(at + (S::kO + 4 * i) * 4);
                 }
+#pragma unroll
+                for (int y = 0; y < kMaxCluster; ++y) M = fmaxf(M, m[y]);
+                if (M != -INFINITY) {
+#pragma unroll
+                    for (int y = 0; y < kMaxCluster; ++y) {
+                        const float e = y < n ? exp2f(m[y] - M) : 0.f;
+                        if (e != 0.f) {
+                            sum += e * l[y];
+                            add4(v, e, o[y]);
+                        }
+                    }
+                }
+                store4(r, i, v, sum > 0.f ? p.v_scale / sum : 0.f);
+            }
         }
-        decode::store_out(out + idx, (S > 0.f ? O / S : 0.f) * p.v_scale);
     }
     cluster_sync();                                         // partners are done reading
 }
 
+// Clusters of `size` CTAs that fit on the current device at once (cached).
+int resident_clusters(const void* kern, int smem, int threads, int size, int* out);
+
 template <class Math, typename QT, int D, int BS, int G, int PAIR>
 int launch(const Args& a) {
-    using P = decode::Pipe<Math, D, BS, G, kNumWarps>;
-    auto kern = sparse_decode_kernel<Math, QT, D, BS, G, kNumWarps, PAIR>;
+    using S = Smem<Math, D, BS, G>;
+    auto kern = sparse_decode_kernel<Math, QT, D, BS, G, PAIR>;
+    const void* fn = reinterpret_cast<const void*>(kern);
+    // three CTAs an SM where their rings fit; alone on its SM a CTA gets a deep ring
+    constexpr int kStages3 = S::stages(kNumWarps, kSmemSm / 3 - 1024);
+    constexpr int kWideWarps = S::kWide ? 2 * kNumWarps : kNumWarps;
+    constexpr int kStages1 = S::stages(kWideWarps, kSmemSm);
+    constexpr int kMost = S::bytes(kWideWarps, kStages1) > S::bytes(kNumWarps, kStages3)
+                              ? S::bytes(kWideWarps, kStages1) : S::bytes(kNumWarps, kStages3);
     int occ = 0;
-    const int st = kernel_setup(reinterpret_cast<const void*>(kern), P::kSmem, kNumWarps * 32, &occ);
+    int st = kernel_setup(fn, kMost, kNumWarps * 32, &occ);
     if (st != PKV_OK) return st;
-    // parts of a row: doubled until the CTAs make two waves, each part keeping a
-    // stage per warp
     const int stages = ((a.p.k < a.p.max_blocks ? a.p.k : a.p.max_blocks) + PAIR - 1) / PAIR;
     const long long rows = (long long)a.num_seqs * a.p.num_kv_heads;
-    const long long wave = (long long)num_sms() * (occ > 0 ? occ : 1);
-    int parts = 1;
-    while (parts < kMaxParts && rows * parts < 2 * wave && 2 * parts * kNumWarps <= stages) parts *= 2;
+    int size = 1, per = 1, warps = kNumWarps, depth = kStages3;
+    if (2 * rows <= num_sms()) {
+        // few rows: each to as many warps as have a stage, one CTA an SM
+        warps = kWideWarps;
+        depth = kStages1;
+        for (int s = kMaxCluster; s > 1; s /= 2) {
+            if (s * rows > num_sms() || s * warps > stages) continue;
+            int fit = 0;
+            st = resident_clusters(fn, S::bytes(warps, depth), warps * 32, s, &fit);
+            if (st != PKV_OK) return st;
+            if (fit >= rows) {
+                size = s;
+                break;
+            }
+        }
+    } else {
+        // a CTA a row, in waves; or one wave of clusters that share their rows evenly,
+        // where that leaves the fullest CTA a fifth less (512 rows of 128 E4M3 blocks,
+        // on 456 places: 67 us in waves of whole rows, 56 us by fours)
+        int fit = 0;
+        st = resident_clusters(fn, S::bytes(warps, depth), warps * 32, 1, &fit);
+        if (st != PKV_OK) return st;
+        double best = 0.8 * (double)((rows + fit - 1) / fit);
+        for (int s = 2; s <= kMaxCluster; s *= 2) {
+            st = resident_clusters(fn, S::bytes(warps, depth), warps * 32, s, &fit);
+            if (st != PKV_OK) return st;
+            const long long r = fit > 0 ? (rows + fit - 1) / fit : kMaxRows + 1;
+            if (r > kMaxRows || r * stages < 2LL * s * warps) continue;
+            const double load = (double)r / s;
+            if (load < best) {
+                best = load;
+                size = s;
+                per = (int)r;
+            }
+        }
+    }
+    const long long ctas = (rows + per - 1) / per * size;
     Params p = a.p;
+    p.num_rows = (int)rows;
+    p.cluster_rows = per;
+    p.stages = depth;
     p.qscale = a.scale * a.k_scale * kLog2e;
     p.v_scale = a.v_scale;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(parts, p.num_kv_heads, a.num_seqs);
-    cfg.blockDim = dim3(kNumWarps * 32);
-    cfg.dynamicSmemBytes = P::kSmem;
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(warps * 32);
+    cfg.dynamicSmemBytes = S::bytes(warps, depth);
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = parts;
+    attr[1].val.clusterDim.x = size;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;

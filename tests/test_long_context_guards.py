@@ -103,6 +103,36 @@ def test_sparse_entry_refuses_before_any_cuda_call(over, status):
     assert c_sparse(**over) == status
 
 
+def test_packed_call_is_the_call():
+    """pkv_bound_call refuses another number of arguments or an unknown call, and
+    passes every argument on: the statuses of the calls' own checks come back."""
+    lib = library()
+    f32 = lambda x: ctypes.c_uint32.from_buffer_copy(ctypes.c_float(x)).value
+    u64 = lambda *a: (ctypes.c_uint64 * len(a))(*[x & 0xffffffffffffffff for x in a])
+    call = lambda c, a: lib.pkv_bound_call(c, ctypes.addressof(a), len(a), None)
+    sections = (ctypes.c_int32 * 1)(32)
+
+    def rotary(T=T, R=64, stride=256, ks=1.0, sec=ctypes.addressof(sections), cache=1):
+        return u64(*[0x1000] * 9, sec, 1, stride, 256, 128, 128, T, HQ, HKV, D, R, 0, BS, NB, 64, 1, cache,
+                   f32(ks), f32(1.0))
+
+    assert call(0, rotary(T=0)) == 0
+    assert call(0, rotary(T=-1)) == -1                     # a sign survives
+    assert call(0, rotary(stride=-256)) == -1
+    assert call(0, rotary(R=24)) == -2
+    assert call(0, rotary(ks=2.0)) == -1                   # a float does
+    assert call(0, rotary(T=0, ks=2.0, cache=2)) == 0
+    assert call(0, rotary(sec=0)) == -1                    # a pointer does
+    assert call(0, u64(*list(rotary())[:-1])) == -1        # one argument short
+    assert call(1, u64(*[0] * 5, 0, MB, NB, HKV, D, BS, 1, 1)) == 0
+    assert call(1, u64(*[0] * 5, 0, MB, NB, HKV, 24, BS, 1, 1)) == -2
+    assert call(2, u64(*[0] * 5, 0, MB, NB, HQ, HKV, D, BS, K, 1, 1, 1, 0, 0)) == 0
+    assert call(2, u64(*[0] * 5, 0, MB, NB, HQ, HKV, D, BS, K, 3, 2, 1, 0, 0)) == -1
+    assert call(3, u64(*[0] * 7, 0, MB, NB, K, HQ, HKV, D, BS, f32(0.1), 1, 1, f32(1.0), f32(1.0))) == 0
+    assert call(3, u64(*[0] * 7, 0, MB, NB, K, HQ, HKV, D, BS, f32(math.nan), 1, 1, f32(1.0), f32(1.0))) == -1
+    assert call(4, rotary(T=0)) == -1 and lib.pkv_bound_call(0, None, 28, None) == -1
+
+
 # -------------------------------------------------------------------- binding
 def pools(dtype=BF):
     ks, vs = pkv.pool_shapes(NB, HKV, BS, D, dtype)
