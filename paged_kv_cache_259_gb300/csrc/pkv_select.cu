@@ -118,13 +118,13 @@ __device__ __forceinline__ void widen(const uint4& raw, uint32_t (&x)[Cmp<KV>::k
 // Bound: HBM bytes of the changed blocks' K; a decode step (one block per
 // sequence) is launch latency.
 template <typename KV>
-__global__ void __launch_bounds__(128, 8) update_key_bounds_kernel(
+__global__ void __launch_bounds__(128, 5) update_key_bounds_kernel(
     const uint4* __restrict__ k_pool, void* __restrict__ bounds, const int32_t* __restrict__ tables,
     const int32_t* __restrict__ lens, const int32_t* __restrict__ first, int max_blocks,
     int num_blocks, int hkv, int d, int bs, int* err) {
     pdl_enter();                                           // launched with launch_pdl
     using C = Cmp<KV>;
-    constexpr int R = C::kRegs;
+    constexpr int R = C::kRegs, QB = R == 8 ? 2 : 4;       // chunks of 4 planes read together
     const int b = blockIdx.y, lane = threadIdx.x & 31;
     int L = lens[b];
     int f = first[b];
@@ -149,56 +149,75 @@ __global__ void __launch_bounds__(128, 8) update_key_bounds_kernel(
         const uint4* tile = k_pool + ((size_t)id * hkv + h) * planes * bs;
         char* out = static_cast<char*>(bounds) +
                     ((size_t)id * hkv + h) * 2 * d * (C::kElt == 4 ? 4 : 2);
-        for (int q = 0; q < planes; q += 4) {
-            const bool in = q + pl < planes;
-            uint32_t x[2 * R];                             // min | max
+        for (int q0 = 0; q0 < planes; q0 += 4 * QB) {
+            uint32_t x[QB][2 * R];                         // min | max
 #pragma unroll
-            for (int i = 0; i < R; ++i) x[i] = C::kInf, x[R + i] = C::kNegInf;
-            for (int g = 0; g * 8 < ntok; ++g) {
-                if (in && g * 8 + tl < ntok) {
-                    uint32_t v[R];
-                    widen<KV>(tile[(g * planes + q + pl) * 8 + tl], v);
+            for (int u = 0; u < QB; ++u)
 #pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        x[i] = min2(x[i], v[i], typename C::T{});
-                        x[R + i] = max2(x[R + i], v[i], typename C::T{});
+                for (int i = 0; i < R; ++i) x[u][i] = C::kInf, x[u][R + i] = C::kNegInf;
+            for (int g0 = 0; g0 * 8 < ntok; g0 += 2) {
+                uint4 raw[2][QB];                          // read together
+                bool ok[2][QB];
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int u = 0; u < QB; ++u) {
+                        const int plane = q0 + 4 * u + pl;
+                        ok[g][u] = plane < planes && (g0 + g) * 8 + tl < ntok;
+                        if (ok[g][u]) raw[g][u] = tile[((g0 + g) * planes + plane) * 8 + tl];
                     }
-                }
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int u = 0; u < QB; ++u)
+                        if (ok[g][u]) {
+                            uint32_t v[R];
+                            widen<KV>(raw[g][u], v);
+#pragma unroll
+                            for (int i = 0; i < R; ++i) {
+                                x[u][i] = min2(x[u][i], v[i], typename C::T{});
+                                x[u][R + i] = max2(x[u][R + i], v[i], typename C::T{});
+                            }
+                        }
             }
             // step 1 (tokens t, t^4): the lower lane keeps the minima, the upper
             // the maxima; steps 2 and 3 halve what is left
             const bool up = (tl & 4) != 0;
-            uint32_t y[R];
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const uint32_t other = __shfl_xor_sync(kFull, up ? x[i] : x[R + i], 4);
-                y[i] = up ? max2(x[R + i], other, typename C::T{}) : min2(x[i], other, typename C::T{});
-            }
+            for (int u = 0; u < QB; ++u) {
+                uint32_t y[R];
 #pragma unroll
-            for (int s = 1; s <= 2; ++s) {
-                const int keep = R >> s;
-                const bool hi = (tl & (4 >> s)) != 0;
-#pragma unroll
-                for (int i = 0; i < R / 2; ++i)
-                    if (i < keep) {
-                        const uint32_t other = __shfl_xor_sync(kFull, hi ? y[i] : y[keep + i], 4 >> s);
-                        const uint32_t mine = hi ? y[keep + i] : y[i];
-                        y[i] = up ? max2(mine, other, typename C::T{}) : min2(mine, other, typename C::T{});
-                    }
-            }
-            if (!in) continue;
-            // lane tl holds registers (tl & 3) * R/4 .. of the chunk's minima or maxima
-            if constexpr (std::is_same<KV, uint8_t>::value) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
-                    const __nv_bfloat162 w = __floats2bfloat162_rn(v.x, v.y);   // exact
-                    y[i] = *reinterpret_cast<const uint32_t*>(&w);
+                for (int i = 0; i < R; ++i) {
+                    const uint32_t other = __shfl_xor_sync(kFull, up ? x[u][i] : x[u][R + i], 4);
+                    y[i] = up ? max2(x[u][R + i], other, typename C::T{}) : min2(x[u][i], other, typename C::T{});
                 }
-                *reinterpret_cast<uint2*>(out + (up ? 2 * d : 0) + (q + pl) * 32 + (tl & 3) * 8) =
-                    make_uint2(y[0], y[1]);
-            } else {
-                *reinterpret_cast<uint32_t*>(out + (up ? d * C::kElt : 0) + (q + pl) * 16 + (tl & 3) * 4) = y[0];
+#pragma unroll
+                for (int s = 1; s <= 2; ++s) {
+                    const int keep = R >> s;
+                    const bool hi = (tl & (4 >> s)) != 0;
+#pragma unroll
+                    for (int i = 0; i < R / 2; ++i)
+                        if (i < keep) {
+                            const uint32_t other = __shfl_xor_sync(kFull, hi ? y[i] : y[keep + i], 4 >> s);
+                            const uint32_t mine = hi ? y[keep + i] : y[i];
+                            y[i] = up ? max2(mine, other, typename C::T{}) : min2(mine, other, typename C::T{});
+                        }
+                }
+                const int plane = q0 + 4 * u + pl;
+                if (plane >= planes) continue;
+                // lane tl holds registers (tl & 3) * R/4 .. of the chunk's minima or maxima
+                if constexpr (std::is_same<KV, uint8_t>::value) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
+                        const __nv_bfloat162 z = __floats2bfloat162_rn(v.x, v.y);   // exact
+                        y[i] = *reinterpret_cast<const uint32_t*>(&z);
+                    }
+                    *reinterpret_cast<uint2*>(out + (up ? 2 * d : 0) + plane * 32 + (tl & 3) * 8) =
+                        make_uint2(y[0], y[1]);
+                } else {
+                    *reinterpret_cast<uint32_t*>(out + (up ? d * C::kElt : 0) + plane * 16 + (tl & 3) * 4) = y[0];
+                }
             }
         }
     }
@@ -243,121 +262,137 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t x) {
     return r;
 }
 
-// Scores of 16 blocks per warp at a time. The k order of the product is free as
-// long as both operands agree on it, so lane (r, c) loads 16 bytes of blocks r
-// and r+8 at dims 32i + 8c .. +7 straight into the A fragments of k-steps 2i and
-// 2i+1 (no shared memory), and the same dims of query head r into the B
-// fragments. Four accumulator chains (by i) shorten the dependency and the
-// rounding. The lower and the upper bounds of a tile are two halves of a software
-// pipeline: the next tile's half is loaded into the registers that the product
-// has just read, so a warp always has 4 to 8 KB on the way.
-// Bound: HBM bytes of the bounds. The 4 warps of a CTA take neighbouring kv heads
-// of the same blocks (as many as there are), so a block's rows are read together.
-template <int D>
-struct ScoreTile {
-    static constexpr int I = D / 32;                       // 16-byte chunks a lane holds per bound
-    uint4 x0[I], x1[I];                                    // blocks r and r+8
+// Scores of 16 blocks of a kv head per warp and stage. A CTA takes `side` neighbouring
+// kv heads of (4 / side) x 16 blocks at a time, so a block's rows of those heads are
+// one contiguous copy (side * 4 D bytes) into a stage of a shared-memory ring, two
+// stages deep (66 KB of copies in flight per CTA, three CTAs an SM); rows lie 16 bytes
+// apart from a multiple of 128 so that the operand reads (ldmatrix) meet no bank
+// twice. Four accumulator chains shorten the dependency and the rounding.
+// Bound: HBM bytes of the bounds.
+constexpr int kScoreStages = 2;
+constexpr int kStageRows = 64;         // rows of 16-bit [2][D], of all warps
 
-    __device__ __forceinline__ void load(const uint4* p0, const uint4* p1, bool ok0, bool ok1) {
-#pragma unroll
-        for (int i = 0; i < I; ++i) {
-            x0[i] = ok0 ? __ldg(p0 + 4 * i) : make_uint4(0, 0, 0, 0);
-            x1[i] = ok1 ? __ldg(p1 + 4 * i) : make_uint4(0, 0, 0, 0);
-        }
-    }
-    template <int CHAIN>                                   // I chains from CHAIN on (mod 4)
-    __device__ __forceinline__ void multiply(float (&acc)[4][4], uint32_t& m, const uint32_t (&q)[I][4]) const {
-#pragma unroll
-        for (int i = 0; i < I; ++i) {
-            mma_bf16(acc[(CHAIN + i) & 3], x0[i].x, x1[i].x, x0[i].y, x1[i].y, q[i][0], q[i][1]);
-            mma_bf16(acc[(CHAIN + i) & 3], x0[i].z, x1[i].z, x0[i].w, x1[i].w, q[i][2], q[i][3]);
-            m = abs_max2(abs_max2(m, x0[i].x), x0[i].y);
-            m = abs_max2(abs_max2(m, x0[i].z), x0[i].w);
-            m = abs_max2(abs_max2(m, x1[i].x), x1[i].y);
-            m = abs_max2(abs_max2(m, x1[i].z), x1[i].w);
-        }
-    }
+template <int D>
+struct ScoreSmem {
+    static constexpr int kRow = 4 * D;                     // bytes of one head's bounds
+    static constexpr int kStage = kStageRows * (kRow + 16);
+    static constexpr int kBytes = kScoreStages * kStage;
 };
 
 template <int D>
-__global__ void __launch_bounds__(128, 4) score_blocks_bf16(const SelectParams p, int tiles_per_warp,
-                                                            int heads_per_cta) {
+__global__ void __launch_bounds__(128) score_blocks_bf16(const SelectParams p, int per, int side) {
     pdl_enter();                                           // launched with launch_pdl
-    using Tile = ScoreTile<D>;
-    constexpr int I = Tile::I;
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.z;
+    using S = ScoreSmem<D>;
+    constexpr int KS = D / 16;                             // k-steps of one bound
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ __align__(8) uint64_t bars[kScoreStages];
+    __shared__ int ids[kScoreStages][kStageRows];
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, b = blockIdx.z;
     const int r = lane >> 2, c = lane & 3, G = p.hq / p.hkv;
-    const int h = blockIdx.y * heads_per_cta + w % heads_per_cta;
-    const int tile0 = (blockIdx.x * (4 / heads_per_cta) + w / heads_per_cta) * tiles_per_warp;
-    // the table and the query are read beside the length: entries past it are in
-    // the table, and unused
-    auto table_at = [&](int tile) {
-        const int j = tile * 16 + (lane & 15);
-        return j < p.max_blocks ? p.tables[(size_t)b * p.max_blocks + j] : -1;
+    const int h0 = blockIdx.y * side, h = h0 + w % side;   // the CTA's first kv head, this warp's
+    const int blocks = kStageRows / side;                  // blocks of a stage
+    const int pitch = side * S::kRow + 16;
+    const int first = blockIdx.x * per;                    // stages first .. first + per - 1 of the row
+    // the table and the query are read beside the length: entries past it are in the
+    // table, and unused
+    auto table_at = [&](int stage) {
+        const int j = stage * blocks + tid;
+        return tid < blocks && j < p.max_blocks ? p.tables[(size_t)b * p.max_blocks + j] : -1;
     };
-    int id_next = table_at(tile0);
-    uint32_t qn[I][4], qp[I][4];                           // min(q, 0), max(q, 0)
+    int next[kScoreStages];
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < G)
-            x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                     ((size_t)b * p.hq + h * G + r) * D + 32 * i + 8 * c));
-        qp[i][0] = x.x, qp[i][1] = x.y, qp[i][2] = x.z, qp[i][3] = x.w;
+    for (int s = 0; s < kScoreStages; ++s) next[s] = s < per ? table_at(first + s) : -1;
+    uint32_t qn[KS][2], qp[KS][2];                         // min(q, 0), max(q, 0)
+    {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                              ((size_t)b * p.hq + h * G + r) * D);
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) qp[i][j] = r < G ? __ldg(q + 8 * i + 4 * j + c) : 0u;
     }
     const int n = row_blocks(p, b, false);
     if (n <= p.k) return;                                  // every block is selected
     const int lo = p.first, hi = n - p.last;               // blocks with a score: [lo, hi)
-    const int first = max(tile0, lo / 16), end = min(tile0 + tiles_per_warp, (hi + 15) / 16);
-    if (first >= end) return;
-    if (first > tile0) id_next = table_at(first);
+    const int count = min(per, (hi + blocks - 1) / blocks - first);
+    if (count <= 0) return;
+    if (tid < kScoreStages) mbar_init(smem_addr(&bars[tid]), 2);
+    fence_mbar_init();
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < I; ++i)
+    for (int i = 0; i < KS; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
             qn[i][j] = min2(qp[i][j], 0u, __nv_bfloat16{});
             qp[i][j] = max2(qp[i][j], 0u, __nv_bfloat16{});
         }
-    const size_t row = (size_t)b * p.hkv + h;
-    const uint4* base = reinterpret_cast<const uint4*>(p.bounds) + (size_t)h * (D / 4) + c;
-    const size_t pitch = (size_t)p.hkv * (D / 4);          // 16-byte units of a block
-    // the ids of a tile's blocks r and r+8 (-1: no score), from the lanes' entries
-    auto blocks_of = [&](int tile, int id, int* id0, int* id1) {
-        const int j = tile * 16 + (lane & 15);
-        if (j < lo || j >= hi) {
+    const char* src = static_cast<const char*>(p.bounds) + (size_t)h0 * S::kRow;
+    const size_t block_bytes = (size_t)p.hkv * S::kRow;
+    // warps 0 and 1, a lane a block: its rows into slot s
+    auto issue = [&](int stage, int s, int id) {
+        if (w >= 2) return;
+        const int j = stage * blocks + tid;
+        if (tid >= blocks || j < lo || j >= hi) {
             id = -1;
         } else if (id < 0 || id >= p.num_blocks) {
             flag_error(p.err, kErrOutOfRange);
             id = -1;
         }
-        *id0 = __shfl_sync(kFull, id, r);
-        *id1 = __shfl_sync(kFull, id, r + 8);
+        ids[s][tid] = id;
+        const unsigned live = __ballot_sync(kFull, id >= 0);
+        const uint32_t bar = smem_addr(&bars[s]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(live) * side * S::kRow);
+        __syncwarp();
+        if (id >= 0)
+            bulk_g2s(smem_addr(smem + s * S::kStage + tid * pitch), src + id * block_bytes, side * S::kRow, bar,
+                     l2_evict_first());
     };
-    Tile lower, upper;
-    int id0, id1;
-    blocks_of(first, id_next, &id0, &id1);
-    id_next = first + 1 < end ? table_at(first + 1) : -1;
-    const uint4 *p0 = base + max(id0, 0) * pitch, *p1 = base + max(id1, 0) * pitch;
-    lower.load(p0, p1, id0 >= 0, id1 >= 0);
-    upper.load(p0 + D / 8, p1 + D / 8, id0 >= 0, id1 >= 0);
-    for (int tile = first; tile < end; ++tile) {
-        const bool ok0 = id0 >= 0, ok1 = id1 >= 0, more = tile + 1 < end;
-        if (more) {
-            blocks_of(tile + 1, id_next, &id0, &id1);
-            id_next = tile + 2 < end ? table_at(tile + 2) : -1;
-            p0 = base + max(id0, 0) * pitch;
-            p1 = base + max(id1, 0) * pitch;
+#pragma unroll
+    for (int s = 0; s < kScoreStages; ++s)
+        if (s < count) issue(first + s, s, next[s]);
+    int id_next = count > kScoreStages ? table_at(first + kScoreStages) : -1;
+    const size_t row = (size_t)b * p.hkv + h;
+    const int tile0 = (w / side) * 16;                     // this warp's blocks within a stage
+    int s = 0;
+    uint32_t phase = 0;
+    for (int k = 0; k < count; ++k) {
+        const bool ok = mbar_wait_bounded(smem_addr(&bars[s]), phase, p.err);
+        if (__syncthreads_or(!ok)) {
+            // gave up: record it, let the copies in flight land, leave
+            if (tid == 0) flag_error(p.err, kErrTimeout);
+            for (int kk = k; kk < min(count, k + kScoreStages); ++kk) {
+                (void)mbar_wait_bounded(smem_addr(&bars[s]), phase, nullptr);
+                if (++s == kScoreStages) s = 0, phase ^= 1;
+            }
+            return;
         }
+        const uint32_t base = smem_addr(smem + s * S::kStage + tile0 * pitch + (w % side) * S::kRow) +
+                              (lane & 15) * pitch + (lane >> 4) * 16;
+        const bool ok0 = ids[s][tile0 + r] >= 0, ok1 = ids[s][tile0 + r + 8] >= 0;
         float acc[4][4];
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[a][e] = 0.f;
-        uint32_t m = 0;
-        lower.template multiply<0>(acc, m, qn);
-        if (more) lower.load(p0, p1, id0 >= 0, id1 >= 0);
-        upper.template multiply<I>(acc, m, qp);
-        if (more) upper.load(p0 + D / 8, p1 + D / 8, id0 >= 0, id1 >= 0);
+        uint32_t m0 = 0, m1 = 0;                           // largest |bound| of blocks r and r+8
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) {
+            uint32_t a0, a1, a2, a3;                       // rows r, r+8; dims 16i + 2c, + 8
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
+                         : "r"(base + i * 32)
+                         : "memory");
+            const uint32_t(&q)[2] = i < KS ? qn[i < KS ? i : 0] : qp[i < KS ? 0 : i - KS];
+            mma_bf16(acc[i & 3], a0, a1, a2, a3, q[0], q[1]);
+            m0 = abs_max2(abs_max2(m0, a0), a2);
+            m1 = abs_max2(abs_max2(m1, a1), a3);
+        }
+        __syncthreads();                                   // the slot is free
+        if (k + kScoreStages < count) {
+            fence_proxy_async_smem();
+            issue(first + k + kScoreStages, s, id_next);
+            id_next = k + 1 + kScoreStages < count ? table_at(first + k + 1 + kScoreStages) : -1;
+        }
         // heads 2c, 2c+1 of blocks r (s0) and r+8 (s1); columns past G are no heads
         float s0 = -INFINITY, s1 = -INFINITY;
 #pragma unroll
@@ -371,14 +406,21 @@ __global__ void __launch_bounds__(128, 4) score_blocks_bf16(const SelectParams p
             s0 = max_nan(s0, __shfl_xor_sync(kFull, s0, o));
             s1 = max_nan(s1, __shfl_xor_sync(kFull, s1, o));
         }
-        float* out = p.scores + row * p.stride + tile * 16;
-        if (c == 0) {
+        const int j0 = (first + k) * blocks + tile0;
+        float* out = p.scores + row * p.stride + j0;
+        if (c == 0 && j0 < p.stride) {
             out[r] = ok0 ? s0 + 0.f : -INFINITY;           // + 0: no negative zero
             out[r + 8] = ok1 ? s1 + 0.f : -INFINITY;
         }
-        m &= 0x7fff7fffu;                                  // bf16 order is its bits' order; NaN above
-        const uint32_t mm = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
-        if (lane == 0) p.tile_max[row * (p.stride / 16) + tile] = __uint_as_float(mm << 16);
+        // bf16 magnitudes order as their bits, NaN on top
+        m0 = ok0 ? m0 & 0x7fff7fffu : 0u;
+        m1 = ok1 ? m1 & 0x7fff7fffu : 0u;
+        const uint32_t mm = __reduce_max_sync(kFull, max(max(m0 & 0xffffu, m0 >> 16), max(m1 & 0xffffu, m1 >> 16)));
+        if (lane == 0 && j0 < p.stride) p.tile_max[row * (p.stride / 16) + j0 / 16] = __uint_as_float(mm << 16);
+        if (++s == kScoreStages) {
+            s = 0;
+            phase ^= 1;
+        }
     }
 }
 
@@ -386,8 +428,7 @@ __global__ void __launch_bounds__(128, 4) score_blocks_bf16(const SelectParams p
 // block at a time, lane l the dims l, l + 32, ..., and the heads' sums are
 // reduced across the lanes.
 template <int D>
-__global__ void __launch_bounds__(128) score_blocks_f32(const SelectParams p, int tiles_per_warp,
-                                                        int) {
+__global__ void __launch_bounds__(128) score_blocks_f32(const SelectParams p, int tiles_per_warp) {
     pdl_enter();                                           // launched with launch_pdl
     const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31;
     const int n = row_blocks(p, b, false);
@@ -543,9 +584,97 @@ __device__ unsigned long long exact_key_f64(const SelectParams& p, int b, int h,
 }
 
 constexpr int kBins = 1024;
-constexpr int kListMax = 1024;         // blocks ranked in shared memory
+constexpr int kListMax = 512;         // blocks ranked in shared memory
 
-// One CTA per (kv head, sequence) over the row's scores. A thread owns chunks of
+// Scores of a row's blocks by one CTA, into shared memory (`out`, and the tiles'
+// largest |bound|): 16 blocks per warp at a time, read straight into the operand
+// fragments. The k order of the product is free as long as both operands agree on it,
+// so lane (r, c) loads 16 bytes of blocks r and r+8 at dims 32i + 8c .. +7 into the A
+// fragments of k-steps 2i and 2i+1, and the same dims of query head r into the B
+// fragments. Four accumulator chains, as above.
+template <int D, int NW>
+__device__ __forceinline__ void score_row(const SelectParams& p, int b, int h, int lo, int hi, float* out,
+                                          float* tile_max) {
+    constexpr int I = D / 32;                              // 16-byte chunks a lane holds per bound
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3, G = p.hq / p.hkv;
+    auto table_at = [&](int tile) {
+        const int j = tile * 16 + (lane & 15);
+        return j >= lo && j < hi ? p.tables[(size_t)b * p.max_blocks + j] : -1;
+    };
+    int id_next = table_at(w);
+    uint32_t qn[I][4], qp[I][4];                           // min(q, 0), max(q, 0)
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < G)
+            x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                     ((size_t)b * p.hq + h * G + r) * D + 32 * i + 8 * c));
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            qn[i][j] = min2(v[j], 0u, __nv_bfloat16{});
+            qp[i][j] = max2(v[j], 0u, __nv_bfloat16{});
+        }
+    }
+    const uint4* base = reinterpret_cast<const uint4*>(p.bounds) + (size_t)h * (D / 4) + c;
+    const size_t pitch = (size_t)p.hkv * (D / 4);          // 16-byte units of a block
+#pragma unroll 1
+    for (int tile = w; tile * 16 < hi; tile += NW) {
+        int id = id_next;
+        id_next = table_at(tile + NW);
+        const int j = tile * 16 + (lane & 15);
+        if (j >= lo && j < hi && (id < 0 || id >= p.num_blocks)) {
+            flag_error(p.err, kErrOutOfRange);
+            id = -1;
+        }
+        const int id0 = __shfl_sync(kFull, id, r), id1 = __shfl_sync(kFull, id, r + 8);
+        const uint4 *p0 = base + max(id0, 0) * pitch, *p1 = base + max(id1, 0) * pitch;
+        uint4 x0[2 * I], x1[2 * I];
+#pragma unroll
+        for (int i = 0; i < 2 * I; ++i) {
+            x0[i] = id0 >= 0 ? __ldg(p0 + 4 * i) : make_uint4(0, 0, 0, 0);
+            x1[i] = id1 >= 0 ? __ldg(p1 + 4 * i) : make_uint4(0, 0, 0, 0);
+        }
+        float acc[4][4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[a][e] = 0.f;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 2 * I; ++i) {
+            const uint32_t(&q)[4] = i < I ? qn[i < I ? i : 0] : qp[i < I ? 0 : i - I];
+            mma_bf16(acc[i & 3], x0[i].x, x1[i].x, x0[i].y, x1[i].y, q[0], q[1]);
+            mma_bf16(acc[i & 3], x0[i].z, x1[i].z, x0[i].w, x1[i].w, q[2], q[3]);
+            m = abs_max2(abs_max2(m, x0[i].x), x0[i].y);
+            m = abs_max2(abs_max2(m, x0[i].z), x0[i].w);
+            m = abs_max2(abs_max2(m, x1[i].x), x1[i].y);
+            m = abs_max2(abs_max2(m, x1[i].z), x1[i].w);
+        }
+        float s0 = -INFINITY, s1 = -INFINITY;              // heads 2c, 2c+1 of blocks r and r+8
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (2 * c + e < G) {
+                s0 = max_nan(s0, (acc[0][e] + acc[1][e]) + (acc[2][e] + acc[3][e]));
+                s1 = max_nan(s1, (acc[0][2 + e] + acc[1][2 + e]) + (acc[2][2 + e] + acc[3][2 + e]));
+            }
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+            s0 = max_nan(s0, __shfl_xor_sync(kFull, s0, o));
+            s1 = max_nan(s1, __shfl_xor_sync(kFull, s1, o));
+        }
+        if (c == 0) {
+            out[tile * 16 + r] = id0 >= 0 ? s0 + 0.f : -INFINITY;
+            out[tile * 16 + r + 8] = id1 >= 0 ? s1 + 0.f : -INFINITY;
+        }
+        m &= 0x7fff7fffu;
+        const uint32_t mm = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
+        if (lane == 0) tile_max[tile] = __uint_as_float(mm << 16);
+    }
+}
+
+// One CTA per (kv head, sequence) over the row's scores (FD: which it computes itself,
+// head_dim FD). A thread owns chunks of
 // 8 blocks (KEEP: one chunk, in registers). The score range is cut into 1,024
 // equal bins; the bin of the last place and its neighbours within the rounding
 // window hold the few blocks that are undecided (the range is cut again when they
@@ -554,7 +683,7 @@ constexpr int kListMax = 1024;         // blocks ranked in shared memory
 // more of them than places. A bin of a score is a monotone function of it, so
 // bins decide soundly whatever the rounding of their edges.
 // Bound: latency (a row's scores are at most a few hundred KB, from L2).
-template <typename T, int NT, bool KEEP>
+template <typename T, int NT, bool KEEP, int FD = 0>
 __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
     constexpr int NW = NT / 32;
     // Launched behind this call's scoring kernel: lengths, tables and queries were
@@ -579,7 +708,9 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
     float* qf = reinterpret_cast<float*>(list_row + kListMax);                     // [8][128]
     uint32_t* hist = reinterpret_cast<uint32_t*>(qf + 8 * 128);                    // [kBins]
     uint32_t* sel = hist + kBins;                                                  // selected blocks
-    uint32_t* cand = sel + words_max;                                              // a crowd
+    uint32_t* cand = sel + (words_max + 3) / 4 * 4;                                // a crowd
+    float* own_scores = reinterpret_cast<float*>(cand + (words_max + 3) / 4 * 4);  // FD: [blocks, padded to 16]
+    float* own_max = own_scores + (p.max_blocks + 15) / 16 * 16;                   // FD: [tiles]
     unsigned char* sel8 = reinterpret_cast<unsigned char*>(sel);
     unsigned char* cand8 = reinterpret_cast<unsigned char*>(cand);
     __shared__ uint32_t sh_a[NW], sh_b[NW], sh_q[NW], sh_m[NW];
@@ -636,9 +767,14 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
         for (int i = tid; i < kBins; i += NT) hist[i] = 0;
         if (tid == 0) sh_cnt = 0, sh_win[0] = 0, sh_win[1] = 0;
         if (p.scored) wait_prerequisites();
+        if constexpr (FD > 0) {
+            score_row<FD, NW>(p, b, h, lo, hi, own_scores, own_max);
+            __syncthreads();
+        }
 
         const T* bounds = static_cast<const T*>(p.bounds);
-        const float* scores = p.scores + row * p.stride;   // 64-byte aligned rows
+        const float* scores = FD > 0 ? own_scores : p.scores + row * p.stride;   // 64-byte aligned rows
+        const float* tm = FD > 0 ? own_max : p.tile_max + row * (p.stride / 16);
         // a chunk's scores, -inf for blocks that have none
         auto load_chunk = [&](int c, float (&s)[8]) {
             const float4 x = *reinterpret_cast<const float4*>(scores + 8 * c);
@@ -665,8 +801,7 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
             }
         };
         uint32_t mx = 0;                                   // |bounds|: their bits' order, NaN on top
-        const float* tm = p.tile_max + row * (p.stride / 16);
-        for (int i = lo / 16 + tid; i * 16 < hi; i += NT) mx = max(mx, __float_as_uint(__ldcg(tm + i)));
+        for (int i = lo / 16 + tid; i * 16 < hi; i += NT) mx = max(mx, __float_as_uint(tm[i]));
         if (KEEP && tid < chunks) load_chunk(tid, kept);
         float smin = INFINITY, smax = -INFINITY;
         for_chunks([&](int, const float (&s)[8]) {
@@ -945,48 +1080,83 @@ constexpr int kMaxBlocks = 1 << 19;    // 128 KB of bitmaps
 
 inline int padded(int max_blocks) { return (max_blocks + 15) / 16 * 16; }
 
-template <typename T, int NT, bool KEEP>
+template <typename T, int NT, bool KEEP, int FD = 0>
 int launch_select(const SelectParams& p, int num_seqs, cudaStream_t stream) {
-    const size_t words = (p.max_blocks + 31) / 32, most = KEEP ? NT / 4 : kMaxBlocks / 32;
-    auto kern = select_rows<T, NT, KEEP>;
+    auto bytes = [](int blocks) {
+        const int words = ((blocks + 31) / 32 + 3) / 4 * 4;
+        return (int)kSelectFixed + words * 8 + (FD > 0 ? padded(blocks) / 16 * 68 : 0);
+    };
+    auto kern = select_rows<T, NT, KEEP, FD>;
     int occ = 0;
-    const int st = kernel_setup(reinterpret_cast<const void*>(kern), (int)(kSelectFixed + most * 8), NT, &occ);
+    const int st = kernel_setup(reinterpret_cast<const void*>(kern), bytes(KEEP ? NT * 8 : kMaxBlocks), NT, &occ);
     if (st != PKV_OK) return st;
     note_launch();
-    const cudaError_t e = launch_pdl(kern, dim3(p.hkv, num_seqs), dim3(NT), kSelectFixed + words * 8, stream, p);
+    const cudaError_t e = launch_pdl(kern, dim3(p.hkv, num_seqs), dim3(NT), bytes(p.max_blocks), stream, p);
     return e == cudaSuccess ? PKV_OK : cuda_fail("select_blocks: selection launch", e);
 }
 
-template <typename T>
-int launch_scores(const SelectParams& p, int num_seqs, cudaStream_t stream) {
+template <int D>
+int launch_scores_bf16(const SelectParams& p, int num_seqs, cudaStream_t stream) {
+    auto kern = score_blocks_bf16<D>;
+    constexpr int kSmem = ScoreSmem<D>::kBytes;
+    int occ = 0;
+    const int st = kernel_setup(reinterpret_cast<const void*>(kern), kSmem, 128, &occ);
+    if (st != PKV_OK) return st;
+    // kv heads side by side in a CTA: the power of two up to 4 that divides them
+    const int side = p.hkv % 4 == 0 ? 4 : p.hkv % 2 == 0 ? 2 : 1;
+    const int blocks = kStageRows / side, stages = (p.max_blocks + blocks - 1) / blocks;
+    // stages a CTA walks: the GPU's share of one wave, at most 8 (rows are ragged)
+    const long long all = (long long)num_seqs * (p.hkv / side) * stages;
+    const long long slots = (long long)num_sms() * (occ > 0 ? occ : 1);
+    const int per = (int)(all <= slots ? 1 : all >= 8 * slots ? 8 : (all + slots - 1) / slots);
+    note_launch();
+    const cudaError_t e = launch_pdl(kern, dim3((stages + per - 1) / per, p.hkv / side, num_seqs), dim3(128), kSmem,
+                                     stream, p, per, side);
+    return e == cudaSuccess ? PKV_OK : cuda_fail("select_blocks: scoring launch", e);
+}
+
+int launch_scores_f32(const SelectParams& p, int num_seqs, cudaStream_t stream) {
     const int tiles = padded(p.max_blocks) / 16;
-    // 16-block tiles a warp walks: more once the warps fill the GPU (20 resident
-    // per SM) twice over
+    // 16-block tiles a warp walks: more once the warps fill the GPU
     int per = 1;
     const long long rows = (long long)num_seqs * p.hkv, fill = 40LL * num_sms();
     while (per < 16 && rows * tiles / (2 * per) >= fill) per *= 2;
-    // kv heads side by side in a CTA (bf16): the power of two up to 4 that divides them
-    const int side = std::is_same<T, float>::value ? 1 : p.hkv % 4 == 0 ? 4 : p.hkv % 2 == 0 ? 2 : 1;
-    const int span = (4 / side) * per;
-    dim3 grid((tiles + span - 1) / span, p.hkv / side, num_seqs);
+    dim3 grid((tiles + 4 * per - 1) / (4 * per), p.hkv, num_seqs);
     note_launch();
-    cudaError_t e;
-    if constexpr (std::is_same<T, float>::value)
-        e = p.d == 64 ? launch_pdl(score_blocks_f32<64>, grid, dim3(128), 0, stream, p, per, side)
-                      : launch_pdl(score_blocks_f32<128>, grid, dim3(128), 0, stream, p, per, side);
-    else
-        e = p.d == 64 ? launch_pdl(score_blocks_bf16<64>, grid, dim3(128), 0, stream, p, per, side)
-                      : launch_pdl(score_blocks_bf16<128>, grid, dim3(128), 0, stream, p, per, side);
+    const cudaError_t e = p.d == 64 ? launch_pdl(score_blocks_f32<64>, grid, dim3(128), 0, stream, p, per)
+                                    : launch_pdl(score_blocks_f32<128>, grid, dim3(128), 0, stream, p, per);
     return e == cudaSuccess ? PKV_OK : cuda_fail("select_blocks: scoring launch", e);
 }
 
 template <typename T>
+int launch_scores(const SelectParams& p, int num_seqs, cudaStream_t stream) {
+    if constexpr (std::is_same<T, float>::value) return launch_scores_f32(p, num_seqs, stream);
+    else return p.d == 64 ? launch_scores_bf16<64>(p, num_seqs, stream) : launch_scores_bf16<128>(p, num_seqs, stream);
+}
+
+// Rows of at most this many blocks are scored by the CTA that selects from them: a tile
+// of 16 blocks a warp. 4 sequences of 63 blocks: 6.6 us in one launch against 7.5 in
+// two; 1 of 256: 9.3 against 8.1; 64 of 256: 25 against 17.
+constexpr int kFuseBlocks = 128;
+
+template <typename T>
 int select_all(const SelectParams& p, int num_seqs, cudaStream_t stream) {
+    if constexpr (!std::is_same<T, float>::value) {
+        if (p.scored && p.max_blocks <= kFuseBlocks) {
+            SelectParams f = p;
+            f.scored = 0;
+            return p.d == 64 ? launch_select<T, 256, true, 64>(f, num_seqs, stream)
+                             : launch_select<T, 256, true, 128>(f, num_seqs, stream);
+        }
+    }
     if (p.scored) {
         const int st = launch_scores<T>(p, num_seqs, stream);
         if (st != PKV_OK) return st;
     }
-    // a thread keeps 8 scores: the smallest CTA that holds the longest row
+    // a thread keeps 8 scores; CTAs of 256 where rows are short (64 sequences of 512
+    // blocks: 23 us, 28 with 512 threads), of 512 up to 4096 blocks (32 of 2048: 35 us, 37
+    // with 256)
+    if (p.max_blocks <= 1024) return launch_select<T, 256, true>(p, num_seqs, stream);
     if (p.max_blocks <= 4096) return launch_select<T, 512, true>(p, num_seqs, stream);
     if (p.max_blocks <= 8192) return launch_select<T, 1024, true>(p, num_seqs, stream);
     return launch_select<T, 1024, false>(p, num_seqs, stream);
