@@ -457,8 +457,8 @@ PKV_API int paged_attention_decode_noalloc(void* out, const void* q,
  *   q_out, q     device, num_heads*head_dim elements per token, dtype src_dtype;
  *                tokens q_out_stride / q_stride elements apart (at least a row, a
  *                multiple of 16 bytes), so q, k and v may be views of one fused
- *                projection. q_out may be q itself (same stride); any other
- *                overlap is not allowed
+ *                projection. q_out may be q itself (same stride); no other
+ *                two of q_out, q, k, v and the pools may overlap
  *   k, v         device, num_kv_heads*head_dim elements per token, k_stride /
  *                v_stride elements apart
  *   slot_mapping device int64 [num_tokens]; distinct where >= 0

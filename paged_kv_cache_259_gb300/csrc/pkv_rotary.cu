@@ -531,6 +531,7 @@ int rotary_and_cache(void* q_out, const void* q, const void* k, const void* v, v
         (q_out_stride * elt) % 16 || (q_stride * elt) % 16 || (k_stride * elt) % 16 ||
         (v_stride * elt) % 16)
         return PKV_ERR_INVALID_ARG;
+    if (q_out && q_out == q && q_out_stride != q_stride) return PKV_ERR_INVALID_ARG;
     const bool fp8 = cache_dtype == PKV_E4M3;
     if (fp8) {
         if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))

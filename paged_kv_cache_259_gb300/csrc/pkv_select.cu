@@ -1259,8 +1259,12 @@ int select_blocks(int32_t* selected, const void* q, const void* key_bounds,
     p.err = error_word();
     if (!p.err) return PKV_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return q_dtype == PKV_F32 ? select_all<float>(p, num_seqs, s)
-                              : select_all<__nv_bfloat16>(p, num_seqs, s);
+    try {
+        return q_dtype == PKV_F32 ? select_all<float>(p, num_seqs, s)
+                                  : select_all<__nv_bfloat16>(p, num_seqs, s);
+    } catch (...) {                                         // the per-kernel records' host memory
+        return cuda_fail("select_blocks: host memory", cudaErrorMemoryAllocation);
+    }
 }
 
 }  // extern "C"

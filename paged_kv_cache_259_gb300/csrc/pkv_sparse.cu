@@ -94,6 +94,10 @@ extern "C" int paged_attention_decode_sparse(
     a.stream = static_cast<cudaStream_t>(stream);
     a.p.err = error_word();
     if (!a.p.err) return PKV_ERR_CUDA;
-    if (f32) return sparse::dispatch_f32(a);
-    return bf16 ? sparse::dispatch_bf16(a) : sparse::dispatch_e4m3(a);
+    try {
+        if (f32) return sparse::dispatch_f32(a);
+        return bf16 ? sparse::dispatch_bf16(a) : sparse::dispatch_e4m3(a);
+    } catch (...) {                                         // the per-kernel records' host memory
+        return cuda_fail("sparse decode: host memory", cudaErrorMemoryAllocation);
+    }
 }

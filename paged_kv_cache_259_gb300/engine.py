@@ -442,7 +442,10 @@ class PagedKVCache:
 
     def enable_key_bounds(self):
         """Keep the key bounds of every block (``update_key_bounds``), which sparse
-        decode steps choose their blocks by."""
+        decode steps choose their blocks by. ``rotary_prefill_step`` and
+        ``sparse_step`` keep them up; after any other write to the pools (``load``,
+        ``step``, ``prefill_step``, ``apply_copies``, ``swap_in``) call
+        ``refresh_key_bounds`` for the sequences it touched."""
         if getattr(self, "key_bounds", None) is None:
             self.key_bounds = torch.zeros(
                 key_bounds_shape(self.num_blocks, self.num_kv_heads, self.head_dim),
@@ -453,8 +456,7 @@ class PagedKVCache:
         """Bounds of every block of these sequences (device tables and lengths),
         e.g. after ``load`` or ``swap_in``."""
         with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
-            first = torch.zeros_like(lens)
-        first.record_stream(stream or torch.cuda.current_stream(self.device))
+            first = torch.zeros_like(lens)         # of the stream that uses it
         update_key_bounds(self.k_pool, self.enable_key_bounds(), tables, lens, first, stream=stream)
 
     def select_workspace(self, batch, max_blocks):

@@ -26,7 +26,7 @@ SOME = ctypes.c_void_p(0x1000)
 
 def c_rotary(sections=(32,), axes=1, strides=(256, 256, 128, 128), T=T, Hq=HQ, Hkv=HKV, D=D, R=64,
              bs=BS, NB=NB, P=64, src=1, cache=1, ks=1.0, vs=1.0, ptrs=None, sec_ptr=True):
-    a = ptrs or [SOME] * 9
+    a = ptrs or [ctypes.c_void_p(0x2000)] + [SOME] * 8
     sec = (ctypes.c_int32 * len(sections))(*sections) if sec_ptr else None
     return library().rotary_and_cache(*a, sec, axes, *strides, T, Hq, Hkv, D, R, 0, bs, NB, P, src,
                                       cache, ks, vs, None)
@@ -38,6 +38,7 @@ def c_rotary(sections=(32,), axes=1, strides=(256, 256, 128, 128), T=T, Hq=HQ, H
     (dict(strides=(255, 256, 128, 128)), -1),           # shorter than a row
     (dict(strides=(260, 256, 128, 128)), -1),           # rows not on 16 bytes
     (dict(strides=(256, 256, 128, 0)), -1),             # one row for all tokens
+    (dict(strides=(264, 256, 128, 128), ptrs=[SOME] * 9), -1),   # in place, rows elsewhere
     (dict(ks=2.0), -1), (dict(cache=2, ks=0.0), -1), (dict(cache=2, vs=math.inf), -1),
     (dict(ptrs=[None] + [SOME] * 8), -1), (dict(ptrs=[SOME] * 8 + [None]), -1),
     (dict(ptrs=[ctypes.c_void_p(0x1008)] + [SOME] * 8), -1),
