@@ -674,15 +674,16 @@ __device__ __forceinline__ void score_row(const SelectParams& p, int b, int h, i
 }
 
 // One CTA per (kv head, sequence) over the row's scores (FD: which it computes itself,
-// head_dim FD). A thread owns chunks of
-// 8 blocks (KEEP: one chunk, in registers). The score range is cut into 1,024
-// equal bins; the bin of the last place and its neighbours within the rounding
-// window hold the few blocks that are undecided (the range is cut again when they
-// are too many), which are ranked among themselves: by their float32 scores, and
-// those within the window of the last place by their 64-bit scores if there are
-// more of them than places. A bin of a score is a monotone function of it, so
-// bins decide soundly whatever the rounding of their edges.
-// Bound: latency (a row's scores are at most a few hundred KB, from L2).
+// head_dim FD). A thread owns chunks of 8 blocks (KEEP: one chunk, in registers). The
+// score range is cut into 1,024 equal bins; the bin of the last place and its
+// neighbours within the rounding window hold the few blocks that are undecided (the
+// range is cut again when they are too many), which are ranked among themselves: by
+// their float32 scores, and those within the window of the last place by their 64-bit
+// scores if there are more of them than places. A bin of a score is a monotone function
+// of it, so bins decide soundly whatever the rounding of their edges.
+// Bound: latency, about 14,000 clocks of dependent steps for 8,192 blocks (loads 2,200,
+// bins 2,300, their scan 1,500, classing 1,600, the list 5,200, writing 1,400); a row's
+// scores are at most a few hundred KB, from L2.
 template <typename T, int NT, bool KEEP, int FD = 0>
 __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
     constexpr int NW = NT / 32;
@@ -833,10 +834,17 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
         bool all = !sane;                                  // and are all that have a score
         int left = need;                                   // places among the undecided blocks
         if (sane && (qm == 0.f || mm == 0.f)) {
-            // every score is zero: the lowest blocks
-            for_chunks([&](int c, const float (&)[8]) {
-                sel8[c] = (unsigned char)(forced_of(c) | (below(c, lo + need) & ~below(c, lo)));
+            // every score is zero: the lowest blocks, of those with a good id
+            bool bad = false;
+            for_chunks([&](int c, const float (&s)[8]) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) bad |= ((scored_of(c) >> j) & 1) && s[j] == -INFINITY;
             });
+            all = __syncthreads_or(bad);
+            if (!all)
+                for_chunks([&](int c, const float (&)[8]) {
+                    sel8[c] = (unsigned char)(forced_of(c) | (below(c, lo + need) & ~below(c, lo)));
+                });
         } else if (sane) {
             // ---- bins over [rlo, rhi]; scores above it are in, scores below out
             int bin0 = 0, bin1 = 0;                        // undecided bins
@@ -979,7 +987,8 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
                 for (int i = w; i < listed * parts; i += NW) {
                     const int e = i / parts, g0 = (i % parts) * heads;
                     const float s = list_s[e];
-                    if (s <= up && s >= dn && g0 < G) {
+                    // an id that is not good has a score only if the scoring kernel gave up
+                    if (s <= up && s >= dn && g0 < G && (unsigned)list_row[e] < (unsigned)p.num_blocks) {
                         const unsigned long long k = exact_key(bounds, (size_t)list_row[e] * p.hkv + h, d, qf, g0,
                                                                min(G, g0 + heads), lane, scale_q, scale_b);
                         if (lane == 0) atomicMax(&list_key[e], k);

@@ -510,6 +510,10 @@ def test_select_flags_bad_entries_and_lengths():
     got = select_gpu(q, b, t, [40 * 16], 16, 1, 20, 1, 1)
     assert pkv.get_device_error() == -4
     assert got[0, 0].tolist() == [0, 1, 2] + list(range(3, 18)) + [38, 39]
+    t = np.arange(40, dtype=np.int32)[None].copy()
+    t[0, [2, 3, 5]] = 50
+    got = select_gpu(q, torch.zeros_like(b), t, [40 * 16], 16, 1, 8, 1, 1)   # all scores are zero
+    assert pkv.get_device_error() == -4 and got[0, 0].tolist() == [0, 1, 4, 6, 7, 8, 9, 39]
     got = select_gpu(q, b, np.arange(40, dtype=np.int32)[None], [40 * 16 + 1], 16, 1, 40, 0, 0)
     assert pkv.get_device_error() == -4 and got[0, 0].tolist() == list(range(40))
     got = select_gpu(q, b, np.arange(40, dtype=np.int32)[None], [-1], 16, 1, 4, 0, 0)
