@@ -122,8 +122,181 @@ struct Smem {
     static constexpr bool kWide = bytes(2 * kNumWarps, kMinStages) <= kSmemSm;
 };
 
+// A 16 x 8 product on the tensor cores: c += a b
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if constexpr (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Tensor-core math for 2, 4 or 8 query heads a kv head, bf16 and E4M3 caches. Scores as
+// in the decode kernel (query heads are the rows of A, half of them zero): lane 4r + c
+// holds the scores of head r, tokens 2c + e of two groups of 8, which is how the B
+// operand of a product over tokens wants them. So O^T = V^T P: 16 dims are the rows
+// of A (the same words that the decode kernel loads as two B operands), the heads its
+// 8 columns, and a product carries 16 dims instead of 8. Lane 4r + c holds dims r and
+// r + 8 of heads 2c, 2c + 1. FULL: no token of the tile is missing.
+template <typename KV, int D, int BS, int G>
+struct HeadsMath {
+    using Lay = decode::Layout<KV, D, BS>;
+    static constexpr bool F8 = std::is_same<KV, uint8_t>::value;
+    static constexpr int KS = D / 16, MT = D / 16, SUB = BS / 16;
+    static constexpr int kWarpSmemFloats = 0;
+    static_assert(G >= 2 && G <= 8 && BS % 16 == 0 && D % 32 == 0, "mma shape");
+
+    struct State {
+        uint32_t qa[KS][2];                                // A fragments of Q (a0, a2)
+        float o[MT][4];
+        float m, l;                                        // of head r, l this lane's tokens'
+    };
+
+    template <bool FULL>
+    __device__ __forceinline__ static void tile(State& st, const unsigned char* kt, const unsigned char* vt, int ntok,
+                                                int lane, float qscale) {
+        const int c = lane & 3, mi = lane >> 3, rr = lane & 7;
+        const uint32_t kbase = smem_addr(kt), vbase = smem_addr(vt);
+#pragma unroll
+        for (int h = 0; h < SUB; ++h) {
+            if (!FULL && 16 * h >= ntok) break;
+            // even and odd k-steps apart: shorter chains
+            float s[2][2][4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
+            uint32_t k8[4];
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t b[2][2];
+                if constexpr (F8) {
+                    // byte pairs: a row is a token's 16 dims, lane (r, c) gets bytes 4c .. 4c+3
+                    if ((ks & 1) == 0)
+                        decode::ldsm_x4(kbase + Lay::k_off(ks + (mi >> 1), 16 * h + 4 * (rr >> 1) + 2 * (mi & 1) + (rr & 1)),
+                                        k8[0], k8[1], k8[2], k8[3]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t x = k8[(ks & 1) * 2 + u];
+                        b[u][0] = decode::e4m3x2_to_f16x2(x);
+                        b[u][1] = decode::e4m3x2_to_f16x2(x >> 16);
+                    }
+                } else {
+                    decode::ldsm_x4(kbase + Lay::k_off(2 * ks + (mi & 1), 16 * h + 8 * (mi >> 1) + rr), b[0][0], b[0][1],
+                                    b[1][0], b[1][1]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) mma<F8>(s[ks & 1][u], st.qa[ks][0], 0u, st.qa[ks][1], 0u, b[u][0], b[u][1]);
+            }
+            // online softmax over this lane's 4 scores of head r
+            float x[2][2], mx = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int tok = F8 ? 16 * h + 4 * c + 2 * u + e : 16 * h + 8 * u + 2 * c + e;
+                    x[u][e] = FULL || tok < ntok ? (s[0][u][e] + s[1][u][e]) * qscale : -INFINITY;
+                    mx = fmaxf(mx, x[u][e]);
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+            const float m_new = fmaxf(st.m, mx), alpha = exp2f(st.m - m_new);
+            float psum = 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[u][e] = exp2f(x[u][e] - m_new);
+                    psum += x[u][e];
+                }
+            st.l = st.l * alpha + psum;
+            st.m = m_new;
+            if (!__all_sync(kFull, alpha == 1.f)) {        // a running max moved
+                const float a0 = __shfl_sync(kFull, alpha, 8 * c), a1 = __shfl_sync(kFull, alpha, 8 * c + 4);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    st.o[i][0] *= a0;
+                    st.o[i][1] *= a1;
+                    st.o[i][2] *= a0;
+                    st.o[i][3] *= a1;
+                }
+            }
+            const uint32_t p0 = F8 ? decode::pack_f16(x[0][0], x[0][1]) : decode::pack_bf16(x[0][0], x[0][1]);
+            const uint32_t p1 = F8 ? decode::pack_f16(x[1][0], x[1][1]) : decode::pack_bf16(x[1][0], x[1][1]);
+            // unwritten slots beyond ntok are zeroed: they may hold anything
+            const int tail = ntok - 16 * h;
+            uint32_t v8[4];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                uint32_t a[2][2];                          // dims 16 i + 8 x + r, tokens' words y
+                if constexpr (F8) {
+                    // byte pairs: a row is a dim's 16 tokens, lane (r, c) gets tokens 4c .. 4c+3
+                    if ((i & 1) == 0)
+                        decode::ldsm_x4(vbase + Lay::v_off(16 * i + 8 * mi + rr, h), v8[0], v8[1], v8[2], v8[3]);
+#pragma unroll
+                    for (int x2 = 0; x2 < 2; ++x2) {
+                        uint32_t v = v8[(i & 1) * 2 + x2];
+                        if (!FULL) {
+                            const int live = min(max(tail - 4 * c, 0), 4);
+                            v &= live == 4 ? ~0u : (1u << (8 * live)) - 1u;
+                        }
+                        a[x2][0] = decode::e4m3x2_to_f16x2(v);
+                        a[x2][1] = decode::e4m3x2_to_f16x2(v >> 16);
+                    }
+                } else {
+                    decode::ldsm_x4(vbase + Lay::v_off(16 * i + 8 * (mi >> 1) + rr, 2 * h + (mi & 1)), a[0][0], a[0][1],
+                                    a[1][0], a[1][1]);
+                    if (!FULL) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int t0 = 8 * y + 2 * c;
+                            const uint32_t keep = t0 + 1 < tail ? ~0u : t0 < tail ? 0xffffu : 0u;
+                            a[0][y] &= keep;
+                            a[1][y] &= keep;
+                        }
+                    }
+                }
+                mma<F8>(st.o[i], a[0][0], a[1][0], a[0][1], a[1][1], p0, p1);
+            }
+        }
+    }
+
+    // f(head, dim, value) of what this lane holds
+    template <typename F>
+    __device__ __forceinline__ static void each(const State& st, int lane, F f) {
+        const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (2 * c + e < G) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    f(2 * c + e, 16 * i + r, st.o[i][e]);
+                    f(2 * c + e, 16 * i + 8 + r, st.o[i][2 + e]);
+                }
+            }
+    }
+    __device__ __forceinline__ static float sum(const State& st) {
+        float l = st.l;
+        l += __shfl_xor_sync(kFull, l, 1);
+        return l + __shfl_xor_sync(kFull, l, 2);
+    }
+    // this warp's part of a row
+    __device__ __forceinline__ static void finish(State& st, float* pm, float* pl, float* po, int, int lane, bool dead) {
+        const float l = sum(st);
+        const int r = lane >> 2;
+        if (r < G && (lane & 3) == 0) {
+            pm[r] = dead ? -INFINITY : st.m;
+            pl[r] = dead ? 0.f : l;
+        }
+        each(st, lane, [&](int g, int d, float v) { po[g * D + d] = dead ? 0.f : v; });
+    }
+};
+
 // The query rows of one (sequence, kv head) into a warp's state. Tensor-core math:
-// straight into the operand fragments (the layouts of MmaMath::init); CUDA-core
+// straight into the operand fragments; CUDA-core
 // math: through the warp's shared-memory rows, scaled.
 template <class Math, typename QT, int D, int G>
 __device__ __forceinline__ void begin_row(typename Math::State& st, const QT* q, float qscale, float* qs, int lane) {
@@ -154,7 +327,7 @@ __device__ __forceinline__ void begin_row(typename Math::State& st, const QT* q,
             st.qa[s][1] = b;
         }
 #pragma unroll
-        for (int nt = 0; nt < Math::NT; ++nt) st.o[nt][0] = st.o[nt][1] = 0.f;
+        for (int i = 0; i < 4 * Math::MT; ++i) st.o[i >> 2][i & 3] = 0.f;
         st.m = -INFINITY;
         st.l = 0.f;
     }
@@ -174,18 +347,10 @@ __device__ __forceinline__ void write_row(typename Math::State& st, QT* out, flo
             for (int k = 0; k < Math::DPL; ++k) decode::store_out(out + g * D + lane + 32 * k, st.acc[g][k] * inv);
         }
     } else {
-        const int r = lane >> 2, c = lane & 3;
-        float l = st.l;
-        l += __shfl_xor_sync(kFull, l, 1);
-        l += __shfl_xor_sync(kFull, l, 2);
-        const float inv = l > 0.f ? v_scale / l : 0.f;
-        if (r < G) {
-#pragma unroll
-            for (int nt = 0; nt < Math::NT; ++nt) {
-                decode::store_out(out + r * D + 8 * nt + 2 * c, st.o[nt][0] * inv);
-                decode::store_out(out + r * D + 8 * nt + 2 * c + 1, st.o[nt][1] * inv);
-            }
-        }
+        const float l = Math::sum(st), inv = l > 0.f ? v_scale / l : 0.f;
+        const int c = lane & 3;
+        const float inv0 = __shfl_sync(kFull, inv, 8 * c), inv1 = __shfl_sync(kFull, inv, 8 * c + 4);
+        Math::each(st, lane, [&](int g, int d, float v) { decode::store_out(out + g * D + d, v * ((g & 1) ? inv1 : inv0)); });
     }
 }
 
@@ -352,8 +517,10 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
             const unsigned char* kt = ring + (size_t)s * 2 * TILE;
             if constexpr (Math::kWarpSmemFloats > 0)
                 Math::tile(st, kt, kt + TILE, ntok, lane, qs, pb);
+            else if (ntok == BS)
+                Math::template tile<true>(st, kt, kt + TILE, ntok, lane, p.qscale);
             else
-                Math::template tile<false>(st, kt, kt + TILE, ntok, lane, p.qscale, qs, pb, -1);
+                Math::template tile<false>(st, kt, kt + TILE, ntok, lane, p.qscale);
         }
         __syncwarp();
         if (k + ST < nk) {
@@ -667,21 +834,16 @@ struct SimtSums : decode::SimtMath<float, float, D, BS, G> {
     }
 };
 
-template <class Math, typename QT, typename KV, int D, int BS, int G>
-int launch_variant(const Args& a) {
-    if constexpr (Math::kPairStages)
-        return launch<decode::MmaMath<KV, D, 2 * BS, G>, QT, D, 2 * BS, G, 2>(a);
-    else
-        return launch<Math, QT, D, BS, G, 1>(a);
-}
-
 // As the decode: float32 caches on CUDA cores, bf16 / E4M3 caches on CUDA cores
-// for one query head per kv head and on the tensor cores for 2, 4, 8.
+// for one query head per kv head and on the tensor cores for 2, 4, 8 (E4M3 tiles of 16
+// tokens: two a stage).
 template <typename QT, typename KV, int D, int BS, int G>
 int launch_heads(const Args& a) {
     if constexpr (std::is_same<KV, float>::value) return launch<SimtSums<D, BS, G>, QT, D, BS, G, 1>(a);
-    else if constexpr (G == 1) return launch_variant<decode::SimtMath<QT, KV, D, BS, 1>, QT, KV, D, BS, 1>(a);
-    else return launch_variant<decode::MmaMath<KV, D, BS, G>, QT, KV, D, BS, G>(a);
+    else if constexpr (G == 1) return launch<decode::SimtMath<QT, KV, D, BS, 1>, QT, D, BS, 1, 1>(a);
+    else if constexpr (BS == 16 && std::is_same<KV, uint8_t>::value)
+        return launch<HeadsMath<KV, D, 2 * BS, G>, QT, D, 2 * BS, G, 2>(a);
+    else return launch<HeadsMath<KV, D, BS, G>, QT, D, BS, G, 1>(a);
 }
 
 template <typename QT, typename KV, int D, int BS>
