@@ -9,7 +9,8 @@
 // borders of rows, and keeps no state but the current row's. A row that lies within
 // one warp's run is written at once; the parts of the others meet in shared memory
 // and are merged at the end (a warp has at most two: the row its run begins in and
-// the one it ends in). So one launch does it without a workspace, few rows are spread
+// the one it ends in): first a CTA's, then the cluster's, or, where the cluster has one
+// row, by every warp pushing its part to the CTAs that merge it. So one launch does it without a workspace, few rows are spread
 // over many warps, and many rows make one wave of equal shares, whatever their
 // lengths, where a CTA a row left a ragged second wave.
 // Bound: HBM bytes of the selected tiles when there are many rows; a chain of
@@ -37,6 +38,7 @@ struct Params {
     int num_rows;                      // (sequence, kv head), kv heads fastest
     int cluster_rows;                  // rows of a cluster, at most kMaxRows
     int stages;                        // of a warp's ring
+    int push;                          // a cluster's one row is merged by pushes (below)
     float qscale, v_scale;
 };
 
@@ -55,6 +57,12 @@ constexpr int kSmemSm = 227 * 1024;    // shared memory of an SM for CTAs, 1 KB 
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// orders nothing: for partners that only have to stay
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -87,11 +95,41 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
     return v;
 }
 
+// 16 or 8 bytes into the shared memory of the cluster's CTA that `addr` lies in, counted
+// by the mbarrier `bar` of that CTA.
+__device__ __forceinline__ void push4(uint32_t addr, float4 v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void push2(uint32_t addr, float x, float y, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr), "f"(x),
+                 "f"(y), "r"(bar)
+                 : "memory");
+}
+// mbar_wait_bounded for what the cluster's other CTAs push
+__device__ __forceinline__ bool pushed_wait_bounded(uint32_t bar, const int* err) {
+    const unsigned long long t0 = global_ns();
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0, %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(20000u)
+            : "memory");
+        if (done) return true;
+        if (global_ns() - t0 > kWaitLimitNs) return false;
+        if (err && (*reinterpret_cast<const volatile int*>(err) & kErrTimeout)) return false;
+    }
+}
+
 // Shared memory: mbarriers | tokens per stage | row borders and lengths per warp |
 // first parts | (CUDA-core math) the warps' query rows and scratch | rings, for a CTA
 // of `nw` warps with rings of `stages`, both chosen at launch. A warp's last part goes
 // into its own ring, which is drained by then, a CTA's parts into the second halves of
-// warp 0's and 1's.
+// warp 0's and 1's. Behind the rings, where a cluster has one row: what is pushed here,
+// an mbarrier and a slot per warp of the cluster.
 template <class Math, int D, int BS, int G>
 struct Smem {
     static constexpr bool kSimt = Math::kWarpSmemFloats > 0;
@@ -115,11 +153,13 @@ struct Smem {
         const int n = (bytes - ring_off(nw)) / (nw * kStage);
         return n < kMinStages ? kMinStages : n > kMaxStages ? kMaxStages : n;
     }
+    static constexpr int kQuads = G * D / 4;               // 16-byte pieces of a part's o
+    static constexpr int recv_bytes(int nw) { return 16 + nw * (kQuads + 8) * 16; }
     static constexpr int bytes(int nw, int stages) { return ring_off(nw) + nw * stages * kStage; }
     static_assert(kStage % 32 == 0, "halves of a ring are 16-byte aligned");
     static_assert(kMinStages <= kMaxStages && bytes(kNumWarps, kMinStages) <= kSmemSm, "shared memory per CTA");
     // eight warps a CTA where their rings fit (not: float32, 8 heads, 32-token blocks)
-    static constexpr bool kWide = bytes(2 * kNumWarps, kMinStages) <= kSmemSm;
+    static constexpr bool kWide = bytes(2 * kNumWarps, kMinStages) + recv_bytes(2 * kNumWarps) <= kSmemSm;
 };
 
 // A 16 x 8 product on the tensor cores: c += a b
@@ -136,13 +176,23 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 2^x, results below the normal range flushed: such weights vanish in their sum
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Tensor-core math for 2, 4 or 8 query heads a kv head, bf16 and E4M3 caches. Scores as
 // in the decode kernel (query heads are the rows of A, half of them zero): lane 4r + c
 // holds the scores of head r, tokens 2c + e of two groups of 8, which is how the B
 // operand of a product over tokens wants them. So O^T = V^T P: 16 dims are the rows
 // of A (the same words that the decode kernel loads as two B operands), the heads its
 // 8 columns, and a product carries 16 dims instead of 8. Lane 4r + c holds dims r and
-// r + 8 of heads 2c, 2c + 1. FULL: no token of the tile is missing.
+// r + 8 of heads 2c, 2c + 1. One softmax step a tile of 16 or 32 tokens. (64 sequences
+// x 128 E4M3 blocks of 8 kv heads: 55.7 us with the decode kernel's math, 47.5 so; bf16:
+// 87 and 84; one sequence of 512 blocks: 13.9 and 12.2. The issue slots bound E4M3: 47%
+// in use before, on 12 warps an SM.)
 template <typename KV, int D, int BS, int G>
 struct HeadsMath {
     using Lay = decode::Layout<KV, D, BS>;
@@ -157,14 +207,32 @@ struct HeadsMath {
         float m, l;                                        // of head r, l this lane's tokens'
     };
 
-    template <bool FULL>
+    // The values of unwritten slots (ntok and up) may be anything: zero, in place.
+    __device__ __forceinline__ static void clear_tail(unsigned char* vt, int ntok, int lane) {
+        constexpr int X = Lay::kX, E = Lay::kElt;
+#pragma unroll 1
+        for (int t = ntok / X; t < BS / X; ++t) {
+            const int keep = max(0, ntok - t * X) * E * 8;  // bits of the 16 bytes
+#pragma unroll 1
+            for (int d = lane; d < D; d += 32) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(vt + Lay::v_off(d, t));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int bits = keep - 32 * i;
+                    if (bits < 32) w[i] = bits > 0 ? w[i] & ((1u << bits) - 1u) : 0u;
+                }
+            }
+        }
+        __syncwarp();
+    }
+
     __device__ __forceinline__ static void tile(State& st, const unsigned char* kt, const unsigned char* vt, int ntok,
                                                 int lane, float qscale) {
         const int c = lane & 3, mi = lane >> 3, rr = lane & 7;
         const uint32_t kbase = smem_addr(kt), vbase = smem_addr(vt);
+        float x[SUB][2][2], mx = -INFINITY;                // scores of head r
 #pragma unroll
         for (int h = 0; h < SUB; ++h) {
-            if (!FULL && 16 * h >= ntok) break;
             // even and odd k-steps apart: shorter chains
             float s[2][2][4];
 #pragma unroll
@@ -180,9 +248,9 @@ struct HeadsMath {
                                         k8[0], k8[1], k8[2], k8[3]);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const uint32_t x = k8[(ks & 1) * 2 + u];
-                        b[u][0] = decode::e4m3x2_to_f16x2(x);
-                        b[u][1] = decode::e4m3x2_to_f16x2(x >> 16);
+                        const uint32_t w = k8[(ks & 1) * 2 + u];
+                        b[u][0] = decode::e4m3x2_to_f16x2(w);
+                        b[u][1] = decode::e4m3x2_to_f16x2(w >> 16);
                     }
                 } else {
                     decode::ldsm_x4(kbase + Lay::k_off(2 * ks + (mi & 1), 16 * h + 8 * (mi >> 1) + rr), b[0][0], b[0][1],
@@ -191,73 +259,68 @@ struct HeadsMath {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) mma<F8>(s[ks & 1][u], st.qa[ks][0], 0u, st.qa[ks][1], 0u, b[u][0], b[u][1]);
             }
-            // online softmax over this lane's 4 scores of head r
-            float x[2][2], mx = -INFINITY;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int tok = F8 ? 16 * h + 4 * c + 2 * u + e : 16 * h + 8 * u + 2 * c + e;
-                    x[u][e] = FULL || tok < ntok ? (s[0][u][e] + s[1][u][e]) * qscale : -INFINITY;
-                    mx = fmaxf(mx, x[u][e]);
-                }
-            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-            const float m_new = fmaxf(st.m, mx), alpha = exp2f(st.m - m_new);
-            float psum = 0.f;
+                for (int e = 0; e < 2; ++e) x[h][u][e] = (s[0][u][e] + s[1][u][e]) * qscale;
+        }
+        if (ntok < BS) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    x[u][e] = exp2f(x[u][e] - m_new);
-                    psum += x[u][e];
-                }
-            st.l = st.l * alpha + psum;
-            st.m = m_new;
-            if (!__all_sync(kFull, alpha == 1.f)) {        // a running max moved
-                const float a0 = __shfl_sync(kFull, alpha, 8 * c), a1 = __shfl_sync(kFull, alpha, 8 * c + 4);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    st.o[i][0] *= a0;
-                    st.o[i][1] *= a1;
-                    st.o[i][2] *= a0;
-                    st.o[i][3] *= a1;
-                }
+            for (int i = 0; i < SUB * 4; ++i) {
+                const int h = i >> 2, u = (i >> 1) & 1, e = i & 1;
+                const int tok = F8 ? 16 * h + 4 * c + 2 * u + e : 16 * h + 8 * u + 2 * c + e;
+                if (tok >= ntok) x[h][u][e] = -INFINITY;
             }
-            const uint32_t p0 = F8 ? decode::pack_f16(x[0][0], x[0][1]) : decode::pack_bf16(x[0][0], x[0][1]);
-            const uint32_t p1 = F8 ? decode::pack_f16(x[1][0], x[1][1]) : decode::pack_bf16(x[1][0], x[1][1]);
-            // unwritten slots beyond ntok are zeroed: they may hold anything
-            const int tail = ntok - 16 * h;
+        }
+#pragma unroll
+        for (int i = 0; i < SUB * 4; ++i) mx = fmaxf(mx, x[i >> 2][(i >> 1) & 1][i & 1]);
+        // ---- online softmax, once a tile
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+        const float m_new = fmaxf(st.m, mx), alpha = ex2(st.m - m_new);
+        float psum = 0.f;
+#pragma unroll
+        for (int h = 0; h < SUB; ++h)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[h][u][e] = ex2(x[h][u][e] - m_new);
+                    psum += x[h][u][e];
+                }
+        st.l = st.l * alpha + psum;
+        st.m = m_new;
+        if (!__all_sync(kFull, alpha == 1.f)) {            // a running max moved
+            const float a0 = __shfl_sync(kFull, alpha, 8 * c), a1 = __shfl_sync(kFull, alpha, 8 * c + 4);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                st.o[i][0] *= a0;
+                st.o[i][1] *= a1;
+                st.o[i][2] *= a0;
+                st.o[i][3] *= a1;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < SUB; ++h) {
+            const uint32_t p0 = F8 ? decode::pack_f16(x[h][0][0], x[h][0][1]) : decode::pack_bf16(x[h][0][0], x[h][0][1]);
+            const uint32_t p1 = F8 ? decode::pack_f16(x[h][1][0], x[h][1][1]) : decode::pack_bf16(x[h][1][0], x[h][1][1]);
             uint32_t v8[4];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                uint32_t a[2][2];                          // dims 16 i + 8 x + r, tokens' words y
+                uint32_t a[2][2];                          // dims 16 i + 8 y + r, tokens' words z
                 if constexpr (F8) {
                     // byte pairs: a row is a dim's 16 tokens, lane (r, c) gets tokens 4c .. 4c+3
                     if ((i & 1) == 0)
                         decode::ldsm_x4(vbase + Lay::v_off(16 * i + 8 * mi + rr, h), v8[0], v8[1], v8[2], v8[3]);
 #pragma unroll
-                    for (int x2 = 0; x2 < 2; ++x2) {
-                        uint32_t v = v8[(i & 1) * 2 + x2];
-                        if (!FULL) {
-                            const int live = min(max(tail - 4 * c, 0), 4);
-                            v &= live == 4 ? ~0u : (1u << (8 * live)) - 1u;
-                        }
-                        a[x2][0] = decode::e4m3x2_to_f16x2(v);
-                        a[x2][1] = decode::e4m3x2_to_f16x2(v >> 16);
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t v = v8[(i & 1) * 2 + y];
+                        a[y][0] = decode::e4m3x2_to_f16x2(v);
+                        a[y][1] = decode::e4m3x2_to_f16x2(v >> 16);
                     }
                 } else {
                     decode::ldsm_x4(vbase + Lay::v_off(16 * i + 8 * (mi >> 1) + rr, 2 * h + (mi & 1)), a[0][0], a[0][1],
                                     a[1][0], a[1][1]);
-                    if (!FULL) {
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int t0 = 8 * y + 2 * c;
-                            const uint32_t keep = t0 + 1 < tail ? ~0u : t0 < tail ? 0xffffu : 0u;
-                            a[0][y] &= keep;
-                            a[1][y] &= keep;
-                        }
-                    }
                 }
                 mma<F8>(st.o[i], a[0][0], a[1][0], a[0][1], a[1][1], p0, p1);
             }
@@ -411,7 +474,6 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
     fence_mbar_init();
     __syncwarp();
     const uint64_t pol = l2_evict_first();
-
     // the tile of entry e of row r (-1: none) and its tokens; j, before: the entry and
     // the one in front of it
     auto tile_of = [&](int r, int e, int j, int before, int* ntok) -> int {
@@ -481,6 +543,18 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
         }
     };
     for (int kk = 0; kk < nk && kk < ST; ++kk) issue(kk, kk);
+    // ---- one row: every CTA will merge a slice of it, the same quads of every warp's part
+    if (p.push) {
+        if (tid == 0) {
+            const uint32_t recv = smem_addr(rings + NW * warp_ring);
+            mbar_init(recv, 1);
+            fence_mbar_init();                             // releases it to the cluster
+            const int active = share > 0 ? (total + share - 1) / share : 0;
+            if (active > 1) mbar_arrive_expect_tx(recv, active * (S::kQuads / csize * 16 + max(1, G / csize) * 8));
+        }
+        __syncwarp();
+        cluster_arrive_relaxed();                          // the others may push from here on
+    }
 
     typename Math::State st;
     int row = -1, row_end = begin;                          // the current row ends before stage row_end
@@ -514,13 +588,13 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
         }
         const int ntok = stage_tok[s];
         if (ntok > 0) {
-            const unsigned char* kt = ring + (size_t)s * 2 * TILE;
-            if constexpr (Math::kWarpSmemFloats > 0)
+            unsigned char* kt = ring + (size_t)s * 2 * TILE;
+            if constexpr (Math::kWarpSmemFloats > 0) {
                 Math::tile(st, kt, kt + TILE, ntok, lane, qs, pb);
-            else if (ntok == BS)
-                Math::template tile<true>(st, kt, kt + TILE, ntok, lane, p.qscale);
-            else
-                Math::template tile<false>(st, kt, kt + TILE, ntok, lane, p.qscale);
+            } else {
+                if (ntok < BS) Math::clear_tail(kt + TILE, ntok, lane);
+                Math::tile(st, kt, kt + TILE, ntok, lane, p.qscale);
+            }
         }
         __syncwarp();
         if (k + ST < nk) {
@@ -551,14 +625,7 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
     }
     finish_row(aborted);
 
-    // ---- the rows that several warps of this CTA share: to the output, or (a row
-    // that reaches into other CTAs of the cluster) to the CTA's part of it. Rolled
-    // loops: this runs once, and fetching straight-line code costs more than it saves.
-    __syncthreads();
-    const int cta_run = NW * share, cta_begin = min(total, rank * cta_run), cta_stop = min(total, cta_begin + cta_run);
-    float* const cta_part = reinterpret_cast<float*>(rings + warp_ring / 2);
-    const int cta_part1 = warp_ring / 4;                    // floats from the first to the last
-    constexpr int kQuads = G * D / 4;                       // a thread's share: four elements
+    constexpr int kQuads = S::kQuads;                       // a thread's share: four elements
     QT* const out = static_cast<QT*>(p.out) + (size_t)row0 * G * D;
     auto store4 = [&](int r, int i, float4 v, float by) {
         QT* dst = out + (size_t)r * G * D + 4 * i;
@@ -573,6 +640,81 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
         v.z += e * o.z;
         v.w += e * o.w;
     };
+    // ---- one row: every warp pushes each CTA its slice of its part, one trip through
+    // the cluster instead of two barriers around a read (1 sequence, 8 rows of 128 blocks:
+    // 7.1 us with the barriers, 6.4 so; 16 blocks: 5.8 and 5.0)
+    if (p.push) {
+        __syncwarp();
+        cluster_wait();                                    // every CTA's mbarrier is up
+        const int active = share > 0 ? (total + share - 1) / share : 0;   // warps with a run
+        if (active <= 1) {                                 // written by its warp, or nothing listed
+            if (active == 0)
+                for (int i = rank * NW * 32 + tid; i < kQuads; i += csize * NW * 32)
+                    store4(0, i, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+            return;
+        }
+        // all of these are powers of two
+        const int cbits = __ffs(csize) - 1, slice = kQuads >> cbits, sbits = __ffs(slice) - 1;
+        const int heads = max(1, G >> cbits);              // whose m, l a slice needs
+        const int slot_bytes = (slice + (heads + 1) / 2) * 16;
+        const uint32_t recv = smem_addr(rings + NW * warp_ring);
+        if (nk > 0) {
+            const float* part = begin == 0 ? reinterpret_cast<const float*>(ring) : part0 + w * S::kPartFloats;
+            const uint32_t slot = recv + 16 + (rank * NW + w) * slot_bytes;
+            __syncwarp();
+            const int hbits = __ffs(heads) - 1, hy = lane >> hbits, hx = lane & (heads - 1), hg = ((hy * G) >> cbits) + hx;
+            if (hy < csize)
+                push2(cluster_map(slot + slice * 16 + hx * 8, hy), part[hg], part[G + hg], cluster_map(recv, hy));
+#pragma unroll 1
+            for (int i = lane; i < kQuads; i += 32)
+                push4(cluster_map(slot + (i & (slice - 1)) * 16, i >> sbits),
+                      *reinterpret_cast<const float4*>(part + S::kO + 4 * i), cluster_map(recv, i >> sbits));
+        }
+        if (__syncthreads_or(!pushed_wait_bounded(recv, p.err))) {
+            // the partners may still push: leave after they have, and after it has landed
+            if (tid == 0) flag_error(p.err, kErrTimeout);
+            cluster_sync_relaxed();
+            (void)pushed_wait_bounded(recv, nullptr);
+            return;
+        }
+        // J lanes a quad, each over every J-th warp's part
+        const int jbits = max(0, min(5, __ffs(NW) + 4 - sbits)), J = 1 << jbits, quad = tid >> jbits, x0 = tid & (J - 1);
+        const int q = min(quad, slice - 1), i = rank * slice + q, g = 4 * i / D - ((rank * G) >> cbits);
+        const unsigned char* const at = rings + NW * warp_ring + 16;
+        auto ml_of = [&](int x) { return *reinterpret_cast<const float2*>(at + x * slot_bytes + slice * 16 + g * 8); };
+        float M = -INFINITY, sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int x = x0; x < active; x += J) M = fmaxf(M, ml_of(x).x);
+#pragma unroll 1
+        for (int o = 1; o < J; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        if (M == -INFINITY) M = 0.f;                       // nothing but empty parts
+#pragma unroll 4
+        for (int x = x0; x < active; x += J) {
+            const float2 ml = ml_of(x);
+            const float e = ex2(ml.x - M);
+            sum += e * ml.y;
+            add4(v, e, *reinterpret_cast<const float4*>(at + x * slot_bytes + q * 16));
+        }
+#pragma unroll 1
+        for (int o = 1; o < J; o <<= 1) {
+            sum += __shfl_xor_sync(kFull, sum, o);
+            v.x += __shfl_xor_sync(kFull, v.x, o);
+            v.y += __shfl_xor_sync(kFull, v.y, o);
+            v.z += __shfl_xor_sync(kFull, v.z, o);
+            v.w += __shfl_xor_sync(kFull, v.w, o);
+        }
+        if (quad < slice && x0 == 0) store4(0, i, v, sum > 0.f ? p.v_scale / sum : 0.f);
+        return;
+    }
+
+    // ---- the rows that several warps of this CTA share: to the output, or (a row
+    // that reaches into other CTAs of the cluster) to the CTA's part of it. Rolled
+    // loops: this runs once, and fetching straight-line code costs more than it saves.
+    __syncthreads();
+    const int cta_run = NW * share, cta_begin = min(total, rank * cta_run), cta_stop = min(total, cta_begin + cta_run);
+    float* const cta_part = reinterpret_cast<float*>(rings + warp_ring / 2);
+    const int cta_part1 = warp_ring / 4;                    // floats from the first to the last
     if (cta_begin < cta_stop) {
         int r = 0;
         while (border[r + 1] <= cta_begin) ++r;
@@ -666,7 +808,7 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
             }
         }
     }
-    cluster_sync();                                         // partners are done reading
+    cluster_sync_relaxed();                                 // partners are done reading
 }
 
 // Clusters of `size` CTAs that fit on the current device at once (cached).
@@ -680,23 +822,26 @@ int launch(const Args& a) {
     // three CTAs an SM where their rings fit; alone on its SM a CTA gets a deep ring
     constexpr int kStages3 = S::stages(kNumWarps, kSmemSm / 3 - 1024);
     constexpr int kWideWarps = S::kWide ? 2 * kNumWarps : kNumWarps;
-    constexpr int kStages1 = S::stages(kWideWarps, kSmemSm);
-    constexpr int kMost = S::bytes(kWideWarps, kStages1) > S::bytes(kNumWarps, kStages3)
-                              ? S::bytes(kWideWarps, kStages1) : S::bytes(kNumWarps, kStages3);
+    constexpr int kRecv = S::recv_bytes(kWideWarps);
+    constexpr int kStages1 = S::stages(kWideWarps, kSmemSm - kRecv);
+    constexpr int kSmem1 = S::bytes(kWideWarps, kStages1) + kRecv, kSmem3 = S::bytes(kNumWarps, kStages3);
+    constexpr int kMost = kSmem1 > kSmem3 ? kSmem1 : kSmem3;
+    static_assert(kMost <= kSmemSm, "shared memory per CTA");
     int occ = 0;
     int st = kernel_setup(fn, kMost, kNumWarps * 32, &occ);
     if (st != PKV_OK) return st;
     const int stages = ((a.p.k < a.p.max_blocks ? a.p.k : a.p.max_blocks) + PAIR - 1) / PAIR;
     const long long rows = (long long)a.num_seqs * a.p.num_kv_heads;
-    int size = 1, per = 1, warps = kNumWarps, depth = kStages3;
+    int size = 1, per = 1, warps = kNumWarps, depth = kStages3, smem = kSmem3;
     if (2 * rows <= num_sms()) {
         // few rows: each to as many warps as have a stage, one CTA an SM
         warps = kWideWarps;
         depth = kStages1;
+        smem = kSmem1;
         for (int s = kMaxCluster; s > 1; s /= 2) {
             if (s * rows > num_sms() || s * warps > stages) continue;
             int fit = 0;
-            st = resident_clusters(fn, S::bytes(warps, depth), warps * 32, s, &fit);
+            st = resident_clusters(fn, smem, warps * 32, s, &fit);
             if (st != PKV_OK) return st;
             if (fit >= rows) {
                 size = s;
@@ -708,11 +853,11 @@ int launch(const Args& a) {
         // where that leaves the fullest CTA a fifth less (512 rows of 128 E4M3 blocks,
         // on 456 places: 67 us in waves of whole rows, 56 us by fours)
         int fit = 0;
-        st = resident_clusters(fn, S::bytes(warps, depth), warps * 32, 1, &fit);
+        st = resident_clusters(fn, smem, warps * 32, 1, &fit);
         if (st != PKV_OK) return st;
         double best = 0.8 * (double)((rows + fit - 1) / fit);
         for (int s = 2; s <= kMaxCluster; s *= 2) {
-            st = resident_clusters(fn, S::bytes(warps, depth), warps * 32, s, &fit);
+            st = resident_clusters(fn, smem, warps * 32, s, &fit);
             if (st != PKV_OK) return st;
             const long long r = fit > 0 ? (rows + fit - 1) / fit : kMaxRows + 1;
             if (r > kMaxRows || r * stages < 2LL * s * warps) continue;
@@ -729,12 +874,13 @@ int launch(const Args& a) {
     p.num_rows = (int)rows;
     p.cluster_rows = per;
     p.stages = depth;
+    p.push = 2 * rows <= num_sms() && size > 1;
     p.qscale = a.scale * a.k_scale * kLog2e;
     p.v_scale = a.v_scale;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(warps * 32);
-    cfg.dynamicSmemBytes = S::bytes(warps, depth);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -618,6 +618,19 @@ def test_sparse_decode_many_rows_is_one_part_a_row(kind, B, Hq, Hkv):
     check_sparse(c, sparse_gpu(c))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 16), (64, 32), (128, 32)])
+def test_sparse_decode_one_row_shared_by_a_cluster(kind, G, D, bs):
+    """Lists for clusters of 2, 4 and 8 CTAs with a row each; rows of every number of
+    parts: none, one, fewer than warps, as many, several stages each."""
+    for K in (17, 40, 70, 130):
+        lens = [K * bs + 5, (K // 2) * bs - 1, 2 * bs, 1, 0, 9 * bs + 7]
+        c = sparse_case(kind, lens, 2 * G, 2, D, bs, K, seed=44)
+        check_sparse(c, sparse_gpu(c))
+    assert pkv.get_device_error() == 0
+
+
 def test_sparse_decode_sharp_logits():
     """Logits over +-60: one token takes nearly all the weight, late or early."""
     for kind in ("bf16", "e4m3", "f32"):
