@@ -585,6 +585,7 @@ __device__ unsigned long long exact_key_f64(const SelectParams& p, int b, int h,
 
 constexpr int kBins = 1024;
 constexpr int kListMax = 512;         // blocks ranked in shared memory
+constexpr int kMaxRounds = 8;         // to a lower bound of the last place's score
 
 // Scores of a row's blocks by one CTA, into shared memory (`out`, and the tiles'
 // largest |bound|): 16 blocks per warp at a time, read straight into the operand
@@ -714,8 +715,8 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
     float* own_max = own_scores + (p.max_blocks + 15) / 16 * 16;                   // FD: [tiles]
     unsigned char* sel8 = reinterpret_cast<unsigned char*>(sel);
     unsigned char* cand8 = reinterpret_cast<unsigned char*>(cand);
-    __shared__ uint32_t sh_a[NW], sh_b[NW], sh_q[NW], sh_m[NW];
-    __shared__ int sh_bin, sh_cnt, sh_win[2];
+    __shared__ uint32_t sh_a[NW], sh_b[NW], sh_c[NW], sh_q[NW], sh_m[NW];
+    __shared__ int sh_bin, sh_cnt, sh_likely, sh_win[2];
     __shared__ float sh_thr;
 
     const int lo = p.first, hi = n - p.last;               // scored blocks
@@ -751,8 +752,8 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
         // terms. bf16: products exact in float32; four chains of at most four
         // mma.sync, each aligning at most 17 terms to the largest and dropping
         // bits below its 24th (17 x 2^-23 of it) and rounding once, chains adding
-        // up to A: 4 x 18 x 2^-23 A < 2^-16 A with the last adds and A's own
-        // rounding. float32: at most 2 D / 32 + 5 roundings of 2^-24: < 2^-19 A.
+        // up to A: D / 32 x 18 x 2^-23 A, and 3 x 2^-23 A for the last adds, A's own
+        // rounding and the window's. float32: at most 2 D / 32 + 6 roundings of 2^-24.
         const int G = p.hq / p.hkv, d = p.d;
         float qsum = 0.f;
         if (w < G) {
@@ -766,7 +767,8 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
             for (int o = 16; o >= 1; o >>= 1) qsum += __shfl_xor_sync(kFull, qsum, o);
         }
         for (int i = tid; i < kBins; i += NT) hist[i] = 0;
-        if (tid == 0) sh_cnt = 0, sh_win[0] = 0, sh_win[1] = 0;
+        for (int c = tid; c < chunks; c += NT) sel8[c] = (unsigned char)forced_of(c);
+        if (tid == 0) sh_cnt = 0, sh_likely = 0, sh_win[0] = 0, sh_win[1] = 0;
         if (p.scored) wait_prerequisites();
         if constexpr (FD > 0) {
             score_row<FD, NW>(p, b, h, lo, hi, own_scores, own_max);
@@ -803,43 +805,74 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
         };
         uint32_t mx = 0;                                   // |bounds|: their bits' order, NaN on top
         for (int i = lo / 16 + tid; i * 16 < hi; i += NT) mx = max(mx, __float_as_uint(tm[i]));
-        if (KEEP && tid < chunks) load_chunk(tid, kept);
         float smin = INFINITY, smax = -INFINITY;
-        for_chunks([&](int, const float (&s)[8]) {
+        bool single = hi - lo <= NT;                       // a thread has one block to look at, at most
+        float s1 = -INFINITY;
+        int blk1 = lo + tid;
+        if (single) {
+            if (blk1 < hi) s1 = scores[blk1];
+            smax = s1;
+            smin = s1 == -INFINITY ? INFINITY : s1;
+        } else {
+            if (KEEP && tid < chunks) load_chunk(tid, kept);
+            for_chunks([&](int, const float (&s)[8]) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                smin = fminf(smin, s[j] == -INFINITY ? INFINITY : s[j]);
-                smax = fmaxf(smax, s[j]);
-            }
-        });
+                for (int j = 0; j < 8; ++j) {
+                    smin = fminf(smin, s[j] == -INFINITY ? INFINITY : s[j]);
+                    smax = fmaxf(smax, s[j]);
+                }
+            });
+        }
         const uint32_t kmin = __reduce_min_sync(kFull, ordered(smin));
         const uint32_t kmax = __reduce_max_sync(kFull, ordered(smax));
+        // Scores read again in every phase (KEEP false): a score that at least `need` are
+        // not below -- the lowest of the warps' r-th largest thread maxima, r warps' worth
+        // being need or more -- leaves few to look at (1 x 16,384 blocks: 24.6 us without,
+        // 21.9 so; where a thread keeps its scores it gained nothing).
+        uint32_t kth = 0xffffffffu;
+        const int r = KEEP ? 0 : (need + NW - 1) / NW;
+        if (!KEEP && r <= kMaxRounds) {                    // a warp without r scores gives -inf: no bound
+            uint32_t v = ordered(smax);
+#pragma unroll 1
+            for (int i = 0;; ++i) {
+                kth = __reduce_max_sync(kFull, v);
+                if (i == r - 1) break;
+                if (lane == __ffs(__ballot_sync(kFull, v == kth)) - 1) v = 0;
+            }
+        }
         mx = __reduce_max_sync(kFull, mx);
         const uint32_t qx = __reduce_max_sync(kFull, __float_as_uint(qsum));
-        if (lane == 0) sh_a[w] = kmin, sh_b[w] = kmax, sh_q[w] = qx, sh_m[w] = mx;
+        if (lane == 0) sh_a[w] = kmin, sh_b[w] = kmax, sh_c[w] = kth, sh_q[w] = qx, sh_m[w] = mx;
         __syncthreads();
         float rlo = unordered(__reduce_min_sync(kFull, lane < NW ? sh_a[lane] : 0xffffffffu));
         float rhi = unordered(__reduce_max_sync(kFull, lane < NW ? sh_b[lane] : 0u));
+        if (!KEEP) kth = __reduce_min_sync(kFull, lane < NW ? sh_c[lane] : 0xffffffffu);
         const float qm = __uint_as_float(__reduce_max_sync(kFull, lane < NW ? sh_q[lane] : 0u));
         const float mm = __uint_as_float(__reduce_max_sync(kFull, lane < NW ? sh_m[lane] : 0u));
         const float A = qm * mm;
         // 1e-35: products too small for float32
-        const float E = A * (std::is_same<T, float>::value ? 0x1p-19f : 0x1p-16f) + 1e-35f;
+        const float E = A * (std::is_same<T, float>::value ? (float)(2 * (d / 32) + 6) * 0x1p-24f
+                                                           : (float)(d / 32 * 18 + 3) * 0x1p-23f) + 1e-35f;
         const float win = 2.02f * E;                       // 2E, and the rounding of what it is added to
         const bool sane = A < 1e37f;                       // false for NaN too
         const bool finite = qm < INFINITY && mm < INFINITY;
         const float scale_q = unit_scale(qm), scale_b = unit_scale(mm);   // for exact_key
+
+        // what could still be undecided lies within the window of that score
+        const bool bounded = !KEEP && !single && r <= kMaxRounds && kth > ordered(-INFINITY);
+        if (bounded) rlo = fmaxf(rlo, unordered(kth) - win);
 
         bool crowd = false;                                // the undecided blocks are in `cand`
         bool all = !sane;                                  // and are all that have a score
         int left = need;                                   // places among the undecided blocks
         if (sane && (qm == 0.f || mm == 0.f)) {
             // every score is zero: the lowest blocks, of those with a good id
-            bool bad = false;
-            for_chunks([&](int c, const float (&s)[8]) {
+            bool bad = single && blk1 < hi && s1 == -INFINITY;
+            if (!single)
+                for_chunks([&](int c, const float (&s)[8]) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) bad |= ((scored_of(c) >> j) & 1) && s[j] == -INFINITY;
-            });
+                    for (int j = 0; j < 8; ++j) bad |= ((scored_of(c) >> j) & 1) && s[j] == -INFINITY;
+                });
             all = __syncthreads_or(bad);
             if (!all)
                 for_chunks([&](int c, const float (&)[8]) {
@@ -853,18 +886,64 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
                 if (s > rhi) return kBins - 1;
                 return s < rlo ? -1 : min(kBins - 2, (int)((s - rlo) * inv));
             };
-            int bins[8];                                   // KEEP: of the scores this thread holds
+            if (bounded) {
+                // the few scores not below it, one to a thread (their places: the list's)
+                float* some_s = reinterpret_cast<float*>(list_key);
+                int* some_id = reinterpret_cast<int*>(list_s);
+                static_assert(NT <= 2 * kListMax, "room for a score and a block per thread");
+                for (int c0 = 0; c0 < chunks; c0 += NT) {
+                    float s[8];
+                    const int c = c0 + tid;
+                    if (c < chunks) load_chunk(c, s);
+                    uint32_t who[8];
+                    int total = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        who[j] = __ballot_sync(kFull, c < chunks && s[j] >= rlo);
+                        total += __popc(who[j]);
+                    }
+                    if (total == 0) continue;
+                    int at = 0;
+                    if (lane == 0) at = atomicAdd(&sh_likely, total);
+                    at = __shfl_sync(kFull, at, 0);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int to = at + __popc(who[j] & ((1u << lane) - 1u));
+                        if (((who[j] >> lane) & 1) && to < NT) {
+                            some_s[to] = s[j];
+                            some_id[to] = 8 * c + j;
+                        }
+                        at += __popc(who[j]);
+                    }
+                }
+                __syncthreads();
+                const int likely = sh_likely;
+                if (likely <= NT) {
+                    single = true;
+                    s1 = tid < likely ? some_s[tid] : -INFINITY;
+                    blk1 = tid < likely ? some_id[tid] : 0;
+                }
+                // the next sync comes before the list is written
+            }
+            int bins[8], bin_1 = -1;                       // KEEP: of the scores this thread holds
+            // read ahead of its use in the list
+            const int row1 = single && s1 != -INFINITY ? p.tables[(size_t)b * p.max_blocks + blk1] : -1;
             for (int round = 0;; ++round) {
                 const float width = (rhi - rlo) * (1.f / (kBins - 2));
                 inv = width > 1e-30f && width < 1e30f ? 1.f / width : 0.f;
-                for_chunks([&](int, const float (&s)[8]) {
+                if (single) {
+                    bin_1 = s1 == -INFINITY ? -1 : bin_of(s1);
+                    if (bin_1 >= 0) atomicAdd(&hist[bin_1], 1u);
+                } else {
+                    for_chunks([&](int, const float (&s)[8]) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int bin = bin_of(s[j]);
-                        if (KEEP) bins[j] = bin;
-                        if (bin >= 0) atomicAdd(&hist[bin], 1u);
-                    }
-                });
+                        for (int j = 0; j < 8; ++j) {
+                            const int bin = bin_of(s[j]);
+                            if (KEEP) bins[j] = bin;
+                            if (bin >= 0) atomicAdd(&hist[bin], 1u);
+                        }
+                    });
+                }
                 __syncthreads();
                 // the bin of the last place: thread t sums bins from the top down
                 constexpr int BPT = kBins / NT;
@@ -911,7 +990,25 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
                 for (int i = tid; i < kBins; i += NT) hist[i] = 0;
                 __syncthreads();
             }
-            if (!all) {
+            if (!all && single) {
+                if (crowd) {
+                    for (int c = tid; c < chunks; c += NT) cand8[c] = 0;
+                    __syncthreads();
+                }
+                if (bin_1 > bin1) {
+                    atomicOr(&sel[blk1 >> 5], 1u << (blk1 & 31));
+                } else if (bin_1 >= bin0) {                // bin0 >= 0
+                    if (crowd) {
+                        atomicOr(&cand[blk1 >> 5], 1u << (blk1 & 31));
+                    } else {
+                        const int at = atomicAdd(&sh_cnt, 1);
+                        list_s[at] = s1;
+                        list_key[at] = 0;
+                        list_row[at] = row1;               // a good id
+                        list_id[at] = blk1;
+                    }
+                }
+            } else if (!all) {
                 for_chunks([&](int c, const float (&s)[8]) {
                     uint32_t in = forced_of(c), un = 0;
 #pragma unroll
@@ -952,8 +1049,11 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
             float up = INFINITY, dn = -INFINITY;           // undecided: dn <= score <= up
             int certain = 0;
             bool crowded = listed > left;
-            if (listed > 4 && crowded) {
-                // only those within the window of T, the left-th largest, are scored again
+            // Only those within the window of T, the left-th largest, are scored again; bf16:
+            // all of them where that is a block a warp, the ranking costing as much (1 x
+            // 8,192 blocks: 15.2 us, 15.6 with the ranking; float32, whose window seldom
+            // holds two, 1 x 4,096 blocks: 27.4 and 25.9)
+            if (listed > (std::is_same<T, float>::value ? 4 : NW) && crowded) {
                 for (int i = w; i < listed; i += NW) {
                     const float s = list_s[i];
                     const int id = list_id[i];
@@ -981,11 +1081,11 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
             }
             if (crowded) {
                 // a warp takes a block and as few heads as there are warps for
-                int parts = 1;
-                while (2 * parts <= G && 2 * parts * listed <= NW) parts *= 2;
-                const int heads = (G + parts - 1) / parts;
-                for (int i = w; i < listed * parts; i += NW) {
-                    const int e = i / parts, g0 = (i % parts) * heads;
+                int bits = 0;
+                while ((2 << bits) <= G && (2 << bits) * listed <= NW) ++bits;
+                const int heads = (G + (1 << bits) - 1) >> bits;
+                for (int i = w; i < listed << bits; i += NW) {
+                    const int e = i >> bits, g0 = (i & ((1 << bits) - 1)) * heads;
                     const float s = list_s[e];
                     // an id that is not good has a score only if the scoring kernel gave up
                     if (s <= up && s >= dn && g0 < G && (unsigned)list_row[e] < (unsigned)p.num_blocks) {

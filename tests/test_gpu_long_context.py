@@ -415,6 +415,26 @@ def test_select_long_row_scores_from_global_memory():
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("K", [3, 100, 258, 259])
+def test_select_long_rows_from_few_likely_blocks(dt, K):
+    """Rows of more blocks than a CTA's threads keep, looked at through a lower bound of
+    the last place's score: rows of every length beside each other, scores in any order,
+    rising (the likely blocks all at the end) and mostly tied (too many likely ones)."""
+    rng = rng_of(34, K)
+    lens, NB, D = [16 * 20001, 16 * 8192 + 1, 16 * 3000, 16 * 700 - 3, 16 * 258, 5], 20100, 64
+    q = normal(rng, (len(lens), 4, D), dt)
+    b = key_like_bounds(rng, NB, 2, D, dt)
+    tables = np.stack([rng.permutation(NB)[:20001] for _ in lens]).astype(np.int32)
+    check_select(q, b, tables, lens, 16, 2, K, 1, 1)
+    c = torch.full_like(b, 0.5)
+    c *= (1 + torch.arange(NB) / NB).to(dt)[:, None, None, None]
+    check_select(q.abs(), c, np.arange(20001, dtype=np.int32)[None].repeat(len(lens), 0), lens, 16, 2, K, 1, 1)
+    tied = torch.full_like(b, 0.25)
+    tied[7000:7010] = 1
+    check_select(q.abs(), tied, tables, lens, 16, 2, K, 0, 0)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("n", [300, 3000])
 def test_select_equal_scores_take_the_lower_index(dt, n):
     """Every block's bounds are one set of numbers in another order and q is
