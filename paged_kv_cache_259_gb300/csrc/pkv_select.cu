@@ -1239,10 +1239,14 @@ int launch_scores_bf16(const SelectParams& p, int num_seqs, cudaStream_t stream)
     // kv heads side by side in a CTA: the power of two up to 4 that divides them
     const int side = p.hkv % 4 == 0 ? 4 : p.hkv % 2 == 0 ? 2 : 1;
     const int blocks = kStageRows / side, stages = (p.max_blocks + blocks - 1) / blocks;
-    // stages a CTA walks: the GPU's share of one wave, at most 8 (rows are ragged)
+    // stages a CTA walks: the GPU's share of one wave, at most 6 (rows are ragged; 32
+    // sequences of up to 2048 blocks: 35.4 us with 8, which left a ragged second wave, 32.2
+    // with 6, 32.6 with 4; 1 of 32768: 42, 38, 39; 40 kv heads: 134, 134, 138. Sharing the
+    // stages there are evenly among the CTAs of one wave: 33.0, 44, 140, as each has to
+    // read the lengths before it knows its first block)
     const long long all = (long long)num_seqs * (p.hkv / side) * stages;
     const long long slots = (long long)num_sms() * (occ > 0 ? occ : 1);
-    const int per = (int)(all <= slots ? 1 : all >= 8 * slots ? 8 : (all + slots - 1) / slots);
+    const int per = (int)(all <= slots ? 1 : all >= 6 * slots ? 6 : (all + slots - 1) / slots);
     note_launch();
     const cudaError_t e = launch_pdl(kern, dim3((stages + per - 1) / per, p.hkv / side, num_seqs), dim3(128), kSmem,
                                      stream, p, per, side);
@@ -1288,9 +1292,10 @@ int select_all(const SelectParams& p, int num_seqs, cudaStream_t stream) {
         if (st != PKV_OK) return st;
     }
     // a thread keeps 8 scores; CTAs of 256 where rows are short (64 sequences of 512
-    // blocks: 23 us, 28 with 512 threads), of 512 up to 4096 blocks (32 of 2048: 35 us, 37
-    // with 256)
-    if (p.max_blocks <= 1024) return launch_select<T, 256, true>(p, num_seqs, stream);
+    // blocks: 23 us, 28 with 512 threads) or too many for one wave of 512 (512 rows of 2048:
+    // 55 us, 60 with 512; 256 rows: 33 and 32), of 512 up to 4096 blocks
+    const bool many = (long long)num_seqs * p.hkv > 2 * num_sms();
+    if (p.max_blocks <= (many ? 2048 : 1024)) return launch_select<T, 256, true>(p, num_seqs, stream);
     if (p.max_blocks <= 4096) return launch_select<T, 512, true>(p, num_seqs, stream);
     if (p.max_blocks <= 8192) return launch_select<T, 1024, true>(p, num_seqs, stream);
     return launch_select<T, 1024, false>(p, num_seqs, stream);

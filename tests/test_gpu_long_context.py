@@ -434,6 +434,22 @@ def test_select_long_rows_from_few_likely_blocks(dt, K):
     check_select(q.abs(), tied, tables, lens, 16, 2, K, 0, 0)
 
 
+@pytest.mark.parametrize("B,blocks,Hkv,D", [(2, 15000, 1, 64), (3, 9000, 2, 128), (40, 1500, 1, 128), (40, 700, 4, 64),
+                                            (129, 400, 3, 64), (300, 300, 4, 128), (1024, 140, 2, 64),
+                                            (1025, 140, 2, 64)])
+def test_select_ragged_batches(B, blocks, Hkv, D):
+    """Rows of every length beside each other: empty, listed whole, full; several stages a
+    CTA, more rows than fit at once."""
+    rng = rng_of(35, B)
+    NB, K = 500, 12
+    lens = rng.integers(0, blocks * 16 + 1, B)
+    lens[rng.integers(0, B, B // 4)] = rng.integers(0, K * 16 + 20, B // 4)
+    lens[0], lens[B - 1] = blocks * 16, rng.integers(0, 2) * blocks * 16
+    q = normal(rng, (B, 2 * Hkv, D), BF)
+    tables = rng.integers(0, NB, (B, blocks)).astype(np.int32)
+    check_select(q, key_like_bounds(rng, NB, Hkv, D, BF), tables, lens.tolist(), 16, Hkv, K, 1, 2)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("n", [300, 3000])
 def test_select_equal_scores_take_the_lower_index(dt, n):
