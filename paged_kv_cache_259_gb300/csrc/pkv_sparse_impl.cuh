@@ -1,18 +1,17 @@
 // Decode attention over selected blocks: paged_attention_decode_sparse.
 //
-// The mathematics is the decode kernel's (online softmax over a sequence's
-// cached tokens, tile by tile) over the tokens of the blocks that a list names
-// for each row (sequence, kv head), and the tile math is that kernel's (SimtMath,
-// MmaMath). What differs is the walk and the merge. A thread-block cluster takes
-// some rows, lays their listed blocks end to end and gives every warp of its CTAs an
-// equal run of them: a warp streams its run through a ring of its own, across the
-// borders of rows, and keeps no state but the current row's. A row that lies within
-// one warp's run is written at once; the parts of the others meet in shared memory
-// and are merged at the end (a warp has at most two: the row its run begins in and
-// the one it ends in): first a CTA's, then the cluster's, or, where the cluster has one
-// row, by every warp pushing its part to the CTAs that merge it. So one launch does it without a workspace, few rows are spread
-// over many warps, and many rows make one wave of equal shares, whatever their
-// lengths, where a CTA a row left a ragged second wave.
+// The mathematics is the decode kernel's (online softmax over a sequence's cached
+// tokens, tile by tile) over the tokens of the blocks that a list names for each row
+// (sequence, kv head). What differs is the walk and the merge. A thread-block cluster
+// takes some rows, lays their listed blocks end to end and gives every warp of its CTAs
+// an equal run of them: a warp streams its run through a ring of its own, across the
+// borders of rows, and keeps no state but the current row's. A row that lies within one
+// warp's run is written at once; the parts of the others meet in shared memory and are
+// merged at the end (a warp has at most two: the row its run begins in and the one it
+// ends in): first a CTA's, then the cluster's, or, where the cluster has one row, by
+// every warp pushing its part to the CTAs that merge it. So one launch does it without
+// a workspace, few rows are spread over many warps, and many rows make one wave of equal
+// shares, whatever their lengths, where a CTA a row left a ragged second wave.
 // Bound: HBM bytes of the selected tiles when there are many rows; a chain of
 // loads (length, list, table, tile, partner's partials) when there are few.
 #pragma once
@@ -183,7 +182,7 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Tensor-core math for 2, 4 or 8 query heads a kv head, bf16 and E4M3 caches. Scores as
+// Tensor-core math for up to 8 query heads a kv head, bf16 and E4M3 caches. Scores as
 // in the decode kernel (query heads are the rows of A, half of them zero): lane 4r + c
 // holds the scores of head r, tokens 2c + e of two groups of 8, which is how the B
 // operand of a product over tokens wants them. So O^T = V^T P: 16 dims are the rows
@@ -199,7 +198,7 @@ struct HeadsMath {
     static constexpr bool F8 = std::is_same<KV, uint8_t>::value;
     static constexpr int KS = D / 16, MT = D / 16, SUB = BS / 16;
     static constexpr int kWarpSmemFloats = 0;
-    static_assert(G >= 2 && G <= 8 && BS % 16 == 0 && D % 32 == 0, "mma shape");
+    static_assert(G >= 1 && G <= 8 && BS % 16 == 0 && D % 32 == 0, "mma shape");
 
     struct State {
         uint32_t qa[KS][2];                                // A fragments of Q (a0, a2)
@@ -980,13 +979,16 @@ struct SimtSums : decode::SimtMath<float, float, D, BS, G> {
     }
 };
 
-// As the decode: float32 caches on CUDA cores, bf16 / E4M3 caches on CUDA cores
-// for one query head per kv head and on the tensor cores for 2, 4, 8 (E4M3 tiles of 16
-// tokens: two a stage).
+// float32 caches on CUDA cores, as in the decode; bf16 caches on the tensor cores for 2, 4,
+// 8 query heads a kv head, on CUDA cores for one, whose weights then stay float32 (1280
+// rows of 64 blocks: 94.5 us, 0.96 of the copy rate; 91.8 on the tensor cores, which would
+// round them to bf16); E4M3 caches on the tensor cores, for one head too (512 rows of 128
+// blocks: 56.0 us on CUDA cores, 47.0 so), the weights rounded to f16, 2^-11 of themselves
+// against the output's 2^-8; their tiles of 16 tokens two a stage.
 template <typename QT, typename KV, int D, int BS, int G>
 int launch_heads(const Args& a) {
     if constexpr (std::is_same<KV, float>::value) return launch<SimtSums<D, BS, G>, QT, D, BS, G, 1>(a);
-    else if constexpr (G == 1) return launch<decode::SimtMath<QT, KV, D, BS, 1>, QT, D, BS, 1, 1>(a);
+    else if constexpr (G == 1 && !std::is_same<KV, uint8_t>::value) return launch<decode::SimtMath<QT, KV, D, BS, 1>, QT, D, BS, 1, 1>(a);
     else if constexpr (BS == 16 && std::is_same<KV, uint8_t>::value)
         return launch<HeadsMath<KV, D, 2 * BS, G>, QT, D, 2 * BS, G, 2>(a);
     else return launch<HeadsMath<KV, D, BS, G>, QT, D, BS, G, 1>(a);

@@ -572,12 +572,12 @@ def sparse_tolerance(kind, G, ref, mag, logit, tokens, vmax, out_half):
     """What the roundings allow. Logits: sums of D products, every operation off by
     at most 2^-23 of the magnitudes (the tensor core truncates), (D + 8) of them,
     and that much relative error in every weight, twice (weight and sum). Weights:
-    bf16 caches with query groups round them to bf16 (2^-8), E4M3 to f16 (2^-11, and
-    2^-25 where they are subnormal). Sums over the tokens and the merges: 2^-24 an
+    bf16 caches with query groups round them to bf16 (2^-8), E4M3 caches always to f16
+    (2^-11, and 2^-25 where they are subnormal). Sums over the tokens and the merges: 2^-24 an
     operation, (tokens + 64). Last, half a step of the result."""
     D = ref.shape[-1]
     w = 0.0
-    if G > 1:
+    if G > 1 or kind == "e4m3":
         w = {"f32": 0.0, "bf16": 2.0 ** -8, "e4m3": 2.0 ** -11}[kind]
     rel = w + 2 * (D + 8) * 2.0 ** -23 * logit[..., None] + (tokens + 64) * 2.0 ** -23
     sub = tokens * 2.0 ** -25 * vmax if kind == "e4m3" else 0.0
