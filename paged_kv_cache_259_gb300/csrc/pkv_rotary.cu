@@ -13,7 +13,9 @@
 // angle of a far position needs 64 bits (1e6 rad has an ulp of 0.06 in float32),
 // which the table is built in once and the step then never pays for.
 //
-// Bound: HBM bytes for many tokens, launch and load latency for few.
+// Bound: HBM bytes for many tokens (8192 tokens of 32 + 2 x 8 bf16 heads of 128, three
+// axes: 34.7 us, 0.85 of the copy rate), a launch and a chain of loads for few (64 tokens
+// 2.9 us; 1071 tokens into an E4M3 cache 8.4).
 //
 // Work split. A warp takes a few tokens and walks over some of the heads with one
 // set of cosines and sines in registers, a batch of heads at a time, the first batch

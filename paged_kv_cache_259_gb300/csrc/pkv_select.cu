@@ -115,8 +115,10 @@ __device__ __forceinline__ void widen(const uint4& raw, uint32_t (&x)[Cmp<KV>::k
 // compared in registers, then the 8 token lanes reduce by halves: each step
 // exchanges half of the registers, so 7 shuffles (14 for E4M3) leave every lane
 // its share of the result, in the order the bounds are stored.
-// Bound: HBM bytes of the changed blocks' K; a decode step (one block per
-// sequence) is launch latency.
+// Bound: HBM bytes of the changed blocks' K (8 sequences of 16384 new tokens, 8 bf16
+// heads of 128: 54 us, 0.82 of the copy rate; 2048 new tokens: 9.6, float32 15.7); a
+// decode step is a chain of loads (length, table, tile): 64 sequences of 40 heads 3.3 us,
+// one sequence 1.9.
 template <typename KV>
 __global__ void __launch_bounds__(128, 5) update_key_bounds_kernel(
     const uint4* __restrict__ k_pool, void* __restrict__ bounds, const int32_t* __restrict__ tables,
@@ -135,20 +137,29 @@ __global__ void __launch_bounds__(128, 5) update_key_bounds_kernel(
     }
     if (f >= L) return;
     const int j0 = f / bs, nblk = (L + bs - 1) / bs;
-    const long long items = (long long)(nblk - j0) * hkv;
+    const int changed = nblk - j0;
     const int planes = d * C::kElt / 16;                   // 16-byte chunks per token
     const int tl = lane & 7, pl = lane >> 3;               // token and chunk of the load
-    for (long long it = blockIdx.x * 4LL + (threadIdx.x >> 5); it < items; it += gridDim.x * 4LL) {
-        const int j = j0 + (int)(it / hkv), h = (int)(it % hkv);
-        const int id = tables[(size_t)b * max_blocks + j];
+    // item (changed block i, kv head h), heads fastest; the next one's id is read ahead
+    const unsigned heads = (unsigned)hkv, start = blockIdx.x * 4u + (threadIdx.x >> 5), step = gridDim.x * 4u;
+    const int step_i = (int)(step / heads), step_h = (int)(step % heads);
+    int i = (int)(start / heads), h = (int)(start % heads);
+    auto id_at = [&](int x) { return x < changed ? tables[(size_t)b * max_blocks + j0 + x] : -1; };
+    int id_next = id_at(i);
+    while (i < changed) {
+        const int id = id_next, j = j0 + i, hc = h;
+        i += step_i;
+        h += step_h;
+        if (h >= hkv) h -= hkv, ++i;
+        id_next = id_at(i);
         if (id < 0 || id >= num_blocks) {
-            if (lane == 0 && h == 0) flag_error(err, kErrOutOfRange);
+            if (lane == 0 && hc == 0) flag_error(err, kErrOutOfRange);
             continue;
         }
         const int ntok = min(bs, L - j * bs);
-        const uint4* tile = k_pool + ((size_t)id * hkv + h) * planes * bs;
+        const uint4* tile = k_pool + ((size_t)id * hkv + hc) * planes * bs;
         char* out = static_cast<char*>(bounds) +
-                    ((size_t)id * hkv + h) * 2 * d * (C::kElt == 4 ? 4 : 2);
+                    ((size_t)id * hkv + hc) * 2 * d * (C::kElt == 4 ? 4 : 2);
         for (int q0 = 0; q0 < planes; q0 += 4 * QB) {
             uint32_t x[QB][2 * R];                         // min | max
 #pragma unroll
@@ -268,7 +279,8 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t x) {
 // stages deep (66 KB of copies in flight per CTA, three CTAs an SM); rows lie 16 bytes
 // apart from a multiple of 128 so that the operand reads (ldmatrix) meet no bank
 // twice. Four accumulator chains shorten the dependency and the rounding.
-// Bound: HBM bytes of the bounds.
+// Bound: HBM bytes of the bounds (32 ragged sequences of up to 2048 blocks, 8 heads: 139 MB
+// in about 25 us, 0.82 of the copy rate); a short stream, its ramp (33 MB in 7.5).
 constexpr int kScoreStages = 2;
 constexpr int kStageRows = 64;         // rows of 16-bit [2][D], of all warps
 
@@ -707,9 +719,10 @@ __device__ __forceinline__ void score_row(const SelectParams& p, int b, int h, i
 // their float32 scores, and those within the window of the last place by their 64-bit
 // scores if there are more of them than places. A bin of a score is a monotone function
 // of it, so bins decide soundly whatever the rounding of their edges.
-// Bound: latency, about 14,000 clocks of dependent steps for 8,192 blocks (loads 2,200,
-// bins 2,300, their scan 1,500, classing 1,600, the list 5,200, writing 1,400); a row's
-// scores are at most a few hundred KB, from L2.
+// Rows of no more blocks than threads have one to a thread.
+// Bound: latency and, with 32 warps, issue: about 13,000 clocks of dependent steps for
+// 8,192 blocks, of which loads 2,000, bins and their scan 3,500, scores in 64 bits 3,000,
+// writing 1,000; a row's scores are at most a few hundred KB, from L2.
 template <typename T, int NT, bool KEEP, int FD = 0>
 __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
     constexpr int NW = NT / 32;
@@ -1329,7 +1342,9 @@ int update_key_bounds(const void* k_pool, void* key_bounds, const int32_t* block
                                           : max_blocks_per_seq;
     if (blocks > max_blocks_per_seq) blocks = max_blocks_per_seq;
     long long gx = (blocks * num_kv_heads + 3) / 4;
-    const long long cap = 64LL * num_sms() / num_seqs + 1;  // 4 waves of 16 CTAs per SM
+    // six waves of 5 CTAs an SM (8 sequences of 1024 changed bf16 blocks: 54 us, 58 with
+    // twice as many CTAs, 60 with a third)
+    const long long cap = 30LL * num_sms() / num_seqs + 1;
     if (gx > cap) gx = cap;
     auto kern = kv_dtype == PKV_F32    ? update_key_bounds_kernel<float>
                 : kv_dtype == PKV_BF16 ? update_key_bounds_kernel<__nv_bfloat16>

@@ -12,8 +12,11 @@
 // every warp pushing its part to the CTAs that merge it. So one launch does it without
 // a workspace, few rows are spread over many warps, and many rows make one wave of equal
 // shares, whatever their lengths, where a CTA a row left a ragged second wave.
-// Bound: HBM bytes of the selected tiles when there are many rows; a chain of
-// loads (length, list, table, tile, partner's partials) when there are few.
+// Bound: HBM bytes of the selected tiles when there are many rows (1280 rows of 64 bf16
+// blocks 94.8 us, 0.96 of the copy rate; 512 rows of 128 E4M3 blocks, 4 heads, 47.7, 0.80:
+// the stream itself is at the copy rate, 5 us lie before it and 7 in the merges); a chain of
+// loads (length, list, table, tile, partner's partials) when there are few (8 rows of 128
+// blocks 6.3 us).
 #pragma once
 
 #include "pkv_decode_impl.cuh"
