@@ -562,7 +562,8 @@ PKV_API size_t select_blocks_workspace_size(int num_seqs, int num_kv_heads, int 
  *                 sequence, not above the entry before it, or directly behind
  *                 padding sets PKV_ERR_OUT_OF_RANGE and is skipped; entries past
  *                 the sequence's number of blocks are not read
- *   the rest      as paged_attention_decode (same supported sizes and types)
+ *   the rest      as paged_attention_decode (same supported sizes and types);
+ *                 E4M3 caches take the queries in fp16 (magnitudes to 65504)
  * One launch, no workspace: the CTAs that share a (sequence, kv head) are a
  * thread-block cluster and merge their partial results in shared memory.
  * ---------------------------------------------------------------------- */
