@@ -933,7 +933,7 @@ class PackedCall(BoundCall):
     def __call__(self, stream=None):
         idx = self._idx
         sptr = _raw_stream(idx) if stream is None else stream.cuda_stream
-        if torch.cuda.current_device() != idx:
+        if _current_device() != idx:
             with _on_device(torch.device("cuda", idx)):
                 st = self._fn(self._call, self._addr, self._n, sptr)
         else:
@@ -949,6 +949,8 @@ def _raw_stream(idx):
 
 # the same without building a Stream object, where torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+# and the current device without a look at whether CUDA is up: it is, a call is bound
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _c_args(values):

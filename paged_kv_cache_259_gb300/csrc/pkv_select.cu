@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
         uint32_t mx = 0;                                   // |bounds|: their bits' order, NaN on top
         for (int i = lo / 16 + tid; i * 16 < hi; i += NT) mx = max(mx, __float_as_uint(tm[i]));
         float smin = INFINITY, smax = -INFINITY;
-        bool single = hi - lo <= NT;                       // a thread has one block to look at, at most
+        bool single = FD > 0 || hi - lo <= NT;             // a thread has one block to look at, at most
         float s1 = -INFINITY;
         int blk1 = lo + tid;
         if (single) {
@@ -1288,7 +1288,7 @@ int launch_scores(const SelectParams& p, int num_seqs, cudaStream_t stream) {
 // Rows of at most this many blocks are scored by the CTA that selects from them: a tile
 // of 16 blocks a warp. 4 sequences of 63 blocks: 6.6 us in one launch against 7.5 in
 // two; 1 of 256: 9.3 against 8.1; 64 of 256: 25 against 17.
-constexpr int kFuseBlocks = 128;
+constexpr int kFuseBlocks = 128;      // at most a block a thread (256)
 
 template <typename T>
 int select_all(const SelectParams& p, int num_seqs, cudaStream_t stream) {
