@@ -440,24 +440,31 @@ class PagedKVCache:
             call(stream, **counts)
         return run
 
-    def enable_key_bounds(self):
+    def _on_stream(self, stream):
+        """Make ``stream`` (None: the device's current one) torch's current stream."""
+        return torch.cuda.stream(stream or torch.cuda.current_stream(self.device))
+
+    def enable_key_bounds(self, stream=None):
         """Keep the key bounds of every block (``update_key_bounds``), which sparse
         decode steps choose their blocks by. ``rotary_prefill_step`` and
         ``sparse_step`` keep them up; after any other write to the pools (``load``,
         ``step``, ``prefill_step``, ``apply_copies``, ``swap_in``) call
-        ``refresh_key_bounds`` for the sequences it touched."""
+        ``refresh_key_bounds`` for the sequences it touched. The first call fills them
+        with zeros on ``stream``."""
         if getattr(self, "key_bounds", None) is None:
-            self.key_bounds = torch.zeros(
-                key_bounds_shape(self.num_blocks, self.num_kv_heads, self.head_dim),
-                dtype=key_bounds_dtype(self.k_pool.dtype), device=self.device)
+            with self._on_stream(stream):
+                self.key_bounds = torch.zeros(
+                    key_bounds_shape(self.num_blocks, self.num_kv_heads, self.head_dim),
+                    dtype=key_bounds_dtype(self.k_pool.dtype), device=self.device)
         return self.key_bounds
 
     def refresh_key_bounds(self, tables, lens, stream=None):
         """Bounds of every block of these sequences (device tables and lengths),
         e.g. after ``load`` or ``swap_in``."""
-        with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
+        bounds = self.enable_key_bounds(stream)
+        with self._on_stream(stream):
             first = torch.zeros_like(lens)         # of the stream that uses it
-        update_key_bounds(self.k_pool, self.enable_key_bounds(), tables, lens, first, stream=stream)
+        update_key_bounds(self.k_pool, bounds, tables, lens, first, stream=stream)
 
     def select_workspace(self, batch, max_blocks):
         """Scratch of a sparse step's block choice."""
@@ -493,7 +500,7 @@ class PagedKVCache:
         blocks of each sequence: CoW copies, rotation (q in place) and append, key
         bounds, block choice into ``selected`` (int32 ``[B, Hkv, K]``), attention
         over the chosen blocks. ``workspace``: ``select_workspace``."""
-        self.enable_key_bounds()
+        self.enable_key_bounds(stream)
         self._rotated_append(q, k_new, v_new, dev_plan, positions, first, rotary, 1, k_scale, v_scale,
                              stream)
         select_blocks(selected, q, self.key_bounds, dev_plan["tables"], dev_plan["lens"],
