@@ -449,14 +449,34 @@ class PagedKVCache:
         decode steps choose their blocks by. ``rotary_prefill_step`` and
         ``sparse_step`` keep them up; after any other write to the pools (``load``,
         ``step``, ``prefill_step``, ``apply_copies``, ``swap_in``) call
-        ``refresh_key_bounds`` for the sequences it touched. The first call fills them
-        with zeros on ``stream``."""
+        ``refresh_key_bounds`` for the sequences it touched.
+
+        The first call (``sparse_step`` and ``refresh_key_bounds`` make it if nobody
+        has) takes the bounds of what the pool holds, each block over all its slots,
+        on ``stream`` and waits for them; a block's unwritten slots cost it nothing, as
+        the next write to it takes its bounds anew over the filled ones. Not while
+        ``stream`` is being captured."""
         if getattr(self, "key_bounds", None) is None:
             with self._on_stream(stream):
-                self.key_bounds = torch.zeros(
-                    key_bounds_shape(self.num_blocks, self.num_kv_heads, self.head_dim),
-                    dtype=key_bounds_dtype(self.k_pool.dtype), device=self.device)
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("call enable_key_bounds before capturing a graph: a replay "
+                                       "would take every block's bounds again")
+                bounds = torch.empty(key_bounds_shape(self.num_blocks, self.num_kv_heads, self.head_dim),
+                                     dtype=key_bounds_dtype(self.k_pool.dtype), device=self.device)
+                self._bound_whole_pool(bounds)
+                torch.cuda.current_stream(self.device).synchronize()
+            self.key_bounds = bounds
         return self.key_bounds
+
+    def _bound_whole_pool(self, bounds):
+        """The bounds of every block over all its slots, on the current stream: the
+        pool as sequences of at most 65,536 blocks."""
+        width = min(self.num_blocks, 1 << 16)
+        rows = -(-self.num_blocks // width)
+        tables = torch.arange(rows * width, dtype=torch.int32, device=self.device).view(rows, width)
+        lens = torch.full((rows,), width * self.block_size, dtype=torch.int32, device=self.device)
+        lens[-1] = (self.num_blocks - (rows - 1) * width) * self.block_size
+        update_key_bounds(self.k_pool, bounds, tables, lens, torch.zeros_like(lens))
 
     def refresh_key_bounds(self, tables, lens, stream=None):
         """Bounds of every block of these sequences (device tables and lengths),

@@ -77,3 +77,55 @@ def test_bounds_made_on_first_use_are_filled_on_the_stream_that_uses_them(rec):
     cache.refresh_key_bounds(tables, lens, stream=s)
     assert cache.key_bounds is not None and rec.named("update")
     assert [e for e in rec.log if e[1] is not s] == []
+
+
+def step_args(B=2, width=4, K=2):
+    """Host tensors of a sparse step, to be called with the library's calls recorded."""
+    plan = {"pairs": torch.zeros(0, 2, dtype=I64), "slots": torch.zeros(B, dtype=I64),
+            "tables": torch.zeros(B, width, dtype=I32), "lens": torch.ones(B, dtype=I32)}
+    q, kv = torch.zeros(B, HQ, D, dtype=BF), torch.zeros(B, HKV, D, dtype=BF)
+    pos = torch.zeros(B, dtype=I32)
+    return dict(q=q, k_new=kv, v_new=kv.clone(), dev_plan=plan, positions=pos, first=pos.clone(),
+                rotary=engine.Rotary(torch.zeros(8, 2, D // 2)), selected=torch.zeros(B, HKV, K, dtype=I32),
+                out=torch.empty_like(q), scale=0.1)
+
+
+def covered(updates):
+    """Blocks whose bounds the recorded updates take whole: (block, tokens seen)."""
+    seen = {}
+    for _, _, (_, _, tables, lens, first, *_) in updates:
+        for row, n, f in zip(tables.tolist(), lens.tolist(), first.tolist()):
+            for j in range(f // BS, -(-n // BS)):
+                seen[row[j]] = min(BS, n - j * BS)
+    return seen
+
+
+@pytest.mark.parametrize("blocks", [1, NB, (1 << 16) + 3])
+def test_enabling_takes_the_bounds_of_every_block(rec, blocks):
+    s = FakeStream("side")
+    cache = engine.PagedKVCache(blocks, 1, 1, 16, 16, BF, range(blocks), device="cpu")
+    cache.enable_key_bounds(s)
+    assert covered(rec.named("update")) == {i: 16 for i in range(blocks)}
+    assert all(e[1] is s for e in rec.log[-3:]) and s.synced == 1
+    n = len(rec.log)
+    assert cache.enable_key_bounds() is cache.key_bounds and len(rec.log) == n
+
+
+def test_a_sparse_step_on_a_cache_without_bounds_takes_them_first(rec, monkeypatch):
+    s = FakeStream("side")
+    cache, a = new_cache(), step_args()
+    monkeypatch.setattr(engine.PagedKVCache, "_rotated_append", lambda self, *x: rec.log.append(("append", s, x)))
+    for name in ("select_blocks", "paged_attention_decode_sparse"):
+        monkeypatch.setattr(engine, name, rec.call(name))
+    cache.sparse_step(**a, stream=s)
+    order = [e[0] for e in rec.log if e[0] in ("update", "append", "select_blocks")]
+    assert order == ["update", "append", "select_blocks"]
+    assert set(covered(rec.named("update"))) == set(range(NB))
+
+
+def test_bounds_are_not_made_while_a_graph_is_captured(rec, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    cache = new_cache()
+    with pytest.raises(RuntimeError, match="before capturing"):
+        cache.enable_key_bounds()
+    assert getattr(cache, "key_bounds", None) is None and not rec.named("update")

@@ -1,0 +1,105 @@
+"""The engine's key bounds on a GPU: whatever order a user's calls come in, the bounds
+of every block that a sparse step scores are those of its filled slots (exact)."""
+import numpy as np
+import pytest
+import torch
+
+from _lib import library, pkv
+from oracle import attention as oatt
+from oracle import long_context as olc
+from paged_kv_cache_259_gb300 import engine
+
+pytestmark = pytest.mark.gpu
+BF, F32, U8, I32, I64 = torch.bfloat16, torch.float32, torch.uint8, torch.int32, torch.int64
+HQ, HKV, D, BS = 8, 2, 64, 16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu_and_library():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU test selected but no CUDA device is visible")
+    library()
+    torch.cuda.set_device(0)
+    pkv.get_device_error()
+
+
+def new_cache(NB=80, cache=BF, seed=0, **over):
+    return engine.PagedKVCache(NB, HQ, HKV, D, BS, cache, np.random.default_rng(seed).permutation(NB), "cuda", **over)
+
+
+def values(rng, *shape, dtype=BF):
+    return torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(dtype)
+
+
+def rotary():
+    return engine.Rotary(pkv.rotary_table(4096, D, device="cuda"))
+
+
+def sparse_step(cache, ids, rng, K=4, act=BF, stream=None):
+    """One sparse decode step of the sequences; checks its choice of blocks against the
+    oracle on bounds taken from the pool's own values."""
+    plan = cache.plan_step(ids, group_prefixes=False)
+    q, k, v = (values(rng, len(ids), h, D, dtype=act).cuda() for h in (HQ, HKV, HKV))
+    sel = torch.empty(len(ids), HKV, K, dtype=I32, device="cuda")
+    ws = cache.select_workspace(len(ids), plan.tables.shape[1])
+    args = (plan.device_tensors("cuda"), torch.from_numpy((plan.lens - 1).astype(np.int32)).cuda(),
+            torch.from_numpy(engine.first_changed(plan)).cuda(), rotary(), sel, torch.empty_like(q), D ** -0.5)
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+    cache.sparse_step(q, k, v, *args, first_blocks=1, last_blocks=1, workspace=ws, stream=stream)
+    if stream is not None:
+        torch.cuda.current_stream().wait_stream(stream)
+    check_bounds(cache, plan.tables, plan.lens)
+    want = olc.select_blocks(q.double().cpu().numpy(), cache.key_bounds.double().cpu().numpy(), plan.tables,
+                             plan.lens, BS, HKV, K, 1, 1)
+    assert np.array_equal(sel.cpu().numpy(), want)
+    assert pkv.get_device_error() == 0
+    return plan
+
+
+def check_bounds(cache, tables, lens):
+    k = oatt.widen(cache.k_view()).reshape(cache.num_blocks, HKV, BS, D)
+    got = cache.key_bounds.double().cpu().numpy()
+    for row, L in zip(tables, lens):
+        for j in range(-(-int(L) // BS)):
+            for h in range(HKV):
+                assert np.array_equal(got[row[j], h], olc.key_bounds(k[row[j], h], min(BS, L - j * BS))), (j, h)
+
+
+def filled(cache, lens, rng, **load):
+    """Sequences of these lengths over values loaded into every slot."""
+    cache.load(*(values(rng, cache.num_blocks, HKV, BS, D, dtype=F32 if cache.k_pool.dtype == U8 else cache.k_pool.dtype)
+                 for _ in range(2)), **load)
+    for s, n in enumerate(lens):
+        cache.bm.add_seq(s)
+        cache.bm.append_n(s, n)
+    return list(range(len(lens)))
+
+
+@pytest.mark.parametrize("cache", [BF, U8, F32])
+@pytest.mark.parametrize("side", [False, True])
+def test_sparse_step_on_a_cache_filled_without_bounds(cache, side):
+    """The first sparse step takes the bounds of all that is cached, on its own stream
+    (the current one kept busy)."""
+    rng = np.random.default_rng(1)
+    c = new_cache(cache=cache)
+    ids = filled(c, [300, 161, 16, 15, 1], rng)
+    s = torch.cuda.Stream() if side else None
+    if side:
+        torch.cuda.synchronize()
+        x = torch.randn(4096, 4096, device="cuda")
+        for _ in range(20):
+            x = x @ x
+    sparse_step(c, ids, rng, act=F32 if cache == F32 else BF, stream=s)
+    sparse_step(c, ids[1:], rng, act=F32 if cache == F32 else BF, stream=s)
+
+
+def test_bounds_of_a_pool_of_more_blocks_than_one_launch_row():
+    """70,000 blocks: the second row of the launch is shorter."""
+    NB = 70000
+    c = engine.PagedKVCache(NB, 1, 1, 16, 16, BF, range(NB), "cuda")
+    c.k_pool.normal_()
+    kb = c.enable_key_bounds()
+    k = c.k_view()
+    want = torch.stack([k.float().amin(2), k.float().amax(2)], 2)
+    assert torch.equal(kb.float(), want)
