@@ -16,6 +16,7 @@ Pools are allocated by torch (device memory is plumbing); all arithmetic runs in
 the library's kernels.
 """
 import ctypes
+import time
 from dataclasses import dataclass
 
 import numpy as np
@@ -154,6 +155,7 @@ class PagedKVCache:
         self.bm = BlockManager(num_blocks, block_size, free_order, prefix_caching=prefix_caching,
                                num_host_blocks=num_host_blocks)
         self.num_host_blocks = num_host_blocks
+        self.key_bounds = None                               # see enable_key_bounds
         if num_host_blocks:
             hk, hv = pool_shapes(num_host_blocks, num_kv_heads, block_size, head_dim, kv_dtype)
             self.host_k = torch.empty(hk, dtype=kv_dtype).pin_memory()
@@ -167,6 +169,8 @@ class PagedKVCache:
         slots = torch.arange(NB * bs, dtype=torch.int64, device=self.device)
         tok = lambda x: x.to(self.device).permute(0, 2, 1, 3).reshape(NB * bs, Hkv, D).contiguous()
         reshape_and_cache(tok(k_vals), tok(v_vals), self.k_pool, self.v_pool, slots, k_scale, v_scale)
+        if self.key_bounds is not None:
+            self._bound_whole_pool(self.key_bounds)
 
     def k_view(self):
         """K pool as ``[NB, Hkv, bs, D]`` (a copy, for inspection and tests)."""
@@ -202,6 +206,11 @@ class PagedKVCache:
         for a, b in copy_waves(pairs):
             t = torch.as_tensor(pairs[a:b], device=self.device)
             copy_blocks(self.k_pool, self.v_pool, t, stream=stream)
+            if self.key_bounds is not None:                  # the bounds move with their blocks
+                good = pairs[a:b][((pairs[a:b] >= 0) & (pairs[a:b] < self.num_blocks)).all(1)]
+                with self._on_stream(stream):
+                    src, dst = torch.as_tensor(np.ascontiguousarray(good.T), device=self.device)
+                    self.key_bounds[dst] = self.key_bounds[src]
 
     def plan_step(self, seq_ids, max_blocks=None, group_prefixes=True):
         """Host half of a step: one slot per sequence (CoW pairs included), dense
@@ -306,6 +315,13 @@ class PagedKVCache:
             scatter = np.stack([np.arange(len(pairs)), pairs[:, 1]], 1)
             swap_blocks(self.k_pool, self.v_pool, sk, sv,
                         torch.as_tensor(scatter, device=self.device), stream)
+        if len(pairs) and self.key_bounds is not None:
+            ids = np.asarray([int(s) for s in seq_ids], dtype=np.int64)
+            width = max(-(-self.bm.seq_len(int(s)) // self.block_size) for s in ids)
+            with self._on_stream(stream):
+                tables, lens = (torch.as_tensor(t, device=self.device)
+                                for t in self.bm.build_tables(ids, max(1, width)))
+            self.refresh_key_bounds(tables, lens, stream)
         return pairs
 
     def preempt_by_recompute(self, seq_ids):
@@ -386,11 +402,16 @@ class PagedKVCache:
         """Device half of a chunked-prefill step: CoW copies, the chunk's K/V into
         its slots, then causal attention of every chunk token (one
         ``paged_prefill_step`` call; the attention reads the tiles before each
-        chunk while the writes finish)."""
-        return paged_prefill_step(out, q, k_new, v_new, self.k_pool, self.v_pool,
-                                  dev_plan["tables"], dev_plan["lens"], dev_plan["query_start"],
-                                  dev_plan["slots"], dev_plan["pairs"], scale, max_query_len,
-                                  stream)
+        chunk while the writes finish), and the key bounds (when kept)."""
+        paged_prefill_step(out, q, k_new, v_new, self.k_pool, self.v_pool,
+                           dev_plan["tables"], dev_plan["lens"], dev_plan["query_start"],
+                           dev_plan["slots"], dev_plan["pairs"], scale, max_query_len,
+                           stream)
+        if self.key_bounds is not None:
+            with self._on_stream(stream):
+                chunks = dev_plan["query_start"].diff()
+            self._bound_newest(dev_plan, chunks, max_query_len, stream)
+        return out
 
     def workspace(self, batch, max_blocks):
         """Split-KV scratch, room for split group lists included."""
@@ -419,7 +440,8 @@ class PagedKVCache:
         (default: every row of the plan's pairs) counts the filled rows of a pairs
         buffer sized for the most a step can raise; with a grouped plan, ``groups
         = (num_groups, max_group_blocks, num_ungrouped)`` counts the filled rows
-        of its group buffers (0 groups: the plain decode)."""
+        of its group buffers (0 groups: the plain decode). Key bounds, when kept, are
+        updated by every run."""
         grouped = "group_members" in dev_plan
         call = bind_paged_decode_step(
             out, q, k_new, v_new, self.k_pool, self.v_pool, dev_plan["tables"], dev_plan["lens"],
@@ -438,6 +460,8 @@ class PagedKVCache:
                 if dev_plan.get("ungrouped") is not None:
                     counts["num_ungrouped"] = nu
             call(stream, **counts)
+            if self.key_bounds is not None:
+                self._bound_newest(dev_plan, 1, 1, stream)
         return run
 
     def _on_stream(self, stream):
@@ -446,17 +470,17 @@ class PagedKVCache:
 
     def enable_key_bounds(self, stream=None):
         """Keep the key bounds of every block (``update_key_bounds``), which sparse
-        decode steps choose their blocks by. ``rotary_prefill_step`` and
-        ``sparse_step`` keep them up; after any other write to the pools (``load``,
-        ``step``, ``prefill_step``, ``apply_copies``, ``swap_in``) call
-        ``refresh_key_bounds`` for the sequences it touched.
+        decode steps choose their blocks by. Every call of this cache that writes keys
+        then keeps them up. A write that does not come through the cache (the
+        library's own calls on ``k_pool``, a graph captured before this call) has to
+        be followed by ``refresh_key_bounds`` for the sequences it touched.
 
         The first call (``sparse_step`` and ``refresh_key_bounds`` make it if nobody
         has) takes the bounds of what the pool holds, each block over all its slots,
         on ``stream`` and waits for them; a block's unwritten slots cost it nothing, as
         the next write to it takes its bounds anew over the filled ones. Not while
         ``stream`` is being captured."""
-        if getattr(self, "key_bounds", None) is None:
+        if self.key_bounds is None:
             with self._on_stream(stream):
                 if torch.cuda.is_current_stream_capturing():
                     raise RuntimeError("call enable_key_bounds before capturing a graph: a replay "
@@ -478,9 +502,17 @@ class PagedKVCache:
         lens[-1] = (self.num_blocks - (rows - 1) * width) * self.block_size
         update_key_bounds(self.k_pool, bounds, tables, lens, torch.zeros_like(lens))
 
+    def _bound_newest(self, dev_plan, new, max_new, stream):
+        """Bounds of the blocks that hold the newest ``new`` (a number, or a device tensor
+        ``[B]``) tokens of a plan's sequences."""
+        with self._on_stream(stream):
+            first = (dev_plan["lens"] - new).clamp_(min=0)
+        update_key_bounds(self.k_pool, self.key_bounds, dev_plan["tables"], dev_plan["lens"], first,
+                          max_new, stream=stream)
+
     def refresh_key_bounds(self, tables, lens, stream=None):
-        """Bounds of every block of these sequences (device tables and lengths),
-        e.g. after ``load`` or ``swap_in``."""
+        """Bounds of every block of these sequences (device tables and lengths), after a
+        write that did not come through the cache."""
         bounds = self.enable_key_bounds(stream)
         with self._on_stream(stream):
             first = torch.zeros_like(lens)         # of the stream that uses it
@@ -497,7 +529,7 @@ class PagedKVCache:
             copy_blocks(self.k_pool, self.v_pool, dev_plan["pairs"], stream)
         rotary_and_cache(q, q, k_new, v_new, self.k_pool, self.v_pool, dev_plan["slots"], positions,
                          rotary.cos_sin, rotary.sections, rotary.interleaved, k_scale, v_scale, stream)
-        if getattr(self, "key_bounds", None) is not None:
+        if self.key_bounds is not None:
             update_key_bounds(self.k_pool, self.key_bounds, dev_plan["tables"], dev_plan["lens"], first,
                               max_new, stream)
 
@@ -754,8 +786,10 @@ class LiveDecodePipeline(StepPipeline):
         the step."""
         self.host_inputs()
         slots_p, pairs_p, tables_p, lens_p, g = self._ptrs[self.n % 2]
+        t0 = time.perf_counter()
         npairs, ng, nu, mgb = self.cache.bm.plan_decode_into(
             self._ids_p, len(self.ids), self.max_blocks, slots_p, pairs_p, tables_p, lens_p, g)
+        self.last_plan_us, self.last_counts = 1e6 * (time.perf_counter() - t0), (npairs, ng, nu, mgb)
         if self.grouped:
             self._step_counts = {"num_pairs": npairs, "groups": (ng, mgb, nu)}
         else:
@@ -805,8 +839,9 @@ class LiveDecodePipeline(StepPipeline):
         """Plan and run the next step. Unless ``plan`` was called for it, the
         planning, the upload, the step's launches and the read-back are one
         library call (``pkv_decode_pipeline_step``; ``last_plan_us`` and
-        ``last_counts`` then report its planning); after ``plan``, the step runs
-        as ``StepPipeline.submit`` does."""
+        ``last_counts`` then report its planning); after ``plan``, and where the cache
+        keeps key bounds (their update belongs between the step and its read-back), the
+        step runs as ``StepPipeline.submit`` does."""
         if self._step_counts:
             try:
                 return super().submit(host_out, scale, k_scale, v_scale, workspace)
@@ -815,6 +850,9 @@ class LiveDecodePipeline(StepPipeline):
         if not (host_out.is_contiguous() and host_out.numel() == self.outs[0].numel() and
                 host_out.dtype == self.outs[0].dtype and not host_out.is_cuda):
             raise ValueError("host_out must be a contiguous CPU tensor shaped like the output")
+        if self.cache.key_bounds is not None:
+            self.plan()
+            return self.submit(host_out, scale, k_scale, v_scale, workspace)
         b = self.n % 2
         self.host_inputs()                                # the slab's previous upload is done
         a = self._native(b, scale, k_scale, v_scale, workspace)

@@ -95,7 +95,7 @@ def covered(updates):
     seen = {}
     for _, _, (_, _, tables, lens, first, *_) in updates:
         for row, n, f in zip(tables.tolist(), lens.tolist(), first.tolist()):
-            for j in range(f // BS, -(-n // BS)):
+            for j in range(f // BS, -(-n // BS)) if f < n else ():
                 seen[row[j]] = min(BS, n - j * BS)
     return seen
 
@@ -129,3 +129,95 @@ def test_bounds_are_not_made_while_a_graph_is_captured(rec, monkeypatch):
     with pytest.raises(RuntimeError, match="before capturing"):
         cache.enable_key_bounds()
     assert getattr(cache, "key_bounds", None) is None and not rec.named("update")
+
+
+# --------------------------------------------------- every write keeps them up
+@pytest.fixture
+def kept(rec, monkeypatch):
+    """A cache that keeps bounds, the library's calls recorded."""
+    for name in ("reshape_and_cache", "copy_blocks", "swap_blocks", "paged_prefill_step"):
+        monkeypatch.setattr(engine, name, rec.call(name))
+    monkeypatch.setattr(engine, "bind_paged_decode_step", lambda *a: lambda s, **k: rec.log.append(("step", s, a)))
+    rec.stack[0] = FakeStream("current")
+    cache = new_cache()
+    cache.key_bounds = torch.zeros(pkv.key_bounds_shape(NB, HKV, D), dtype=BF)
+    return cache
+
+
+def seq_table(cache, s):
+    n = cache.bm.seq_len(s)
+    return cache.bm.build_tables([s], -(-n // BS))[0][0].tolist(), n
+
+
+def last(rec, name):
+    """The index of the last record of this name (-1: none)."""
+    return max((i for i, e in enumerate(rec.log) if e[0] == name), default=-1)
+
+
+def test_load_takes_the_bounds_of_every_block(kept, rec):
+    kept.load(torch.zeros(NB, HKV, BS, D), torch.zeros(NB, HKV, BS, D))
+    assert covered(rec.named("update")) == {i: BS for i in range(NB)}
+    assert last(rec, "update") > last(rec, "reshape_and_cache")
+
+
+def test_copies_move_the_bounds_with_their_blocks(kept):
+    for i in range(NB):
+        kept.key_bounds[i] = i
+    kept.apply_copies([(0, 5), (1, 6), (5, 7), (2, 1), (NB, 3), (4, -1)])      # the last two are not blocks
+    want = list(range(NB))
+    want[5], want[6], want[7], want[1] = 0, 1, 0, 2
+    assert kept.key_bounds[:, 0, 0, 0].tolist() == want
+
+
+@pytest.mark.parametrize("n", [1, BS, BS + 1, 3 * BS])
+def test_decode_steps_take_the_bounds_of_the_last_block(kept, rec, n):
+    s = FakeStream("side")
+    kept.bm.add_seq(0)
+    kept.bm.append_n(0, n - 1)
+    plan = kept.plan_step([0]).host_tensors(pin=False)
+    q, kv = torch.zeros(1, HQ, D, dtype=BF), torch.zeros(1, HKV, D, dtype=BF)
+    kept.step(q, kv, kv, plan, torch.empty_like(q), 0.1, stream=s)
+    table, _ = seq_table(kept, 0)
+    assert covered(rec.named("update")) == {table[(n - 1) // BS]: (n - 1) % BS + 1}
+    assert rec.log[last(rec, "update")][1] is s and last(rec, "update") > last(rec, "step")
+
+
+def test_prefill_steps_take_the_bounds_of_the_chunks_blocks(kept, rec):
+    s = FakeStream("side")
+    chunks, before = [BS + 3, 1, 0], [BS - 2, 0, 5]
+    for i, n in enumerate(before):
+        kept.bm.add_seq(i)
+        kept.bm.append_n(i, n)
+    plan = kept.plan_prefill([0, 1, 2], chunks)
+    T = sum(chunks)
+    q, kv = torch.zeros(T, HQ, D, dtype=BF), torch.zeros(T, HKV, D, dtype=BF)
+    out = torch.empty_like(q)
+    assert kept.prefill_step(q, kv, kv, plan.host_tensors(pin=False), out, 0.1, plan.max_query_len, s) is out
+    t = [seq_table(kept, i)[0] for i in range(3)]
+    assert covered(rec.named("update")) == {t[0][0]: BS, t[0][1]: BS, t[0][2]: 1, t[1][0]: 1}
+    assert rec.log[last(rec, "update")][1] is s and last(rec, "update") > last(rec, "paged_prefill_step")
+
+
+def test_swapped_in_sequences_get_their_bounds(kept, rec, monkeypatch):
+    s = FakeStream("side")
+    kept.bm = pkv.BlockManager(NB, BS, range(NB), num_host_blocks=8)
+    kept.host_k = kept.host_v = None
+    for i, n in enumerate([2 * BS + 1, 4]):
+        kept.bm.add_seq(i)
+        kept.bm.append_n(i, n)
+    kept.swap_out([0, 1])
+    assert not rec.named("update")
+    kept.swap_in([0, 1], s)
+    t = [seq_table(kept, i)[0] for i in range(2)]
+    assert covered(rec.named("update")) == {t[0][0]: BS, t[0][1]: BS, t[0][2]: 1, t[1][0]: 4}
+    assert rec.log[last(rec, "update")][1] is s and last(rec, "update") > last(rec, "swap_blocks")
+
+
+def test_nothing_is_updated_where_no_bounds_are_kept(kept, rec):
+    kept.key_bounds = None
+    kept.load(torch.zeros(NB, HKV, BS, D), torch.zeros(NB, HKV, BS, D))
+    kept.apply_copies([(0, 5)])
+    kept.bm.add_seq(0)
+    q, kv = torch.zeros(1, HQ, D, dtype=BF), torch.zeros(1, HKV, D, dtype=BF)
+    kept.step(q, kv, kv, kept.plan_step([0]).host_tensors(pin=False), torch.empty_like(q), 0.1)
+    assert not rec.named("update")

@@ -103,3 +103,74 @@ def test_bounds_of_a_pool_of_more_blocks_than_one_launch_row():
     k = c.k_view()
     want = torch.stack([k.float().amin(2), k.float().amax(2)], 2)
     assert torch.equal(kb.float(), want)
+
+
+def decode_args(cache, ids, rng):
+    plan = cache.plan_step(ids, group_prefixes=False)
+    q, k, v = (values(rng, len(ids), h, D).cuda() for h in (HQ, HKV, HKV))
+    return plan, (q, k, v, plan.device_tensors("cuda"), torch.empty_like(q), D ** -0.5)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_bounds_follow_every_write_of_the_cache(side):
+    """Prompts, decode steps, copies, swapping and loads between sparse steps: each
+    sparse step's choice is the oracle's on the pool's own values."""
+    rng = np.random.default_rng(2)
+    s = torch.cuda.Stream() if side else None
+    c = new_cache(num_host_blocks=40)
+    c.enable_key_bounds()
+    for i in range(3):
+        c.bm.add_seq(i)
+    chunks = [130, 47, 16]
+    plan = c.plan_prefill([0, 1, 2], chunks)
+    q, k, v = (values(rng, sum(chunks), h, D).cuda() for h in (HQ, HKV, HKV))
+    torch.cuda.synchronize()
+    c.prefill_step(q, k, v, plan.device_tensors("cuda"), torch.empty_like(q), D ** -0.5, plan.max_query_len, s)
+    torch.cuda.synchronize()
+    check_bounds(c, plan.tables, plan.lens)
+    sparse_step(c, [0, 1, 2], rng, stream=s)
+    c.bm.fork(0, 7)                                        # the next step copies its last block
+    for _ in range(18):                                    # over a block border
+        plan, a = decode_args(c, [0, 1, 2, 7], rng)
+        torch.cuda.synchronize()
+        c.step(*a, workspace=c.workspace(4, plan.tables.shape[1]), stream=s)
+    torch.cuda.synchronize()
+    check_bounds(c, plan.tables, plan.lens)
+    sparse_step(c, [0, 1, 2, 7], rng, stream=s)
+    torch.cuda.synchronize()
+    c.swap_out([0, 2], s)
+    c.swap_in([2, 0], s)
+    torch.cuda.synchronize()
+    sparse_step(c, [0, 1, 2], rng, stream=s)
+    torch.cuda.synchronize()
+    c.swap_out([1], copy_engines=True)
+    c.swap_in([1], copy_engines=True)
+    sparse_step(c, [1, 7], rng)
+    c.load(*(values(rng, c.num_blocks, HKV, BS, D) for _ in range(2)))
+    sparse_step(c, [0, 1, 2, 7], rng, stream=s)
+    torch.cuda.synchronize()
+    table = c.bm.build_tables([0], 12)[0][0]
+    c.apply_copies([(int(table[1]), int(table[2])), (int(table[2]), int(table[3]))], stream=s)
+    sparse_step(c, [0], rng, stream=s)
+
+
+def test_bounds_follow_a_live_decode_pipeline():
+    rng = np.random.default_rng(3)
+    c = new_cache()
+    ids = filled(c, [60, 31, 200], rng)
+    c.enable_key_bounds()
+    q, k, v = (values(rng, 3, h, D) for h in (HQ, HKV, HKV))
+    pipe = engine.LiveDecodePipeline(c, ids, q, k, v, torch.empty_like(q), 16, group_prefixes=False)
+    outs = [torch.empty_like(q).pin_memory() for _ in range(6)]
+    ws = c.workspace(3, 16)
+    for i in range(6):
+        views = pipe.host_inputs()
+        for name, h in (("q", HQ), ("k_new", HKV), ("v_new", HKV)):
+            views[name].copy_(values(rng, 3, h, D))
+        _, done = pipe.submit(outs[i], D ** -0.5, workspace=ws)
+        assert pipe.last_counts[0] == 0 and pipe.last_plan_us > 0
+    done.synchronize()
+    tables, lens = c.bm.build_tables(ids, 16)
+    assert list(lens) == [66, 37, 206]
+    check_bounds(c, tables, lens)
+    sparse_step(c, ids, rng)
