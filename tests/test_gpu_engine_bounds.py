@@ -58,7 +58,7 @@ def sparse_step(cache, ids, rng, K=4, act=BF, stream=None):
 
 
 def check_bounds(cache, tables, lens):
-    k = oatt.widen(cache.k_view()).reshape(cache.num_blocks, HKV, BS, D)
+    k = oatt.widen(cache.k_view().cpu()).reshape(cache.num_blocks, HKV, BS, D)
     got = cache.key_bounds.double().cpu().numpy()
     for row, L in zip(tables, lens):
         for j in range(-(-int(L) // BS)):
