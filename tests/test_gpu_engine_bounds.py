@@ -11,7 +11,7 @@ from paged_kv_cache_259_gb300 import engine
 
 pytestmark = pytest.mark.gpu
 BF, F32, U8, I32, I64 = torch.bfloat16, torch.float32, torch.uint8, torch.int32, torch.int64
-HQ, HKV, D, BS = 8, 2, 64, 16
+HQ, HKV, D, BS = 8, 2, 128, 16
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -134,7 +134,7 @@ def test_bounds_follow_every_write_of_the_cache(side):
         plan, a = decode_args(c, [0, 1, 2, 7], rng)
         torch.cuda.synchronize()
         c.step(*a, workspace=c.workspace(4, plan.tables.shape[1]), stream=s)
-    torch.cuda.synchronize()
+        torch.cuda.synchronize()
     check_bounds(c, plan.tables, plan.lens)
     sparse_step(c, [0, 1, 2, 7], rng, stream=s)
     torch.cuda.synchronize()
