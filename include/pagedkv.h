@@ -577,24 +577,30 @@ PKV_API int paged_attention_decode_sparse(void* out, const void* q, const void* 
                                           void* stream);
 
 /* ------------------------------------------------------------------------
- * pkv_bound_call -- one of the four calls above with its arguments packed, for
- * callers to which passing each argument costs (a foreign-function interface takes
- * more time over twenty-odd arguments than the call itself over its launch).
+ * pkv_bound_call -- one of the four calls above, or paged_attention_prefill, with its
+ * arguments packed, for callers to which passing each argument costs (a
+ * foreign-function interface takes more time over twenty-odd arguments than the call
+ * itself over its launch).
+ * pkv_bound_check -- what that call would return for its arguments, without running
+ * it (no CUDA call is made): a step of several calls checks them all before the first
+ * one changes anything.
  *
  *   call      which one
  *   args      host, one 64-bit slot per argument in the call's order, its stream left
  *             out: pointers and integers by value (sign-extended), a float's bits in
  *             the lower half
  *   num_args  slots; not the call's number of arguments: PKV_ERR_INVALID_ARG
- * Returns what the call returns.
+ * Both return what the call returns.
  * ---------------------------------------------------------------------- */
 typedef enum {
     PKV_CALL_ROTARY_AND_CACHE = 0,
     PKV_CALL_UPDATE_KEY_BOUNDS = 1,
     PKV_CALL_SELECT_BLOCKS = 2,
-    PKV_CALL_DECODE_SPARSE = 3
+    PKV_CALL_DECODE_SPARSE = 3,
+    PKV_CALL_PREFILL = 4
 } pkv_call;
 PKV_API int pkv_bound_call(int call, const uint64_t* args, int num_args, void* stream);
+PKV_API int pkv_bound_check(int call, const uint64_t* args, int num_args);
 
 /* ------------------------------------------------------------------------
  * Stream plumbing of a pipelined step (no counterpart in the pages: it is how

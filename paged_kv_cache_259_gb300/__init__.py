@@ -30,7 +30,7 @@ __all__ = [
     "paged_attention_prefill", "swap_blocks",
     "reshape_and_cache", "copy_blocks", "get_device_error", "check_wait_timeout",
     "BoundCall", "bind_paged_attention_decode", "bind_paged_attention_decode_grouped",
-    "bind_reshape_and_cache", "bind_copy_blocks", "paged_decode_step", "bind_paged_decode_step", "paged_prefill_step",
+    "bind_reshape_and_cache", "bind_copy_blocks", "bind_paged_attention_prefill", "paged_decode_step", "bind_paged_decode_step", "paged_prefill_step",
     "rotary_and_cache", "bind_rotary_and_cache", "rotary_table", "key_bounds_shape",
     "key_bounds_dtype", "update_key_bounds", "bind_update_key_bounds", "select_blocks",
     "bind_select_blocks", "select_blocks_workspace_size", "paged_attention_decode_sparse",
@@ -46,7 +46,7 @@ _LIB = None
 PKV_F32, PKV_BF16, PKV_E4M3 = 0, 1, 2
 PKV_ERR_POOL_EXHAUSTED = -5
 (PKV_CALL_ROTARY_AND_CACHE, PKV_CALL_UPDATE_KEY_BOUNDS, PKV_CALL_SELECT_BLOCKS,
- PKV_CALL_DECODE_SPARSE) = range(4)
+ PKV_CALL_DECODE_SPARSE, PKV_CALL_PREFILL) = range(5)
 _STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported configuration",
            -3: "CUDA runtime error", -4: "index out of range", -5: "block pool exhausted",
            -6: "device wait timed out"}
@@ -144,6 +144,7 @@ def load_library():
                                                   c_int, c_int, c_int, c_int, c_int, c_float,
                                                   c_int, c_int, c_float, c_float, vp]),
         "pkv_bound_call": (c_int, [c_int, vp, c_int, vp]),
+        "pkv_bound_check": (c_int, [c_int, vp, c_int]),
         "pkv_get_device_error": (c_int, [ip, vp]),
         "pkv_check_wait_timeout": (c_int, [vp]),
         "pkv_stage_upload": (c_int, [vp, vp, c_size, vp, vp, vp, vp, vp]),
@@ -542,6 +543,14 @@ def paged_attention_prefill(out, q, k_pool, v_pool, block_tables, seq_lens, quer
     library layout; block_tables int32 ``[B, max_blocks]``; seq_lens int32
     ``[B]``; query_start int32 ``[B + 1]``; ``max_query_len`` >= every C_b.
     """
+    bind_paged_attention_prefill(out, q, k_pool, v_pool, block_tables, seq_lens, query_start, scale,
+                                 max_query_len)(stream)
+    return out
+
+
+def bind_paged_attention_prefill(out, q, k_pool, v_pool, block_tables, seq_lens, query_start,
+                                 scale, max_query_len):
+    """``paged_attention_prefill`` checked once and bound to these tensors (``BoundCall``)."""
     lib = load_library()
     named = ((out, "out"), (q, "q"), (k_pool, "k_pool"), (v_pool, "v_pool"),
              (block_tables, "block_tables"), (seq_lens, "seq_lens"), (query_start, "query_start"))
@@ -561,14 +570,10 @@ def paged_attention_prefill(out, q, k_pool, v_pool, block_tables, seq_lens, quer
         raise ValueError("inconsistent shapes: block_tables [B, max_blocks], query_start "
                          "[B + 1], pools of q's head_dim")
     dev = _on_gpu(named)
-    with _on_device(dev):
-        st = lib.paged_attention_prefill(
-            out.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-            block_tables.data_ptr(), seq_lens.data_ptr(), query_start.data_ptr(), B,
-            int(max_query_len), block_tables.shape[1], NB, Hq, Hkv, D, bs, float(scale),
-            _dt(q, "q"), _dt(k_pool, "k_pool"), _stream_ptr(stream, dev))
-    _check(st, "paged_attention_prefill")
-    return out
+    args = [_ptr(t) for t, _ in named]
+    args += _c_args([B, int(max_query_len), block_tables.shape[1], NB, Hq, Hkv, D, bs, float(scale),
+                     _dt(q, "q"), _dt(k_pool, "k_pool")])
+    return PackedCall(lib, PKV_CALL_PREFILL, args, "paged_attention_prefill", dev)
 
 
 def paged_prefill_step(out, q, k_new, v_new, k_pool, v_pool, block_tables, seq_lens,
@@ -912,13 +917,15 @@ class BoundCall:
 class PackedCall(BoundCall):
     """A ``BoundCall`` whose arguments lie packed for ``pkv_bound_call``: the
     library unpacks them, so a call passes four arguments instead of twenty-odd
-    (1.6 us of host time on a Grace core for the 29 of ``rotary_and_cache``)."""
+    (1.6 us of host time on a Grace core for the 29 of ``rotary_and_cache``).
+    ``check`` raises what a call with these arguments would raise for them, and runs
+    nothing."""
 
-    __slots__ = ("_call", "_packed", "_addr", "_n", "_keep")
+    __slots__ = ("_call", "_packed", "_addr", "_n", "_keep", "_checks")
 
     def __init__(self, lib, call, args, what, device):
         super().__init__(lib.pkv_bound_call, args, what, device)
-        self._call, self._n = call, len(args)
+        self._call, self._n, self._checks = call, len(args), lib.pkv_bound_check
         self._packed = (ctypes.c_uint64 * self._n)()
         self._keep = args                                  # host arrays the slots point to
         for i, a in enumerate(args):
@@ -929,6 +936,9 @@ class PackedCall(BoundCall):
             else:
                 self._packed[i] = (a.value or 0) & 0xffffffffffffffff
         self._addr = ctypes.addressof(self._packed)
+
+    def check(self):
+        _check(self._checks(self._call, self._addr, self._n), self._what)
 
     def __call__(self, stream=None):
         idx = self._idx

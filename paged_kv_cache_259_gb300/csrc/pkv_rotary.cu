@@ -31,6 +31,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "pkv_check.cuh"
 #include "pkv_internal.cuh"
 
 namespace pkv {
@@ -574,6 +575,7 @@ int rotary_and_cache(void* q_out, const void* q, const void* k, const void* v, v
     auto scale_of = [](float s) { return Scale{s, s > 0x1p-100f && s < 0x1p100f ? 1.f / s : 0.f}; };
     p.k_scale = scale_of(k_scale);
     p.v_scale = scale_of(v_scale);
+    if (checking()) return PKV_OK;
     p.err = error_word();
     if (!p.err) return PKV_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -28,6 +28,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "pkv_check.cuh"
 #include "pkv_internal.cuh"
 
 namespace pkv {
@@ -1334,6 +1335,7 @@ int update_key_bounds(const void* k_pool, void* key_bounds, const int32_t* block
     if (!k_pool || !key_bounds || !block_tables || !seq_lens || !first_changed || !aligned16(k_pool) ||
         !aligned16(key_bounds))
         return PKV_ERR_INVALID_ARG;
+    if (checking()) return PKV_OK;
     int* err = error_word();
     if (!err) return PKV_ERR_CUDA;
     // changed blocks of a sequence (at most one more than the new tokens fill); the
@@ -1387,6 +1389,7 @@ int select_blocks(int32_t* selected, const void* q, const void* key_bounds,
     if (scored && (!workspace || !aligned16(workspace) ||
                    workspace_bytes < select_blocks_workspace_size(num_seqs, num_kv_heads, max_blocks_per_seq)))
         return PKV_ERR_INVALID_ARG;
+    if (checking()) return PKV_OK;
     SelectParams p{};
     p.selected = selected;
     p.q = q;

@@ -4,6 +4,7 @@
 #include <mutex>
 #include <tuple>
 
+#include "pkv_check.cuh"
 #include "pkv_sparse_impl.cuh"
 
 namespace pkv {
@@ -72,6 +73,7 @@ extern "C" int paged_attention_decode_sparse(
         return PKV_ERR_INVALID_ARG;
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(q) || !aligned16(out))
         return PKV_ERR_INVALID_ARG;
+    if (checking()) return PKV_OK;
     sparse::Args a{};
     a.p.out = out;
     a.p.q = q;

@@ -23,11 +23,12 @@ import numpy as np
 import torch
 
 from . import (PKV_ERR_POOL_EXHAUSTED, BlockManager, DecodePipelineStepArgs, PagedKVError, _check,
-               _decode_shapes, _dt, _workspace, bind_paged_decode_step, copy_blocks, key_bounds_dtype,
-               key_bounds_shape, paged_attention_decode, paged_attention_decode_sparse, paged_attention_prefill,
+               PackedCall, _decode_shapes, _dt, _workspace, bind_copy_blocks, bind_paged_attention_decode_sparse,
+               bind_paged_attention_prefill, bind_paged_decode_step, bind_rotary_and_cache, bind_select_blocks,
+               bind_update_key_bounds, copy_blocks, key_bounds_dtype, key_bounds_shape, paged_attention_decode,
                paged_prefill_step, paged_attention_decode_grouped, load_library, paged_attention_workspace_size,
-               pool_shapes, pool_views, reshape_and_cache, rotary_and_cache, select_blocks,
-               select_blocks_workspace_size, swap_blocks, update_key_bounds)
+               pool_shapes, pool_views, reshape_and_cache, select_blocks_workspace_size, swap_blocks,
+               update_key_bounds)
 
 
 @dataclass
@@ -523,27 +524,50 @@ class PagedKVCache:
         n = select_blocks_workspace_size(batch, self.num_kv_heads, max_blocks)
         return torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
 
+    def _bind_append(self, q, k_new, v_new, dev_plan, positions, first, rotary, max_new,
+                     k_scale, v_scale):
+        """The calls of a rotated append, in order, bound."""
+        calls = []
+        if dev_plan["pairs"].shape[0]:
+            calls.append(bind_copy_blocks(self.k_pool, self.v_pool, dev_plan["pairs"]))
+        calls.append(bind_rotary_and_cache(q, q, k_new, v_new, self.k_pool, self.v_pool, dev_plan["slots"],
+                                           positions, rotary.cos_sin, rotary.sections, rotary.interleaved,
+                                           k_scale, v_scale))
+        if self.key_bounds is not None:
+            calls.append(bind_update_key_bounds(self.k_pool, self.key_bounds, dev_plan["tables"],
+                                                dev_plan["lens"], first, max_new))
+        return calls
+
+    @staticmethod
+    def _run_checked(calls, stream):
+        """Every call's arguments are checked before the first one runs: the append
+        turns q in place, so a step that failed behind it could not be tried again."""
+        for c in calls:
+            if isinstance(c, PackedCall):
+                c.check()
+        for c in calls:
+            c(stream)
+
     def _rotated_append(self, q, k_new, v_new, dev_plan, positions, first, rotary, max_new,
                         k_scale, v_scale, stream):
-        if dev_plan["pairs"].shape[0]:
-            copy_blocks(self.k_pool, self.v_pool, dev_plan["pairs"], stream)
-        rotary_and_cache(q, q, k_new, v_new, self.k_pool, self.v_pool, dev_plan["slots"], positions,
-                         rotary.cos_sin, rotary.sections, rotary.interleaved, k_scale, v_scale, stream)
-        if self.key_bounds is not None:
-            update_key_bounds(self.k_pool, self.key_bounds, dev_plan["tables"], dev_plan["lens"], first,
-                              max_new, stream)
+        self._run_checked(self._bind_append(q, k_new, v_new, dev_plan, positions, first, rotary, max_new,
+                                            k_scale, v_scale), stream)
 
     def rotary_prefill_step(self, q, k_new, v_new, dev_plan, positions, first, rotary, out, scale,
                             max_query_len, stream=None):
         """Device half of a chunked-prefill step on keys and queries as the
         projection left them: CoW copies, rotation (q in place) and append, key
         bounds (when kept), causal attention. ``positions``: int32 ``[T]`` or
-        ``[axes, T]``; ``first``: ``first_changed(plan)`` on the device."""
-        self._rotated_append(q, k_new, v_new, dev_plan, positions, first, rotary, max_query_len,
-                             1.0, 1.0, stream)
-        return paged_attention_prefill(out, q, self.k_pool, self.v_pool, dev_plan["tables"],
-                                       dev_plan["lens"], dev_plan["query_start"], scale,
-                                       max_query_len, stream)
+        ``[axes, T]``; ``first``: ``first_changed(plan)`` on the device. k_new and v_new
+        may be views of a fused projection, q has to be contiguous. bfloat16 caches
+        (the prefill attention's). Refused arguments leave q and the cache as they were."""
+        calls = self._bind_append(q, k_new, v_new, dev_plan, positions, first, rotary, max_query_len,
+                                  1.0, 1.0)
+        calls.append(bind_paged_attention_prefill(out, q, self.k_pool, self.v_pool, dev_plan["tables"],
+                                                  dev_plan["lens"], dev_plan["query_start"], scale,
+                                                  max_query_len))
+        self._run_checked(calls, stream)
+        return out
 
     def sparse_step(self, q, k_new, v_new, dev_plan, positions, first, rotary, selected, out, scale,
                     first_blocks=1, last_blocks=1, k_scale=1.0, v_scale=1.0, workspace=None,
@@ -551,14 +575,19 @@ class PagedKVCache:
         """Device half of a decode step that attends over ``selected.shape[2]``
         blocks of each sequence: CoW copies, rotation (q in place) and append, key
         bounds, block choice into ``selected`` (int32 ``[B, Hkv, K]``), attention
-        over the chosen blocks. ``workspace``: ``select_workspace``."""
+        over the chosen blocks. ``workspace``: ``select_workspace`` (None only where
+        nothing is scored: no table wider than ``selected.shape[2]`` blocks, or first and
+        last blocks alone). k_new and v_new may be views of
+        a fused projection, q has to be contiguous. Refused arguments leave q and the cache
+        as they were."""
         self.enable_key_bounds(stream)
-        self._rotated_append(q, k_new, v_new, dev_plan, positions, first, rotary, 1, k_scale, v_scale,
-                             stream)
-        select_blocks(selected, q, self.key_bounds, dev_plan["tables"], dev_plan["lens"],
-                      self.block_size, first_blocks, last_blocks, workspace, stream)
-        return paged_attention_decode_sparse(out, q, self.k_pool, self.v_pool, dev_plan["tables"],
-                                             dev_plan["lens"], selected, scale, k_scale, v_scale, stream)
+        calls = self._bind_append(q, k_new, v_new, dev_plan, positions, first, rotary, 1, k_scale, v_scale)
+        calls += [bind_select_blocks(selected, q, self.key_bounds, dev_plan["tables"], dev_plan["lens"],
+                                     self.block_size, first_blocks, last_blocks, workspace),
+                  bind_paged_attention_decode_sparse(out, q, self.k_pool, self.v_pool, dev_plan["tables"],
+                                                     dev_plan["lens"], selected, scale, k_scale, v_scale)]
+        self._run_checked(calls, stream)
+        return out
 
     def step(self, q, k_new, v_new, dev_plan, out, scale, k_scale=1.0, v_scale=1.0,
              workspace=None, stream=None):

@@ -2,6 +2,7 @@
 goes to and which calls bring the bounds up to date, with the library's calls and the
 streams recorded instead of run."""
 import contextlib
+import ctypes
 
 import numpy as np
 import pytest
@@ -41,6 +42,7 @@ class Recorder:
             monkeypatch.setattr(engine.torch, name, fill)
 
     def call(self, name):
+        """A library call, or a bound one, that records itself."""
         def fn(*a, stream=None, **k):
             self.log.append((name, self.stack[-1] if stream is None else stream, a))
         return fn
@@ -79,7 +81,7 @@ def test_bounds_made_on_first_use_are_filled_on_the_stream_that_uses_them(rec):
     assert [e for e in rec.log if e[1] is not s] == []
 
 
-def step_args(B=2, width=4, K=2):
+def step_args(B=2, width=4, K=3):
     """Host tensors of a sparse step, to be called with the library's calls recorded."""
     plan = {"pairs": torch.zeros(0, 2, dtype=I64), "slots": torch.zeros(B, dtype=I64),
             "tables": torch.zeros(B, width, dtype=I32), "lens": torch.ones(B, dtype=I32)}
@@ -114,12 +116,13 @@ def test_enabling_takes_the_bounds_of_every_block(rec, blocks):
 def test_a_sparse_step_on_a_cache_without_bounds_takes_them_first(rec, monkeypatch):
     s = FakeStream("side")
     cache, a = new_cache(), step_args()
-    monkeypatch.setattr(engine.PagedKVCache, "_rotated_append", lambda self, *x: rec.log.append(("append", s, x)))
-    for name in ("select_blocks", "paged_attention_decode_sparse"):
-        monkeypatch.setattr(engine, name, rec.call(name))
+    for name in ("bind_rotary_and_cache", "bind_update_key_bounds", "bind_select_blocks",
+                 "bind_paged_attention_decode_sparse"):
+        monkeypatch.setattr(engine, name, lambda *x, name=name: rec.call(name[5:]))
     cache.sparse_step(**a, stream=s)
-    order = [e[0] for e in rec.log if e[0] in ("update", "append", "select_blocks")]
-    assert order == ["update", "append", "select_blocks"]
+    order = [e[0] for e in rec.log if e[0] not in ("arange", "full", "zeros", "zeros_like")]
+    assert order == ["update", "rotary_and_cache", "update_key_bounds", "select_blocks",
+                     "paged_attention_decode_sparse"]
     assert set(covered(rec.named("update"))) == set(range(NB))
 
 
@@ -221,3 +224,133 @@ def test_nothing_is_updated_where_no_bounds_are_kept(kept, rec):
     q, kv = torch.zeros(1, HQ, D, dtype=BF), torch.zeros(1, HKV, D, dtype=BF)
     kept.step(q, kv, kv, kept.plan_step([0]).host_tensors(pin=False), torch.empty_like(q), 0.1)
     assert not rec.named("update")
+
+
+# ------------------------------------------------- refused before anything runs
+class Launches:
+    """The library with its packed calls and its block copy recorded, not run."""
+
+    def __init__(self, lib):
+        self.lib, self.ran = lib, []
+
+    def __getattr__(self, name):
+        if name == "pkv_bound_call":
+            return lambda call, addr, n, stream: self.ran.append(call) or 0
+        if name in ("copy_blocks", "paged_attention_prefill"):
+            return lambda *a: self.ran.append(name) or 0
+        return getattr(self.lib, name)
+
+
+@pytest.fixture
+def host_step(monkeypatch):
+    """A cache whose steps take host tensors; what they would launch is recorded."""
+    ran = Launches(library())
+    monkeypatch.setattr(pkv, "load_library", lambda: ran)
+
+    def host(t, what, contiguous=True):                    # the check of the device left out
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+        return t
+
+    monkeypatch.setattr(pkv, "_cuda", host)
+    monkeypatch.setattr(pkv, "_current_device", lambda: 0)
+    monkeypatch.setattr(pkv, "_raw_stream", lambda idx: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: FakeStream("current"))
+    return ran
+
+
+def prefill_args(D=128):
+    """Host tensors of a prompt step of 2 sequences of 3 and 2 tokens."""
+    B, T = 2, 5
+    plan = {"pairs": torch.zeros(1, 2, dtype=I64), "slots": torch.zeros(T, dtype=I64),
+            "tables": torch.zeros(B, 4, dtype=I32), "lens": torch.ones(B, dtype=I32),
+            "query_start": torch.tensor([0, 3, 5], dtype=I32)}
+    q, kv = torch.zeros(T, HQ, D, dtype=BF), torch.zeros(T, HKV, D, dtype=BF)
+    return dict(q=q, k_new=kv, v_new=kv.clone(), dev_plan=plan, positions=torch.zeros(T, dtype=I32),
+                first=torch.zeros(B, dtype=I32), rotary=engine.Rotary(torch.zeros(8, 2, D // 2)),
+                out=torch.empty_like(q), scale=0.1, max_query_len=3)
+
+
+def cache_of(D=D, dtype=BF, bs=BS):
+    c = engine.PagedKVCache(NB, HQ, HKV, D, bs, dtype, range(NB), device="cpu")
+    c.key_bounds = torch.zeros(pkv.key_bounds_shape(NB, HKV, D), dtype=pkv.key_bounds_dtype(dtype))
+    return c
+
+
+WS = torch.zeros(1 << 16, dtype=torch.uint8)
+
+
+def fused(T, D):
+    """q of a fused projection: rows of all heads."""
+    return torch.zeros(T, HQ + 2 * HKV, D, dtype=BF)[:, :HQ]
+
+
+@pytest.mark.parametrize("over", [
+    dict(), dict(q=fused(2, D)), dict(workspace=WS[:64]), dict(workspace=None), dict(first_blocks=3),
+    dict(scale=float("nan")), dict(out=torch.zeros(2, HQ, D)), dict(selected=torch.zeros(2, HQ, 2, dtype=I32)),
+    dict(k_scale=2.0),
+    dict(out=torch.zeros(2 * HQ * D + 1, dtype=BF)[1:].view(2, HQ, D)),       # rows not on 16 bytes
+], ids=lambda o: "-".join(o) or "good")
+def test_a_refused_sparse_step_has_run_nothing(host_step, over):
+    a = step_args()
+    a["dev_plan"]["pairs"] = torch.zeros(1, 2, dtype=I64)
+    a.update(workspace=WS)
+    a.update(over)
+    if not over:
+        cache_of().sparse_step(**a)
+        assert host_step.ran == ["copy_blocks", 0, 1, 2, 3]
+        return
+    with pytest.raises((ValueError, TypeError, pkv.PagedKVError)):
+        cache_of().sparse_step(**a)
+    assert host_step.ran == []
+
+
+@pytest.mark.parametrize("cache,over", [
+    (dict(D=128), dict()), (dict(D=128), dict(q=fused(5, 128))), (dict(D=128), dict(scale=float("inf"))),
+    (dict(D=128), dict(max_query_len=-1)), (dict(D=128), dict(out=torch.zeros(4, HQ, 128, dtype=BF))),
+    (dict(D=128, dtype=torch.uint8), dict()), (dict(D=64), dict()),
+    (dict(D=128), dict(out=torch.zeros(5 * HQ * 128 + 1, dtype=BF)[1:].view(5, HQ, 128))),
+], ids=lambda o: "-".join(f"{k}" for k in o) or "none")
+def test_a_refused_prefill_step_has_run_nothing(host_step, cache, over):
+    """Caches that the prefill attention does not have among them: E4M3, heads of 64."""
+    a = prefill_args(cache["D"])
+    a.update(over)
+    if cache == dict(D=128) and not over:
+        cache_of(**cache).rotary_prefill_step(**a)
+        assert host_step.ran == ["copy_blocks", 0, 1, 4]
+        return
+    with pytest.raises((ValueError, pkv.PagedKVError)):
+        cache_of(**cache).rotary_prefill_step(**a)
+    assert host_step.ran == []
+
+
+def test_checked_calls_return_what_the_calls_return():
+    """pkv_bound_check on good arguments and on one error of each kind, for each call."""
+    lib, f32, at = library(), lambda x: np.float32(x).view(np.uint32).item(), ctypes.addressof
+    sections = (ctypes.c_int32 * 1)(32)
+
+    def check(call, *args):
+        a = (ctypes.c_uint64 * len(args))(*[x & 0xffffffffffffffff for x in args])
+        return lib.pkv_bound_check(call, at(a), len(a))
+
+    P = 0x1000
+    rotary = lambda q=P, R=64, cache=1, ks=1.0: check(
+        0, 0x2000, q, *[P] * 7, at(sections), 1, 256, 256, 128, 128, 3, 4, 2, 64, R, 0, 16, 8, 64, 1, cache,
+        f32(ks), f32(1.0))
+    assert (rotary(), rotary(q=0), rotary(q=P + 8), rotary(R=24), rotary(cache=0), rotary(ks=2.0)) == \
+        (0, -1, -1, -2, -2, -1)
+    bounds = lambda k=P, D=64: check(1, k, *[P] * 4, 3, 5, 8, 2, D, 16, 1, 1)
+    assert (bounds(), bounds(k=0), bounds(D=24)) == (0, -1, -2)
+    select = lambda ws=P, n=1 << 20, D=64: check(2, *[P] * 5, 3, 5, 8, 4, 2, D, 16, 4, 1, 1, 1, ws, n)
+    assert (select(), select(ws=0), select(n=64), select(D=96)) == (0, -1, -1, -2)
+    sparse = lambda q=P, bs=16, kv=1: check(3, P, q, *[P] * 5, 3, 5, 8, 4, 4, 2, 64, bs, f32(0.1), 1, kv, f32(1.0),
+                                            f32(1.0))
+    assert (sparse(), sparse(q=P + 2), sparse(bs=48), sparse(kv=0)) == (0, -1, -2, -2)
+    prefill = lambda q=P, B=3, n=7, Hq=4, D=128, bs=16, kv=1, scale=0.1, kp=P: check(
+        4, P, q, kp, P, P, P, P, B, n, 5, 8, Hq, 2, D, bs, f32(scale), 1, kv)
+    assert (prefill(), prefill(q=0), prefill(q=P + 8), prefill(kp=0), prefill(n=-1), prefill(Hq=3),
+            prefill(scale=float("nan"))) == (0, -1, -1, -1, -1, -1, -1)
+    assert (prefill(D=64), prefill(bs=48), prefill(kv=2)) == (-2, -2, -2)
+    assert (prefill(B=0), prefill(n=0), prefill(B=0, kp=0), prefill(B=0, D=64)) == (0, 0, 0, -2)
+    assert check(4, P) == -1 and check(5, P) == -1 and lib.pkv_bound_check(0, None, 28) == -1

@@ -174,3 +174,46 @@ def test_bounds_follow_a_live_decode_pipeline():
     assert list(lens) == [66, 37, 206]
     check_bounds(c, tables, lens)
     sparse_step(c, ids, rng)
+
+
+def test_a_refused_step_leaves_q_and_the_cache_as_they_were():
+    """q as a view of a fused projection, and a workspace that is too small: refused before
+    q is turned in place, so the step can be tried again."""
+    rng = np.random.default_rng(4)
+    c = new_cache()
+    ids = filled(c, [200, 90], rng)
+    c.enable_key_bounds()
+    plan = c.plan_step(ids, group_prefixes=False)
+    x = values(rng, 2, HQ + 2 * HKV, D).cuda()
+    q, k, v = x.split([HQ, HKV, HKV], 1)
+    sel, out = torch.empty(2, HKV, 4, dtype=I32, device="cuda"), torch.zeros(2, HQ, D, dtype=BF, device="cuda")
+    a = (plan.device_tensors("cuda"), torch.from_numpy((plan.lens - 1).astype(np.int32)).cuda(),
+         torch.from_numpy(engine.first_changed(plan)).cuda(), rotary(), sel, out, D ** -0.5)
+    ws = c.select_workspace(2, plan.tables.shape[1])
+    before = [t.clone() for t in (x, c.k_pool, c.v_pool, c.key_bounds)]
+    for q_, kw in ((q, dict(workspace=ws)), (q.contiguous(), dict(workspace=ws[:64])), (q.contiguous(), {})):
+        keep = q_.clone()
+        with pytest.raises((ValueError, pkv.PagedKVError)):
+            c.sparse_step(q_, k, v, *a, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(q_, keep)
+    assert all(torch.equal(t, b) for t, b in zip((x, c.k_pool, c.v_pool, c.key_bounds), before))
+    q = q.contiguous()
+    c.sparse_step(q, k, v, *a, workspace=ws)               # k and v as views
+    check_bounds(c, plan.tables, plan.lens)
+    assert pkv.get_device_error() == 0 and bool(out.any())
+
+
+def test_a_refused_prompt_step_leaves_q_and_the_cache_as_they_were():
+    rng = np.random.default_rng(5)
+    c = new_cache(cache=U8)                                # the prefill attention has bf16 caches
+    c.load(*(values(rng, c.num_blocks, HKV, BS, D, dtype=F32) for _ in range(2)))
+    c.bm.add_seq(0)
+    plan = c.plan_prefill([0], [40])
+    q, k, v = (values(rng, 40, h, D).cuda() for h in (HQ, HKV, HKV))
+    before = [t.clone() for t in (q, c.k_pool, c.v_pool)]
+    with pytest.raises(pkv.PagedKVError):
+        c.rotary_prefill_step(q, k, v, plan.device_tensors("cuda"), torch.arange(40, dtype=I32, device="cuda"),
+                              torch.zeros(1, dtype=I32, device="cuda"), rotary(), torch.empty_like(q), 0.1, 40)
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, b) for t, b in zip((q, c.k_pool, c.v_pool), before))
