@@ -553,8 +553,10 @@ PKV_API size_t select_blocks_workspace_size(int num_seqs, int num_kv_heads, int 
  * selected blocks alone: query head h of sequence b attends over the positions
  * t < seq_lens[b] whose block t/block_size is listed in selected[b][h/G]:
  *     out[b][h] = v_scale * sum_t softmax(scale * k_scale * <q[b][h], K[t]>)_t * V[t]
- * No listed token (an empty sequence, a list of padding) gives a zero row. With
- * every block listed it is paged_attention_decode's result up to rounding.
+ * No listed token (an empty sequence, a list of padding) gives a zero row, as do
+ * logits that are all -infinity; beside finite ones they have no weight. A logit that
+ * is NaN or +infinity makes its row NaN. With every block listed it is
+ * paged_attention_decode's result up to rounding, for finite logits.
  *
  *   selected      device int32 [num_seqs][num_kv_heads][num_selected]: logical
  *                 blocks, strictly ascending, the rest -1 (select_blocks' output

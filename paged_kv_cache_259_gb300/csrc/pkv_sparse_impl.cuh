@@ -178,6 +178,17 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A maximum that is NaN if an operand is: a NaN logit has to reach its whole row,
+// whichever warp sees it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// What logits are taken relative to: their maximum; 0 where all so far are -infinity, so
+// that their weights are 0 and not the NaN of -infinity less -infinity.
+__device__ __forceinline__ float softmax_base(float m) { return m == -INFINITY ? 0.f : m; }
+
 // 2^x, results below the normal range flushed: such weights vanish in their sum
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -275,11 +286,11 @@ struct HeadsMath {
             }
         }
 #pragma unroll
-        for (int i = 0; i < SUB * 4; ++i) mx = fmaxf(mx, x[i >> 2][(i >> 1) & 1][i & 1]);
+        for (int i = 0; i < SUB * 4; ++i) mx = max_nan(mx, x[i >> 2][(i >> 1) & 1][i & 1]);
         // ---- online softmax, once a tile
-        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-        const float m_new = fmaxf(st.m, mx), alpha = ex2(st.m - m_new);
+        mx = max_nan(mx, __shfl_xor_sync(kFull, mx, 1));
+        mx = max_nan(mx, __shfl_xor_sync(kFull, mx, 2));
+        const float m_new = max_nan(st.m, mx), base = softmax_base(m_new), alpha = ex2(st.m - base);
         float psum = 0.f;
 #pragma unroll
         for (int h = 0; h < SUB; ++h)
@@ -287,7 +298,7 @@ struct HeadsMath {
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    x[h][u][e] = ex2(x[h][u][e] - m_new);
+                    x[h][u][e] = ex2(x[h][u][e] - base);
                     psum += x[h][u][e];
                 }
         st.l = st.l * alpha + psum;
@@ -687,10 +698,10 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
         float M = -INFINITY, sum = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int x = x0; x < active; x += J) M = fmaxf(M, ml_of(x).x);
+        for (int x = x0; x < active; x += J) M = max_nan(M, ml_of(x).x);
 #pragma unroll 1
-        for (int o = 1; o < J; o <<= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        if (M == -INFINITY) M = 0.f;                       // nothing but empty parts
+        for (int o = 1; o < J; o <<= 1) M = max_nan(M, __shfl_xor_sync(kFull, M, o));
+        M = softmax_base(M);                               // nothing but empty parts
 #pragma unroll 4
         for (int x = x0; x < active; x += J) {
             const float2 ml = ml_of(x);
@@ -739,7 +750,7 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
                 float M = -INFINITY, sum = 0.f;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-                for (int x = x0; x <= x1; ++x) M = fmaxf(M, part_of(x)[g]);
+                for (int x = x0; x <= x1; ++x) M = max_nan(M, part_of(x)[g]);
                 if (M != -INFINITY) {
 #pragma unroll 4
                     for (int x = x0; x <= x1; ++x) {
@@ -795,12 +806,12 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
                     o[y] = cluster_ld4(at + (S::kO + 4 * i) * 4);
                 }
 #pragma unroll
-                for (int y = 0; y < kMaxCluster; ++y) M = fmaxf(M, m[y]);
+                for (int y = 0; y < kMaxCluster; ++y) M = max_nan(M, m[y]);
                 if (M != -INFINITY) {
 #pragma unroll
                     for (int y = 0; y < kMaxCluster; ++y) {
-                        const float e = y < n ? exp2f(m[y] - M) : 0.f;
-                        if (e != 0.f) {
+                        if (y < n) {
+                            const float e = exp2f(m[y] - M);
                             sum += e * l[y];
                             add4(v, e, o[y]);
                         }
@@ -898,12 +909,13 @@ int launch(const Args& a) {
     return e == cudaSuccess ? PKV_OK : cuda_fail("sparse decode: kernel launch", e);
 }
 
-// float32 caches: the decode's CUDA-core math with a logit's products in four sums (by
-// the place in the 16-byte chunk) instead of one chain of D / 2 or D: of 128 dims and 32-token
-// blocks the outputs' error against 64 bits falls from 1.1e-6 to half of that.
-template <int D, int BS, int G>
-struct SimtSums : decode::SimtMath<float, float, D, BS, G> {
-    using Base = decode::SimtMath<float, float, D, BS, G>;
+// CUDA-core math: the decode's with a logit's products in four sums (by the place in the
+// 16-byte chunk) instead of one chain of D / 2 or D, and with infinite and NaN logits as
+// above. Of float32 caches with 128 dims and 32-token blocks the outputs' error against 64
+// bits falls from 1.1e-6 to half of that.
+template <typename QT, typename KV, int D, int BS, int G>
+struct SimtSums : decode::SimtMath<QT, KV, D, BS, G> {
+    using Base = decode::SimtMath<QT, KV, D, BS, G>;
     using typename Base::Lay;
     using typename Base::State;
     using Base::CPP;
@@ -915,11 +927,11 @@ struct SimtSums : decode::SimtMath<float, float, D, BS, G> {
     __device__ __forceinline__ static void tile(State& st, const unsigned char* kt, const unsigned char* vt,
                                                 int ntok, int lane, const float* qs, float* pb) {
         const int t = lane % BS, cp = lane / BS;
-        float s4[G][X];
+        float s4[G][4];
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int x = 0; x < X; ++x) s4[g][x] = 0.f;
+            for (int x = 0; x < 4; ++x) s4[g][x] = 0.f;
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             const int j = i * CPP + cp;
@@ -930,7 +942,7 @@ struct SimtSums : decode::SimtMath<float, float, D, BS, G> {
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
                     const float qv = Base::kQRegs ? st.qr[Base::kQRegs ? i * X + x : 0] : qs[g * D + j * X + x];
-                    s4[g][x] = fmaf(qv, kf[x], s4[g][x]);
+                    s4[g][x & 3] = fmaf(qv, kf[x], s4[g][x & 3]);
                 }
         }
         float alpha[G];
@@ -942,10 +954,10 @@ struct SimtSums : decode::SimtMath<float, float, D, BS, G> {
             if (t >= ntok) s = -INFINITY;
             float mx = s;
 #pragma unroll
-            for (int o = BS / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-            const float m_new = fmaxf(st.m[g], mx);        // finite: token 0 is valid
-            alpha[g] = exp2f(st.m[g] - m_new);
-            const float pv = exp2f(s - m_new);
+            for (int o = BS / 2; o >= 1; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(kFull, mx, o));
+            const float m_new = max_nan(st.m[g], mx), base = softmax_base(m_new);
+            alpha[g] = exp2f(st.m[g] - base);
+            const float pv = exp2f(s - base);
             st.m[g] = m_new;
             st.l[g] = st.l[g] * alpha[g] + (cp == 0 ? pv : 0.f);
             if (cp == 0) pb[g * BS + t] = pv;
@@ -969,13 +981,15 @@ struct SimtSums : decode::SimtMath<float, float, D, BS, G> {
                 for (int x = 0; x < X; ++x)
                     if (ch * X + x >= ntok) vf[x] = 0.f;   // unwritten slots
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const float4 pp = *reinterpret_cast<const float4*>(pb + g * BS + ch * X);
-                    st.acc[g][k] = fmaf(pp.x, vf[0], st.acc[g][k]);
-                    st.acc[g][k] = fmaf(pp.y, vf[1], st.acc[g][k]);
-                    st.acc[g][k] = fmaf(pp.z, vf[2], st.acc[g][k]);
-                    st.acc[g][k] = fmaf(pp.w, vf[3], st.acc[g][k]);
-                }
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int x = 0; x < X; x += 4) {
+                        const float4 pp = *reinterpret_cast<const float4*>(pb + g * BS + ch * X + x);
+                        st.acc[g][k] = fmaf(pp.x, vf[x], st.acc[g][k]);
+                        st.acc[g][k] = fmaf(pp.y, vf[x + 1], st.acc[g][k]);
+                        st.acc[g][k] = fmaf(pp.z, vf[x + 2], st.acc[g][k]);
+                        st.acc[g][k] = fmaf(pp.w, vf[x + 3], st.acc[g][k]);
+                    }
             }
         }
         __syncwarp();
@@ -990,8 +1004,8 @@ struct SimtSums : decode::SimtMath<float, float, D, BS, G> {
 // against the output's 2^-8; their tiles of 16 tokens two a stage.
 template <typename QT, typename KV, int D, int BS, int G>
 int launch_heads(const Args& a) {
-    if constexpr (std::is_same<KV, float>::value) return launch<SimtSums<D, BS, G>, QT, D, BS, G, 1>(a);
-    else if constexpr (G == 1 && !std::is_same<KV, uint8_t>::value) return launch<decode::SimtMath<QT, KV, D, BS, 1>, QT, D, BS, 1, 1>(a);
+    if constexpr (std::is_same<KV, float>::value || (G == 1 && !std::is_same<KV, uint8_t>::value))
+        return launch<SimtSums<QT, KV, D, BS, G>, QT, D, BS, G, 1>(a);
     else if constexpr (BS == 16 && std::is_same<KV, uint8_t>::value)
         return launch<HeadsMath<KV, D, 2 * BS, G>, QT, D, 2 * BS, G, 2>(a);
     else return launch<HeadsMath<KV, D, BS, G>, QT, D, BS, G, 1>(a);

@@ -1,0 +1,132 @@
+"""paged_attention_decode_sparse where its arithmetic or its split of the work can go
+wrong: infinite and NaN logits, weights far below the largest, queries outside fp16's
+range, rows shared by several CTAs. Against the definition in float64."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from _lib import library, pkv
+from test_gpu_long_context import BF, F32, I32, U8, f64, rng_of, sparse_case, sparse_gpu, tables_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu_and_library():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU test selected but no CUDA device is visible")
+    library()
+    torch.cuda.set_device(0)
+    pkv.get_device_error()
+
+
+def definition(c):
+    """(out, sum_t p_t |V_t|, largest sum_d |q_d K_td| scale) of a case in float64: logits of
+    -infinity have no weight, a NaN or +infinite one makes the row NaN, no weight at all a
+    zero row."""
+    q, (k, v) = c["q"].double().numpy(), (f64(x).reshape(x.shape) for x in (c["kv"], c["vv"]))
+    B, Hq, D = q.shape
+    Hkv, bs = k.shape[1], c["bs"]
+    ks, vs = float(np.float32(c["ks"])), float(np.float32(c["vs"]))
+    out, mag, logit = np.zeros(q.shape), np.zeros(q.shape), np.zeros((B, Hq))
+    for b, L in enumerate(c["lens"]):
+        for h in range(Hkv):
+            t = [t for j in c["sel"][b, h] if j >= 0 for t in range(j * bs, min(L, (j + 1) * bs))]
+            if not t:
+                continue
+            t = np.array(t)
+            ids = c["tables"][b][t // bs]
+            K, V = k[ids, h, t % bs], v[ids, h, t % bs]
+            for g in range(h * Hq // Hkv, (h + 1) * Hq // Hkv):
+                with np.errstate(invalid="ignore"):
+                    x = (K * q[b, g]).sum(1) * (ks * c["scale"])
+                if np.isnan(x).any() or (x == np.inf).any():
+                    out[b, g] = np.nan
+                    continue
+                fine = np.isfinite(x)
+                if not fine.any():
+                    continue
+                p = np.exp(x[fine] - x[fine].max())
+                p /= p.sum()
+                out[b, g], mag[b, g] = p @ V[fine] * vs, p @ np.abs(V[fine]) * vs
+                logit[b, g] = (np.abs(K[fine]) @ np.abs(q[b, g])).max() * ks * c["scale"]
+    return out, mag, logit
+
+
+def check(c, got):
+    """Logits: sums of D products, (D + 8) roundings of 2^-23 of the magnitudes, in the
+    weight and in their sum; 2^-22 for a power of two and 2^-23 a token and merge for the
+    sums. Weights of tensor-core products are rounded to bf16, 2^-8 of themselves, or to
+    f16, 2^-11 and 2^-25 of the largest. Half a step of the result (2^-8; float32 2^-24)."""
+    ref, mag, logit = definition(c)
+    kind, D, G = c["kind"], ref.shape[-1], c["q"].shape[1] // c["kv"].shape[1]
+    tokens = c["sel"].shape[2] * c["bs"]
+    w = {"f32": 0.0, "bf16": 2.0 ** -8 if G > 1 else 0.0, "e4m3": 2.0 ** -11}[kind]
+    rel = w + 2 * (D + 8) * 2.0 ** -23 * logit[..., None] + (tokens + 64) * 2.0 ** -23 + 2.0 ** -21
+    tiny = tokens * 2.0 ** -25 * 448 * float(np.float32(c["vs"])) if kind == "e4m3" else 0.0
+    half = 2.0 ** -24 if kind == "f32" else 2.0 ** -8
+    err = rel * mag + tiny
+    got = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    fine = ~np.isnan(ref)
+    off, tol = np.abs(got - ref)[fine], (err + half * (np.abs(ref) + err))[fine]
+    assert np.all(off <= tol), f"worst {np.max(off / np.maximum(tol, 1e-300)):.3g} of the tolerance"
+
+
+# ------------------------------------------------------------ infinite and NaN logits
+# rows that one warp holds, that warps of a CTA share, that a cluster shares (few rows: by
+# pushes; many: by its own merge)
+SPLITS = [(1, 2), (3, 9), (2, 40), (1, 130), (70, 40)]
+
+
+def with_keys(kind, G, B, K, bad, where, D=64, bs=16, Hkv=2):
+    """Sequences whose last block holds one token; its key (where = 'last'), the first
+    token's ('first') or all of a middle block's ('block') get ``bad`` in dim 5, which q
+    meets with positive numbers in every head but the first of the last sequence."""
+    c = sparse_case(kind, [(K - 1) * bs + 1] * B, Hkv * G, Hkv, D, bs, K, seed=91)
+    c["q"][:, :, 5] = c["q"][:, :, 5].abs() + 0.25
+    for b in range(B):
+        t = c["tables"][b]
+        if where == "last":
+            c["kv"][t[K - 1], :, 0, 5] = bad
+        elif where == "first":
+            c["kv"][t[0], :, 0, 5] = bad
+        else:
+            c["kv"][t[(K - 1) // 2], :, :, 5] = bad
+    return c
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 4, 8])
+@pytest.mark.parametrize("where", ["last", "first", "block"])
+@pytest.mark.parametrize("B,K", SPLITS)
+def test_keys_at_minus_infinity_have_no_weight(kind, G, where, B, K):
+    c = with_keys(kind, G, B, K, -math.inf, where)
+    c["q"][B - 1, 0, 5] = -1.0                             # +infinity: that row is NaN
+    check(c, sparse_gpu(c))
+    assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 4])
+def test_rows_whose_logits_are_all_minus_infinity_are_zero(kind, G):
+    for B, K in SPLITS[:4]:
+        c = with_keys(kind, G, B, K, -math.inf, "last")
+        c["kv"][c["tables"][0][:K], :, :, 5] = -math.inf
+        got = sparse_gpu(c)
+        assert bool((got[0] == 0).all())
+        check(c, got)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("G", [1, 4, 8])
+@pytest.mark.parametrize("where", ["last", "block"])
+@pytest.mark.parametrize("B,K", SPLITS)
+def test_a_nan_key_makes_its_row_nan(kind, G, where, B, K):
+    c = with_keys(kind, G, B, K, 0x7f if kind == "e4m3" else math.nan, where)
+    if B > 1:                                              # and no other row
+        c["sel"][1] = np.where(np.arange(K) < K // 2 - 1, np.arange(K), -1)
+    check(c, sparse_gpu(c))
+    assert pkv.get_device_error() == 0
