@@ -565,7 +565,8 @@ PKV_API size_t select_blocks_workspace_size(int num_seqs, int num_kv_heads, int 
  *                 padding sets PKV_ERR_OUT_OF_RANGE and is skipped; entries past
  *                 the sequence's number of blocks are not read
  *   the rest      as paged_attention_decode (same supported sizes and types);
- *                 E4M3 caches take the queries in fp16 (magnitudes to 65504)
+ *                 queries of any magnitude (an element below 2^-39 of its head's
+ *                 largest may count as zero beside an E4M3 cache)
  * One launch, no workspace: the CTAs that share a (sequence, kv head) are a
  * thread-block cluster and merge their partial results in shared memory.
  * ---------------------------------------------------------------------- */

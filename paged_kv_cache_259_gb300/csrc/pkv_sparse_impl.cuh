@@ -218,6 +218,7 @@ struct HeadsMath {
         uint32_t qa[KS][2];                                // A fragments of Q (a0, a2)
         float o[MT][4];
         float m, l;                                        // of head r, l this lane's tokens'
+        float qscale;                                      // E4M3: what head r's scores are times
     };
 
     // The values of unwritten slots (ntok and up) may be anything: zero, in place.
@@ -242,6 +243,7 @@ struct HeadsMath {
     __device__ __forceinline__ static void tile(State& st, const unsigned char* kt, const unsigned char* vt, int ntok,
                                                 int lane, float qscale) {
         const int c = lane & 3, mi = lane >> 3, rr = lane & 7;
+        const float by = F8 ? st.qscale : qscale;
         const uint32_t kbase = smem_addr(kt), vbase = smem_addr(vt);
         float x[SUB][2][2], mx = -INFINITY;                // scores of head r
 #pragma unroll
@@ -275,7 +277,7 @@ struct HeadsMath {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) x[h][u][e] = (s[0][u][e] + s[1][u][e]) * qscale;
+                for (int e = 0; e < 2; ++e) x[h][u][e] = (s[0][u][e] + s[1][u][e]) * by;
         }
         if (ntok < BS) {
 #pragma unroll
@@ -371,9 +373,16 @@ struct HeadsMath {
     }
 };
 
+// 2^n, -126 <= n <= 127
+__device__ __forceinline__ float pow2(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }
+
 // The query rows of one (sequence, kv head) into a warp's state. Tensor-core math:
 // straight into the operand fragments; CUDA-core
 // math: through the warp's shared-memory rows, scaled.
+// E4M3 caches multiply in f16: a head's query is brought to f16's upper range by the power
+// of two that takes its largest element into [2^14, 2^15), exactly but for elements below
+// 2^-28 of that (f16 keeps 2^-24, half a step of it 2^-39 of the largest), and its scores
+// are scaled back.
 template <class Math, typename QT, int D, int G>
 __device__ __forceinline__ void begin_row(typename Math::State& st, const QT* q, float qscale, float* qs, int lane) {
     if constexpr (Math::kWarpSmemFloats > 0) {
@@ -384,23 +393,31 @@ __device__ __forceinline__ void begin_row(typename Math::State& st, const QT* q,
     } else {
         const int r = lane >> 2, c = lane & 3;
         const bool live = r < G;
+        if constexpr (Math::F8) {
+            uint2 x[Math::KS];
+            uint32_t top = 0;                              // largest magnitude: bf16 bits order as numbers
 #pragma unroll
-        for (int s = 0; s < Math::KS; ++s) {
-            uint32_t a = 0, b = 0;
-            if constexpr (Math::F8) {
-                if (live) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(q + r * D + 16 * s + 4 * c));
-                    a = decode::pack_f16(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u));
-                    b = decode::pack_f16(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
-                }
-            } else {
-                if (live) {
-                    a = __ldg(reinterpret_cast<const uint32_t*>(q + r * D + 16 * s + 2 * c));
-                    b = __ldg(reinterpret_cast<const uint32_t*>(q + r * D + 16 * s + 8 + 2 * c));
-                }
+            for (int s = 0; s < Math::KS; ++s) {
+                x[s] = live ? __ldg(reinterpret_cast<const uint2*>(q + r * D + 16 * s + 4 * c)) : make_uint2(0, 0);
+                top = __vmaxu2(top, __vmaxu2(x[s].x & 0x7fff7fffu, x[s].y & 0x7fff7fffu));
             }
-            st.qa[s][0] = a;
-            st.qa[s][1] = b;
+            top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(kFull, top, 2));
+            // infinite and NaN elements stay so under any scale; 2^106 is enough for zeros and subnormals
+            const int e = min((int)(max(top & 0xffffu, top >> 16) >> 7), 254) - 127, up = min(14 - e, 106);
+            const float by = pow2(up);
+            st.qscale = qscale * pow2(-up);
+#pragma unroll
+            for (int s = 0; s < Math::KS; ++s) {
+                st.qa[s][0] = decode::pack_f16(__uint_as_float(x[s].x << 16) * by, __uint_as_float(x[s].x & 0xffff0000u) * by);
+                st.qa[s][1] = decode::pack_f16(__uint_as_float(x[s].y << 16) * by, __uint_as_float(x[s].y & 0xffff0000u) * by);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < Math::KS; ++s) {
+                st.qa[s][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + r * D + 16 * s + 2 * c)) : 0u;
+                st.qa[s][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(q + r * D + 16 * s + 8 + 2 * c)) : 0u;
+            }
         }
 #pragma unroll
         for (int i = 0; i < 4 * Math::MT; ++i) st.o[i >> 2][i & 3] = 0.f;

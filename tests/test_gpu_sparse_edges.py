@@ -130,3 +130,30 @@ def test_a_nan_key_makes_its_row_nan(kind, G, where, B, K):
         c["sel"][1] = np.where(np.arange(K) < K // 2 - 1, np.arange(K), -1)
     check(c, sparse_gpu(c))
     assert pkv.get_device_error() == 0
+
+
+# ------------------------------------------------------------ queries of any magnitude
+@pytest.mark.parametrize("gain", [1e-36, 1e-30, 2.0 ** -20, 1e-4, 2e4, 1e6, 1e30])
+@pytest.mark.parametrize("G", [1, 4, 8])
+def test_e4m3_queries_of_any_magnitude(gain, G):
+    """The products run in f16; bf16 queries past 65504 and below 2^-14 keep their bits, each
+    head by its own scale (head 0 is 2^30 times smaller, with its logits near zero)."""
+    for B, K in SPLITS[:4]:
+        c = sparse_case("e4m3", [K * 16 - 5] * B, 2 * G, 2, 64, 16, K, seed=92)
+        c["q"] = (c["q"].float() * gain).to(BF)
+        if G > 1:
+            c["q"][:, 0] = (c["q"][:, 0].float() * 2.0 ** -30).to(BF)
+        c["scale"] = 0.125 / gain
+        check(c, sparse_gpu(c))
+    assert pkv.get_device_error() == 0
+
+
+def test_e4m3_queries_of_mixed_magnitude():
+    """Elements 2^-14 of their head's largest, below f16's normal range as they stand:
+    their keys are the ones that differ."""
+    c = sparse_case("e4m3", [64 * 16], 4, 1, 64, 16, 64, seed=93)
+    c["q"] = c["q"] * 2.0 ** -24
+    c["q"][:, :, 7] = 2.0 ** -10
+    c["kv"][:, :, :, 7] = 0x38                             # 1.0 in every key
+    c["scale"] = 2.0 ** 16 / c["ks"]
+    check(c, sparse_gpu(c))
