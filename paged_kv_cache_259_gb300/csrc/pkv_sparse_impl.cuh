@@ -189,6 +189,27 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // that their weights are 0 and not the NaN of -infinity less -infinity.
 __device__ __forceinline__ float softmax_base(float m) { return m == -INFINITY ? 0.f : m; }
 
+// Two weights as 16-bit numbers, and what that rounding left of each as two more: hi + lo
+// is a weight up to 2^-16 of itself in bf16 (2^-8 twice), in f16 up to 2^-22 (2^-11 twice)
+// and half of f16's smallest step, 2^-25. Both go through the product, so the output is
+// that of float32 weights but for its own rounding, and their sum, of float32 weights, is
+// theirs. (A second product a tile: 64 sequences x 128 blocks of 128 dims, E4M3 46.0 us
+// without and 46.0 with it, 8 heads a kv head 48.3 and 50.0; bf16 83 and 84.5; 64 dims in
+// E4M3 blocks of 32 tokens 44.1 and 47.7; 1 sequence 6.0 and 6.25. What is left over in the
+// columns of absent heads instead, for up to 4: 46.8, -, 85.5, 46.8, 6.15.)
+template <bool F16>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(x, y);
+        const float2 f = __half22float2(h);
+        hi = *reinterpret_cast<const uint32_t*>(&h);
+        lo = decode::pack_f16(x - f.x, y - f.y);
+    } else {
+        hi = decode::pack_bf16(x, y);
+        lo = decode::pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+    }
+}
+
 // 2^x, results below the normal range flushed: such weights vanish in their sum
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -212,6 +233,9 @@ struct HeadsMath {
     static constexpr bool F8 = std::is_same<KV, uint8_t>::value;
     static constexpr int KS = D / 16, MT = D / 16, SUB = BS / 16;
     static constexpr int kWarpSmemFloats = 0;
+    // weights are 2^kLift times themselves, and so are their sums: E4M3 caches take them in
+    // f16, whose smallest step is then 2^-38 of the largest weight instead of 2^-24
+    static constexpr float kLift = F8 ? 14.f : 0.f;
     static_assert(G >= 1 && G <= 8 && BS % 16 == 0 && D % 32 == 0, "mma shape");
 
     struct State {
@@ -300,7 +324,7 @@ struct HeadsMath {
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    x[h][u][e] = ex2(x[h][u][e] - base);
+                    x[h][u][e] = ex2(x[h][u][e] - base + kLift);
                     psum += x[h][u][e];
                 }
         st.l = st.l * alpha + psum;
@@ -317,8 +341,9 @@ struct HeadsMath {
         }
 #pragma unroll
         for (int h = 0; h < SUB; ++h) {
-            const uint32_t p0 = F8 ? decode::pack_f16(x[h][0][0], x[h][0][1]) : decode::pack_bf16(x[h][0][0], x[h][0][1]);
-            const uint32_t p1 = F8 ? decode::pack_f16(x[h][1][0], x[h][1][1]) : decode::pack_bf16(x[h][1][0], x[h][1][1]);
+            uint32_t p0, p1, r0, r1;
+            split_pair<F8>(x[h][0][0], x[h][0][1], p0, r0);
+            split_pair<F8>(x[h][1][0], x[h][1][1], p1, r1);
             uint32_t v8[4];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -338,6 +363,7 @@ struct HeadsMath {
                                     a[1][0], a[1][1]);
                 }
                 mma<F8>(st.o[i], a[0][0], a[1][0], a[0][1], a[1][1], p0, p1);
+                mma<F8>(st.o[i], a[0][0], a[1][0], a[0][1], a[1][1], r0, r1);
             }
         }
     }
@@ -1015,10 +1041,9 @@ struct SimtSums : decode::SimtMath<QT, KV, D, BS, G> {
 
 // float32 caches on CUDA cores, as in the decode; bf16 caches on the tensor cores for 2, 4,
 // 8 query heads a kv head, on CUDA cores for one, whose weights then stay float32 (1280
-// rows of 64 blocks: 94.5 us, 0.96 of the copy rate; 91.8 on the tensor cores, which would
-// round them to bf16); E4M3 caches on the tensor cores, for one head too (512 rows of 128
-// blocks: 56.0 us on CUDA cores, 47.0 so), the weights rounded to f16, 2^-11 of themselves
-// against the output's 2^-8; their tiles of 16 tokens two a stage.
+// rows of 64 blocks: 94.5 us, 0.96 of the copy rate; 91.8 on the tensor cores with weights
+// of one bf16 number); E4M3 caches on the tensor cores, for one head too (512 rows of 128
+// blocks: 56.0 us on CUDA cores, 45.5 so); their tiles of 16 tokens two a stage.
 template <typename QT, typename KV, int D, int BS, int G>
 int launch_heads(const Args& a) {
     if constexpr (std::is_same<KV, float>::value || (G == 1 && !std::is_same<KV, uint8_t>::value))

@@ -58,14 +58,15 @@ def definition(c):
 def check(c, got):
     """Logits: sums of D products, (D + 8) roundings of 2^-23 of the magnitudes, in the
     weight and in their sum; 2^-22 for a power of two and 2^-23 a token and merge for the
-    sums. Weights of tensor-core products are rounded to bf16, 2^-8 of themselves, or to
-    f16, 2^-11 and 2^-25 of the largest. Half a step of the result (2^-8; float32 2^-24)."""
+    sums. Weights of tensor-core products are two 16-bit numbers: 2^-16 of themselves off
+    in bf16, 2^-22 in f16 and, lifted by 2^14, 2^-39 of the largest. Half a step of the
+    result (2^-8; float32 2^-24)."""
     ref, mag, logit = definition(c)
     kind, D, G = c["kind"], ref.shape[-1], c["q"].shape[1] // c["kv"].shape[1]
     tokens = c["sel"].shape[2] * c["bs"]
-    w = {"f32": 0.0, "bf16": 2.0 ** -8 if G > 1 else 0.0, "e4m3": 2.0 ** -11}[kind]
+    w = {"f32": 0.0, "bf16": 2.0 ** -16 if G > 1 else 0.0, "e4m3": 2.0 ** -22}[kind]
     rel = w + 2 * (D + 8) * 2.0 ** -23 * logit[..., None] + (tokens + 64) * 2.0 ** -23 + 2.0 ** -21
-    tiny = tokens * 2.0 ** -25 * 448 * float(np.float32(c["vs"])) if kind == "e4m3" else 0.0
+    tiny = tokens * 2.0 ** -39 * 448 * float(np.float32(c["vs"])) if kind == "e4m3" else 0.0
     half = 2.0 ** -24 if kind == "f32" else 2.0 ** -8
     err = rel * mag + tiny
     got = got.double().cpu().numpy()
@@ -156,4 +157,38 @@ def test_e4m3_queries_of_mixed_magnitude():
     c["q"][:, :, 7] = 2.0 ** -10
     c["kv"][:, :, :, 7] = 0x38                             # 1.0 in every key
     c["scale"] = 2.0 ** 16 / c["ks"]
+    check(c, sparse_gpu(c))
+
+
+# ------------------------------------------------------------------------ weights
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("bits", [9, 14.4, 20, 25.4, 30])
+def test_a_flat_tail_of_small_weights_counts(kind, G, bits):
+    """One token of weight 1 with values 0 beside tokens of 2^-bits with values 448, and
+    half of them with 1 - 2^-8 of that: the output is the tail alone."""
+    for K in (3, 64, 130):
+        c = sparse_case(kind, [K * 32] * 2, 2 * G, 2, 64, 32, K, seed=94)
+        one, top = (0x38, 0x7e) if kind == "e4m3" else (1.0, 448.0)
+        c["kv"].fill_(0)
+        c["vv"].fill_(top)
+        c["vv"][:, :, ::2] = 0x7d if kind == "e4m3" else 446.0
+        c["q"].zero_()
+        c["q"][:, :, 3] = 1.0
+        c["ks"] = c["vs"] = 1.0
+        c["scale"] = bits * math.log(2.0)
+        first = c["tables"][:, 0]
+        c["kv"][first, :, 5, 3], c["vv"][first, :, 5] = one, 0
+        check(c, sparse_gpu(c))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G", [2, 4, 8])
+def test_weights_are_those_of_float32(kind, G):
+    """Values that cancel: tokens of +448 and -448 in turn under nearly equal weights, so
+    that the output is far smaller than the values and weights of one 16-bit number would
+    be off by more than everything else allows."""
+    c = sparse_case(kind, [32] * 64, 2 * G, 2, 128, 16, 2, seed=95, qgain=0.05)
+    top = (0x7e, 0xfe) if kind == "e4m3" else (448.0, -448.0)
+    c["vv"][:, :, ::2], c["vv"][:, :, 1::2] = top
     check(c, sparse_gpu(c))
