@@ -19,8 +19,11 @@
 // that of the exact scores: the float32 scores s' are off by at most E (below),
 // so with T the k-th largest s', a block with s' > T + 2E is in, one with s' <
 // T - 2E is out, and only if the window between holds more blocks than places
-// left are those few scored again in 64 bits and ranked, equal scores by the
-// lower index.
+// left are those few scored again, as 64-bit whole numbers of 2^-51 of the row's largest
+// magnitudes, and ranked, equal scores by the lower index. Where terms had more bits
+// than that and scores lie within their roundings of the last place, those blocks'
+// scores are compared as whole numbers of 1024 bits. (What the look at the last place
+// costs rows that need no more: 4 rows of 63 blocks 4.96 -> 5.2 us, 8 of 8,192 13.5 -> 14.0.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -533,10 +536,6 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t k) {
     return __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
 }
-__device__ __forceinline__ unsigned long long ordered64(double x) {
-    const unsigned long long u = __double_as_longlong(x);
-    return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
-}
 
 // 2^(127 - e) for the biased exponent e of a finite float: brings it into [1, 2)
 // (below 1 if it is subnormal).
@@ -548,44 +547,55 @@ __device__ __forceinline__ float unit_scale(float x) {
 // What a term leaves of itself in three exact float32 sums: x is cut at 2^-19, the
 // rest at 2^-35, the rest of that at 2^-51 (adding and subtracting 1.5 x 2^23 units
 // rounds to the unit). With sums of magnitudes below 4 every sum is a whole number
-// of its unit below 2^24, so it is exact in any order.
-__device__ __forceinline__ void add_exact(float (&s)[3], float x) {
+// of its unit below 2^24, so it is exact in any order. Returns what is left.
+__device__ __forceinline__ float add_exact(float (&s)[3], float x) {
     const float a = __fadd_rn(__fadd_rn(x, 24.f), -24.f);
     s[0] = __fadd_rn(s[0], a);
     x = __fadd_rn(x, -a);
     const float b = __fadd_rn(__fadd_rn(x, 0x1.8p-12f), -0x1.8p-12f);
     s[1] = __fadd_rn(s[1], b);
     x = __fadd_rn(x, -b);
-    s[2] = __fadd_rn(s[2], __fadd_rn(__fadd_rn(x, 0x1.8p-28f), -0x1.8p-28f));
+    const float c = __fadd_rn(__fadd_rn(x, 0x1.8p-28f), -0x1.8p-28f);
+    s[2] = __fadd_rn(s[2], c);
+    return __fadd_rn(x, -c);
 }
 
-// The score of a block (row `id_row` of the bounds) under heads g0 .. g1-1 (rows
+// The score of a block (row `id_row` of the bounds) under the heads of `heads` (rows
 // of `qs`, float32 in shared memory) in 64 bits, as an ordered key above 0 (the
 // whole warp). The query times scale_q and the bounds times scale_b make a score's
 // magnitudes sum to less than 4; its terms, exact products (float32 inputs: with
-// the rest of the product), are summed exactly down to 2^-51. (In float64, at two
-// multiply-adds a clock per SM, a block with 8 heads took 3 us.)
-template <typename T>
+// the rest of the product), are summed exactly down to 2^-51; MORE: *vague is set where one has
+// bits below that. (In float64, at two multiply-adds a clock per SM, a block with 8 heads
+// took 3 us. Looking for lower bits costs a choice of 64 blocks 0.3 us, float32 0.8, so it
+// is left until keys lie too close to tell without.)
+template <typename T, bool MORE>
 __device__ __forceinline__ unsigned long long exact_key(const T* bounds, size_t id_row, int d, const float* qs,
-                                                        int g0, int g1, int lane, float scale_q, float scale_b) {
+                                                        unsigned heads, int lane, float scale_q, float scale_b,
+                                                        int* vague) {
     const T* bl = bounds + id_row * 2 * d + lane;
     float lo[4], hi[4];                                     // d is 64 or 128
+    bool more = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        lo[i] = 32 * i < d ? (float)bl[32 * i] * scale_b : 0.f;
-        hi[i] = 32 * i < d ? (float)bl[d + 32 * i] * scale_b : 0.f;
+        const float l = 32 * i < d ? (float)bl[32 * i] : 0.f, u = 32 * i < d ? (float)bl[d + 32 * i] : 0.f;
+        lo[i] = l * scale_b;
+        hi[i] = u * scale_b;
+        if constexpr (MORE) more |= (lo[i] == 0.f && l != 0.f) || (hi[i] == 0.f && u != 0.f);
     }
     unsigned long long best = 0;
-    for (int g = g0; g < g1; ++g) {
+    for (; heads; heads &= heads - 1) {
+        const int g = __ffs(heads) - 1;
         float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (32 * i >= d) break;
-            const float q = qs[g * d + lane + 32 * i] * scale_q;
-            const float x = q < 0.f ? lo[i] : hi[i];
-            const float t = __fmul_rn(q, x);
-            add_exact(s, t);
-            if constexpr (std::is_same<T, float>::value) add_exact(s, __fmaf_rn(q, x, -t));
+            const float q = qs[g * d + lane + 32 * i], u = q * scale_q;
+            const float x = u < 0.f ? lo[i] : hi[i];
+            const float t = __fmul_rn(u, x);
+            float rest = add_exact(s, t);
+            if constexpr (std::is_same<T, float>::value) rest = fabsf(rest) + fabsf(add_exact(s, __fmaf_rn(u, x, -t)));
+            // what float32's range cuts off leaves something, unless it leaves nothing at all
+            if constexpr (MORE) more |= rest != 0.f || (t == 0.f && q != 0.f && x != 0.f);
         }
         const long long i0 = __reduce_add_sync(kFull, (int)(s[0] * 0x1p19f));
         const long long i1 = __reduce_add_sync(kFull, (int)(s[1] * 0x1p35f));
@@ -593,32 +603,179 @@ __device__ __forceinline__ unsigned long long exact_key(const T* bounds, size_t 
         const long long sum = i0 * (1ll << 32) + i1 * (1ll << 16) + i2;
         best = max(best, (unsigned long long)sum ^ (1ull << 63));
     }
+    if constexpr (MORE)
+        if (__any_sync(kFull, more) && lane == 0) *vague = 1;
     return best;
 }
-// The same in float64, for rows with values that are not finite: a block that no
-// finite score describes comes first.
+
+// How far a key of terms with lower bits can be off: half a unit a term (float32: two terms
+// a product), and one for what float32's range cut off.
 template <typename T>
-__device__ unsigned long long exact_key_f64(const SelectParams& p, int b, int h, int id, int lane) {
-    const int G = p.hq / p.hkv, d = p.d;
-    const T* bl = static_cast<const T*>(p.bounds) + ((size_t)id * p.hkv + h) * 2 * d;
-    double best = -INFINITY;
-    bool nan = false;
-    for (int g = 0; g < G; ++g) {
-        const T* qr = static_cast<const T*>(p.q) + ((size_t)b * p.hq + h * G + g) * d;
+__device__ __forceinline__ unsigned long long key_error(int d) {
+    return (std::is_same<T, float>::value ? d : d / 2) + 1;
+}
+
+// Whether a block's score is not finite, in rows with values that are not: some head's
+// is NaN or +infinity, or none is finite. Heads of finite queries are finite on all other
+// blocks. In float64, whose range no sum of these products leaves.
+template <typename T>
+__device__ __noinline__ bool score_not_finite(const T* bounds, size_t id_row, int d, const float* qs, int heads, int lane) {
+    const T* bl = bounds + id_row * 2 * d;
+    bool top = false, some = false;
+    for (int g = 0; g < heads; ++g) {
         double s = 0.0;
         for (int i = lane; i < d; i += 32) {
-            const double q = (double)(float)qr[i];
+            const double q = (double)qs[g * d + i];
             const double neg = q > 0.0 ? 0.0 : q, pos = q < 0.0 ? 0.0 : q;   // NaN stays
             s = fma(neg, (double)(float)bl[i], s);
             s = fma(pos, (double)(float)bl[d + i], s);
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-        nan |= s != s;
-        best = s > best ? s : best;
+        top |= !(s < INFINITY);
+        some |= fabs(s) < INFINITY;
     }
-    if (nan || !(fabs(best) < INFINITY)) best = INFINITY;
-    return ordered64(best + 0.0);
+    return top || !some;
+}
+
+// m 2^(e) for a finite float, m below 2^24
+__device__ __forceinline__ void take_apart(float x, uint32_t& m, int& e) {
+    const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+    const int field = (int)(u >> 23);
+    m = (u & 0x7fffffu) | (field ? 0x800000u : 0u);
+    e = max(field, 1) - 150;
+}
+
+// A finite block's score with every bit: a whole number of 2^-320 in two's complement,
+// lane l of the warp holding bits 32 l .. 32 l + 31 (the top one biased, so that the
+// lanes' words compare as unsigned from the highest down). A product of two floats is
+// below 2^48 times 2^-298 to 2^208, so a sum fits with room to spare.
+template <typename T>
+__device__ __forceinline__ uint32_t score_word(const T* bounds, size_t id_row, int d, const float* qs, unsigned heads,
+                                               int lane) {
+    const T* bl = bounds + id_row * 2 * d;
+    uint32_t best = 0;                                     // below every number
+#pragma unroll 1
+    for (; heads; heads &= heads - 1) {
+        const float* qr = qs + (__ffs(heads) - 1) * d;
+        long long sum = 0;                                 // of the terms' words here: 128 of them
+#pragma unroll 1
+        for (int i = lane; i < d; i += 32) {
+            const float q = qr[i], x = (float)bl[q < 0.f ? i : d + i];
+            uint32_t mq, mx;
+            int eq, ex;
+            take_apart(q, mq, eq);
+            take_apart(x, mx, ex);
+            const unsigned long long m = (unsigned long long)mq * mx;
+            const int at = (eq + ex + 320) | ((__float_as_uint(q) ^ __float_as_uint(x)) & 0x80000000u ? 1 << 16 : 0);
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j) {
+                const unsigned long long mj = __shfl_sync(kFull, m, j);
+                const int a = __shfl_sync(kFull, at, j), k = lane - ((a & 0xffff) >> 5), bit = a & 31;
+                uint32_t word = 0;
+                if (k == 0) word = (uint32_t)(mj << bit);
+                if (k == 1) word = (uint32_t)(mj >> (32 - bit));
+                if (k == 2 && bit > 0) word = (uint32_t)(mj >> (64 - bit));
+                sum += a >> 16 ? -(long long)word : (long long)word;
+            }
+        }
+        uint32_t word = 0;
+        long long carry = 0;
+#pragma unroll 1
+        for (int j = 0; j < 32; ++j) {
+            const long long v = __shfl_sync(kFull, sum, j) + carry;
+            if (lane == j) word = (uint32_t)v;
+            carry = v >> 32;
+        }
+        if (lane == 31) word ^= 0x80000000u;
+        if (__ballot_sync(kFull, word > best) > __ballot_sync(kFull, word < best)) best = word;
+    }
+    return best;
+}
+
+// The `left` blocks of the highest scores among those of `cand`, equal ones by the lower
+// index, into `sel` (bitmaps; the whole CTA). Each round compares every candidate with one
+// of them, exactly, and keeps those above or those below it; the round's one lies in the
+// middle of the candidates by index first, then at changing places. `mark`: a word per
+// block for the comparisons' results. Rare, and out of the way of the code that is not.
+template <typename T, int NT>
+__device__ __forceinline__ void settle(const T* bounds, const int32_t* table, int hkv, int h, int d, const float* qs,
+                                    unsigned heads, int lo, int hi, int left, unsigned char* sel, unsigned char* cand,
+                                    unsigned long long* mark) {
+    constexpr int NW = NT / 32;
+    __shared__ uint32_t pivot[32], part[NW];
+    __shared__ int where;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, c0 = lo / 8, c1 = (hi + 7) / 8;
+    auto total = [&](uint32_t v) -> int {
+        v = __reduce_add_sync(kFull, v);
+        __syncthreads();
+        if (lane == 0) part[w] = v;
+        __syncthreads();
+        return (int)__reduce_add_sync(kFull, lane < NW ? part[lane] : 0u);
+    };
+    // exclusive prefix over the threads
+    auto under = [&](uint32_t v) -> int {
+        uint32_t incl = v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += t;
+        }
+        __syncthreads();
+        if (lane == 31) part[w] = incl;
+        __syncthreads();
+        return (int)(__reduce_add_sync(kFull, lane < w ? part[lane] : 0u) + incl - v);
+    };
+    const int per = (c1 - c0 + NT - 1) / NT;               // bytes of the bitmaps a thread owns, in order
+    const int b0 = min(c1, c0 + tid * per), b1 = min(c1, b0 + per);
+    for (uint32_t round = 0; left > 0; ++round) {
+        __syncthreads();
+        uint32_t mine = 0;
+        for (int c = b0; c < b1; ++c) mine += __popc(cand[c]);
+        const int count = total(mine);
+        if (count <= left) {
+            for (int c = b0; c < b1; ++c) sel[c] |= cand[c];
+            break;
+        }
+        // the candidate to compare with
+        const int rank = (int)(((unsigned long long)(round * 0x9e3779b9u + 0x80000000u) * (uint32_t)count) >> 32);
+        int at = under(mine);
+        for (int c = b0; c < b1; ++c)
+            for (uint32_t m = cand[c]; m; m &= m - 1, ++at)
+                if (at == rank) where = 8 * c + __ffs(m) - 1;
+        __syncthreads();
+        if (w == 0) pivot[lane] = score_word(bounds, (size_t)table[where] * hkv + h, d, qs, heads, lane);
+        __syncthreads();
+        for (int blk = 8 * c0 + w; blk < 8 * c1; blk += NW)
+            if ((cand[blk >> 3] >> (blk & 7)) & 1) {
+                const uint32_t x = score_word(bounds, (size_t)table[blk] * hkv + h, d, qs, heads, lane), y = pivot[lane];
+                const unsigned up = __ballot_sync(kFull, x > y), dn = __ballot_sync(kFull, x < y);
+                if (lane == 0) mark[blk] = up > dn ? 2 : up < dn ? 0 : 1;
+            }
+        __syncthreads();
+        uint32_t more = 0, same = 0;
+        for (int c = b0; c < b1; ++c)
+            for (uint32_t m = cand[c]; m; m &= m - 1) {
+                const int r = (int)mark[8 * c + __ffs(m) - 1];
+                more += r == 2;
+                same += r == 1;
+            }
+        const int above = total(more), equal = total(same);
+        int rest = left - above, first = under(same);      // places for the equal ones; how many lie before
+        for (int c = b0; c < b1; ++c) {
+            uint32_t in = 0, keep = 0;
+            for (uint32_t m = cand[c]; m; m &= m - 1) {
+                const uint32_t bit = m & -m;
+                const int r = (int)mark[8 * c + __ffs(m) - 1];
+                if (above >= left) keep |= r == 2 ? bit : 0u;
+                else if (r == 2 || (r == 1 && first++ < rest)) in |= bit;
+                else if (r == 0) keep |= bit;
+            }
+            sel[c] |= in;
+            cand[c] = above + equal >= left && above < left ? 0 : keep;
+        }
+        if (above < left) left = max(0, rest - equal);
+    }
+    __syncthreads();
 }
 
 constexpr int kBins = 1024;
@@ -717,8 +874,8 @@ __device__ __forceinline__ void score_row(const SelectParams& p, int b, int h, i
 // score range is cut into 1,024 equal bins; the bin of the last place and its
 // neighbours within the rounding window hold the few blocks that are undecided (the
 // range is cut again when they are too many), which are ranked among themselves: by
-// their float32 scores, and those within the window of the last place by their 64-bit
-// scores if there are more of them than places. A bin of a score is a monotone function
+// their float32 scores, those within the window of the last place by their 64-bit scores
+// if there are more of them than places, and what those cannot tell by every bit. A bin of a score is a monotone function
 // of it, so bins decide soundly whatever the rounding of their edges.
 // Rows of no more blocks than threads have one to a thread.
 // Bound: latency and, with 32 warps, issue: about 13,000 clocks of dependent steps for
@@ -755,8 +912,9 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
     unsigned char* sel8 = reinterpret_cast<unsigned char*>(sel);
     unsigned char* cand8 = reinterpret_cast<unsigned char*>(cand);
     __shared__ uint32_t sh_a[NW], sh_b[NW], sh_c[NW], sh_q[NW], sh_m[NW];
-    __shared__ int sh_bin, sh_cnt, sh_likely, sh_win[2];
+    __shared__ int sh_bin, sh_cnt, sh_likely, sh_vague, sh_win[2];
     __shared__ float sh_thr;
+    __shared__ unsigned long long sh_key[2];
 
     const int lo = p.first, hi = n - p.last;               // scored blocks
     const int need = p.k - p.first - p.last;               // 0 <= need < hi - lo
@@ -807,7 +965,7 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
         }
         for (int i = tid; i < kBins; i += NT) hist[i] = 0;
         for (int c = tid; c < chunks; c += NT) sel8[c] = (unsigned char)forced_of(c);
-        if (tid == 0) sh_cnt = 0, sh_likely = 0, sh_win[0] = 0, sh_win[1] = 0;
+        if (tid == 0) sh_cnt = 0, sh_likely = 0, sh_vague = 0, sh_win[0] = 0, sh_win[1] = 0;
         if (p.scored) wait_prerequisites();
         if constexpr (FD > 0) {
             score_row<FD, NW>(p, b, h, lo, hi, own_scores, own_max);
@@ -895,7 +1053,8 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
         const float win = 2.02f * E;                       // 2E, and the rounding of what it is added to
         const bool sane = A < 1e37f;                       // false for NaN too
         const bool finite = qm < INFINITY && mm < INFINITY;
-        const float scale_q = unit_scale(qm), scale_b = unit_scale(mm);   // for exact_key
+        float scale_q = unit_scale(qm), scale_b = unit_scale(mm);   // for exact_key
+        unsigned heads = (1u << G) - 1;                    // whose scores are finite
 
         // what could still be undecided lies within the window of that score
         const bool bounded = !KEEP && !single && r <= kMaxRounds && kth > ordered(-INFINITY);
@@ -1082,6 +1241,8 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
             left = need;
         }
         __syncthreads();
+        int open = 0;                                      // places among `cand` that keys cannot tell
+        const int32_t* table = p.tables + (size_t)b * p.max_blocks;
         const int listed = sh_cnt;
         if (listed > 0) {
             // ---- the list: `left` of its blocks are selected
@@ -1122,14 +1283,15 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
                 // a warp takes a block and as few heads as there are warps for
                 int bits = 0;
                 while ((2 << bits) <= G && (2 << bits) * listed <= NW) ++bits;
-                const int heads = (G + (1 << bits) - 1) >> bits;
+                const int some = (G + (1 << bits) - 1) >> bits;
                 for (int i = w; i < listed << bits; i += NW) {
-                    const int e = i >> bits, g0 = (i & ((1 << bits) - 1)) * heads;
+                    const int e = i >> bits, g0 = (i & ((1 << bits) - 1)) * some;
                     const float s = list_s[e];
                     // an id that is not good has a score only if the scoring kernel gave up
                     if (s <= up && s >= dn && g0 < G && (unsigned)list_row[e] < (unsigned)p.num_blocks) {
-                        const unsigned long long k = exact_key(bounds, (size_t)list_row[e] * p.hkv + h, d, qf, g0,
-                                                               min(G, g0 + heads), lane, scale_q, scale_b);
+                        const unsigned mine = heads & (((1u << some) - 1) << g0);
+                        const unsigned long long k = exact_key<T, false>(bounds, (size_t)list_row[e] * p.hkv + h, d, qf,
+                                                                         mine, lane, scale_q, scale_b, nullptr);
                         if (lane == 0) atomicMax(&list_key[e], k);
                     }
                 }
@@ -1152,8 +1314,39 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
                         before += __popc(__ballot_sync(kFull, ahead));
                     }
                     take = before < left;
+                    if (lane == 0 && before == left - 1) sh_key[0] = k;
+                    if (lane == 0 && before == left) sh_key[1] = k;
                 }
                 if (take && lane == 0) atomicOr(&sel[id >> 5], 1u << (id & 31));
+            }
+            if (crowded) {
+                __syncthreads();
+                // ---- the last place's key and the first one's behind it: within the keys' errors?
+                const unsigned long long last = sh_key[0], reach = 2 * key_error<T>(d);
+                if (last - sh_key[1] <= reach && sh_key[1] != 0) {
+                    auto near = [&](int i) {
+                        const unsigned long long k = list_key[i];
+                        return list_s[i] <= up && list_s[i] >= dn && k + reach >= last && k <= last + reach;
+                    };
+                    if (tid == 0) sh_cnt = 0;
+                    for (int c = tid; c < chunks; c += NT) cand8[c] = 0;
+                    for (int i = w; i < listed; i += NW)
+                        if (near(i))
+                            exact_key<T, true>(bounds, (size_t)list_row[i] * p.hkv + h, d, qf, heads, lane, scale_q, scale_b,
+                                               &sh_vague);
+                    __syncthreads();
+                    if (sh_vague) {                        // (keys without lower bits are the scores)
+                        for (int i = tid; i < listed; i += NT)
+                            if (near(i)) {
+                                const int id = list_id[i];
+                                const uint32_t bit = 1u << (id & 31);
+                                if (atomicAnd(&sel[id >> 5], ~bit) & bit) atomicAdd(&sh_cnt, 1);
+                                atomicOr(&cand[id >> 5], bit);
+                            }
+                        __syncthreads();
+                        open = sh_cnt;                     // the places they had
+                    }
+                }
             }
         } else if (crowd) {
             // ---- a crowd (many equal scores, or none finite): 64-bit keys to the
@@ -1167,13 +1360,47 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
                 __syncthreads();
                 return (int)__reduce_add_sync(kFull, lane < NW ? sh_a[lane] : 0u);
             };
+            if (!finite) {
+                // ---- blocks whose score is not finite come first; the others are scaled by the
+                // largest of their bounds and of the finite heads' queries (times d: no sum
+                // of them passes float32's range)
+                if (tid == 0) sh_win[0] = sh_win[1] = 0, sh_cnt = 0;
+                __syncthreads();
+                if (w < G) {
+                    uint32_t top = 0;
+                    for (int i = lane; i < d; i += 32) top = max(top, __float_as_uint(qf[w * d + i]) & 0x7fffffffu);
+                    top = __reduce_max_sync(kFull, top);
+                    if (lane == 0 && top < 0x7f800000u) atomicOr(&sh_cnt, 1 << w), atomicMax(&sh_win[0], (int)top);
+                }
+                for (int blk = lo + w; blk < hi; blk += NW)
+                    if (is_cand(blk)) {
+                        const int id = table[blk];
+                        if (id < 0 || id >= p.num_blocks) continue;
+                        const size_t id_row = (size_t)id * p.hkv + h;
+                        const bool first = score_not_finite(bounds, id_row, d, qf, G, lane);
+                        if (lane == 0) key[blk] = first ? ~0ull : 0ull;
+                        if (first) continue;
+                        uint32_t top = 0;
+                        for (int i = lane; i < 2 * d; i += 32)
+                            top = max(top, __float_as_uint((float)bounds[id_row * 2 * d + i]) & 0x7fffffffu);
+                        top = __reduce_max_sync(kFull, top);
+                        if (lane == 0) atomicMax(&sh_win[1], (int)top);
+                    }
+                __syncthreads();
+                heads = (unsigned)sh_cnt;
+                scale_q = unit_scale(__int_as_float(sh_win[0])) * 0x1p-7f;
+                scale_b = unit_scale(__int_as_float(sh_win[1]));
+            }
             for (int blk = lo + w; blk < hi; blk += NW)
                 if (is_cand(blk)) {
-                    const int id = p.tables[(size_t)b * p.max_blocks + blk];
+                    const int id = table[blk];
                     unsigned long long k = 0;              // a bad id (flagged when it was scored)
-                    if (id >= 0 && id < p.num_blocks)
-                        k = finite ? exact_key(bounds, (size_t)id * p.hkv + h, d, qf, 0, G, lane, scale_q, scale_b)
-                                   : exact_key_f64<T>(p, b, h, id, lane);
+                    if (id >= 0 && id < p.num_blocks) {
+                        if (!finite && key[blk] != 0) continue;
+                        k = exact_key<T, true>(bounds, (size_t)id * p.hkv + h, d, qf, heads, lane, scale_q, scale_b,
+                                               &sh_vague);
+                    }
+                    __syncwarp();
                     if (lane == 0) key[blk] = k;
                 }
             __syncthreads();
@@ -1184,13 +1411,34 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
                 for (int blk = lo + tid; blk < hi; blk += NT) c += is_cand(blk) && key[blk] >= t;
                 if (block_count(c) >= left) thr = t;
             }
+            if (sh_vague && thr != 0 && thr != ~0ull) {
+                // more within the keys' errors of the last place than places?
+                const unsigned long long reach = 2 * key_error<T>(d);
+                uint32_t over = 0, near = 0;
+                for (int blk = lo + tid; blk < hi; blk += NT)
+                    if (is_cand(blk)) over += key[blk] > thr + reach, near += key[blk] >= thr - reach && key[blk] <= thr + reach;
+                const int above = block_count(over);
+                if (above + block_count(near) > left) {
+                    open = left - above;
+                    for (int ch = tid; ch < chunks; ch += NT) {
+                        uint32_t in = 0, keep = 0;
+                        for (uint32_t m = cand8[ch]; m; m &= m - 1) {
+                            const unsigned long long k = key[8 * ch + __ffs(m) - 1];
+                            if (k > thr + reach) in |= m & -m;
+                            else if (k >= thr - reach) keep |= m & -m;
+                        }
+                        sel8[ch] |= (unsigned char)in;
+                        cand8[ch] = (unsigned char)keep;
+                    }
+                }
+            }
             uint32_t c = 0;
-            for (int blk = lo + tid; blk < hi; blk += NT)
+            for (int blk = lo + tid; blk < hi && open == 0; blk += NT)
                 if (is_cand(blk) && key[blk] > thr) {
                     atomicOr(&sel[blk >> 5], 1u << (blk & 31));
                     ++c;
                 }
-            int places = left - block_count(c);
+            int places = open ? 0 : left - block_count(c);
             for (int base = 0; base < chunks && places > 0; base += NT) {
                 const int ch = base + tid;
                 uint32_t eq = 0;
@@ -1208,6 +1456,8 @@ __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
                 places -= min(places, (int)total);
             }
         }
+        if (open > 0)
+            settle<T, NT>(bounds, table, p.hkv, h, d, qf, heads, lo, hi, open, sel8, cand8, p.exact + row * p.stride);
     } else {
         for (int c = tid; c < chunks; c += NT) sel8[c] = (unsigned char)forced_of(c);
     }
