@@ -668,7 +668,7 @@ __device__ __forceinline__ uint32_t score_word(const T* bounds, size_t id_row, i
             take_apart(x, mx, ex);
             const unsigned long long m = (unsigned long long)mq * mx;
             const int at = (eq + ex + 320) | ((__float_as_uint(q) ^ __float_as_uint(x)) & 0x80000000u ? 1 << 16 : 0);
-#pragma unroll 1
+#pragma unroll 8
             for (int j = 0; j < 32; ++j) {
                 const unsigned long long mj = __shfl_sync(kFull, m, j);
                 const int a = __shfl_sync(kFull, at, j), k = lane - ((a & 0xffff) >> 5), bit = a & 31;
@@ -743,12 +743,25 @@ __device__ __forceinline__ void settle(const T* bounds, const int32_t* table, in
             for (uint32_t m = cand[c]; m; m &= m - 1, ++at)
                 if (at == rank) where = 8 * c + __ffs(m) - 1;
         __syncthreads();
-        if (w == 0) pivot[lane] = score_word(bounds, (size_t)table[where] * hkv + h, d, qs, heads, lane);
-        __syncthreads();
+        // blocks of the same bounds (mark 1) need no score
+        const size_t pivot_row = (size_t)table[where] * hkv + h;
+        bool differ = false;
         for (int blk = 8 * c0 + w; blk < 8 * c1; blk += NW)
             if ((cand[blk >> 3] >> (blk & 7)) & 1) {
+                const T *x = bounds + pivot_row * 2 * d, *y = bounds + ((size_t)table[blk] * hkv + h) * 2 * d;
+                bool same = true;
+                for (int i = lane; i < 2 * d; i += 32) same &= (float)x[i] == (float)y[i];
+                same = __all_sync(kFull, same);
+                differ |= !same;
+                if (lane == 0) mark[blk] = same ? 1 : 3;
+            }
+        if (__syncthreads_or(differ) && w == 0) pivot[lane] = score_word(bounds, pivot_row, d, qs, heads, lane);
+        __syncthreads();
+        for (int blk = 8 * c0 + w; blk < 8 * c1; blk += NW)
+            if (((cand[blk >> 3] >> (blk & 7)) & 1) && mark[blk] == 3) {
                 const uint32_t x = score_word(bounds, (size_t)table[blk] * hkv + h, d, qs, heads, lane), y = pivot[lane];
                 const unsigned up = __ballot_sync(kFull, x > y), dn = __ballot_sync(kFull, x < y);
+                __syncwarp();
                 if (lane == 0) mark[blk] = up > dn ? 2 : up < dn ? 0 : 1;
             }
         __syncthreads();
