@@ -192,3 +192,163 @@ def test_weights_are_those_of_float32(kind, G):
     top = (0x7e, 0xfe) if kind == "e4m3" else (448.0, -448.0)
     c["vv"][:, :, ::2], c["vv"][:, :, 1::2] = top
     check(c, sparse_gpu(c))
+
+
+# ----------------------------------------------- many rows, shared by clusters of CTAs
+def many_rows(kind, G, D, bs, B, K, how, seed=96, Hkv=8):
+    """B sequences of 8 kv heads on the GPU: ragged lengths and lists, an empty sequence, one
+    of a single token, empty lists. ``how``: 'ragged', or 'one long' among sequences of
+    one or two blocks."""
+    g = torch.Generator(device="cuda").manual_seed(seed + B + K + G)
+    act, cache = {"f32": (F32, F32), "bf16": (BF, BF), "e4m3": (BF, U8)}[kind]
+    n, NB = 3 * K, 700
+    def pool(shape):
+        x = torch.randn(shape, generator=g, device="cuda")
+        return (x / 0.05).to(torch.float8_e4m3fn).view(U8) if kind == "e4m3" else x.to(cache)
+    ks, vs = pkv.pool_shapes(NB, Hkv, bs, D, cache)
+    c = dict(kind=kind, kp=pool(ks), vp=pool(vs), bs=bs, scale=D ** -0.5, ks=0.05 if kind == "e4m3" else 1.0,
+             q=(torch.randn(B, Hkv * G, D, generator=g, device="cuda") * 1.5).to(act))
+    c["vs"] = c["ks"]
+    lens = torch.randint(1, n * bs + 1, (B,), generator=g, device="cuda")
+    if how == "one long":
+        lens = torch.randint(1, 2 * bs + 1, (B,), generator=g, device="cuda")
+        lens[B // 2] = n * bs
+    lens[1], lens[B - 3], lens[B - 1] = 0, 1, n * bs
+    c["lens"] = lens.to(I32)
+    c["tables"] = torch.randint(0, NB, (B, n), generator=g, device="cuda").to(I32)
+    blocks = (lens + bs - 1) // bs
+    rank = torch.rand(B, Hkv, n, generator=g, device="cuda")
+    rank[torch.arange(n, device="cuda").expand(B, Hkv, n) >= blocks[:, None, None]] = 2.0
+    take = torch.randint(0, K + 1, (B, Hkv), generator=g, device="cuda")
+    take[torch.rand(B, Hkv, generator=g, device="cuda") < 0.5] = K
+    order = rank.argsort(-1)[..., :K]
+    listed = (torch.arange(K, device="cuda") < take[..., None]) & (rank.gather(-1, order) < 1.5)
+    sel = torch.where(listed, order, n).sort(-1).values
+    c["sel"] = torch.where(sel < n, sel, -1).to(I32)
+    return c
+
+
+def many_definition(c):
+    """(out, sum_t p_t |V_t|, largest sum_d |q_d K_td| scale) in float64, on the GPU."""
+    B, Hkv, K = c["sel"].shape
+    bs, (Hq, D) = c["bs"], c["q"].shape[1:]
+    G, ks, vs = Hq // Hkv, float(np.float32(c["ks"])), float(np.float32(c["vs"]))
+    val = lambda t: (t.view(torch.float8_e4m3fn) if t.dtype == U8 else t).double()
+    out, mag = torch.zeros(2, B, Hkv, G, D, dtype=torch.float64, device="cuda")
+    logit = torch.zeros(B, Hkv, G, dtype=torch.float64, device="cuda")
+    k, v = pkv.pool_views(c["kp"], c["vp"])                # [NB, Hkv, bs, D]
+    heads = torch.arange(Hkv, device="cuda")[:, None]
+    for b in range(B):
+        j = c["sel"][b].long()
+        ids = c["tables"][b].long()[j.clamp(min=0)]
+        K_, V_ = (val(x[ids, heads]).reshape(Hkv, K * bs, D) for x in (k, v))
+        at = j[..., None] * bs + torch.arange(bs, device="cuda")
+        seen = ((j[..., None] >= 0) & (at < c["lens"][b])).reshape(Hkv, 1, K * bs)
+        q = c["q"][b].double().reshape(Hkv, G, D)
+        x = (q @ K_.transpose(1, 2) * (ks * c["scale"])).masked_fill(~seen, -math.inf)
+        p = torch.where(seen.any(-1, keepdim=True), torch.softmax(x, -1), 0.0).nan_to_num(0.0)
+        out[b], mag[b] = p @ V_ * vs, p @ V_.abs() * vs
+        logit[b] = (q.abs() @ K_.abs().transpose(1, 2)).masked_fill(~seen, 0).amax(-1) * (ks * c["scale"])
+    return out.reshape(B, Hq, D), mag.reshape(B, Hq, D), logit.reshape(B, Hq)
+
+
+def check_many(c):
+    q = c["q"]
+    got = torch.full_like(q, math.nan)
+    pkv.paged_attention_decode_sparse(got, q, c["kp"], c["vp"], c["tables"], c["lens"], c["sel"], c["scale"], c["ks"],
+                                      c["vs"])
+    ref, mag, logit = many_definition(c)
+    kind, D, G = c["kind"], q.shape[2], q.shape[1] // c["kp"].shape[1]
+    tokens = c["sel"].shape[2] * c["bs"]
+    w = {"f32": 0.0, "bf16": 2.0 ** -16 if G > 1 else 0.0, "e4m3": 2.0 ** -22}[kind]     # as in check
+    err = (w + 2 * (D + 8) * 2.0 ** -23 * logit[..., None] + (tokens + 64) * 2.0 ** -23 + 2.0 ** -21) * mag
+    if kind == "e4m3":
+        err += tokens * 2.0 ** -39 * 448 * c["vs"]
+    tol = err + (2.0 ** -24 if kind == "f32" else 2.0 ** -8) * (ref.abs() + err)
+    off = (got.double() - ref).abs()
+    assert bool((off <= tol).all()), f"worst {float((off / tol.clamp(min=1e-300)).nan_to_num(9e9).max()):.3g} of the tolerance"
+    assert pkv.get_device_error() == 0
+    return got
+
+
+# Batches of 8 kv heads whose rows make clusters of 2 (20, 24, 80), 4 (40, 64, 115) and 8
+# (30, 70) on 152 SMs with three CTAs each, or a CTA a row (50)
+@pytest.mark.parametrize("B", [20, 24, 30, 40, 50, 64, 70, 80, 115])
+@pytest.mark.parametrize("kind,G,D,bs", [("bf16", 1, 128, 16), ("bf16", 4, 128, 32), ("bf16", 8, 128, 16),
+                                         ("e4m3", 1, 128, 16), ("e4m3", 4, 128, 16), ("e4m3", 8, 64, 32),
+                                         ("f32", 1, 128, 32), ("f32", 8, 128, 16), ("f32", 8, 128, 32)])
+def test_rows_shared_by_clusters(kind, G, D, bs, B):
+    for K, how in ((64, "ragged"), (128, "one long")):
+        check_many(many_rows(kind, G, D, bs, B, K, how))
+
+
+@pytest.mark.parametrize("kind,G,D,bs", [("bf16", 4, 128, 16), ("e4m3", 4, 128, 16), ("f32", 1, 64, 32)])
+def test_rows_shared_by_clusters_repeat_their_bits(kind, G, D, bs):
+    c = many_rows(kind, G, D, bs, 64, 64, "ragged")
+    want = check_many(c)
+    for _ in range(10):
+        got = torch.empty_like(want)
+        pkv.paged_attention_decode_sparse(got, c["q"], c["kp"], c["vp"], c["tables"], c["lens"], c["sel"], c["scale"],
+                                          c["ks"], c["vs"])
+        assert torch.equal(got, want)
+
+
+def test_rows_shared_by_clusters_with_infinite_and_nan_keys():
+    """What crosses the merge of several CTAs: a row of -infinite logits alone, one with some,
+    one with a NaN; the others as without them."""
+    for kind, G in (("bf16", 4), ("f32", 1)):
+        c = many_rows(kind, G, 128, 16, 64, 64, "ragged", seed=97)
+        want = check_many(c)
+        full = torch.nonzero((c["sel"][:, 0] >= 0).all(-1) & (c["sel"][:, 0] < 100).any(-1))[:, 0][:3].tolist()
+        k, v = pkv.pool_views(c["kp"], c["vp"])
+        NB = k.shape[0]
+        k = torch.cat([k, k[:3]])                          # blocks of their own
+        k[NB:, :, :, 5], k[NB + 1, :, 1:, 5] = -math.inf, 0.0
+        k[NB + 2, :, 3, 7] = math.nan
+        c["kp"], c["vp"] = pkv.pools_from_views(k, torch.cat([v, v[:3]]))
+        c["q"][:, :, 5] = c["q"][:, :, 5].abs() + 0.1
+        before = check_many(c)
+        for b, blk in zip(full, (NB, NB + 1, NB + 2)):
+            j = c["sel"][b, 0]
+            c["tables"][b, (j if blk == NB else j[30:31]).long()] = blk
+        got = torch.empty_like(want)
+        pkv.paged_attention_decode_sparse(got, c["q"], c["kp"], c["vp"], c["tables"], c["lens"], c["sel"], c["scale"],
+                                          c["ks"], c["vs"])
+        assert bool((got[full[0], :G] == 0).all()) and bool(got[full[1]].isfinite().all())
+        assert bool(got[full[2], :G].isnan().all())
+        others = [b for b in range(64) if b not in full]
+        assert torch.equal(got[others], before[others])
+    assert pkv.get_device_error() == 0
+
+
+# ------------------------------------------------------------------------ bound calls
+def test_bound_calls_are_called_again_and_on_other_streams():
+    """Each of the four bound calls, kept and called many times: on the current stream, on two
+    others in turn and at once (each with its own buffers), with new inputs in place."""
+    from test_gpu_long_context import bits, step_calls, step_state
+
+    def bind(s):
+        return [pkv.bind_rotary_and_cache(s["qr"], s["q"], s["k"], s["v"], s["kp"], s["vp"], s["slots"], s["pos"],
+                                          s["table"]),
+                pkv.bind_update_key_bounds(s["kp"], s["kb"], s["tables"], s["lens"], s["pos"], 1),
+                pkv.bind_select_blocks(s["sel"], s["qr"], s["kb"], s["tables"], s["lens"], s["bs"], 1, 1, s["ws"]),
+                pkv.bind_paged_attention_decode_sparse(s["out"], s["qr"], s["kp"], s["vp"], s["tables"], s["lens"],
+                                                       s["sel"], s["scale"])]
+
+    ref, s, t = (step_state(51) for _ in range(3))
+    inputs = [{k: torch.randn_like(s[k]) for k in ("q", "k", "v")} for _ in range(3)]
+    calls, others = bind(s), bind(t)
+    streams = [None, torch.cuda.Stream(), torch.cuda.Stream()]
+    for i, stream in enumerate(streams + streams):
+        for k, x in inputs[i % 3].items():
+            for state in (ref, s, t):
+                state[k].copy_(x)
+        step_calls(ref)
+        torch.cuda.synchronize()
+        for c, o in zip(calls, others):
+            c(stream)
+            o(streams[(i + 1) % 3])
+        torch.cuda.synchronize()
+        for state in (s, t):
+            assert all(torch.equal(a, b) for a, b in zip(bits(state), bits(ref)))
+    assert pkv.get_device_error() == 0
