@@ -217,3 +217,45 @@ def test_a_refused_prompt_step_leaves_q_and_the_cache_as_they_were():
                               torch.zeros(1, dtype=I32, device="cuda"), rotary(), torch.empty_like(q), 0.1, 40)
     torch.cuda.synchronize()
     assert all(torch.equal(t, b) for t, b in zip((q, c.k_pool, c.v_pool), before))
+
+
+def test_a_captured_sparse_step_replays():
+    """The engine's sparse step captured once and replayed for three steps of one batch,
+    its plan, positions and inputs rewritten in place; the same steps run eagerly."""
+    rng = np.random.default_rng(6)
+    runs = []
+    for graph in (False, True):
+        step_rng = np.random.default_rng(7)
+        c = new_cache(seed=3)
+        ids = filled(c, [300, 161, 31], np.random.default_rng(8))
+        c.enable_key_bounds()
+        width, B = 24, len(ids)
+        dev = {"pairs": torch.empty(0, 2, dtype=I64, device="cuda"), "slots": torch.empty(B, dtype=I64, device="cuda"),
+               "tables": torch.empty(B, width, dtype=I32, device="cuda"), "lens": torch.empty(B, dtype=I32, device="cuda")}
+        q, k, v = (torch.empty(B, h, D, dtype=BF, device="cuda") for h in (HQ, HKV, HKV))
+        pos, first = (torch.empty(B, dtype=I32, device="cuda") for _ in range(2))
+        sel, out = torch.empty(B, HKV, 5, dtype=I32, device="cuda"), torch.empty_like(q)
+        ws, rot, g = c.select_workspace(B, width), rotary(), None
+        results = []
+        for _ in range(3):
+            plan = c.plan_step(ids, width, group_prefixes=False)
+            for name in ("slots", "tables", "lens"):
+                dev[name].copy_(torch.from_numpy(getattr(plan, name)))
+            for t, h in ((q, HQ), (k, HKV), (v, HKV)):
+                t.copy_(values(step_rng, B, h, D))
+            pos.copy_(torch.from_numpy((plan.lens - 1).astype(np.int32)))
+            first.copy_(pos)
+            run = lambda: c.sparse_step(q, k, v, dev, pos, first, rot, sel, out, D ** -0.5, workspace=ws)
+            if graph and g is None:
+                torch.cuda.synchronize()
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g):
+                    run()
+            g.replay() if graph else run()
+            torch.cuda.synchronize()
+            check_bounds(c, plan.tables, plan.lens)
+            results.append([t.clone() for t in (q, sel, out)])
+        runs.append(results)
+    for a, b in zip(*runs):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert pkv.get_device_error() == 0
