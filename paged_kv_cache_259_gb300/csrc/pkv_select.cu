@@ -891,9 +891,10 @@ __device__ __forceinline__ void score_row(const SelectParams& p, int b, int h, i
 // if there are more of them than places, and what those cannot tell by every bit. A bin of a score is a monotone function
 // of it, so bins decide soundly whatever the rounding of their edges.
 // Rows of no more blocks than threads have one to a thread.
-// Bound: latency and, with 32 warps, issue: about 13,000 clocks of dependent steps for
-// 8,192 blocks, of which loads 2,000, bins and their scan 3,500, scores in 64 bits 3,000,
-// writing 1,000; a row's scores are at most a few hundred KB, from L2.
+// Bound: latency and, with 32 warps, issue: about 14,000 clocks of dependent steps for
+// 8,192 blocks, of which loads 2,000, bins and their scan 3,500, scores in 64 bits 3,000, the
+// look at the last place 900, writing 1,000; a row's scores are at most a few hundred KB,
+// from L2.
 template <typename T, int NT, bool KEEP, int FD = 0>
 __global__ void __launch_bounds__(NT) select_rows(const SelectParams p) {
     constexpr int NW = NT / 32;

@@ -13,10 +13,10 @@
 // a workspace, few rows are spread over many warps, and many rows make one wave of equal
 // shares, whatever their lengths, where a CTA a row left a ragged second wave.
 // Bound: HBM bytes of the selected tiles when there are many rows (1280 rows of 64 bf16
-// blocks 94.8 us, 0.96 of the copy rate; 512 rows of 128 E4M3 blocks, 4 heads, 47.7, 0.80:
+// blocks 94.3 us, 0.96 of the copy rate; 512 rows of 128 E4M3 blocks, 4 heads, 49.3, 0.77:
 // the stream itself is at the copy rate, 5 us lie before it and 7 in the merges); a chain of
 // loads (length, list, table, tile, partner's partials) when there are few (8 rows of 128
-// blocks 6.3 us).
+// blocks 6.3 us on the GPU).
 #pragma once
 
 #include "pkv_decode_impl.cuh"
@@ -225,8 +225,9 @@ __device__ __forceinline__ float ex2(float x) {
 // 8 columns, and a product carries 16 dims instead of 8. Lane 4r + c holds dims r and
 // r + 8 of heads 2c, 2c + 1. One softmax step a tile of 16 or 32 tokens. (64 sequences
 // x 128 E4M3 blocks of 8 kv heads: 55.7 us with the decode kernel's math, 47.5 so; bf16:
-// 87 and 84; one sequence of 512 blocks: 13.9 and 12.2. The issue slots bound E4M3: 47%
-// in use before, on 12 warps an SM.)
+// 87 and 84; one sequence of 512 blocks: 13.9 and 12.2; all with one product a tile for the
+// weights, where there are two now. The issue slots bound E4M3: 47% in use before, on 12
+// warps an SM, 29% now.)
 template <typename KV, int D, int BS, int G>
 struct HeadsMath {
     using Lay = decode::Layout<KV, D, BS>;
@@ -698,7 +699,7 @@ __global__ void __maxnreg__(168) sparse_decode_kernel(const Params p) {
     };
     // ---- one row: every warp pushes each CTA its slice of its part, one trip through
     // the cluster instead of two barriers around a read (1 sequence, 8 rows of 128 blocks:
-    // 7.1 us with the barriers, 6.4 so; 16 blocks: 5.8 and 5.0)
+    // 0.7 us less than with the barriers, of 7.1; 16 blocks: 0.8 of 5.8)
     if (p.push) {
         __syncwarp();
         cluster_wait();                                    // every CTA's mbarrier is up
