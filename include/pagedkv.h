@@ -580,8 +580,173 @@ PKV_API int paged_attention_decode_sparse(void* out, const void* q, const void* 
                                           void* stream);
 
 /* ------------------------------------------------------------------------
- * pkv_bound_call -- one of the four calls above, or paged_attention_prefill, with its
- * arguments packed, for callers to which passing each argument costs (a
+ * Caches of bounded size: the append of models that normalise their heads, and
+ * eviction of the tokens that got the least attention. The pages have no counterpart.
+ * A cache's token weights say how much attention each cached token has drawn, for each
+ * kv head; the tokens of the highest weight move to fresh blocks and the others go:
+ *     norm_rotary_and_cache (or another append) -> paged_attention_decode_weighed, or
+ *     paged_attention_prefill -> weigh_prefill_tokens; and, where a sequence has outgrown
+ *     its budget, select_tokens -> bm_plan_keep -> keep_tokens.
+ * A kept key stays rotated by the position that it was appended at, so the sequence's
+ * positions go on counting where its cached length does not. All five are asynchronous on
+ * `stream`, allocate nothing and are launched with programmatic stream serialisation, as
+ * paged_attention_decode is (weigh_prefill_tokens excepted).
+ *
+ *   token_weights device float32 [num_rows][num_kv_heads][max_tokens], 16-byte aligned,
+ *                 max_tokens a multiple of 4: place t of a row is the weight of cached
+ *                 token t. Never needs clearing: a token's weight begins with the call that
+ *                 has it among its new tokens
+ *   weight_rows   device int32 [num_seqs]: the row of each sequence; NULL: sequence b has
+ *                 row b (num_rows >= num_seqs). A row outside [0, num_rows), or one that an
+ *                 earlier sequence of the call has, sets PKV_ERR_OUT_OF_RANGE, and that
+ *                 sequence's weights are left as they were (select_tokens: see there)
+ *
+ * norm_rotary_and_cache -- rotary_and_cache of normalised heads: every head x of q and k is
+ * first replaced by
+ *     y_d = x_d * rsqrt(mean(x^2) + eps) * weight[d]
+ * in float32, unrounded; the rest, and every argument not named here, is rotary_and_cache's
+ * (values are not normalised).
+ *
+ *   q_weight, k_weight  device, head_dim elements (stride 0: shared by the heads) or one row
+ *                 of head_dim per query / kv head, q_weight_stride / k_weight_stride
+ *                 elements apart (at least head_dim, a multiple of 16 bytes); 16-byte aligned
+ *   weight_dtype  src_dtype or F32
+ *   eps           finite, >= 0
+ * Supported: what rotary_and_cache supports, head_dim at most 512.
+ * ---------------------------------------------------------------------- */
+PKV_API int norm_rotary_and_cache(void* q_out, const void* q, const void* k, const void* v,
+                                  const void* q_weight, const void* k_weight, void* k_pool,
+                                  void* v_pool, const int64_t* slot_mapping,
+                                  const int32_t* positions, const float* cos_sin,
+                                  const int32_t* sections, int num_axes, int64_t q_out_stride,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                  int64_t q_weight_stride, int64_t k_weight_stride,
+                                  int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                  int rotary_dim, int interleaved, int block_size, int num_blocks,
+                                  int num_positions, int src_dtype, int cache_dtype,
+                                  int weight_dtype, float eps, float k_scale, float v_scale,
+                                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * paged_attention_decode_weighed -- paged_attention_decode that also adds up the weight
+ * that every cached token gets: with p[b][h][t] the softmax weight of token t < L =
+ * seq_lens[b] under query head h, G = num_heads / num_kv_heads and r = weight_rows[b],
+ *     token_weights[r][hk][t] = (t < L - 1 ? decay * token_weights[r][hk][t] : 0)
+ *                               + sum_{g < G} p[b][hk*G + g][t]
+ * The weight of token L - 1, the newest, is begun; places >= L are left as they were, and
+ * an empty sequence's row is.
+ * Logits that are all -infinity give a zero row and no weight; beside finite ones they get
+ * none. A NaN or +infinite logit makes its head's output row NaN, and the weights that the
+ * head adds to.
+ *
+ *   decay         finite, in [0, 1]
+ *   max_tokens    at least max_blocks_per_seq * block_size
+ *   workspace     device scratch of weighed_decode_workspace_size bytes, 16-byte aligned
+ *                 (the logits, 4 bytes per query head and cached token, and the partitions'
+ *                 results). Needs no clearing; calls that overlap on the GPU need one each
+ *   the rest      as paged_attention_decode (same supported sizes and types; queries of any
+ *                 magnitude, as paged_attention_decode_sparse)
+ * A table entry outside the pool sets PKV_ERR_OUT_OF_RANGE; its tokens are given no weight.
+ * A length that the table cannot hold is clamped and sets PKV_ERR_OUT_OF_RANGE.
+ * ---------------------------------------------------------------------- */
+PKV_API int paged_attention_decode_weighed(void* out, float* token_weights,
+                                           const int32_t* weight_rows, const void* q,
+                                           const void* k_pool, const void* v_pool,
+                                           const int32_t* block_tables, const int32_t* seq_lens,
+                                           int num_seqs, int max_blocks_per_seq, int num_blocks,
+                                           int num_rows, int max_tokens, int num_heads,
+                                           int num_kv_heads, int head_dim, int block_size,
+                                           float scale, float decay, int q_dtype, int kv_dtype,
+                                           float k_scale, float v_scale, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+PKV_API size_t weighed_decode_workspace_size(int num_seqs, int num_heads, int head_dim,
+                                             int block_size, int max_blocks_per_seq);
+
+/* ------------------------------------------------------------------------
+ * weigh_prefill_tokens -- the token weights of a prefill step: those that the last queries
+ * of each sequence's chunk give. Sequence b has L = seq_lens[b] cached tokens, the last C =
+ * query_start[b+1] - query_start[b] of them its chunk (paged_attention_prefill's arguments);
+ * with w = min(window, C) (window 0: C) and p[i][h][t] the causal softmax weight of token
+ * t <= L - C + i under head h of chunk query i,
+ *     token_weights[r][hk][t] = (t < L - C ? decay * token_weights[r][hk][t] : 0)
+ *                               + sum_{C-w <= i < C} sum_{g < G} p[i][hk*G + g][t],  t < L
+ * The weights of the chunk's tokens are begun. A sequence without a chunk is left as it was.
+ *
+ *   q             device [query_start[num_seqs]][num_heads][head_dim] bf16, 16-byte aligned:
+ *                 the rotated queries of the whole chunks
+ *   k_pool        device pool, bf16, the chunks' keys written
+ *   window        host int >= 0
+ *   decay, max_tokens  as paged_attention_decode_weighed
+ *   workspace     device scratch of weigh_prefill_workspace_size bytes, 16-byte aligned; needs
+ *                 no clearing; calls that overlap on the GPU need one each
+ *   the rest      as paged_attention_prefill
+ * Supported: BF16 / BF16, head_dim in {64,128}, block_size in {16,32}, any num_heads /
+ * num_kv_heads up to 128. A sequence with C > L, L beyond its table or rows outside q, or a
+ * table entry outside the pool, sets PKV_ERR_OUT_OF_RANGE (the sequence's weights are left as
+ * they were, or the entry's tokens are given no weight). Chunk queries past max_query_len,
+ * counted from the chunk's first, are an error of the caller: such a sequence is left as it
+ * was and sets PKV_ERR_OUT_OF_RANGE.
+ * ---------------------------------------------------------------------- */
+PKV_API int weigh_prefill_tokens(float* token_weights, const int32_t* weight_rows, const void* q,
+                                 const void* k_pool, const int32_t* block_tables,
+                                 const int32_t* seq_lens, const int32_t* query_start, int num_seqs,
+                                 int max_query_len, int window, int max_blocks_per_seq,
+                                 int num_blocks, int num_rows, int max_tokens, int num_heads,
+                                 int num_kv_heads, int head_dim, int block_size, float scale,
+                                 float decay, int q_dtype, int kv_dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+PKV_API size_t weigh_prefill_workspace_size(int num_seqs, int num_heads, int max_query_len,
+                                            int window);
+
+/* ------------------------------------------------------------------------
+ * select_tokens -- the tokens that each kv head of a sequence keeps: kept[b][h] lists, in
+ * ascending order and -1 padded to num_kept, every token if L = seq_lens[b] <= num_kept;
+ * else tokens 0 .. first_tokens-1, L-last_tokens .. L-1 and the num_kept - first_tokens -
+ * last_tokens others of the highest token_weights[r][h], equal weights by the lower token.
+ * A weight that is not finite ranks above every finite one; 0 and -0 are equal.
+ *
+ *   kept          device int32 [num_seqs][num_kv_heads][num_kept], written
+ *   seq_lens      0 <= L <= max_tokens (else clamped, with PKV_ERR_OUT_OF_RANGE)
+ *   num_kept      >= 1; first_tokens, last_tokens >= 0, adding up to at most num_kept
+ * A sequence without a good row gets a list of padding; a row may be given twice here.
+ * ---------------------------------------------------------------------- */
+PKV_API int select_tokens(int32_t* kept, const float* token_weights, const int32_t* weight_rows,
+                          const int32_t* seq_lens, int num_seqs, int num_kv_heads, int num_rows,
+                          int max_tokens, int num_kept, int first_tokens, int last_tokens,
+                          void* stream);
+
+/* ------------------------------------------------------------------------
+ * keep_tokens -- move the kept tokens to the front of fresh blocks: with t = kept[b][h][i],
+ * for every i that the list fills,
+ *     K, V[kept_tables[b][i / block_size]][h][i % block_size]
+ *                      = K, V[block_tables[b][t / block_size]][h][t % block_size]
+ *     token_weights[r][h][i] = token_weights[r][h][t]      (the old weights on the right)
+ * Every other slot and weight is left as it was.
+ *
+ *   kept          device int32 [num_seqs][num_kv_heads][num_kept]: tokens of the sequence,
+ *                 strictly ascending, the rest -1 (select_tokens' output or the caller's
+ *                 own choice). An entry that is not below seq_lens[b] or not above the entry
+ *                 before it, one directly behind padding, one below its own index, or one
+ *                 whose blocks are not in the pool, sets PKV_ERR_OUT_OF_RANGE and is skipped
+ *   token_weights may be NULL (then weight_rows, num_rows and max_tokens are not looked at);
+ *                 max_tokens at least max_blocks_per_seq * block_size
+ *   block_tables, seq_lens  the sequences before the move
+ *   kept_tables   device int32 [num_seqs][max_kept_blocks], max_kept_blocks * block_size >=
+ *                 num_kept: the blocks after it. Distinct, and no block of any sequence's
+ *                 block_tables (bm_plan_keep gives such); otherwise which bytes land is
+ *                 unspecified
+ * Supported: head_dim and block_size multiples of 16, head_dim at most 512; F32, BF16, E4M3.
+ * ---------------------------------------------------------------------- */
+PKV_API int keep_tokens(const int32_t* kept, float* token_weights, const int32_t* weight_rows,
+                        void* k_pool, void* v_pool, const int32_t* block_tables,
+                        const int32_t* kept_tables, const int32_t* seq_lens, int num_seqs,
+                        int num_kept, int max_blocks_per_seq, int max_kept_blocks, int num_blocks,
+                        int num_rows, int max_tokens, int num_kv_heads, int head_dim,
+                        int block_size, int kv_dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pkv_bound_call -- one of the calls of the two sections above, or paged_attention_prefill,
+ * with its arguments packed, for callers to which passing each argument costs (a
  * foreign-function interface takes more time over twenty-odd arguments than the call
  * itself over its launch).
  * pkv_bound_check -- what that call would return for its arguments, without running
@@ -600,7 +765,12 @@ typedef enum {
     PKV_CALL_UPDATE_KEY_BOUNDS = 1,
     PKV_CALL_SELECT_BLOCKS = 2,
     PKV_CALL_DECODE_SPARSE = 3,
-    PKV_CALL_PREFILL = 4
+    PKV_CALL_PREFILL = 4,
+    PKV_CALL_NORM_ROTARY_AND_CACHE = 5,
+    PKV_CALL_DECODE_WEIGHED = 6,
+    PKV_CALL_WEIGH_PREFILL = 7,
+    PKV_CALL_SELECT_TOKENS = 8,
+    PKV_CALL_KEEP_TOKENS = 9
 } pkv_call;
 PKV_API int pkv_bound_call(int call, const uint64_t* args, int num_args, void* stream);
 PKV_API int pkv_bound_check(int call, const uint64_t* args, int num_args);

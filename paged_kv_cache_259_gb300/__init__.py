@@ -14,6 +14,10 @@ Entry points (same names as the C ABI):
 * ``rotary_and_cache``       -- slot-mapped write with the position rotation of q and k.
 * ``update_key_bounds``, ``select_blocks``, ``paged_attention_decode_sparse`` --
   decode attention over the blocks a bound on their logits selects.
+* ``norm_rotary_and_cache``  -- the rotated append of normalised heads.
+* ``paged_attention_decode_weighed``, ``weigh_prefill_tokens``, ``select_tokens``,
+  ``keep_tokens`` -- the attention weight each cached token draws, and eviction of
+  the tokens that drew the least.
 * ``paged_attention_workspace_size``, ``get_device_error``.
 * ``BlockManager``           -- the host block manager (free list, tables,
                                 reference counts, fork, copy-on-write).
@@ -34,7 +38,11 @@ __all__ = [
     "rotary_and_cache", "bind_rotary_and_cache", "rotary_table", "key_bounds_shape",
     "key_bounds_dtype", "update_key_bounds", "bind_update_key_bounds", "select_blocks",
     "bind_select_blocks", "select_blocks_workspace_size", "paged_attention_decode_sparse",
-    "bind_paged_attention_decode_sparse", "kernel_launches", "BlockManager",
+    "bind_paged_attention_decode_sparse", "norm_rotary_and_cache", "bind_norm_rotary_and_cache",
+    "token_weights_shape", "paged_attention_decode_weighed", "bind_paged_attention_decode_weighed",
+    "weighed_decode_workspace_size", "weigh_prefill_tokens", "bind_weigh_prefill_tokens",
+    "weigh_prefill_workspace_size", "select_tokens", "bind_select_tokens", "keep_tokens",
+    "bind_keep_tokens", "kernel_launches", "BlockManager",
     "library_path", "load_library", "pool_shapes", "pool_views", "pools_from_views", "PKV_F32",
     "PKV_BF16", "PKV_E4M3", "PKV_ERR_POOL_EXHAUSTED",
 ]
@@ -46,7 +54,8 @@ _LIB = None
 PKV_F32, PKV_BF16, PKV_E4M3 = 0, 1, 2
 PKV_ERR_POOL_EXHAUSTED = -5
 (PKV_CALL_ROTARY_AND_CACHE, PKV_CALL_UPDATE_KEY_BOUNDS, PKV_CALL_SELECT_BLOCKS,
- PKV_CALL_DECODE_SPARSE, PKV_CALL_PREFILL) = range(5)
+ PKV_CALL_DECODE_SPARSE, PKV_CALL_PREFILL, PKV_CALL_NORM_ROTARY_AND_CACHE, PKV_CALL_DECODE_WEIGHED,
+ PKV_CALL_WEIGH_PREFILL, PKV_CALL_SELECT_TOKENS, PKV_CALL_KEEP_TOKENS) = range(10)
 _STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported configuration",
            -3: "CUDA runtime error", -4: "index out of range", -5: "block pool exhausted",
            -6: "device wait timed out"}
@@ -143,6 +152,16 @@ def load_library():
         "paged_attention_decode_sparse": (c_int, [vp, vp, vp, vp, vp, vp, vp, c_int, c_int, c_int,
                                                   c_int, c_int, c_int, c_int, c_int, c_float,
                                                   c_int, c_int, c_float, c_float, vp]),
+        "norm_rotary_and_cache": (c_int, [vp] * 11 + [i32p, c_int] + [ctypes.c_int64] * 6 +
+                                  [c_int] * 12 + [c_float] * 3 + [vp]),
+        "paged_attention_decode_weighed": (c_int, [vp] * 8 + [c_int] * 9 + [c_float] * 2 +
+                                           [c_int] * 2 + [c_float] * 2 + [vp, c_size, vp]),
+        "weighed_decode_workspace_size": (c_size, [c_int] * 5),
+        "weigh_prefill_tokens": (c_int, [vp] * 7 + [c_int] * 11 + [c_float] * 2 + [c_int] * 2 +
+                                 [vp, c_size, vp]),
+        "weigh_prefill_workspace_size": (c_size, [c_int] * 4),
+        "select_tokens": (c_int, [vp] * 4 + [c_int] * 7 + [vp]),
+        "keep_tokens": (c_int, [vp] * 8 + [c_int] * 11 + [vp]),
         "pkv_bound_call": (c_int, [c_int, vp, c_int, vp]),
         "pkv_bound_check": (c_int, [c_int, vp, c_int]),
         "pkv_get_device_error": (c_int, [ip, vp]),
@@ -326,6 +345,13 @@ def _pool_dims(k_pool, v_pool):
             tuple(v_pool.shape) != (NB, Hkv, bs // X, D // 8, 8, X):
         raise ValueError("pool shapes do not match the library layout (see pool_shapes)")
     return NB, Hkv, bs, D
+
+
+def _k_pool_dims(k_pool):
+    """(NB, Hkv, bs, D) of a K pool in the library layout."""
+    if k_pool.dim() != 6 or k_pool.shape[4] != 8 or k_pool.shape[5] * k_pool.element_size() != 16:
+        raise ValueError("k_pool must be [NB, Hkv, bs/8, D/X, 8, X] (see pool_shapes)")
+    return k_pool.shape[0], k_pool.shape[1], k_pool.shape[2] * 8, k_pool.shape[3] * k_pool.shape[5]
 
 
 def paged_attention_workspace_size(num_seqs, num_heads, head_dim, block_size, max_blocks_per_seq):
@@ -698,6 +724,16 @@ def bind_rotary_and_cache(q_out, q, k, v, k_pool, v_pool, slot_mapping, position
                           sections=None, interleaved=False, k_scale=1.0, v_scale=1.0):
     """``rotary_and_cache`` checked once and bound to these tensors (``BoundCall``)."""
     lib = load_library()
+    pointers, strides, sizes, dev = _rotary_args(q_out, q, k, v, k_pool, v_pool, slot_mapping,
+                                                 positions, cos_sin, sections, interleaved)
+    args = pointers + strides + sizes + _c_args([float(k_scale), float(v_scale)])
+    return PackedCall(lib, PKV_CALL_ROTARY_AND_CACHE, args, "rotary_and_cache", dev)
+
+
+def _rotary_args(q_out, q, k, v, k_pool, v_pool, slot_mapping, positions, cos_sin, sections,
+                 interleaved):
+    """The checked arguments of a rotated append: its pointers and sections, the token
+    strides, the sizes up to the dtypes; and the device."""
     rows = ((q_out, "q_out"), (q, "q"), (k, "k"), (v, "v"))
     rest = ((k_pool, "k_pool"), (v_pool, "v_pool"), (slot_mapping, "slot_mapping"),
             (positions, "positions"), (cos_sin, "cos_sin"))
@@ -730,12 +766,52 @@ def bind_rotary_and_cache(q_out, q, k, v, k_pool, v_pool, slot_mapping, position
     for t, n in rows:
         if _cuda(t, n, contiguous=False).device != dev:
             raise ValueError(f"{n} is on {t.device}, the other tensors on {dev}")
-    args = [_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool), _ptr(slot_mapping),
-            _ptr(positions), _ptr(cos_sin), (ctypes.c_int32 * axes)(*sections), ctypes.c_int(axes)]
-    args += [ctypes.c_int64(s) for s in strides]
-    args += _c_args([T, Hq, Hkv, D, 2 * half, bool(interleaved), bs, NB, cos_sin.shape[0], _dt(q, "q"),
-                     _dt(k_pool, "k_pool"), float(k_scale), float(v_scale)])
-    return PackedCall(lib, PKV_CALL_ROTARY_AND_CACHE, args, "rotary_and_cache", dev)
+    pointers = [_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_pool), _ptr(v_pool), _ptr(slot_mapping),
+                _ptr(positions), _ptr(cos_sin), (ctypes.c_int32 * axes)(*sections), ctypes.c_int(axes)]
+    sizes = _c_args([T, Hq, Hkv, D, 2 * half, bool(interleaved), bs, NB, cos_sin.shape[0], _dt(q, "q"),
+                     _dt(k_pool, "k_pool")])
+    return pointers, [ctypes.c_int64(s) for s in strides], sizes, dev
+
+
+def norm_rotary_and_cache(q_out, q, k, v, q_weight, k_weight, k_pool, v_pool, slot_mapping,
+                          positions, cos_sin, eps=1e-6, sections=None, interleaved=False,
+                          k_scale=1.0, v_scale=1.0, stream=None):
+    """``rotary_and_cache`` with every head x of q and k first replaced by ``x *
+    rsqrt(mean(x**2) + eps) * weight``, in float32 and unrounded.
+
+    ``q_weight``, ``k_weight``: ``[D]``, or ``[Hq, D]`` and ``[Hkv, D]`` for weights of
+    each head, both in the dtype of q or both float32; the rest as ``rotary_and_cache``
+    (D at most 512)."""
+    bind_norm_rotary_and_cache(q_out, q, k, v, q_weight, k_weight, k_pool, v_pool, slot_mapping,
+                               positions, cos_sin, eps, sections, interleaved, k_scale,
+                               v_scale)(stream)
+    return q_out
+
+
+def bind_norm_rotary_and_cache(q_out, q, k, v, q_weight, k_weight, k_pool, v_pool, slot_mapping,
+                               positions, cos_sin, eps=1e-6, sections=None, interleaved=False,
+                               k_scale=1.0, v_scale=1.0):
+    """``norm_rotary_and_cache`` checked once and bound to these tensors (``BoundCall``)."""
+    lib = load_library()
+    weights = ((q_weight, "q_weight"), (k_weight, "k_weight"))
+    _tensors(weights + ((q, "q"), (k, "k")))
+    if q_weight.dtype != k_weight.dtype or q_weight.dtype not in (q.dtype, torch.float32):
+        raise TypeError("q_weight and k_weight must both have the dtype of q, or float32")
+    steps = []
+    for (t, n), x in zip(weights, (q, k)):
+        if x.dim() != 3 or tuple(t.shape) not in ((x.shape[2],), tuple(x.shape[1:])):
+            raise ValueError(f"{n} must be [D], or [heads, D]")
+        if x.shape[2] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{n}: the weights of a head must be contiguous")
+        steps.append(ctypes.c_int64(0 if t.dim() == 1 or t.shape[0] == 1 else t.stride(0)))
+    pointers, strides, sizes, dev = _rotary_args(q_out, q, k, v, k_pool, v_pool, slot_mapping,
+                                                 positions, cos_sin, sections, interleaved)
+    for t, n in weights:
+        if _cuda(t, n, contiguous=False).device != dev:
+            raise ValueError(f"{n} is on {t.device}, the other tensors on {dev}")
+    args = pointers[:4] + [_ptr(q_weight), _ptr(k_weight)] + pointers[4:] + strides + steps + sizes
+    args += _c_args([_dt(q_weight, "q_weight"), float(eps), float(k_scale), float(v_scale)])
+    return PackedCall(lib, PKV_CALL_NORM_ROTARY_AND_CACHE, args, "norm_rotary_and_cache", dev)
 
 
 def key_bounds_shape(num_blocks, num_kv_heads, head_dim):
@@ -775,10 +851,7 @@ def bind_update_key_bounds(k_pool, key_bounds, block_tables, seq_lens, first_cha
     named = ((k_pool, "k_pool"), (key_bounds, "key_bounds"), (block_tables, "block_tables"),
              (seq_lens, "seq_lens"), (first_changed, "first_changed"))
     _tensors(named)
-    if k_pool.dim() != 6 or k_pool.shape[4] != 8 or k_pool.shape[5] * k_pool.element_size() != 16:
-        raise ValueError("k_pool must be [NB, Hkv, bs/8, D/X, 8, X] (see pool_shapes)")
-    NB, Hkv, bs, D = k_pool.shape[0], k_pool.shape[1], k_pool.shape[2] * 8, \
-        k_pool.shape[3] * k_pool.shape[5]
+    NB, Hkv, bs, D = _k_pool_dims(k_pool)
     _check_bounds(key_bounds, NB, Hkv, D, key_bounds_dtype(k_pool.dtype))
     for t in (block_tables, seq_lens, first_changed):
         if t.dtype != torch.int32:
@@ -871,6 +944,190 @@ def bind_paged_attention_decode_sparse(out, q, k_pool, v_pool, block_tables, seq
     args += _c_args([B, block_tables.shape[1], NB, selected.shape[2], Hq, Hkv, D, bs, float(scale),
                      _dt(q, "q"), _dt(k_pool, "k_pool"), float(k_scale), float(v_scale)])
     return PackedCall(lib, PKV_CALL_DECODE_SPARSE, args, "paged_attention_decode_sparse", dev)
+
+
+def token_weights_shape(num_rows, num_kv_heads, max_tokens):
+    """Shape of the token weights of ``num_rows`` sequences of up to ``max_tokens`` cached
+    tokens (the last dim a multiple of 4). float32; they need no clearing."""
+    return (num_rows, num_kv_heads, -(-max_tokens // 4) * 4)
+
+
+def _weights_args(token_weights, weight_rows, num_seqs, num_kv_heads):
+    """The named tensors of token weights ``[rows, Hkv, max_tokens]`` and their rows, checked."""
+    named = [(token_weights, "token_weights")]
+    if weight_rows is not None:
+        named.append((weight_rows, "weight_rows"))
+    _tensors(named)
+    if token_weights.dtype != torch.float32:
+        raise TypeError("token_weights must be float32")
+    if token_weights.dim() != 3 or token_weights.shape[1] != num_kv_heads:
+        raise ValueError("token_weights must be [rows, Hkv, max_tokens] (see token_weights_shape)")
+    if weight_rows is None:
+        if token_weights.shape[0] < num_seqs:
+            raise ValueError("token_weights has fewer rows than there are sequences")
+    elif weight_rows.dtype != torch.int32:
+        raise TypeError("weight_rows must be int32")
+    elif tuple(weight_rows.shape) != (num_seqs,):
+        raise ValueError("weight_rows must be [B]")
+    return tuple(named)
+
+
+def weighed_decode_workspace_size(num_seqs, num_heads, head_dim, block_size, max_blocks_per_seq):
+    """Bytes of scratch that ``paged_attention_decode_weighed`` needs for these sizes."""
+    return int(load_library().weighed_decode_workspace_size(num_seqs, num_heads, head_dim, block_size,
+                                                            max_blocks_per_seq))
+
+
+def paged_attention_decode_weighed(out, token_weights, weight_rows, q, k_pool, v_pool, block_tables,
+                                   seq_lens, scale, decay=1.0, k_scale=1.0, v_scale=1.0,
+                                   workspace=None, stream=None):
+    """``paged_attention_decode`` that also adds the softmax weight of every cached token,
+    summed over the query heads of a kv head, to ``token_weights`` (float32 ``[rows, Hkv,
+    max_tokens]``; sequence b's row is ``weight_rows[b]``, int32 ``[B]``, distinct, or b if
+    None), times ``decay`` before; the newest token's weight is begun. ``workspace``: a CUDA
+    tensor of ``weighed_decode_workspace_size`` bytes."""
+    bind_paged_attention_decode_weighed(out, token_weights, weight_rows, q, k_pool, v_pool,
+                                        block_tables, seq_lens, scale, decay, k_scale, v_scale,
+                                        workspace)(stream)
+    return out
+
+
+def bind_paged_attention_decode_weighed(out, token_weights, weight_rows, q, k_pool, v_pool,
+                                        block_tables, seq_lens, scale, decay=1.0, k_scale=1.0,
+                                        v_scale=1.0, workspace=None):
+    """``paged_attention_decode_weighed`` checked once and bound to these tensors
+    (``BoundCall``)."""
+    lib = load_library()
+    B, Hq, D, NB, Hkv, bs = _decode_shapes(out, q, k_pool, v_pool, block_tables, seq_lens)
+    named = _weights_args(token_weights, weight_rows, B, Hkv)
+    named += ((out, "out"), (q, "q"), (k_pool, "k_pool"), (v_pool, "v_pool"),
+              (block_tables, "block_tables"), (seq_lens, "seq_lens"))
+    dev = _on_gpu(named)
+    ws_ptr, ws_bytes = _workspace(workspace, dev)
+    args = [_ptr(t) for t in (out, token_weights, weight_rows, q, k_pool, v_pool, block_tables, seq_lens)]
+    args += _c_args([B, block_tables.shape[1], NB, token_weights.shape[0], token_weights.shape[2], Hq,
+                     Hkv, D, bs, float(scale), float(decay), _dt(q, "q"), _dt(k_pool, "k_pool"),
+                     float(k_scale), float(v_scale)])
+    args += [ctypes.c_void_p(ws_ptr), ctypes.c_size_t(ws_bytes)]
+    return PackedCall(lib, PKV_CALL_DECODE_WEIGHED, args, "paged_attention_decode_weighed", dev)
+
+
+def weigh_prefill_workspace_size(num_seqs, num_heads, max_query_len, window=0):
+    """Bytes of scratch that ``weigh_prefill_tokens`` needs for these sizes."""
+    return int(load_library().weigh_prefill_workspace_size(num_seqs, num_heads, max_query_len, window))
+
+
+def weigh_prefill_tokens(token_weights, weight_rows, q, k_pool, block_tables, seq_lens, query_start,
+                         scale, max_query_len, window=0, decay=1.0, workspace=None, stream=None):
+    """The token weights of a prefill step: the causal softmax weights that the last
+    ``window`` queries of each sequence's chunk (0: all of them) give to its cached tokens,
+    added to ``token_weights`` times ``decay``; the chunk's tokens are begun. q bfloat16
+    ``[T, Hq, D]``, k_pool bfloat16, the rest as ``paged_attention_prefill`` and
+    ``paged_attention_decode_weighed``; ``workspace``: a CUDA tensor of
+    ``weigh_prefill_workspace_size`` bytes."""
+    bind_weigh_prefill_tokens(token_weights, weight_rows, q, k_pool, block_tables, seq_lens,
+                              query_start, scale, max_query_len, window, decay, workspace)(stream)
+    return token_weights
+
+
+def bind_weigh_prefill_tokens(token_weights, weight_rows, q, k_pool, block_tables, seq_lens,
+                              query_start, scale, max_query_len, window=0, decay=1.0,
+                              workspace=None):
+    """``weigh_prefill_tokens`` checked once and bound to these tensors (``BoundCall``)."""
+    lib = load_library()
+    named = ((q, "q"), (k_pool, "k_pool"), (block_tables, "block_tables"), (seq_lens, "seq_lens"),
+             (query_start, "query_start"))
+    _tensors(named)
+    for t in (block_tables, seq_lens, query_start):
+        if t.dtype != torch.int32:
+            raise TypeError("block_tables, seq_lens and query_start must be int32")
+    NB, Hkv, bs, D = _k_pool_dims(k_pool)
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError("q must be [T, Hq, D], with the pool's D")
+    if seq_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != seq_lens.shape[0] or \
+            tuple(query_start.shape) != (seq_lens.shape[0] + 1,):
+        raise ValueError("inconsistent shapes: block_tables [B, max_blocks], seq_lens [B], "
+                         "query_start [B + 1]")
+    B = seq_lens.shape[0]
+    named += _weights_args(token_weights, weight_rows, B, Hkv)
+    dev = _on_gpu(named)
+    ws_ptr, ws_bytes = _workspace(workspace, dev)
+    args = [_ptr(t) for t in (token_weights, weight_rows, q, k_pool, block_tables, seq_lens, query_start)]
+    args += _c_args([B, int(max_query_len), int(window), block_tables.shape[1], NB, token_weights.shape[0],
+                     token_weights.shape[2], q.shape[1], Hkv, D, bs, float(scale), float(decay),
+                     _dt(q, "q"), _dt(k_pool, "k_pool")])
+    args += [ctypes.c_void_p(ws_ptr), ctypes.c_size_t(ws_bytes)]
+    return PackedCall(lib, PKV_CALL_WEIGH_PREFILL, args, "weigh_prefill_tokens", dev)
+
+
+def select_tokens(kept, token_weights, weight_rows, seq_lens, first_tokens=0, last_tokens=0,
+                  stream=None):
+    """The tokens that each kv head of a sequence keeps, into ``kept`` (int32 ``[B, Hkv, K]``:
+    ascending, -1 padded): the first and last tokens and the heaviest others by
+    ``token_weights`` (equal weights by the lower token); every token of a sequence that has
+    at most K."""
+    bind_select_tokens(kept, token_weights, weight_rows, seq_lens, first_tokens, last_tokens)(stream)
+    return kept
+
+
+def bind_select_tokens(kept, token_weights, weight_rows, seq_lens, first_tokens=0, last_tokens=0):
+    """``select_tokens`` checked once and bound to these tensors (``BoundCall``)."""
+    lib = load_library()
+    named = ((kept, "kept"), (seq_lens, "seq_lens"))
+    _tensors(named)
+    if kept.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError("kept and seq_lens must be int32")
+    if kept.dim() != 3 or tuple(seq_lens.shape) != (kept.shape[0],):
+        raise ValueError("kept must be [B, Hkv, K], seq_lens [B]")
+    B, Hkv, K = kept.shape
+    named += _weights_args(token_weights, weight_rows, B, Hkv)
+    dev = _on_gpu(named)
+    args = [_ptr(t) for t in (kept, token_weights, weight_rows, seq_lens)]
+    args += _c_args([B, Hkv, token_weights.shape[0], token_weights.shape[2], K, int(first_tokens),
+                     int(last_tokens)])
+    return PackedCall(lib, PKV_CALL_SELECT_TOKENS, args, "select_tokens", dev)
+
+
+def keep_tokens(kept, token_weights, weight_rows, k_pool, v_pool, block_tables, kept_tables, seq_lens,
+                stream=None):
+    """Move the tokens listed in ``kept`` (int32 ``[B, Hkv, K]``: tokens of the sequence,
+    strictly ascending, -1 padded) to the front of fresh blocks ``kept_tables`` (int32
+    ``[B, n]``, n blocks of room for K tokens), and their ``token_weights`` (None: not kept)
+    to the front of their row. ``block_tables`` and ``seq_lens``: the sequences before."""
+    bind_keep_tokens(kept, token_weights, weight_rows, k_pool, v_pool, block_tables, kept_tables,
+                     seq_lens)(stream)
+
+
+def bind_keep_tokens(kept, token_weights, weight_rows, k_pool, v_pool, block_tables, kept_tables,
+                     seq_lens):
+    """``keep_tokens`` checked once and bound to these tensors (``BoundCall``)."""
+    lib = load_library()
+    named = ((kept, "kept"), (k_pool, "k_pool"), (v_pool, "v_pool"), (block_tables, "block_tables"),
+             (kept_tables, "kept_tables"), (seq_lens, "seq_lens"))
+    _tensors(named)
+    for t in (kept, block_tables, kept_tables, seq_lens):
+        if t.dtype != torch.int32:
+            raise TypeError("kept, block_tables, kept_tables and seq_lens must be int32")
+    NB, Hkv, bs, D = _pool_dims(k_pool, v_pool)
+    if kept.dim() != 3 or kept.shape[1] != Hkv or seq_lens.dim() != 1:
+        raise ValueError("kept must be [B, Hkv, K], with the pools' Hkv, seq_lens [B]")
+    B, _, K = kept.shape
+    if seq_lens.shape[0] != B or block_tables.dim() != 2 or kept_tables.dim() != 2 or \
+            block_tables.shape[0] != B or kept_tables.shape[0] != B:
+        raise ValueError("inconsistent shapes: kept [B, Hkv, K], block_tables [B, max_blocks], "
+                         "kept_tables [B, n], seq_lens [B]")
+    rows, tokens = 0, 0
+    if token_weights is not None:
+        named += _weights_args(token_weights, weight_rows, B, Hkv)
+        rows, tokens = token_weights.shape[0], token_weights.shape[2]
+    else:
+        weight_rows = None
+    dev = _on_gpu(named)
+    args = [_ptr(t) for t in (kept, token_weights, weight_rows, k_pool, v_pool, block_tables, kept_tables,
+                              seq_lens)]
+    args += _c_args([B, K, block_tables.shape[1], kept_tables.shape[1], NB, rows, tokens, Hkv, D, bs,
+                     _dt(k_pool, "k_pool")])
+    return PackedCall(lib, PKV_CALL_KEEP_TOKENS, args, "keep_tokens", dev)
 
 
 class BoundCall:

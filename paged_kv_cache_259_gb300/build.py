@@ -30,6 +30,13 @@ CUDA_SOURCES = [
     "pkv_sparse_f32.cu",
     "pkv_sparse_bf16.cu",
     "pkv_sparse_e4m3.cu",
+    "pkv_norm_rotary.cu",
+    "pkv_weighed.cu",
+    "pkv_weighed_f32.cu",
+    "pkv_weighed_bf16.cu",
+    "pkv_weighed_e4m3.cu",
+    "pkv_evict.cu",
+    "pkv_weigh_prefill.cu",
     "pkv_bound.cu",
 ]
 CXX_SOURCES = ["block_manager.cpp"]

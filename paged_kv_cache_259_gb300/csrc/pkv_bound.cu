@@ -82,6 +82,11 @@ extern "C" int pkv_bound_call(int call, const uint64_t* args, int num_args, void
         case PKV_CALL_DECODE_SPARSE: return call_packed(&paged_attention_decode_sparse, args, num_args, stream);
         case PKV_CALL_PREFILL:
             return call_packed(checking() ? &check_prefill : &paged_attention_prefill, args, num_args, stream);
+        case PKV_CALL_NORM_ROTARY_AND_CACHE: return call_packed(&norm_rotary_and_cache, args, num_args, stream);
+        case PKV_CALL_DECODE_WEIGHED: return call_packed(&paged_attention_decode_weighed, args, num_args, stream);
+        case PKV_CALL_WEIGH_PREFILL: return call_packed(&weigh_prefill_tokens, args, num_args, stream);
+        case PKV_CALL_SELECT_TOKENS: return call_packed(&select_tokens, args, num_args, stream);
+        case PKV_CALL_KEEP_TOKENS: return call_packed(&keep_tokens, args, num_args, stream);
         default: return PKV_ERR_INVALID_ARG;
     }
 }

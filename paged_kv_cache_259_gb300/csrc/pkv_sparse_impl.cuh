@@ -217,6 +217,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// What a tile's logits (in units of log2 e) are also given to, as runs of consecutive tokens
+// of one head: nothing here; decode with token weights keeps them.
+struct NoSink {
+    __device__ __forceinline__ void put(int, int, float, float) const {}
+    __device__ __forceinline__ void put(int, int, float, float, float, float) const {}
+    __device__ __forceinline__ void put(int, int, float) const {}
+};
+
 // Tensor-core math for up to 8 query heads a kv head, bf16 and E4M3 caches. Scores as
 // in the decode kernel (query heads are the rows of A, half of them zero): lane 4r + c
 // holds the scores of head r, tokens 2c + e of two groups of 8, which is how the B
@@ -265,8 +273,9 @@ struct HeadsMath {
         __syncwarp();
     }
 
+    template <class Sink = NoSink>
     __device__ __forceinline__ static void tile(State& st, const unsigned char* kt, const unsigned char* vt, int ntok,
-                                                int lane, float qscale) {
+                                                int lane, float qscale, const Sink& sink = Sink()) {
         const int c = lane & 3, mi = lane >> 3, rr = lane & 7;
         const float by = F8 ? st.qscale : qscale;
         const uint32_t kbase = smem_addr(kt), vbase = smem_addr(vt);
@@ -310,6 +319,15 @@ struct HeadsMath {
                 const int h = i >> 2, u = (i >> 1) & 1, e = i & 1;
                 const int tok = F8 ? 16 * h + 4 * c + 2 * u + e : 16 * h + 8 * u + 2 * c + e;
                 if (tok >= ntok) x[h][u][e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < SUB; ++h) {
+            if constexpr (F8) {
+                sink.put(lane >> 2, 16 * h + 4 * c, x[h][0][0], x[h][0][1], x[h][1][0], x[h][1][1]);
+            } else {
+                sink.put(lane >> 2, 16 * h + 2 * c, x[h][0][0], x[h][0][1]);
+                sink.put(lane >> 2, 16 * h + 8 + 2 * c, x[h][1][0], x[h][1][1]);
             }
         }
 #pragma unroll
@@ -968,8 +986,10 @@ struct SimtSums : decode::SimtMath<QT, KV, D, BS, G> {
     using Base::PASSES;
     using Base::X;
 
+    template <class Sink = NoSink>
     __device__ __forceinline__ static void tile(State& st, const unsigned char* kt, const unsigned char* vt,
-                                                int ntok, int lane, const float* qs, float* pb) {
+                                                int ntok, int lane, const float* qs, float* pb,
+                                                const Sink& sink = Sink()) {
         const int t = lane % BS, cp = lane / BS;
         float s4[G][4];
 #pragma unroll
@@ -996,6 +1016,7 @@ struct SimtSums : decode::SimtMath<QT, KV, D, BS, G> {
             float s = (s4[g][0] + s4[g][1]) + (s4[g][2] + s4[g][3]);
             if constexpr (CPP == 2) s += __shfl_xor_sync(kFull, s, 16);
             if (t >= ntok) s = -INFINITY;
+            if (cp == 0) sink.put(g, t, s);
             float mx = s;
 #pragma unroll
             for (int o = BS / 2; o >= 1; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(kFull, mx, o));
