@@ -271,11 +271,30 @@ __global__ void __launch_bounds__(kFinishThreads) weighed_finish_kernel(const Pa
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int row = blockIdx.y, b = row / p.num_kv_heads, hk = row - b * p.num_kv_heads;
     const int L = min(max(p.seq_lens[b], 0), max_len);     // flagged by the first kernel
-    const int t0 = blockIdx.x * kFinishTokens;
-    if (t0 >= L && blockIdx.x > 0) return;
+    const bool merges = p.parts > 1 && blockIdx.x == 0;    // the first CTA of a row in several partitions
+    const int t0 = ((int)blockIdx.x - (p.parts > 1)) * kFinishTokens, t = t0 + 4 * tid;
+    if (!merges && t0 >= L) return;                        // the whole CTA
     const int stages = (L + stage_tokens - 1) / stage_tokens;
     const int parts = max(1, (stages + p.part_stages - 1) / p.part_stages);
     const float* const ml = p.part_ml + (size_t)row * p.parts * 2 * G;
+    // what does not wait for the heads' sums is read ahead of them
+    int to = b;
+    bool bad = false;
+    float4 x[G], before = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!merges) {
+        if (p.rows) {                                      // good, and no earlier sequence's
+            to = p.rows[b];
+            bad = to < 0 || to >= p.num_rows;
+            for (int i = tid; i < b; i += kFinishThreads) bad |= p.rows[i] == to;
+        }
+        if (t < L) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                x[g] = *reinterpret_cast<const float4*>(p.logits + ((size_t)row * G + g) * p.pitch + t);
+        }
+    }
+    float* const at = p.weights + ((size_t)to * p.num_kv_heads + hk) * p.max_tokens + t;
+    if (!merges && t < L && to >= 0 && to < p.num_rows) before = *reinterpret_cast<const float4*>(at);
     if (w < G) {
         float M = -INFINITY, sum = 0.f;
         for (int i = lane; i < parts; i += 32) M = max_nan(M, ml[i * 2 * G + w]);
@@ -290,52 +309,69 @@ __global__ void __launch_bounds__(kFinishThreads) weighed_finish_kernel(const Pa
             head_inv[w] = M == -INFINITY ? 0.f : 1.f / sum;   // a NaN sum stays one
         }
     }
-    // the sequence's row of weights: good, and no earlier sequence's
-    int to = b;
-    if (p.rows) {
-        to = p.rows[b];
-        bool bad = to < 0 || to >= p.num_rows;
-        for (int i = tid; i < b; i += kFinishThreads) bad |= p.rows[i] == to;
-        if (__syncthreads_or(bad)) {
-            if (tid == 0) flag_error(p.err, kErrOutOfRange);
-            to = -1;
-        }
-    } else {
-        __syncthreads();
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) flag_error(p.err, kErrOutOfRange);
+        return;
     }
-    const int t = t0 + 4 * tid;
-    if (to >= 0 && t < L) {
-        const float* const x = p.logits + (size_t)row * G * p.pitch + t;
+    if (!merges) {
+        if (t >= L) return;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            const float4 v = *reinterpret_cast<const float4*>(x + (size_t)g * p.pitch);
             const float m = head_m[g], by = head_inv[g] * p.lift;
-            sum[0] += ex2(v.x - m) * by;
-            sum[1] += ex2(v.y - m) * by;
-            sum[2] += ex2(v.z - m) * by;
-            sum[3] += ex2(v.w - m) * by;
+            sum[0] += ex2(x[g].x - m) * by;
+            sum[1] += ex2(x[g].y - m) * by;
+            sum[2] += ex2(x[g].z - m) * by;
+            sum[3] += ex2(x[g].w - m) * by;
         }
-        float* const at = p.weights + ((size_t)to * p.num_kv_heads + hk) * p.max_tokens + t;
         if (t + 4 < L) {                                   // four older ones
-            const float4 v = *reinterpret_cast<const float4*>(at);
-            *reinterpret_cast<float4*>(at) = make_float4(fmaf(p.decay, v.x, sum[0]), fmaf(p.decay, v.y, sum[1]),
-                                                         fmaf(p.decay, v.z, sum[2]), fmaf(p.decay, v.w, sum[3]));
+            *reinterpret_cast<float4*>(at) = make_float4(fmaf(p.decay, before.x, sum[0]), fmaf(p.decay, before.y, sum[1]),
+                                                         fmaf(p.decay, before.z, sum[2]), fmaf(p.decay, before.w, sum[3]));
         } else {
+            const float old[4] = {before.x, before.y, before.z, before.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (t + j < L) at[j] = t + j < L - 1 ? fmaf(p.decay, at[j], sum[j]) : sum[j];
+                if (t + j < L) at[j] = t + j < L - 1 ? fmaf(p.decay, old[j], sum[j]) : sum[j];
         }
+        return;
     }
-    if (blockIdx.x > 0 || p.parts == 1) return;
-    // ---- the partitions' outputs
-    for (int i = tid; i < G * D; i += kFinishThreads) {
-        const int g = i / D;
+    // ---- the partitions' outputs: J threads a piece of four dims, over every J-th partition each
+    constexpr int kQuads = G * D / 4, J = kQuads < kFinishThreads ? kFinishThreads / kQuads : 1;
+    __shared__ float4 halves[J > 1 ? kFinishThreads : 1];
+    const float4* const o = reinterpret_cast<const float4*>(p.part_o) + (size_t)row * p.parts * kQuads;
+#pragma unroll
+    for (int i0 = 0; i0 < kQuads; i0 += kFinishThreads) {
+        const int i = i0 + tid % (J > 1 ? kQuads : kFinishThreads), g = 4 * i / D;
         const float m = head_m[g];
-        float v = 0.f;
-        for (int x = 0; x < parts; ++x)
-            v += ex2(ml[x * 2 * G + g] - m) * p.part_o[((size_t)row * p.parts + x) * G * D + i];
-        decode::store_out(static_cast<QT*>(p.out) + (size_t)row * G * D + i, v * head_inv[g] * p.v_scale);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = tid / (J > 1 ? kQuads : kFinishThreads); k < parts; k += J) {
+            const float e = ex2(ml[k * 2 * G + g] - m);
+            const float4 a = o[(size_t)k * kQuads + i];
+            v.x += e * a.x;
+            v.y += e * a.y;
+            v.z += e * a.z;
+            v.w += e * a.w;
+        }
+        if constexpr (J > 1) {
+            halves[tid] = v;
+            __syncthreads();
+            if (tid >= kQuads) return;
+#pragma unroll
+            for (int j = 1; j < J; ++j) {
+                const float4 a = halves[tid + j * kQuads];
+                v.x += a.x;
+                v.y += a.y;
+                v.z += a.z;
+                v.w += a.w;
+            }
+        }
+        const float by = head_inv[g] * p.v_scale;
+        QT* const dst = static_cast<QT*>(p.out) + (size_t)row * G * D + 4 * i;
+        decode::store_out(dst, v.x * by);
+        decode::store_out(dst + 1, v.y * by);
+        decode::store_out(dst + 2, v.z * by);
+        decode::store_out(dst + 3, v.w * by);
     }
 }
 
@@ -366,7 +402,7 @@ int launch(const Args& a) {
     cudaError_t e = launch_pdl(kern, dim3((unsigned)(rows * p.parts)), dim3(kWarps * 32), S::kBytes, a.stream, p);
     if (e != cudaSuccess) return cuda_fail("weighed decode: kernel launch", e);
     note_launch();
-    const dim3 grid((unsigned)((p.max_blocks * (BS / PAIR) + kFinishTokens - 1) / kFinishTokens), (unsigned)rows);
+    const dim3 grid((unsigned)((p.max_blocks * (BS / PAIR) + kFinishTokens - 1) / kFinishTokens + (p.parts > 1)), (unsigned)rows);
     e = launch_pdl(weighed_finish_kernel<QT, D, G>, grid, dim3(kFinishThreads), 0, a.stream, p, (int)BS,
                    p.max_blocks * (BS / PAIR));
     return e == cudaSuccess ? PKV_OK : cuda_fail("weighed decode: weights launch", e);
