@@ -33,8 +33,8 @@ namespace pkv {
 namespace weigh {
 
 constexpr int kTile = 128;             // rows, keys of a tile
-constexpr int kThreads = 192;
-constexpr int kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kThreads = 320;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;               // warps 0-3, 4-7: a lane of tensor memory a thread
 constexpr uint32_t kTmemCols = 256;    // two products
 constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kTile, kTile);
 constexpr int kTargetCtas = 608;       // of the stats pass: two waves of two CTAs an SM
@@ -53,7 +53,8 @@ struct Params {
     int* err;
     int num_seqs, max_query_len, window, max_blocks, num_blocks, num_rows, max_tokens;
     int num_heads, num_kv_heads, G, row_tiles, splits, key_tiles, per;
-    float scale_log2, decay;
+    float scale_log2, decay;           // the scale's magnitude,
+    uint32_t q_sign;                   // and what turns its sign on pairs of query elements
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -66,14 +67,60 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Two float32 numbers an instruction
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
         "r"(bytes), "r"(bar)
         : "memory");
 }
-// The four warps that own tensor memory's lanes
-__device__ __forceinline__ void lanes_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The four warps of a warpgroup; both of them
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+__device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float cluster_ld(const float* p, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
 
 // One sequence's chunk, or w == 0: nothing to do
 struct Chunk {
@@ -161,7 +208,7 @@ struct Pipe {
         const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarDone + s), (i >> 1) & 1, err));
         if (!ok) return false;
         tc::fence_after_sync();
-        const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + s * kTile;
+        const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + s * kTile;
         uint32_t v[2][32];
         tc::ld32(at, v[0]);
 #pragma unroll
@@ -205,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_stats_kernel(const Params p
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) uint64_t bars[kNumBars];
     __shared__ uint32_t tmem_slot;
+    __shared__ float2 other[kTile];                        // the second warpgroup's statistics
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = blockIdx.x, rt = blockIdx.y, item = blockIdx.z, b = item / p.num_kv_heads, hk = item - b * p.num_kv_heads;
     const Chunk ch(p, b, BS, tid == 0);
@@ -229,16 +277,18 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_stats_kernel(const Params p
         tc::alloc(smem_addr(&tmem_slot), kTmemCols);
         tc::relinquish_alloc_permit();
     }
-    if (warp < 4) {                                        // row r0 + tid: to shared memory and the workspace
-        const int r = r0 + tid;
+    if (warp < 8) {                                        // half a row: to shared memory and the workspace
+        const int r = r0 + (tid & 127), c0 = (tid >> 7) * (D / 16);
         const bool valid = r < nr;
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + ((size_t)(ch.q_first + (valid ? r / p.G : 0)) * p.num_heads + hk * p.G + (valid ? r % p.G : 0)) * D);
-        const int at = (tid >> 3) * P::kGroup + (tid & 7) * 16;
+        const int at = ((tid & 127) >> 3) * P::kGroup + (tid & 7) * 16;
         unsigned char* const to = p.q_tiles + ((size_t)item * p.row_tiles + rt) * P::kTileBytes + at;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = valid ? src[c] : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < D / 16; ++i) {
+            const int c = c0 + i;
+            uint4 v = valid ? src[c] : make_uint4(0, 0, 0, 0);
+            v = make_uint4(v.x ^ p.q_sign, v.y ^ p.q_sign, v.z ^ p.q_sign, v.w ^ p.q_sign);
             *reinterpret_cast<uint4*>(smem + at + c * 128) = v;
             if (split == 0) *reinterpret_cast<uint4*>(to + c * 128) = v;
         }
@@ -255,41 +305,59 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_stats_kernel(const Params p
     } else if (warp == kMmaWarp) {
         pipe.run_mma(n, lane, false, true);
     } else {
-        const int r = r0 + tid, pr = ch.L - ch.w + min(r, nr - 1) / p.G;
-        float m = -INFINITY, l = 0.f;
+        const int group = warp >> 2, me = tid & 127;
+        const int r = r0 + me, pr = ch.L - ch.w + min(r, nr - 1) / p.G;
+        const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
+        float m = -INFINITY, l = 0.f;                      // of the raw products; the scale is not negative
         bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
+        for (int i = group; i < n && ok; i += 2) {         // the groups take turns
             const int key0 = (k0 + i) * kTile;
             const bool masked = any_bad || key0 + kTile - 1 > p_min;
-            ok = pipe.take(i, warp, [&](int c0, const uint32_t (&v)[32]) {
-                float x[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(v[c]) * p.scale_log2;
+            ok = pipe.take(i, warp, [&](int c0, uint32_t (&v)[32]) {
                 if (masked) {
+                    constexpr uint32_t kNone = 0xff800000u;   // -infinity
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) x[c] = key0 + c0 + c <= pr ? x[c] : -INFINITY;
+                    for (int c = 0; c < 32; ++c) v[c] = key0 + c0 + c <= pr ? v[c] : kNone;
                     if (any_bad)
                         for (int s = 0; s < 32 / BS; ++s) {
                             const int blk = (key0 + c0) / BS + s;
                             const int id = blk <= p_max / BS ? table[blk] : 0;
                             if (id < 0 || id >= p.num_blocks)
 #pragma unroll
-                                for (int c = 0; c < 32; ++c) x[c] = c / BS == s ? -INFINITY : x[c];
+                                for (int c = 0; c < 32; ++c) v[c] = c / BS == s ? kNone : v[c];
                         }
                 }
-                float mx = m;
+                float m4[4] = {m, m, m, m};
 #pragma unroll
-                for (int c = 0; c < 32; ++c) mx = max_nan(mx, x[c]);
-                const float base = mx == -INFINITY ? 0.f : mx;
-                float sum = 0.f;
+                for (int c = 0; c < 32; c += 2)
+                    m4[(c >> 1) & 3] = max_nan(m4[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                const float mx = max_nan(max_nan(m4[0], m4[1], m4[2]), m4[3]);
+                const float base = mx == -INFINITY ? 0.f : mx * p.scale_log2;
+                const uint64_t nb2 = f2(-base, -base);
+                uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
-                for (int c = 0; c < 32; ++c) sum += ex2(x[c] - base);
-                l = fmaf(l, ex2(m - base), sum);
+                for (int c = 0; c < 32; c += 2) {
+                    float a, b;
+                    f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nb2), a, b);
+                    s2[(c >> 1) & 1] = add2(s2[(c >> 1) & 1], f2(ex2(a), ex2(b)));
+                }
+                float a, b, c, d;
+                f2_split(s2[0], a, b);
+                f2_split(s2[1], c, d);
+                l = fmaf(l, ex2(fmaf(m, p.scale_log2, -base)), (a + b) + (c + d));
                 m = mx;
             });
         }
         if (!ok) flag_error(p.err, kErrTimeout);
-        p.stats[(((size_t)item * p.row_tiles + rt) * p.splits + split) * kTile + tid] = make_float2(m, l);
+        m = m == -INFINITY ? m : m * p.scale_log2;
+        if (group == 1) other[me] = make_float2(m, l);
+        groups_sync();
+        if (group == 0) {
+            const float2 o = other[me];
+            const float mx = max_nan(m, o.x), base = mx == -INFINITY ? 0.f : mx;
+            p.stats[(((size_t)item * p.row_tiles + rt) * p.splits + split) * kTile + me] =
+                make_float2(mx, l * ex2(m - base) + o.y * ex2(o.x - base));
+        }
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -300,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_stats_kernel(const Params p
 }
 
 // kStreamKeys: one row tile, held, and p.per key tiles; else a key tile, held, and the row
-// tiles that see it.
+// tiles that see it, every csize-th for each CTA of a cluster, whose gains meet in its first.
 template <int D, int BS, bool kStreamKeys>
 __global__ void __launch_bounds__(kThreads, 2) weigh_gain_kernel(const Params p) {
     pdl_enter();
@@ -308,18 +376,20 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_gain_kernel(const Params p)
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(8) uint64_t bars[kNumBars];
     __shared__ uint32_t tmem_slot;
-    __shared__ __align__(16) float base[2][kTile];         // M_r of a row tile
+    __shared__ __align__(16) float base[2][kTile];         // M_r of the row tile a warpgroup works on
+    __shared__ float part[2][kTile];                       // gains of the second group, of the CTA
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = kStreamKeys ? 0 : (int)cluster_rank(), csize = kStreamKeys ? 1 : (int)cluster_size();
     // the items that the first pass read last come first: their keys may still be in L2
     const int item = gridDim.y - 1 - blockIdx.y, b = item / p.num_kv_heads, hk = item - b * p.num_kv_heads;
     const Chunk ch(p, b, BS, false);
-    if (ch.w == 0) return;                                 // the whole CTA
+    if (ch.w == 0) return;                                 // the whole cluster
     const int tiles = (ch.L + kTile - 1) / kTile, nr = ch.w * p.G, row_tiles = (nr + kTile - 1) / kTile;
-    const int kt0 = kStreamKeys ? blockIdx.x * p.per : blockIdx.x;
+    const int kt0 = kStreamKeys ? blockIdx.x * p.per : blockIdx.x / csize;
     if (kt0 >= tiles) return;
     const int first_pos = ch.L - ch.w;                     // of the first query that counts
-    const int rt0 = kStreamKeys ? 0 : max(0, kt0 * kTile - first_pos) * p.G / kTile;
-    const int n = kStreamKeys ? min(p.per, tiles - kt0) : row_tiles - rt0;
+    const int rt0 = kStreamKeys ? 0 : max(0, kt0 * kTile - first_pos) * p.G / kTile + rank;
+    const int n = kStreamKeys ? min(p.per, tiles - kt0) : max(0, (row_tiles - rt0 + csize - 1) / csize);
     int to = b;
     bool lost = false;
     if (p.rows) {
@@ -359,22 +429,32 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_gain_kernel(const Params p)
     if (warp == kLoadWarp) {
         pipe.run_load(n, lane, true, [&](int i, uint32_t dst, uint32_t bar) {
             if (kStreamKeys) load_keys<D, BS>(p, b, hk, ch.L, kt0 + i, lane, dst, bar);
-            else load_rows(rt0 + i, dst, bar);
+            else load_rows(rt0 + i * csize, dst, bar);
         });
     } else if (warp == kMmaWarp) {
         pipe.run_mma(n, lane, true, !kStreamKeys);
     } else {
-        // M of row tid of a tile: +infinity (no gain) for rows that are not there or have no weight
-        auto row_base = [&](int rt) {
-            if (rt * kTile + tid >= nr) return INFINITY;
-            const int last = first_pos + (min(nr, (rt + 1) * kTile) - 1) / p.G;
-            const int tiles_r = last / kTile + 1, per = (tiles_r + p.splits - 1) / p.splits, splits = (tiles_r + per - 1) / per;
-            const float2* at = p.stats + ((size_t)item * p.row_tiles + rt) * p.splits * kTile + tid;
-            float m = -INFINITY, l = 0.f;
-            for (int s = 0; s < splits; ++s) m = max_nan(m, at[s * kTile].x);
-            if (m == -INFINITY) return INFINITY;
-            for (int s = 0; s < splits; ++s) l += ex2(at[s * kTile].x - m) * at[s * kTile].y;
-            return m + log2f(l);
+        const int group = warp >> 2, me = tid & 127;
+        // Row me of tile rt: its first statistics, and M: +infinity (no gain) for rows that are not
+        // there or that see no token
+        auto stats_at = [&](int rt) { return p.stats + ((size_t)item * p.row_tiles + rt) * p.splits * kTile + me; };
+        auto first_of = [&](int rt) {
+            return rt < row_tiles && rt * kTile + me < nr ? stats_at(rt)[0] : make_float2(-INFINITY, 0.f);
+        };
+        auto base_of = [&](int rt, float2 first) {
+            float m = first.x, l = first.y;
+            if (p.splits > 1 && rt * kTile + me < nr) {
+                const int last = first_pos + (min(nr, (rt + 1) * kTile) - 1) / p.G;
+                const int tiles_r = last / kTile + 1, per = (tiles_r + p.splits - 1) / p.splits, splits = (tiles_r + per - 1) / per;
+                const float2* at = stats_at(rt);
+#pragma unroll 8
+                for (int s = 1; s < splits; ++s) m = max_nan(m, at[s * kTile].x);
+                l = 0.f;
+                const float by = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
+                for (int s = 0; s < splits; ++s) l += ex2(at[s * kTile].x - by) * at[s * kTile].y;
+            }
+            return m == -INFINITY ? INFINITY : m + log2f(l);
         };
         const int32_t* const table = p.block_tables + (size_t)b * p.max_blocks;
         float* const out = p.weights + ((size_t)to * p.num_kv_heads + hk) * p.max_tokens;
@@ -384,49 +464,80 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_gain_kernel(const Params p)
             if (id < 0 || id >= p.num_blocks) gain = 0.f;
             out[t] = t < ch.L - ch.C ? fmaf(p.decay, out[t], gain) : gain;
         };
+        const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
         float total = 0.f;
         bool ok = true;
+        float2 first = first_of(rt0 + (kStreamKeys ? 0 : group * csize));
         if (kStreamKeys) {
-            base[0][tid] = row_base(0);
-            lanes_sync();
+            base[group][me] = base_of(0, first);
+            group_sync(group);
         }
-        for (int i = 0; i < n; ++i) {                      // to the end: all four warps meet in lanes_sync
-            const int kt = kStreamKeys ? kt0 + i : kt0, rt = kStreamKeys ? 0 : rt0 + i, t = kt * kTile + tid;
-            const float* const bs = base[kStreamKeys ? 0 : i & 1];
+        const float* const bs = base[group];
+        for (int i = group; i < n; i += 2) {               // to the end: a group's warps meet in group_sync
+            const int kt = kStreamKeys ? kt0 + i : kt0, rt = kStreamKeys ? 0 : rt0 + i * csize, t = kt * kTile + me;
             if (!kStreamKeys) {
-                base[i & 1][tid] = row_base(rt);
-                lanes_sync();                              // the other buffer is read before the next one
+                const float mine = base_of(rt, first);
+                group_sync(group);                         // the last tile's are read
+                base[group][me] = mine;
+                group_sync(group);
+                first = first_of(rt + 2 * csize);
             }
             // token t is seen by the rows from column `from` of this tile on; past the last row a
             // product may be a NaN (zeros times an infinite key)
             const int from = max(0, t - first_pos) * p.G - rt * kTile, until = nr - rt * kTile;
             const bool masked = kt * kTile + kTile - 1 > first_pos + rt * kTile / p.G || until < kTile;
-            float g4[4] = {0.f, 0.f, 0.f, 0.f};
-            ok = ok && pipe.take(i, warp, [&](int c0, const uint32_t (&v)[32]) {
+            uint64_t g2[2] = {0ull, 0ull};
+            ok = ok && pipe.take(i, warp, [&](int c0, uint32_t (&v)[32]) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) {
                     const float4 m = *reinterpret_cast<const float4*>(bs + c0 + c);
-                    float x[4] = {ex2(fmaf(__uint_as_float(v[c]), p.scale_log2, -m.x)),
-                                  ex2(fmaf(__uint_as_float(v[c + 1]), p.scale_log2, -m.y)),
-                                  ex2(fmaf(__uint_as_float(v[c + 2]), p.scale_log2, -m.z)),
-                                  ex2(fmaf(__uint_as_float(v[c + 3]), p.scale_log2, -m.w))};
+                    float x[4];
+                    f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, f2(-m.x, -m.y)), x[0], x[1]);
+                    f2_split(fma2(f2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), sc2, f2(-m.z, -m.w)), x[2], x[3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = ex2(x[j]);
                     if (masked) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) x[j] = c0 + c + j >= from && c0 + c + j < until ? x[j] : 0.f;
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) g4[j] += x[j];
+                    g2[0] = add2(g2[0], f2(x[0], x[1]));
+                    g2[1] = add2(g2[1], f2(x[2], x[3]));
                 }
             });
-            const float gain = (g4[0] + g4[1]) + (g4[2] + g4[3]);
+            float x, y, z, w;
+            f2_split(g2[0], x, y);
+            f2_split(g2[1], z, w);
+            const float gain = (x + y) + (z + w);
             if (kStreamKeys) {
                 if (ok) write(t, gain);
             } else {
                 total += gain;
             }
         }
-        if (!kStreamKeys && ok) write(kt0 * kTile + tid, total);
         if (!ok) flag_error(p.err, kErrTimeout);
+        if (!kStreamKeys) {
+            if (group == 1) part[0][me] = total;
+            groups_sync();
+            if (group == 0) {
+                total += part[0][me];
+                if (csize == 1) write(kt0 * kTile + me, total);
+                else part[1][me] = total;
+            }
+        }
+    }
+    if (!kStreamKeys && csize > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (rank == 0 && tid < kTile && kt0 * kTile + tid < ch.L) {
+            const int t = kt0 * kTile + tid, id = p.block_tables[(size_t)b * p.max_blocks + t / BS];
+            float gain = 0.f;
+            for (int r = 0; r < csize; ++r) gain += cluster_ld(&part[1][tid], r);
+            if (id < 0 || id >= p.num_blocks) gain = 0.f;
+            float* const at = p.weights + ((size_t)to * p.num_kv_heads + hk) * p.max_tokens + t;
+            *at = t < ch.L - ch.C ? fmaf(p.decay, *at, gain) : gain;
+        }
+        __syncwarp();
+        cluster_sync();                                    // the others' shared memory is read
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -471,9 +582,27 @@ int launch(Params p, cudaStream_t stream) {
         p.per = (int)(all / kTargetCtas);
         p.per = p.per < 1 ? 1 : p.per > 16 ? 16 : p.per;
     }
+    // CTAs that share a key tile's rows: a few row tiles each, seven waves or so
+    const long long key_ctas = ((long long)p.key_tiles + p.per - 1) / p.per;
+    int size = 1;
+    if (p.row_tiles > 1)
+        while (size < 8 && key_ctas * items * size < 2048 && p.row_tiles / size > 4) size *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(key_ctas * size), (unsigned)items);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = P::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     note_launch();
-    e = launch_pdl(gain, dim3((unsigned)((p.key_tiles + p.per - 1) / p.per), (unsigned)items), dim3(kThreads), P::kSmem,
-                   stream, p);
+    e = cudaLaunchKernelEx(&cfg, gain, p);
     return e == cudaSuccess ? PKV_OK : cuda_fail("weigh_prefill_tokens: weights launch", e);
 }
 
@@ -542,7 +671,9 @@ extern "C" int weigh_prefill_tokens(float* token_weights, const int32_t* weight_
     p.row_tiles = (int)shape.row_tiles;
     p.splits = (int)shape.splits;
     p.key_tiles = (max_blocks_per_seq * block_size + weigh::kTile - 1) / weigh::kTile;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    // never 0: hidden logits are -infinity times it
+    p.scale_log2 = scale == 0.f ? 1.17549435e-38f : std::fabs(scale) * 1.4426950408889634f;
+    p.q_sign = scale < 0.f ? 0x80008000u : 0u;
     p.decay = decay;
     p.q_tiles = static_cast<unsigned char*>(workspace);
     p.stats = reinterpret_cast<float2*>(p.q_tiles + (size_t)(shape.items * shape.row_tiles) * weigh::kTile * head_dim * 2);
