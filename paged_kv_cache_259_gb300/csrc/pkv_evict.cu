@@ -4,14 +4,15 @@
 // select_tokens. A row is one (sequence, kv head): up to hundreds of thousands of float32
 // weights, of which the R = num_kept - first - last largest between the always-kept ends are
 // wanted, ties to the lower token. The weights become 32-bit keys that order as unsigned
-// numbers, are read once into the shared memory of a cluster of CTAs (a contiguous slice
-// each), and the R-th largest is found digit by digit (11, 11 and 10 bits): every CTA
-// counts its keys' digits, the counts are summed over the cluster through distributed shared
-// memory, and the digit in which the R-th falls narrows the keys of the next pass. The taken
-// keys are those above the threshold and the first few equal to it; every warp counts both in
-// its run of the slice, and prefix sums over warps and CTAs give each its places in the list,
-// which so comes out ascending. Bound: the reads (4 bytes a token) for many rows, the chain of
-// passes and cluster barriers for few.
+// numbers, are read once into registers (of one CTA, or of a cluster's, a contiguous slice
+// each), and the R-th largest is found by narrowing the range of keys that it lies in: from the
+// smallest and largest key there are, 2048 bins over the range are counted, summed over the
+// cluster through distributed shared memory, and the bin that holds the R-th is the next range
+// (at most three times; once or twice where weights differ, as the bins begin where the weights
+// do: a fixed first digit left a tenth of the keys in one bin). The taken keys are those above
+// the threshold and the first few equal to it; prefix sums over threads, warps and CTAs give
+// each its place in the list, which so comes out ascending. Bound: the reads (4 bytes a token)
+// for many rows, the chain of passes and barriers for few.
 //
 // keep_tokens. K: 16-byte pieces, one per (token, X dims), to their new place: eight
 // neighbouring threads write a whole 128-byte core matrix. V is stored transposed: a thread
@@ -45,10 +46,8 @@ __device__ __forceinline__ int weight_row(const int32_t* rows, int b, int num_ro
 }
 
 // ------------------------------------------------------------------ select_tokens
-constexpr int kSelWarps = 16, kSelThreads = kSelWarps * 32;
-constexpr int kBins = 2048, kPasses = 3;
-constexpr int kMaxCached = 45056;      // keys of a CTA's slice in shared memory (176 KB)
-constexpr int kMaxCluster = 8;         // the portable size
+constexpr int kBins = 2048, kPasses = 3;                   // 11 bits a pass, of 32
+constexpr int kMaxCluster = 8;                             // the portable size
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -63,19 +62,38 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
-// a word of the cluster's CTA `rank`, at this CTA's address of it
-__device__ __forceinline__ uint32_t cluster_ld(const void* p, uint32_t rank) {
-    uint32_t a, v;
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return a;
+}
+__device__ __forceinline__ uint2 cluster_ld2(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 cluster_ld4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
     return v;
 }
 
-// A weight as an unsigned number of the same order; -0 as 0; what is not finite on top.
+// A weight as an unsigned number of the same order; -0 as 0; what is not finite above the rest.
+// Below all of them the key of no token, above them that of a token which is always kept.
+constexpr uint32_t kNoKey = 0u, kNotFinite = 0xfffffffeu, kAlways = 0xffffffffu;
 __device__ __forceinline__ uint32_t key_of(float w) {
-    uint32_t x = __float_as_uint(w + 0.f);
-    if ((x & 0x7f800000u) == 0x7f800000u) return 0xffffffffu;
-    return x & 0x80000000u ? ~x : x | 0x80000000u;
+    const uint32_t x = __float_as_uint(w + 0.f);
+    const uint32_t key = x ^ ((uint32_t)((int)x >> 31) | 0x80000000u);
+    return fabsf(w) <= 3.402823466e38f ? key : kNotFinite;
+}
+// One more in bin d >> shift, where d <= span: a predicated instruction, no branch
+__device__ __forceinline__ void count_key(uint32_t bins, uint32_t d, uint32_t span, int shift) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.le.u32 p, %0, %1;\n\t@p red.shared.add.u32 [%2], 1;\n\t}" ::"r"(d), "r"(span),
+                 "r"(bins + (d >> shift) * 4u)
+                 : "memory");
 }
 
 struct SelectParams {
@@ -85,16 +103,21 @@ struct SelectParams {
     const int32_t* seq_lens;
     int* err;
     int num_kv_heads, num_rows, max_tokens, k, first, last;
-    int cached;                        // keys that a CTA's shared memory holds
 };
 
-__global__ void __launch_bounds__(kSelThreads) select_tokens_kernel(const SelectParams p) {
+// A CTA's slice of a row: NT threads, V pieces of 4 tokens each in registers (piece j of thread i
+// at token 4 (j NT + i)); kLong: slices may be longer, further rounds are read from memory in
+// every pass.
+template <int NT, int V, bool kLong>
+__global__ void __launch_bounds__(NT, 2048 / NT >= 8 ? 4 : 2) select_tokens_kernel(const SelectParams p) {
     pdl_enter();
-    extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ uint32_t hist[kPasses][kBins];
-    __shared__ uint32_t warp_sum[kSelWarps];
-    __shared__ uint32_t found[2];                          // digit, keys above it
-    __shared__ uint32_t taken[kSelWarps][2], cta_taken[2]; // above the threshold, equal to it
+    constexpr int kWarps = NT / 32, kRound = NT * 4 * V, kQuads = kBins / 4 / NT;
+    static_assert(kBins % (4 * NT) == 0, "bins a thread");
+    __shared__ __align__(16) uint32_t hist[kPasses][kBins];
+    __shared__ uint32_t warp_sum[kWarps], warp_min[kWarps], warp_max[kWarps];
+    __shared__ uint32_t found[3];                          // digit, keys above it, keys of it
+    __shared__ uint32_t run[V * kWarps];                   // taken in each piece of each warp; then before it
+    __shared__ __align__(8) uint32_t cta_range[2], cta_taken[2], round_taken;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank(), csize = (int)cluster_size();
     const int item = (int)(blockIdx.x / csize), b = item / p.num_kv_heads, h = item - b * p.num_kv_heads;
@@ -107,44 +130,120 @@ __global__ void __launch_bounds__(kSelThreads) select_tokens_kernel(const Select
     if (row < 0) n = 0;
     int32_t* const out = p.kept + (size_t)item * p.k;
     if (n <= p.k) {                                        // the whole cluster
-        for (int i = rank * kSelThreads + tid; i < p.k; i += csize * kSelThreads) out[i] = i < n ? i : -1;
+        for (int i = rank * NT + tid; i < p.k; i += csize * NT) out[i] = i < n ? i : -1;
         return;
     }
-    const float* const src = p.weights + ((size_t)row * p.num_kv_heads + h) * p.max_tokens;
-    // this CTA's slice, a multiple of 4 tokens
-    const int slice = ((n + csize - 1) / csize + 3) & ~3;
+    // a row that one CTA holds is its own: no trips through the cluster
+    const bool alone = csize == 1 || n <= kRound;
+    if (alone && rank > 0) return;
+    const int slice = alone ? n : ((n + csize - 1) / csize + 3) & ~3;
     const int begin = min(n, rank * slice), count = min(n, begin + slice) - begin;
-    const int cached = min(count, p.cached);
-    for (int i = tid; i < kPasses * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
-    for (int i = 4 * tid; i < cached; i += 4 * kSelThreads) {   // the last piece may pass n, not the row
-        const float4 v = *reinterpret_cast<const float4*>(src + begin + i);
-        *reinterpret_cast<uint4*>(keys + i) = make_uint4(key_of(v.x), key_of(v.y), key_of(v.z), key_of(v.w));
-    }
-    auto key = [&](int i) { return i < cached ? keys[i] : key_of(src[begin + i]); };
-    // ---- the R-th largest of the tokens between the ends
+    const float* const src = p.weights + ((size_t)row * p.num_kv_heads + h) * p.max_tokens + begin;
+    // the tokens between the ends
     const int lo = max(0, p.first - begin), hi = min(count, n - p.last - begin);
-    uint32_t need = (uint32_t)(p.k - p.first - p.last);    // still to be found at or below `prefix`
-    uint32_t threshold = 0xffffffffu;                      // taken: keys above it, `need` equal ones
-    __syncthreads();
-    if (need > 0) {
-        uint32_t prefix = 0;
-        for (int pass = 0; pass < kPasses; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-            const uint32_t mask = (1u << bits) - 1u;
-            for (int i = lo + tid; i < hi; i += kSelThreads) {
-                const uint32_t x = key(i);
-                if (pass == 0 || (x >> (shift + bits)) == prefix) atomicAdd(&hist[pass][(x >> shift) & mask], 1u);
-            }
-            if (csize > 1) cluster_sync();
-            else __syncthreads();
-            // bins 4 tid .. 4 tid + 3 counted from the top
-            uint32_t c[4], sum = 0;
+    uint32_t key[V][4];
+    auto load = [&](int round) {
+        float4 v[V];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int bin = kBins - 1 - (4 * tid + j);
-                c[j] = 0;
-                for (int r = 0; r < csize; ++r) c[j] += csize > 1 ? cluster_ld(&hist[pass][bin], r) : hist[pass][bin];
-                sum += c[j];
+        for (int j = 0; j < V; ++j) {                      // a piece may pass n, not the row's end
+            const int i = round * kRound + 4 * (j * NT + tid);
+            v[j] = i < count ? *reinterpret_cast<const float4*>(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = round * kRound + 4 * (j * NT + tid);
+            const float f[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) key[j][e] = key_of(f[e]);
+            if (i < lo || i + 3 >= hi) {                   // an end of the sequence
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i + e < lo || i + e >= hi) key[j][e] = i + e < count ? kAlways : kNoKey;
+            }
+        }
+    };
+    const int rounds = kLong ? (count + kRound - 1) / kRound : 1;
+    auto each_round = [&](auto f) {                        // f(round) with its keys in registers
+        for (int r = 0; r < rounds; ++r) {
+            if (kLong && rounds > 1) load(r);
+            f(r);
+        }
+    };
+    auto sync = [&] {
+        if (alone) __syncthreads();
+        else cluster_sync();
+    };
+    if (!kLong || rounds <= 1) load(0);
+    for (int i = tid; i < kPasses * kBins / 4; i += NT) reinterpret_cast<uint4*>(&hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+    uint32_t need = (uint32_t)(p.k - p.first - p.last);    // still to be found at or below the range
+    uint32_t threshold = kNotFinite;                       // taken: keys above it, `need` equal ones
+    if (need > 0) {
+        // ---- the range of the keys: the first digit then tells apart what is there
+        uint32_t mn = 0xffffffffu, mx = 0;
+        each_round([&](int) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    mn = min(mn, key[j][e] - 1u);          // no key, always: they wrap to the other end
+                    mx = max(mx, key[j][e] + 1u);
+                }
+        });
+        mn = __reduce_min_sync(kFull, mn);
+        mx = __reduce_max_sync(kFull, mx);
+        if (lane == 0) {
+            warp_min[w] = mn;
+            warp_max[w] = mx;
+        }
+        __syncthreads();
+        mn = __reduce_min_sync(kFull, warp_min[lane % kWarps]);
+        mx = __reduce_max_sync(kFull, warp_max[lane % kWarps]);
+        if (!alone) {
+            if (tid == 0) {
+                cta_range[0] = mn;
+                cta_range[1] = mx;
+            }
+            cluster_sync();
+            const uint2 r = lane < csize ? cluster_ld2(cluster_addr(cta_range, lane)) : make_uint2(0xffffffffu, 0u);
+            mn = __reduce_min_sync(kFull, r.x);
+            mx = __reduce_max_sync(kFull, r.y);
+        }
+        mx -= 1u;
+        uint32_t base = mn + 1u, span = mx - base;         // keys base .. base + span hold the wanted one
+        for (int pass = 0;; ++pass) {
+            const int shift = max(0, 21 - __clz(span | 1u));
+            uint32_t* const bins = hist[pass];
+            const uint32_t at = smem_addr(bins);
+            each_round([&](int) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) count_key(at, key[j][e] - base, span, shift);
+            });
+            sync();
+            // this thread's bins, from the top down, and how many are above them
+            uint4 c[kQuads];
+            uint32_t sum = 0;
+            const int top = kBins - 4 - 4 * kQuads * tid;
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q) {
+                c[q] = make_uint4(0, 0, 0, 0);
+                if (alone) {
+                    c[q] = *reinterpret_cast<const uint4*>(&bins[top - 4 * q]);
+                } else {
+                    uint4 x[kMaxCluster];
+#pragma unroll
+                    for (int r = 0; r < kMaxCluster; ++r)
+                        x[r] = r < csize ? cluster_ld4(cluster_addr(&bins[top - 4 * q], r)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < kMaxCluster; ++r) {
+                        c[q].x += x[r].x;
+                        c[q].y += x[r].y;
+                        c[q].z += x[r].z;
+                        c[q].w += x[r].w;
+                    }
+                }
+                sum += c[q].x + c[q].y + c[q].z + c[q].w;
             }
             uint32_t before = sum;                         // inclusive scan over the block
 #pragma unroll
@@ -154,70 +253,124 @@ __global__ void __launch_bounds__(kSelThreads) select_tokens_kernel(const Select
             }
             if (lane == 31) warp_sum[w] = before;
             __syncthreads();
-            for (int i = 0; i < w; ++i) before += warp_sum[i];
-            before -= sum;
+            const uint32_t others = lane < w ? warp_sum[lane] : 0u;
+            before += __reduce_add_sync(kFull, others) - sum;
             if (before < need && need <= before + sum) {   // one thread
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (before < need && need <= before + c[j]) {
-                        found[0] = (uint32_t)(kBins - 1 - (4 * tid + j));
-                        found[1] = before;
+                for (int q = 0; q < kQuads; ++q) {
+                    const uint32_t four[4] = {c[q].w, c[q].z, c[q].y, c[q].x};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (before < need && need <= before + four[j]) {
+                            found[0] = (uint32_t)(top - 4 * q + 3 - j);
+                            found[1] = before;
+                            found[2] = four[j];
+                        }
+                        before += four[j];
                     }
-                    before += c[j];
                 }
             }
             __syncthreads();
-            prefix = pass == 0 ? found[0] : (prefix << bits) | found[0];
+            base += found[0] << shift;
             need -= found[1];
+            if (need == found[2]) {                        // every key of the digit
+                threshold = base - 1u;
+                need = 0;
+                break;
+            }
+            if (shift == 0) {
+                threshold = base;
+                break;
+            }
+            span = min((1u << shift) - 1u, mx - base);     // no further than the keys go
         }
-        threshold = prefix;
     }
-    // ---- the places: this warp's run of the slice
-    const int run = ((count + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int from = min(count, w * run), to = min(count, from + run);
-    const bool none = p.k == p.first + p.last;
-    auto above = [&](int i, uint32_t x) { return i < lo || i >= hi || (!none && x > threshold); };
-    uint32_t gt = 0, eq = 0;
-    for (int i = from + lane; i - lane < to; i += 32) {
-        const bool in = i < to;
-        const uint32_t x = in ? key(i) : 0u;
-        const bool a = in && above(i, x);
-        gt += __popc(__ballot_sync(kFull, a));
-        eq += __popc(__ballot_sync(kFull, in && !a && !none && x == threshold));
-    }
-    if (lane == 0) {
-        taken[w][0] = gt;
-        taken[w][1] = eq;
-    }
-    __syncthreads();
-    if (tid < 2) {
-        uint32_t s = 0;
-        for (int i = 0; i < kSelWarps; ++i) {
-            const uint32_t x = taken[i][tid];
-            taken[i][tid] = s;
-            s += x;
+    // ---- the places. Taken: the ends, keys above the threshold, the first `need` equal ones
+    // (counts of both in one word, equal ones in the upper half)
+    auto counts = [&](int j, int e) { return (key[j][e] > threshold ? 1u : 0u) + (key[j][e] == threshold ? 0x10000u : 0u); };
+    uint32_t before[V];
+    auto count_round = [&] {                               // -> before[], run[]: taken before a piece
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            uint32_t mine = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mine += counts(j, e);
+            uint32_t x = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o) x += y;
+            }
+            before[j] = x - mine;
+            if (lane == 31) run[j * kWarps + w] = x;
         }
-        cta_taken[tid] = s;
+        __syncthreads();
+        if (w == 0) {
+            constexpr int kEach = (V * kWarps + 31) / 32;
+            uint32_t r[kEach], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int at = lane * kEach + i;
+                r[i] = at < V * kWarps ? run[at] : 0u;
+                sum += r[i];
+            }
+            uint32_t x = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) round_taken = x;
+            x -= sum;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int at = lane * kEach + i;
+                if (at < V * kWarps) run[at] = x;
+                x += r[i];
+            }
+        }
+        __syncthreads();
+    };
+    uint32_t gt = 0, eq = 0;                               // taken before this CTA's current round
+    if (!alone) {
+        uint32_t all_gt = 0, all_eq = 0;
+        each_round([&](int) {
+            count_round();
+            all_gt += round_taken & 0xffffu;
+            all_eq += round_taken >> 16;
+            if (kLong) __syncthreads();
+        });
+        if (tid == 0) {
+            cta_taken[0] = all_gt;
+            cta_taken[1] = all_eq;
+        }
+        cluster_sync();
+        const uint2 x = lane < rank ? cluster_ld2(cluster_addr(cta_taken, lane)) : make_uint2(0u, 0u);
+        gt = __reduce_add_sync(kFull, x.x);
+        eq = __reduce_add_sync(kFull, x.y);
+        cluster_sync();                                    // nobody leaves while others read
     }
-    if (csize > 1) cluster_sync();
-    else __syncthreads();
-    uint32_t base_gt = taken[w][0], base_eq = taken[w][1];
-    for (int r = 0; r < rank; ++r) {
-        base_gt += cluster_ld(&cta_taken[0], r);
-        base_eq += cluster_ld(&cta_taken[1], r);
-    }
-    if (csize > 1) cluster_sync();                         // nobody leaves while others read
-    const uint32_t below = (1u << lane) - 1u;
-    for (int i = from + lane; i - lane < to; i += 32) {
-        const bool in = i < to;
-        const uint32_t x = in ? key(i) : 0u;
-        const bool a = in && above(i, x), e = in && !a && !none && x == threshold;
-        const uint32_t ga = __ballot_sync(kFull, a), ge = __ballot_sync(kFull, e);
-        const uint32_t ea = base_eq + __popc(ge & below);
-        if (a || (e && ea < need)) out[base_gt + __popc(ga & below) + min(ea, need)] = begin + i;
-        base_gt += __popc(ga);
-        base_eq += __popc(ge);
-    }
+    each_round([&](int r) {
+        if (alone || (kLong && rounds > 1)) count_round();
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint32_t at = before[j] + run[j * kWarps + w];
+            uint32_t g = gt + (at & 0xffffu), q = eq + (at >> 16);
+            const int i = begin + r * kRound + 4 * (j * NT + tid);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool above = key[j][e] > threshold, equal = key[j][e] == threshold;
+                if (above || (equal && q < need)) out[g + min(q, need)] = i + e;
+                g += above;
+                q += equal;
+            }
+        }
+        if (kLong) {
+            gt += round_taken & 0xffffu;
+            eq += round_taken >> 16;
+            __syncthreads();                               // run[] is read
+        }
+    });
 }
 
 // -------------------------------------------------------------------- keep_tokens
@@ -405,23 +558,23 @@ int select_tokens(int32_t* kept, const float* token_weights, const int32_t* weig
     p.k = num_kept;
     p.first = first_tokens;
     p.last = last_tokens;
-    int size = 1;
-    while (size < kMaxCluster && max_tokens / size > 4096 && items * size < 2LL * num_sms()) size *= 2;
-    while (size < kMaxCluster && max_tokens / size > kMaxCached) size *= 2;
-    const int slice = ((max_tokens + size - 1) / size + 3) & ~3;
-    p.cached = slice < kMaxCached ? slice : kMaxCached;
-    const void* kern = reinterpret_cast<const void*>(&select_tokens_kernel);
-    try {
-        int occ = 0;
-        const int st = kernel_setup(kern, kMaxCached * 4, kSelThreads, &occ);
-        if (st != PKV_OK) return st;
-    } catch (...) {
-        return cuda_fail("select_tokens: host memory", cudaErrorMemoryAllocation);
-    }
+    // the smallest slices that one CTA, then a cluster of up to 8, holds in registers
+    void (*kern)(SelectParams) = select_tokens_kernel<512, 8, true>;
+    int size = 1, threads = 512;
+    auto choose = [&](void (*k)(SelectParams), int nt, int v) {
+        kern = k;
+        threads = nt;
+        while (size < kMaxCluster && nt * 4 * v * size < max_tokens) size *= 2;
+    };
+    if (max_tokens <= 1024) choose(select_tokens_kernel<256, 1, false>, 256, 1);
+    else if (max_tokens <= 2048) choose(select_tokens_kernel<256, 2, false>, 256, 2);
+    else if (max_tokens <= 4096) choose(select_tokens_kernel<256, 4, false>, 256, 4);
+    else if (max_tokens <= 8192 * kMaxCluster) choose(select_tokens_kernel<256, 8, false>, 256, 8);
+    else if (max_tokens <= 16384 * kMaxCluster) choose(select_tokens_kernel<512, 8, false>, 512, 8);
+    else choose(select_tokens_kernel<512, 8, true>, 512, 8);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items * size));
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = (size_t)p.cached * 4;
+    cfg.blockDim = dim3(threads);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -433,7 +586,7 @@ int select_tokens(int32_t* kept, const float* token_weights, const int32_t* weig
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     note_launch();
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, select_tokens_kernel, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
     return e == cudaSuccess ? PKV_OK : cuda_fail("select_tokens: kernel launch", e);
 }
 
