@@ -22,6 +22,8 @@
 // overwrites nothing that a later chunk reads. Bound: HBM bytes.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "pkv_check.cuh"
 #include "pkv_internal.cuh"
 
@@ -436,16 +438,15 @@ __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const KeepPar
         keep_weights(p, blockIdx.x);
         return;
     }
-    __shared__ long long src_tile[kKeepTokens], dst_tile[kKeepTokens];   // bytes; -1: skipped
-    __shared__ int src_slot[kKeepTokens], dst_slot[kKeepTokens];
+    // of each token: its first 16-byte piece of K, its element of V's first dim; -1: skipped
+    __shared__ long long src_k[kKeepTokens], dst_k[kKeepTokens], src_v[kKeepTokens], dst_v[kKeepTokens];
     const long long unit = (long long)blockIdx.x - p.weight_ctas;
     const int item = (int)(unit / p.chunks), b = item / p.num_kv_heads, h = item - b * p.num_kv_heads;
     const int i0 = (int)(unit - (long long)item * p.chunks) * kKeepTokens;
-    const int tid = threadIdx.x;
-    const long long tile = (long long)p.d * p.bs * ES;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     if (tid < kKeepTokens) {
-        long long s = -1, o = -1;
-        int ss = 0, os = 0;
+        const long long tile = (long long)p.d * p.bs * ES;
+        long long sk = -1, dk = -1, sv = -1, dv = -1;
         const int i = i0 + tid;
         if (i < p.k) {
             int n = p.seq_lens[b];
@@ -455,13 +456,16 @@ __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const KeepPar
             }
             const int t = kept_token(p.kept + (size_t)item * p.k, i, n);
             if (t >= 0) {
-                const int from = p.tables[(size_t)b * p.max_blocks + t / p.bs];
-                const int to = p.kept_tables[(size_t)b * p.max_kept_blocks + i / p.bs];
+                const int sb = t / p.bs, s = t - sb * p.bs, ob = i / p.bs, o = i - ob * p.bs;
+                const int from = p.tables[(size_t)b * p.max_blocks + sb];
+                const int to = p.kept_tables[(size_t)b * p.max_kept_blocks + ob];
                 if (from >= 0 && from < p.num_blocks && to >= 0 && to < p.num_blocks) {
-                    s = ((long long)from * p.num_kv_heads + h) * tile;
-                    o = ((long long)to * p.num_kv_heads + h) * tile;
-                    ss = t % p.bs;
-                    os = i % p.bs;
+                    const long long st = ((long long)from * p.num_kv_heads + h) * tile;
+                    const long long ot = ((long long)to * p.num_kv_heads + h) * tile;
+                    sk = st + (long long)(s >> 3) * p.d * 8 * ES + (s & 7) * 16;
+                    dk = ot + (long long)(o >> 3) * p.d * 8 * ES + (o & 7) * 16;
+                    sv = st + (long long)(s / X) * p.d * 16 + s % X * ES;
+                    dv = ot + (long long)(o / X) * p.d * 16 + o % X * ES;
                 } else {
                     flag_error(p.err, kErrOutOfRange);
                 }
@@ -469,59 +473,70 @@ __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const KeepPar
                 flag_error(p.err, kErrOutOfRange);
             }
         }
-        src_tile[tid] = s;
-        dst_tile[tid] = o;
-        src_slot[tid] = ss;
-        dst_slot[tid] = os;
+        src_k[tid] = sk;
+        dst_k[tid] = dk;
+        src_v[tid] = sv;
+        dst_v[tid] = dv;
     }
     __syncthreads();
-    // ---- K: pieces of 16 bytes
+    // ---- K: a warp's 8 tokens, 4 pieces of each at a time
     const int planes = p.d / X;
-    for (int x = tid; x < kKeepTokens * planes; x += kKeepThreads) {
-        const int c = (x >> 3) % planes, j = (x & 7) + 8 * (x / (8 * planes));
-        if (src_tile[j] < 0) continue;
-        const int s = src_slot[j], o = dst_slot[j];
-        const uint4 v = *reinterpret_cast<const uint4*>(p.k_pool + src_tile[j] + ((s >> 3) * planes + c) * 128 + (s & 7) * 16);
-        *reinterpret_cast<uint4*>(p.k_pool + dst_tile[j] + ((o >> 3) * planes + c) * 128 + (o & 7) * 16) = v;
-    }
-    // ---- V: rows of X tokens of one dim (chunks begin at multiples of X, blocks hold whole ones)
-    for (int x = tid; x < kKeepTokens / X * p.d; x += kKeepThreads) {
-        const int d = x % p.d, j0 = x / p.d * X;
-        uint32_t word[4] = {0, 0, 0, 0};
-        bool all = true;
-        long long last = -1;
-        uint4 r = make_uint4(0, 0, 0, 0);
+    {
+        const int j = 8 * w + (lane & 7);
+        if (src_k[j] >= 0) {
+            const char* from = p.k_pool + src_k[j] + (lane >> 3) * 128;
+            char* to = p.k_pool + dst_k[j] + (lane >> 3) * 128;
+            for (int c = lane >> 3; c < planes; c += 16, from += 16 * 128, to += 16 * 128) {
+                uint4 v[4];
 #pragma unroll
-        for (int e = 0; e < X; ++e) {
-            const int j = j0 + e;
-            if (src_tile[j] < 0) {                         // the same for all dims
-                all = false;
-                continue;
+                for (int u = 0; u < 4; ++u)
+                    if (c + 4 * u < planes) v[u] = *reinterpret_cast<const uint4*>(from + 4 * u * 128);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (c + 4 * u < planes) *reinterpret_cast<uint4*>(to + 4 * u * 128) = v[u];
             }
-            const int s = src_slot[j];
-            const long long at = src_tile[j] + ((long long)(s / X) * (p.d / 8) * 8 + d) * 16;
-            if (at != last) r = *reinterpret_cast<const uint4*>(p.v_pool + at);
-            last = at;
-            const int byte = s % X * ES;
-            const uint32_t two = byte & 8 ? (byte & 4 ? r.w : r.z) : (byte & 4 ? r.y : r.x);
-            uint32_t v = two >> (8 * (byte & 3));
-            if constexpr (ES < 4) v &= (1u << (8 * (ES & 3))) - 1u;
-            word[e * ES / 4] |= v << (8 * (e * ES & 3));
         }
-        // the first token of the row that goes somewhere: they share its target row
+    }
+    // ---- V: rows of X tokens of one dim (chunks begin at multiples of X, blocks hold whole ones),
+    // an element at a time: neighbouring tokens' are in the same 16 bytes, which the first brings in.
+    // A warp takes rows of 32 dims; the groups of X tokens are shared by kSame warps, or it takes several
+    using E = typename std::conditional<ES == 4, uint32_t, typename std::conditional<ES == 2, uint16_t, uint8_t>::type>::type;
+    constexpr int kGroups = kKeepTokens / X, kWarps = kKeepThreads / 32, kSame = kGroups < kWarps ? kWarps / kGroups : 1;
+    constexpr int kU = X >= 16 ? 1 : 2;                    // rows in flight
+    for (int g = w / kSame; g < kGroups; g += kWarps / kSame) {
+        const char* from[X];
+        bool all = true;
 #pragma unroll
         for (int e = 0; e < X; ++e) {
-            const int j = j0 + e;
-            if (dst_tile[j] < 0) continue;
-            char* const to = p.v_pool + dst_tile[j] + ((long long)(dst_slot[j] / X) * (p.d / 8) * 8 + d) * 16;
-            if (all) {
-                *reinterpret_cast<uint4*>(to) = make_uint4(word[0], word[1], word[2], word[3]);
-                break;
+            const long long at = src_v[g * X + e];
+            all &= at >= 0;
+            from[e] = p.v_pool + at;
+        }
+        const long long first = dst_v[g * X];
+        for (int d0 = (w % kSame) * 32 * kU + lane; d0 < p.d; d0 += kSame * 32 * kU) {
+            E v[kU][X];
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+#pragma unroll
+                for (int e = 0; e < X; ++e) {
+                    const bool has = (all || src_v[g * X + e] >= 0) && d0 + 32 * u < p.d;
+                    v[u][e] = has ? *reinterpret_cast<const E*>(from[e] + (d0 + 32 * u) * 16) : (E)0;
+                }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int d = d0 + 32 * u;
+                if (d >= p.d) break;
+                if (all) {
+                    uint32_t word[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int e = 0; e < X; ++e) word[e * ES / 4] |= (uint32_t)v[u][e] << (8 * (e * ES & 3));
+                    *reinterpret_cast<uint4*>(p.v_pool + first + d * 16) = make_uint4(word[0], word[1], word[2], word[3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < X; ++e)
+                        if (dst_v[g * X + e] >= 0) *reinterpret_cast<E*>(p.v_pool + dst_v[g * X + e] + d * 16) = v[u][e];
+                }
             }
-            const uint32_t v = word[e * ES / 4] >> (8 * (e * ES & 3));
-            if constexpr (ES == 4) reinterpret_cast<uint32_t*>(to)[e] = v;
-            else if constexpr (ES == 2) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)v;
-            else reinterpret_cast<uint8_t*>(to)[e] = (uint8_t)v;
         }
     }
 }
