@@ -11,8 +11,12 @@
 // Work split. A lane holds the 16 dims of rotary_and_cache (the two chunks of 8 that turn
 // together); the lanes of a row (8 for 128 dims) are neighbours, so the sum of squares is
 // log2 of them shuffles. A warp takes 32 / lanes tokens and walks over some of the heads with
-// one set of cosines, sines and (if shared by the heads) weights in registers, a batch of
-// heads read while the one before it turns. V goes through rotary_and_cache's own path.
+// one set of cosines, sines and (if shared by the heads) weights in registers, the next heads on
+// their way through asynchronous copies: a lane's own 32 bytes of each, which cost no registers
+// and wait for no other lane. V goes through rotary_and_cache's own path.
+// Bound: HBM bytes for many tokens (8192 tokens of 32 + 2 x 8 bf16 heads of 128, three axes,
+// weights of each head: 41 us, 0.73 of the copy rate; the issue slots are half in use), a launch
+// and a chain of loads for few (64 tokens 3.6 us).
 #include "pkv_rotary_impl.cuh"
 
 namespace pkv {
@@ -31,6 +35,47 @@ struct NormParams {
     long long v_warps;                 // the first ones of the launch
 };
 
+// Two float32 numbers an instruction: half the heads' arithmetic. The products' sums are fused
+// (a rounding less than rotary_and_cache's, whose bits are given).
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 16 bytes from memory to shared memory, in the background
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {            // all but the last N groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Heads a warp has on their way, and the CTAs of an SM the registers are shared by (8192 bf16
+// tokens: 41.0 us; with 4 heads 41.5; 6 or 8 CTAs 43 and 47; registers for two batches of two
+// heads instead of the ring 44.4, of one 43.5).
+template <typename ST> struct Ring {
+    static constexpr int kDepth = 3, kCtas = sizeof(ST) == 4 ? 6 : 7;
+    static constexpr int kHead = 32 * 16 * (int)sizeof(ST), kWarp = kDepth * kHead;   // bytes: 16 dims a lane
+};
+
 template <typename ST>
 __device__ __forceinline__ void load_weights(const void* w, int f32, long long at, float (&f)[8]) {
     if (f32) {
@@ -42,10 +87,11 @@ __device__ __forceinline__ void load_weights(const void* w, int f32, long long a
     }
 }
 
-// Heads h .. h_end-1 of q (KEYS false) or k of the tokens of group tg
+// Heads h .. h_end-1 of q (KEYS false) or k of the tokens of group tg. Every lane copies its own
+// dims of the heads ahead to its own places of `ring`, so nothing but its own copies has to land.
 template <typename ST, typename CT, bool INTERLEAVED, bool KEYS>
-__device__ __forceinline__ void norm_heads(const NormParams& n, long long tg, int h, int h_end) {
-    constexpr int HB = Batching<ST>::kHeads;
+__device__ __forceinline__ void norm_heads(const NormParams& n, long long tg, int h, int h_end, unsigned char* ring) {
+    constexpr int DEP = Ring<ST>::kDepth, HEAD = Ring<ST>::kHead, PIECES = sizeof(ST) == 4 ? 2 : 1;   // of 8 dims
     const RotaryParams& p = n.r;
     const int lane = threadIdx.x & 31, lanes = 1 << n.lanes_log2, u = lane & (lanes - 1);
     const long long t = (tg << (5 - n.lanes_log2)) + (lane >> n.lanes_log2);
@@ -64,24 +110,22 @@ __device__ __forceinline__ void norm_heads(const NormParams& n, long long tg, in
     if (has) token.read(p, t);
     const ST* src = (KEYS ? static_cast<const ST*>(p.k) + t * p.k_stride
                           : static_cast<const ST*>(p.q) + t * p.q_stride) + (long long)h * d;
-    struct Batch {
-        Raw8<ST> a[HB], b[HB];
-    };
-    auto read = [&](Batch& x, int left) {                  // the next batch, `left` heads at most
+    const int heads = h_end - h;
+    unsigned char* const mine = ring + lane * 16;
+    auto send = [&](int i, int slot) {                     // head i of these, if there is one
+        if (has && i < heads) {
+            const uint32_t to = smem_addr(mine) + slot * HEAD;
+            const ST* from = src + (long long)i * d;
 #pragma unroll
-        for (int i = 0; i < HB; ++i) {
-            x.a[i].clear();
-            x.b[i].clear();
-            if (has && i < left) {
-                x.a[i].load(src + i * d + da);
-                x.b[i].load(src + i * d + db);
+            for (int k = 0; k < PIECES; ++k) {
+                copy16(to + k * 512, from + da + k * 4);
+                copy16(to + (PIECES + k) * 512, from + db + k * 4);
             }
         }
-        src += HB * d;
+        copies_sent();
     };
-    int left = h_end - h;
-    Batch now, next;
-    read(now, left);
+#pragma unroll
+    for (int i = 0; i < DEP; ++i) send(i, i);
     const void* const weight = KEYS ? n.k_weight : n.q_weight;
     const int step = KEYS ? n.k_weight_step : n.q_weight_step;
     float wa[8], wb[8];
@@ -98,61 +142,84 @@ __device__ __forceinline__ void norm_heads(const NormParams& n, long long tg, in
     const int off = live ? (int)(token.slot - blk * p.bs) : 0;
     CT* tile = static_cast<CT*>(p.k_pool) + (blk * p.hkv + h) * tile_elems;
     ST* dst = static_cast<ST*>(p.q_out) + t * p.q_out_stride + (long long)h * d;
-    auto turn = [&](const Batch& batch) {
+    int slot = 0;
+#pragma unroll 1
+    for (int i = 0; i < heads; ++i) {
+        copies_wait<DEP - 1>();
+        float x[8], y[8];
+        if constexpr (PIECES == 2) {
 #pragma unroll
-        for (int i = 0; i < HB; ++i) {
-            if (i >= left) break;                          // the whole warp
-            float x[8], y[8];
-            batch.a[i].floats(x);
-            batch.b[i].floats(y);
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], fmaf(y[j], y[j], sum));
-            for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (!live) continue;
-            const float by = rsqrtf(fmaf(sum, n.inv_d, n.eps));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = x[j] * by * wa[j];
-                y[j] = y[j] * by * wb[j];
+            for (int k = 0; k < 2; ++k) {
+                const float4 a = *reinterpret_cast<const float4*>(mine + slot * HEAD + k * 512);
+                const float4 b = *reinterpret_cast<const float4*>(mine + slot * HEAD + (2 + k) * 512);
+                x[4 * k] = a.x, x[4 * k + 1] = a.y, x[4 * k + 2] = a.z, x[4 * k + 3] = a.w;
+                y[4 * k] = b.x, y[4 * k + 1] = b.y, y[4 * k + 2] = b.z, y[4 * k + 3] = b.w;
             }
-            if (step && i + 1 < left) {                    // the next head's own weights
+        } else {
+            Raw8<ST> a, b;
+            a.load(reinterpret_cast<const ST*>(mine + slot * HEAD));
+            b.load(reinterpret_cast<const ST*>(mine + slot * HEAD + 512));
+            a.floats(x);
+            b.floats(y);
+        }
+        uint64_t s2 = 0ull;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const uint64_t a = f2(x[j], x[j + 1]), b = f2(y[j], y[j + 1]);
+            s2 = fma2(a, a, fma2(b, b, s2));
+        }
+        float sum = has ? split(s2).x + split(s2).y : 0.f;
+        for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        send(i + DEP, slot);                               // the place has been read
+        if (++slot == DEP) slot = 0;
+        if (live) {
+            const float by = rsqrtf(fmaf(sum, n.inv_d, n.eps));
+            const uint64_t by2 = f2(by, by);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                uint64_t a = mul2(mul2(f2(x[j], x[j + 1]), by2), f2(wa[j], wa[j + 1]));
+                uint64_t b = mul2(mul2(f2(y[j], y[j + 1]), by2), f2(wb[j], wb[j + 1]));
+                if (!INTERLEAVED && turns) {
+                    const uint64_t c = f2(cs[j], cs[j + 1]), t = f2(sn[j], sn[j + 1]), m = f2(-sn[j], -sn[j + 1]);
+                    const uint64_t r = fma2(a, c, mul2(b, m));
+                    b = fma2(b, c, mul2(a, t));
+                    a = r;
+                }
+                x[j] = split(a).x, x[j + 1] = split(a).y;
+                y[j] = split(b).x, y[j + 1] = split(b).y;
+            }
+            if (step && i + 1 < heads) {                   // the next head's own weights
                 load_weights<ST>(weight, n.weights_f32, (long long)(h + i + 1) * step + da, wa);
                 load_weights<ST>(weight, n.weights_f32, (long long)(h + i + 1) * step + db, wb);
             }
-            if (turns) turn16<INTERLEAVED>(x, y, cs, sn);
+            if (INTERLEAVED && turns) turn16<INTERLEAVED>(x, y, cs, sn);
             if constexpr (KEYS) {
-                store_k8(tile + i * tile_elems, d, da, off, x, p.k_scale);
-                store_k8(tile + i * tile_elems, d, db, off, y, p.k_scale);
+                store_k8(tile, d, da, off, x, p.k_scale);
+                store_k8(tile, d, db, off, y, p.k_scale);
             } else {
-                store8(dst + i * d + da, x);
-                store8(dst + i * d + db, y);
+                store8(dst + da, x);
+                store8(dst + db, y);
             }
         }
-        left -= HB;
-        h += HB;
-        if constexpr (KEYS) tile += HB * tile_elems;
-        else dst += HB * d;
-    };
-#pragma unroll 1
-    while (left > 0) {
-        read(next, left - HB);
-        turn(now);
-        now = next;
+        if constexpr (KEYS) tile += tile_elems;
+        else dst += d;
     }
+    copies_wait<0>();
 }
 
 template <typename ST, typename CT, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 5) norm_rotary_and_cache_kernel(const NormParams n) {
+__global__ void __launch_bounds__(kThreads, Ring<ST>::kCtas) norm_rotary_and_cache_kernel(const NormParams n) {
     pdl_enter();                                           // launched with launch_pdl
-    __shared__ __align__(16) unsigned char turn[kThreads / 32][Turn<CT>::kWarp];
+    constexpr int kBytes = Turn<CT>::kWarp > Ring<ST>::kWarp ? Turn<CT>::kWarp : Ring<ST>::kWarp;
+    __shared__ __align__(16) unsigned char scratch[kThreads / 32][kBytes];   // of v's or of the other heads' warps
+    unsigned char* const mine = scratch[threadIdx.x >> 5];
     const RotaryParams& p = n.r;
     long long warp = blockIdx.x * (long long)(kThreads / 32) + (threadIdx.x >> 5);
     if (warp < n.v_warps) {                                // columns fastest, then heads, then tokens
         const int cg = (int)(warp % p.cols);
         const long long rest = warp / p.cols;
         const int h = (int)(rest % p.kv_chunks) * p.kv_step;
-        write_v_heads<ST, CT>(p, rest / p.kv_chunks, cg, h, min(p.hkv, h + p.kv_step), turn[threadIdx.x >> 5]);
+        write_v_heads<ST, CT>(p, rest / p.kv_chunks, cg, h, min(p.hkv, h + p.kv_step), mine);
         return;
     }
     warp -= n.v_warps;
@@ -162,10 +229,10 @@ __global__ void __launch_bounds__(kThreads, 5) norm_rotary_and_cache_kernel(cons
     if ((tg << (5 - n.lanes_log2)) >= p.num_tokens) return;    // the whole warp
     if (chunk < p.kv_chunks) {
         const int h = chunk * p.kv_step;
-        norm_heads<ST, CT, INTERLEAVED, true>(n, tg, h, min(p.hkv, h + p.kv_step));
+        norm_heads<ST, CT, INTERLEAVED, true>(n, tg, h, min(p.hkv, h + p.kv_step), mine);
     } else {
         const int h = (chunk - p.kv_chunks) * p.q_step;
-        norm_heads<ST, CT, INTERLEAVED, false>(n, tg, h, min(p.hq, h + p.q_step));
+        norm_heads<ST, CT, INTERLEAVED, false>(n, tg, h, min(p.hq, h + p.q_step), mine);
     }
 }
 
