@@ -11,16 +11,19 @@
 // tensor memory) and its maximum and sum run along the thread's own columns. Second pass
 // (gain): the operands change places, A = 128 keys, B = 128 rows: a thread owns a token, and
 // the sum over the rows again runs along its own columns. Both operands lie in shared memory
-// in the same K-major core matrices (the cache's own tiles; the rows, which the first pass
-// also writes to the workspace so), so the second pass only exchanges two descriptors, and
-// neither pass reduces across threads.
+// in the same K-major core matrices (the cache's own tiles, the rows copied into such), so the
+// second pass only exchanges two descriptors, and neither pass reduces across threads.
 //
-// Work split. Stats: a CTA holds a row tile and streams a run of the key tiles (several CTAs a
-// row tile where there are few). Gain: with one row tile a kv head (a short window) a CTA
-// holds it and streams key tiles; with more, it holds a key tile and streams the row tiles
-// that see it. Warps 0-3: one thread a lane of tensor memory; warp 4 issues the products, warp
-// 5 the copies; two buffers for the streamed operand and for the products, so the tensor
-// cores work on the next tile while the exponentials of this one are taken. Two CTAs an SM.
+// Work split. One CTA an SM, which takes units of work one after another, the copies of the
+// next one on their way while this one's products and exponentials run. A unit holds H tiles
+// and streams others past them: stats, H row tiles and a run of their key tiles; gain, with one
+// row tile a kv head (a short window), the row tile and a run of key tiles, else two key tiles
+// and a run of the row tiles that see them. H is 2 wherever there are two to hold: what is
+// streamed comes from L2 at 6.5 TB/s, which bounds a unit that holds one. Warps 0-15: four groups
+// with a product (128 columns of tensor memory) and a thread a lane each; tile i of the stream
+// is, for held tile h, group h 4/H + i % (4/H)'s. Warp 16 issues the products, 17 copies keys, 18
+// rows, 19 picks the units and joins the groups' results of each. Row runs of the same key
+// tiles leave their gains in the workspace; the last of them adds all up, in order.
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -33,12 +36,16 @@ namespace pkv {
 namespace weigh {
 
 constexpr int kTile = 128;             // rows, keys of a tile
-constexpr int kThreads = 320;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;               // warps 0-3, 4-7: a lane of tensor memory a thread
-constexpr uint32_t kTmemCols = 256;    // two products
+constexpr int kGroups = 4;             // of 128 threads; products and streamed tiles in flight
+constexpr int kMmaWarp = 16, kKeyWarp = 17, kRowWarp = 18, kPickWarp = 19;
+constexpr int kThreads = 20 * 32;
+constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kTile, kTile);
-constexpr int kTargetCtas = 608;       // of the stats pass: two waves of two CTAs an SM
+constexpr int kTargetUnits = 1216;     // of the stats pass: eight an SM
 constexpr int kMaxGroup = 128;
+constexpr int kRing = 4;               // units picked ahead
+
+enum Pass : int { kStats, kGainRows, kGainKeys };          // kGainRows: the row tiles stream
 
 struct Params {
     float* weights;
@@ -50,11 +57,17 @@ struct Params {
     const int32_t* query_start;
     unsigned char* q_tiles;            // [items][row_tiles] tiles of 128 rows, core matrices
     float2* stats;                     // [items][row_tiles][splits][128] maximum, sum
+    float* bases;                      // [items][row_tiles][128] M_r
+    int* next;                         // the gain pass's next unit,
+    int* arrived;                      // and the row runs of each pair of key tiles that are through
+    float* parts;                      // their gains [pairs][row_parts][2][128]
     int* err;
     int num_seqs, max_query_len, window, max_blocks, num_blocks, num_rows, max_tokens;
-    int num_heads, num_kv_heads, G, row_tiles, splits, key_tiles, per;
+    int num_heads, num_kv_heads, G, row_tiles, splits, per;   // per: key tiles of a unit's stream
+    int key_pairs, row_parts;          // of a sequence, at most; row runs of a pair
+    uint32_t g_magic;                  // floor(2^32 / G) + 1: r / G for r < 2^32 / G
     float scale_log2, decay;           // the scale's magnitude,
-    uint32_t q_sign;                   // and what turns its sign on pairs of query elements
+    uint32_t sign;                     // and what turns the sign of two query elements
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -91,518 +104,748 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+// Memory to shared memory, completing on `bar`, by a whole converged warp, one lane of it: the
+// operands stay warp-uniform (lanes that send a copy each go one after another, 120 cycles each).
+__device__ __forceinline__ void bulk_load_elect(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-        "r"(bytes), "r"(bar)
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
         : "memory");
 }
-// The four warps of a warpgroup; both of them
-__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
-__device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
+// Shared memory to memory (one lane); all of this thread's have been read, have been written
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(dst), "r"(src),
+                 "r"(bytes)
+                 : "memory");
 }
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float cluster_ld(const float* p, uint32_t rank) {
-    uint32_t a;
-    float v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+__device__ __forceinline__ void bulk_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// A copy of 16 bytes (none: zeros) in the background
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
 }
 
-// One sequence's chunk, or w == 0: nothing to do
+// M_r from a row's maximum and sum: +infinity (no gain) for a row that sees no token
+__device__ __forceinline__ float row_base(float m, float l) { return m == -INFINITY ? INFINITY : m + log2f(l); }
+
+// One unit: `n` stream tiles from `first` on, past the held tiles from `held` on; -1: no more
+struct Unit {
+    int n, first, held, item, b, hk, split, bad;           // bad: some block of the keys is not in the pool
+    int L, C, w, q_first, nr, to, splits;                  // splits: units that share the held tiles
+};
+
+// Barriers. Every waiter is at most one phase behind: a phase's successor needs the waiter's
+// own next step.
+enum : int {
+    kBarHeldFull = 0,                  // [2] the held tiles of a unit are there (H = 1: units in turn)
+    kBarHeldFree = 2,                  // [2] their products are done
+    kBarFull = 4,                      // [4] a streamed tile is there
+    kBarFree = 8,                      // [4] its products are done
+    kBarDone = 12,                     // [4] a group's product is
+    kBarRead = 16,                     // [4] and is read (128 threads)
+    kBarPart = 20,                     // [2] a unit's results are there (512)
+    kBarPartFree = 22,                 // [2] they are joined
+    kBarUnit = 24,                     // [kRing] a unit is picked
+    kBarUnitFree = 28,                 // [kRing] everybody has seen it (19 warps)
+    kBarBase = 32,                     // [4] a row tile's M_r
+    kBarDrain = 36,
+    kNumBars
+};
+
+template <int D>
+struct Shared {
+    static constexpr int kTileBytes = kTile * D * 2, kGroupBytes = D / 8 * 128;   // 8 rows
+    static constexpr int kHeld = 0, kStream = 2 * kTileBytes;
+    static constexpr int kPart = kStream + kGroups * kTileBytes;                  // [2][4][128] of 8 bytes
+    static constexpr int kBase = kPart + 2 * kGroups * kTile * 8;                 // [4][128] float
+    static constexpr int kUnits = kBase + 4 * kTile * 4;
+    static constexpr int kBars = kUnits + (kRing * (int)sizeof(Unit) + 15) / 16 * 16;
+    static constexpr int kBytes = kBars + kNumBars * 8;
+    static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+};
+
+// One sequence's chunk; w == 0: nothing to do
 struct Chunk {
-    int L, C, w, q_first;              // q_first: row of q of the first query that counts
-    __device__ __forceinline__ Chunk(const Params& p, int b, int bs, bool flag) {
+    int L = 0, C = 0, w = 0, q_first = 0;                  // q_first: row of q of the first query that counts
+    __device__ __forceinline__ void read(const Params& p, int b, int bs) {
         L = p.seq_lens[b];
         const int q0 = p.query_start[b], q1 = p.query_start[b + 1], T = p.query_start[p.num_seqs];
         C = q1 - q0;
         w = p.window > 0 && p.window < C ? p.window : C;
         if (C < 0 || C > L || L > p.max_blocks * bs || q0 < 0 || q1 > T || C > p.max_query_len) {
-            if (flag && C != 0) flag_error(p.err, kErrOutOfRange);
+            if (C != 0) flag_error(p.err, kErrOutOfRange);
             w = 0;
         }
         q_first = q1 - w;
     }
 };
 
-enum : int { kBarHeld = 0, kBarFull = 1, kBarDone = 3, kBarRead = 5, kBarDrain = 7, kNumBars };
-
-// The pipeline both passes share: tile i of the stream, i < n, goes through buffer i % 2.
-// `load(i, dst, bar)`: the loading warp arms `bar` and sends tile i's copies. `use(i, taddr)`:
-// the lanes' warps read their products and return; held_is_a: the held tile is A.
-template <int D>
-struct Pipe {
-    static constexpr int kTileBytes = kTile * D * 2, kGroup = D / 8 * 128;   // 8 rows
-    static constexpr int kSmem = 3 * kTileBytes;                             // held | streamed x 2
-
-    uint32_t sbase, bar0, tmem;
-    const int* err;
-
-    __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
-    __device__ __forceinline__ static void init(uint32_t bar0) {             // one thread
-        auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-        mbar_init(bar(kBarHeld), 1);
+template <Pass PASS, int H, int D, int BS>
+__global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
+    pdl_enter();
+    using S = Shared<D>;
+    static_assert(H == 1 || H == 2, "held tiles");
+    constexpr int kBlocks = kTile / BS, kTurn = kGroups / H;    // groups that share a held tile
+    // place and use of what unit u holds: two places in turn, or one of two tiles
+    auto held_at = [](int u) { return H == 1 ? u & 1 : 0; };
+    auto held_use = [](int u) { return H == 1 ? u >> 1 : u; };
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ uint32_t tmem_slot;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sbase = smem_addr(smem), bar0 = sbase + S::kBars;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    auto wait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar(i), parity & 1, p.err)) != 0; };
+    auto row_div = [&](int r) { return p.G == 1 ? r : (int)__umulhi((uint32_t)r, p.g_magic); };
+    Unit* const units = reinterpret_cast<Unit*>(smem + S::kUnits);
+    float* const base_at = reinterpret_cast<float*>(smem + S::kBase);
+    if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarHeldFull + i), 1);
+            mbar_init(bar(kBarHeldFree + i), 1);
+            mbar_init(bar(kBarPart + i), kGroups * 128);
+            mbar_init(bar(kBarPartFree + i), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(bar(kBarFull + i), 1);
+            mbar_init(bar(kBarFree + i), 1);
             mbar_init(bar(kBarDone + i), 1);
+            mbar_init(bar(kBarBase + i), 1);
             mbar_init(bar(kBarRead + i), 128);
+            mbar_init(bar(kBarUnit + i), 1);
+            mbar_init(bar(kBarUnitFree + i), kPickWarp);
         }
         mbar_init(bar(kBarDrain), 1);
         fence_mbar_init();
+        if (PASS == kStats && blockIdx.x == 0) *p.next = 0;
     }
-    template <class Load>
-    __device__ __forceinline__ void run_load(int n, int lane, bool held, Load load) const {
-        int sent = 0;
-        bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
-            if (i >= 2) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarDone + (i & 1)), ((i - 2) >> 1) & 1, err));
-            if (!ok) break;
-            load(i, sbase + (1 + (i & 1)) * kTileBytes, bar(kBarFull + (i & 1)));
-            sent = i + 1;
-        }
-        // every copy lands before the CTA may exit
-        for (int i = max(0, sent - 2); i < sent; ++i) (void)mbar_wait_bounded(bar(kBarFull + (i & 1)), (i >> 1) & 1, nullptr);
-        if (held) (void)mbar_wait_bounded(bar(kBarHeld), 0, nullptr);
+    if (PASS == kStats && p.row_parts > 1)
+        for (int i = blockIdx.x * kThreads + tid; i < p.num_seqs * p.num_kv_heads * p.key_pairs; i += gridDim.x * kThreads)
+            p.arrived[i] = 0;
+    if (warp == kMmaWarp) {
+        tc::alloc(smem_addr(&tmem_slot), kTmemCols);
+        tc::relinquish_alloc_permit();
     }
-    __device__ __forceinline__ void run_mma(int n, int lane, bool held, bool held_is_a) const {
-        bool ok = true;
-        auto wait = [&](int b, int parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(bar(b), parity, err)); };
-        if (held) wait(kBarHeld, 0);
-        constexpr uint32_t hi = tc::desc_hi(kGroup);
-        const uint32_t h_lo = tc::desc_lo(sbase, 128);
-        for (int i = 0; i < n && ok; ++i) {
-            const int s = i & 1;
-            wait(kBarFull + s, (i >> 1) & 1);
-            if (i >= 2) wait(kBarRead + s, ((i - 2) >> 1) & 1);
-            if (!ok) break;
-            tc::fence_after_sync();
-            const uint32_t s_lo = tc::desc_lo(sbase + (1 + s) * kTileBytes, 128);
-            const uint32_t a = held_is_a ? h_lo : s_lo, b = held_is_a ? s_lo : h_lo;
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+
+    // Before a copying warp leaves: what it sent has landed (after a wait that gave up, too)
+    auto land = [&](int full, int parts, int sent) {
+        for (int i = max(0, sent - parts); i < sent; ++i)
+            (void)mbar_wait_bounded(bar(full + i % parts), (uint32_t)(i / parts) & 1u, nullptr);
+    };
+
+    // The u-th unit of this CTA (every warp but the picking one); false: no more, or a wait gave up
+    Unit unit;
+    auto next_unit = [&](int u) {
+        if (!wait(kBarUnit + u % kRing, u / kRing)) return false;
+        unit = units[u % kRing];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarUnitFree + u % kRing));
+        return unit.n >= 0;
+    };
+
+    if (warp == kPickWarp) {
+        // ------------------------------------------------------------ units
+        // 32 sequences at a time, one a lane: how many units each has, and where they begin
+        int b0 = 0, mine = 0, begin = 0, seen = 0;         // seen: units of the sequences before b0
+        Chunk ch;
+        int tiles = 0, row_tiles = 0, splits = 1, total = 0;
+        auto load = [&] {
+            ch = Chunk();
+            mine = 0;
+            const int b = b0 + lane;
+            if (b < p.num_seqs) {
+                ch.read(p, b, BS);
+                tiles = (ch.L + kTile - 1) / kTile;
+                row_tiles = (ch.w * p.G + kTile - 1) / kTile;
+                if (ch.w > 0) {
+                    if (PASS == kStats) {
+                        splits = min(p.splits, (tiles + p.per - 1) / p.per);
+                        mine = p.num_kv_heads * ((row_tiles + H - 1) / H) * splits;
+                    } else if (PASS == kGainRows) {
+                        mine = p.num_kv_heads * ((tiles + H - 1) / H) * p.row_parts;
+                    } else {
+                        mine = p.num_kv_heads * ((tiles + p.per - 1) / p.per);
+                    }
+                }
+            }
+            begin = mine;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                tc::mma_ss2_elect(tmem + s * kTile, a + k * 16, hi, b + k * 16, hi, kIdesc, k > 0);
-            tc::commit_elect(bar(kBarDone + s));
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, begin, o);
+                if (lane >= o) begin += x;
+            }
+            total = __shfl_sync(0xffffffffu, begin, 31);
+            begin -= mine;
+        };
+        load();
+        int to = -1, to_of = -1;                           // the weight row of sequence to_of
+        bool ok = true, more = true;
+        int at = blockIdx.x, picked = 0;
+        auto pick = [&] {                                  // the next unit, or that there is none
+          for (;;) {
+            if (PASS != kStats) {
+                if (lane == 0) at = atomicAdd(p.next, 1);
+                at = __shfl_sync(0xffffffffu, at, 0);
+            }
+            while (at >= seen + total && b0 + 32 < p.num_seqs) {
+                seen += total;
+                b0 += 32;
+                load();
+            }
+            Unit x;
+            x.n = -1;
+            more = at < seen + total;
+            if (more) {
+                const int k = at - seen, src = __ffs(__ballot_sync(0xffffffffu, k >= begin && k < begin + mine)) - 1;
+                auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+                const int local = k - of(begin);
+                x.b = b0 + src;
+                x.L = of(ch.L), x.C = of(ch.C), x.w = of(ch.w), x.q_first = of(ch.q_first);
+                x.nr = x.w * p.G;
+                const int nt = of(tiles), nrt = of(row_tiles), ns = of(splits), first_pos = x.L - x.w;
+                x.split = 0;
+                x.splits = 1;
+                if (PASS == kStats) {                      // row tiles' neighbours share their keys: they go side by side
+                    const int held = (nrt + H - 1) / H, rest = local / held;
+                    x.held = (held - 1 - (local - rest * held)) * H;
+                    x.hk = rest / ns;
+                    x.split = rest - x.hk * ns;
+                    const int seen_tiles = (first_pos + (min(x.nr, (x.held + H) * kTile) - 1) / p.G) / kTile + 1;
+                    const int per = (seen_tiles + ns - 1) / ns;
+                    x.first = x.split * per;
+                    x.n = min(seen_tiles, x.first + per) - x.first;
+                } else if (PASS == kGainRows) {            // the tiles that most rows see first
+                    const int rest = local / p.row_parts;
+                    x.split = local - rest * p.row_parts;
+                    x.held = rest / p.num_kv_heads * H;
+                    x.hk = rest % p.num_kv_heads;
+                    x.first = max(0, x.held * kTile - first_pos) * p.G / kTile;
+                    const int all = nrt - x.first, per = (all + p.row_parts - 1) / p.row_parts;
+                    x.splits = (all + per - 1) / per;
+                    x.first += x.split * per;
+                    x.n = min(nrt, x.first + per) - x.first;
+                } else {
+                    const int run = local / p.num_kv_heads;
+                    x.hk = local - run * p.num_kv_heads;
+                    x.held = 0;
+                    x.first = run * p.per;
+                    x.n = min(p.per, nt - x.first);
+                }
+                x.item = x.b * p.num_kv_heads + x.hk;
+                // blocks of its keys that are not in the pool
+                const int kt = PASS == kGainRows ? x.held : x.first, kn = PASS == kGainRows ? H : x.n;
+                const int32_t* const table = p.block_tables + (size_t)x.b * p.max_blocks;
+                bool bad = false;
+                for (int i = kt * kBlocks + lane; i < min((kt + kn) * kBlocks, (x.L + BS - 1) / BS); i += 32)
+                    bad |= table[i] < 0 || table[i] >= p.num_blocks;
+                x.bad = __any_sync(0xffffffffu, bad);
+                x.to = x.b;
+                if (PASS != kStats && p.rows) {            // good, and no earlier sequence's
+                    if (to_of != x.b) {
+                        to_of = x.b;
+                        to = p.rows[x.b];
+                        bool lost = to < 0 || to >= p.num_rows;
+                        for (int i = lane; i < x.b; i += 32) lost |= p.rows[i] == to;
+                        if (__any_sync(0xffffffffu, lost)) {
+                            if (lane == 0) flag_error(p.err, kErrOutOfRange);
+                            to = -1;
+                        }
+                    }
+                    x.to = to;
+                }
+                if (PASS == kStats) at += gridDim.x;
+                if (x.n <= 0 || (PASS != kStats && x.to < 0)) continue;
+            }
+            if (picked >= kRing) ok = wait(kBarUnitFree + picked % kRing, picked / kRing - 1);
+            if (!ok) return;
+            if (lane == 0) {
+                units[picked % kRing] = x;
+                mbar_arrive(bar(kBarUnit + picked % kRing));
+            }
+            __syncwarp();
+            ++picked;
+            return;
+          }
+        };
+        if (PASS == kGainKeys) {
+            while (ok && more) pick();
+        } else {
+            while (ok && more && picked < kRing - 1) pick();
         }
-        if (!ok && lane == 0) flag_error(const_cast<int*>(err), kErrTimeout);
+        // ------------------------------------------------------------ a unit's results
+        for (int u = 0; PASS != kGainKeys && ok && u < picked; ++u) {
+            unit = units[u % kRing];                       // this warp's own
+            if (unit.n < 0 || !wait(kBarPart + (u & 1), u >> 1)) break;
+            const unsigned char* const part = smem + S::kPart + (u & 1) * kGroups * kTile * 8;
+            if constexpr (PASS == kStats) {
+#pragma unroll
+                for (int k = 0; k < 4 * H; ++k) {
+                    const int me = lane + 32 * (k & 3), h = k >> 2, rt = unit.held + h;
+                    float2 x[kTurn];
+                    float m = -INFINITY, l = 0.f;
+#pragma unroll
+                    for (int g = 0; g < kTurn; ++g) x[g] = reinterpret_cast<const float2*>(part)[(h * kTurn + g) * kTile + me];
+#pragma unroll
+                    for (int g = 0; g < kTurn; ++g) m = max_nan(m, x[g].x);
+                    const float by = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int g = 0; g < kTurn; ++g) l += ex2(x[g].x - by) * x[g].y;
+                    if (rt * kTile >= unit.nr) continue;
+                    const size_t tile = (size_t)unit.item * p.row_tiles + rt;
+                    if (p.splits > 1) p.stats[(tile * p.splits + unit.split) * kTile + me] = make_float2(m, l);
+                    else p.bases[tile * kTile + me] = rt * kTile + me < unit.nr ? row_base(m, l) : INFINITY;
+                }
+            } else {
+                float gain[4 * H];
+#pragma unroll
+                for (int k = 0; k < 4 * H; ++k) {
+                    gain[k] = 0.f;
+#pragma unroll
+                    for (int g = 0; g < kTurn; ++g)
+                        gain[k] += reinterpret_cast<const float*>(part)[((k >> 2) * kTurn + g) * kTile + lane + 32 * (k & 3)];
+                }
+                bool write = true;
+                if (unit.splits > 1) {                     // one of several row runs: the last adds them up
+                    const int pair = unit.item * p.key_pairs + unit.held / H;
+                    float* const all = p.parts + (size_t)pair * p.row_parts * H * kTile + lane;
+#pragma unroll
+                    for (int k = 0; k < 4 * H; ++k) all[(unit.split * H * 4 + k) * 32] = gain[k];
+                    __threadfence();
+                    __syncwarp();
+                    int before = 0;
+                    if (lane == 0) before = atomicAdd(&p.arrived[pair], 1);
+                    write = __shfl_sync(0xffffffffu, before, 0) == unit.splits - 1;
+                    if (write) {
+                        __threadfence();
+#pragma unroll
+                        for (int k = 0; k < 4 * H; ++k) {
+                            gain[k] = 0.f;
+                            for (int x = 0; x < unit.splits; ++x) gain[k] += __ldcg(&all[(x * H * 4 + k) * 32]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4 * H; ++k) {
+                    const int t = unit.held * kTile + lane + 32 * k;
+                    if (write && t < unit.L) {
+                        const int id = unit.bad ? p.block_tables[(size_t)unit.b * p.max_blocks + t / BS] : 0;
+                        float* const at = p.weights + ((size_t)unit.to * p.num_kv_heads + unit.hk) * p.max_tokens + t;
+                        const float g = id < 0 || id >= p.num_blocks ? 0.f : gain[k];
+                        *at = t < unit.L - unit.C ? fmaf(p.decay, *at, g) : g;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarPartFree + (u & 1)));
+            if (more) pick();
+        }
+    } else if (warp == kKeyWarp) {
+        // ------------------------------------------------------------ keys
+        // Block ids, 32 a lane each, the next 32 read ahead. Blocks that are not in the pool are
+        // read from block 0 (what comes of them is left out by those who use them).
+        int ids = 0, next_ids = 0, first_block = 0, window = 0;
+        auto read_ids = [&](int k) {
+            const int blk = first_block + 32 * k + lane;
+            if (blk >= (unit.L + BS - 1) / BS) return 0;
+            return p.block_tables[(size_t)unit.b * p.max_blocks + blk];
+        };
+        auto begin_ids = [&](int tile) {
+            first_block = tile * kBlocks;
+            window = 0;
+            ids = read_ids(0);
+            next_ids = read_ids(1);
+        };
+        auto blocks_left = [&](int j) { return (unit.L + BS - 1) / BS - first_block - j * kBlocks; };
+        auto load_keys = [&](int j, uint32_t dst, uint32_t full) {   // the j-th tile from there; `full` is armed
+            if (j * kBlocks / 32 != window) {
+                ++window;
+                ids = next_ids;
+                next_ids = read_ids(window + 1);
+            }
+            const int n = min(kBlocks, blocks_left(j));
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+                int id = __shfl_sync(0xffffffffu, ids, j * kBlocks % 32 + k);
+                if (k >= n) break;                         // the whole warp
+                if (id < 0 || id >= p.num_blocks) {
+                    if (lane == 0) flag_error(p.err, kErrOutOfRange);
+                    __syncwarp();
+                    id = 0;
+                }
+                bulk_load_elect(dst + k * BS * D * 2, p.k_pool + ((size_t)id * p.num_kv_heads + unit.hk) * (BS * D), BS * D * 2, full);
+            }
+        };
+        int it = 0, sent = 0;
+        for (int u = 0; next_unit(u); ++u) {
+            begin_ids(PASS == kGainRows ? unit.held : unit.first);
+            if (PASS == kGainRows) {
+                const int full = bar(kBarHeldFull + held_at(u));
+                if (held_use(u) > 0 && !wait(kBarHeldFree + held_at(u), held_use(u) - 1)) break;
+                const int there = min(H, (unit.L + kTile - 1) / kTile - unit.held);
+                mbar_arrive_expect_tx_elect(full, (uint32_t)(min(there * kBlocks, blocks_left(0)) * BS * D * 2));
+                for (int h = 0; h < there; ++h) load_keys(h, sbase + S::kHeld + (held_at(u) + h) * S::kTileBytes, full);
+                sent = u + 1;
+            } else {
+                bool ok = true;
+                for (int j = 0; j < unit.n && ok; ++j, ++it) {
+                    const int s = it & 3;
+                    if (it >= 4) ok = wait(kBarFree + s, (it >> 2) - 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx_elect(bar(kBarFull + s), (uint32_t)(min(kBlocks, blocks_left(j)) * BS * D * 2));
+                    load_keys(j, sbase + S::kStream + s * S::kTileBytes, bar(kBarFull + s));
+                    sent = it + 1;
+                }
+                if (!ok) break;
+            }
+        }
+        land(PASS == kGainRows ? kBarHeldFull : kBarFull, PASS == kGainRows ? 3 - H : 4, sent);
+    } else if (warp == kRowWarp) {
+        // ------------------------------------------------------------ rows
+        // Row tile rt in core matrices: 8 rows x 4 pieces of 16 bytes an instruction; zeros past the last
+        auto send_rows = [&](int rt, uint32_t dst) {
+            const __nv_bfloat16* const q = p.q + ((size_t)unit.q_first * p.num_heads + unit.hk * p.G) * D + (lane >> 3) * 8;
+            const uint32_t to = dst + (lane >> 3) * 128 + (lane & 7) * 16;
+#pragma unroll 4
+            for (int g = 0; g < kTile / 8; ++g) {
+                const int r = rt * kTile + g * 8 + (lane & 7);
+                const bool some = r < unit.nr;
+                const int rr = some ? r : 0;
+                const __nv_bfloat16* src = q + ((size_t)row_div(rr) * (p.num_heads - p.G) + rr) * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) copy16(to + g * S::kGroupBytes + c * 512, src + c * 32, some);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        auto tile_of = [&](int rt) { return p.q_tiles + ((size_t)unit.item * p.row_tiles + rt) * S::kTileBytes; };
+        auto load_rows = [&](int rt, uint32_t dst, uint32_t full) {
+            mbar_arrive_expect_tx_elect(full, S::kTileBytes);
+            bulk_load_elect(dst, tile_of(rt), S::kTileBytes, full);
+        };
+        auto load_bases = [&](int rt, int place) {         // their M_r
+            mbar_arrive_expect_tx_elect(bar(kBarBase + place), kTile * 4);
+            bulk_load_elect(smem_addr(base_at + place * kTile), p.bases + ((size_t)unit.item * p.row_tiles + rt) * kTile, kTile * 4,
+                            bar(kBarBase + place));
+        };
+        int it = 0, sent = 0, based = 0;
+        for (int u = 0; next_unit(u); ++u) {
+            const uint32_t held = sbase + S::kHeld + held_at(u) * S::kTileBytes, held_full = bar(kBarHeldFull + held_at(u));
+            if (PASS != kGainRows && held_use(u) > 0 && !wait(kBarHeldFree + held_at(u), held_use(u) - 1)) break;
+            if (PASS == kStats) {
+                bulk_stores_read();                        // of the unit that had the place
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < H; ++h) send_rows(unit.held + h, held + h * S::kTileBytes);
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncwarp();
+                if (p.sign)                                // a negative scale: the rows turn it
+                    for (int i = lane; i < H * S::kTileBytes / 16; i += 32) {
+                        uint4* const at = reinterpret_cast<uint4*>(smem + (held - sbase)) + i;
+                        const uint4 v = *at;
+                        *at = make_uint4(v.x ^ p.sign, v.y ^ p.sign, v.z ^ p.sign, v.w ^ p.sign);
+                    }
+                fence_proxy_async_smem();                  // to the tensor cores and the copy below
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(held_full);
+                    if (unit.split == 0)                   // for the second pass
+                        bulk_store(tile_of(unit.held), held, min(H, (unit.nr + kTile - 1) / kTile - unit.held) * S::kTileBytes);
+                }
+                __syncwarp();
+                continue;
+            }
+            if (PASS == kGainKeys) {
+                load_rows(0, held, held_full);
+                sent = u + 1;
+                // the unit before last, which had the place, is through
+                if (u >= 2 && !wait(kBarPart + (u & 1), (u >> 1) - 1)) break;
+                load_bases(0, u & 1);
+                based = u + 1;
+                continue;
+            }
+            // streamed, three tiles ahead of the one whose M_r follow
+            auto send = [&](int j, int i) {
+                if (j >= unit.n) return true;
+                if (i >= 4 && !wait(kBarFree + (i & 3), (i >> 2) - 1)) return false;
+                load_rows(unit.first + j, sbase + S::kStream + (i & 3) * S::kTileBytes, bar(kBarFull + (i & 3)));
+                sent = i + 1;
+                return true;
+            };
+            bool ok = true;
+            for (int j = 0; j < 3 && ok; ++j) ok = send(j, it + j);
+            for (int j = 0; j < unit.n && ok; ++j, ++it) {
+                // their place was tile it - 4's, whose groups are through once they have read the product
+                // of tile it - kTurn
+                for (int g = it % kTurn; g < kGroups && ok && it >= kTurn; g += kTurn) ok = wait(kBarRead + g, it / kTurn - 1);
+                if (!ok) break;
+                load_bases(unit.first + j, it & 3);
+                based = it + 1;
+                ok = send(j + 3, it + 3);
+            }
+            if (!ok) break;
+        }
+        bulk_stores_done();
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (PASS != kStats) {
+            land(PASS == kGainKeys ? kBarHeldFull : kBarFull, PASS == kGainKeys ? 2 : 4, sent);
+            land(kBarBase, PASS == kGainKeys ? 2 : 4, based);
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ products
+        constexpr uint32_t hi = tc::desc_hi(S::kGroupBytes);
+        bool ok = true;
+        int it = 0;
+        for (int u = 0; ok && next_unit(u); ++u) {
+            ok = wait(kBarHeldFull + held_at(u), held_use(u));
+            if (!ok) break;
+            const uint32_t h_lo = tc::desc_lo(sbase + S::kHeld + held_at(u) * S::kTileBytes, 128);
+            for (int j = 0; j < unit.n && ok; ++j, ++it) {
+                const int s = it & 3;
+                ok = wait(kBarFull + s, it >> 2);
+                const uint32_t s_lo = tc::desc_lo(sbase + S::kStream + s * S::kTileBytes, 128);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const int g = h * kTurn + it % kTurn;
+                    if (ok && it >= kTurn) ok = wait(kBarRead + g, it / kTurn - 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint32_t held = h_lo + h * (S::kTileBytes / 16);
+                    const uint32_t a = PASS == kGainKeys ? s_lo : held, b = PASS == kGainKeys ? held : s_lo;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc::mma_ss2_elect(tmem + g * kTile, a + k * 16, hi, b + k * 16, hi, kIdesc, k > 0);
+                    tc::commit_elect(bar(kBarDone + g));
+                }
+                if (ok) tc::commit_elect(bar(kBarFree + s));
+            }
+            tc::commit_elect(bar(kBarHeldFree + held_at(u)));
+        }
         tc::commit_elect(bar(kBarDrain));                  // all of them complete before tensor memory goes
         (void)mbar_wait_bounded(bar(kBarDrain), 0, nullptr);
         __syncwarp();
-    }
-    // Products of stream tile i, 32 columns at a time: use(column, values). False: a wait gave up.
-    template <class Use>
-    __device__ __forceinline__ bool take(int i, int warp, Use use) const {
-        const int s = i & 1;
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kBarDone + s), (i >> 1) & 1, err));
-        if (!ok) return false;
-        tc::fence_after_sync();
-        const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + s * kTile;
-        uint32_t v[2][32];
-        tc::ld32(at, v[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            tc::wait_ld();
-            if (c < 3) tc::ld32(at + 32 * (c + 1), v[(c + 1) & 1]);
-            else {
-                tc::fence_before_sync();
-                mbar_arrive(bar(kBarRead + s));
-            }
-            use(32 * c, v[c & 1]);
-        }
-        return true;
-    }
-};
-
-// Key tile j of a sequence into shared memory; blocks that are not in the pool are read from
-// block 0 (what comes of them is left out by those who use them).
-template <int D, int BS>
-__device__ __forceinline__ void load_keys(const Params& p, int b, int hk, int L, int j, int lane, uint32_t dst, uint32_t bar) {
-    constexpr int kBlocks = kTile / BS, kBytes = BS * D * 2;
-    const int first = j * kBlocks, n = min(kBlocks, (L + BS - 1) / BS - first);
-    int id = 0;
-    if (lane < n) {
-        id = p.block_tables[(size_t)b * p.max_blocks + first + lane];
-        if (id < 0 || id >= p.num_blocks) {
-            flag_error(p.err, kErrOutOfRange);
-            id = 0;
-        }
-    }
-    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * kBytes));
-    __syncwarp();
-    if (lane < n)
-        bulk_load(dst + lane * kBytes, p.k_pool + ((size_t)id * p.num_kv_heads + hk) * (BS * D), kBytes, bar);
-}
-
-template <int D, int BS>
-__global__ void __launch_bounds__(kThreads, 2) weigh_stats_kernel(const Params p) {
-    pdl_enter();
-    using P = Pipe<D>;
-    extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(8) uint64_t bars[kNumBars];
-    __shared__ uint32_t tmem_slot;
-    __shared__ float2 other[kTile];                        // the second warpgroup's statistics
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int split = blockIdx.x, rt = blockIdx.y, item = blockIdx.z, b = item / p.num_kv_heads, hk = item - b * p.num_kv_heads;
-    const Chunk ch(p, b, BS, tid == 0);
-    const int r0 = rt * kTile, nr = ch.w * p.G;
-    if (r0 >= nr) return;                                  // the whole CTA
-    const int p_min = ch.L - ch.w + r0 / p.G, p_max = ch.L - ch.w + (min(nr, r0 + kTile) - 1) / p.G;
-    const int tiles = p_max / kTile + 1, per = (tiles + p.splits - 1) / p.splits;
-    const int k0 = split * per, n = min(tiles, k0 + per) - k0;
-    if (n <= 0) return;
-    // blocks that are not in the pool: rare, so the lanes look them up themselves then
-    constexpr int kBlocks = kTile / BS;
-    const int32_t* const table = p.block_tables + (size_t)b * p.max_blocks;
-    bool bad = false;
-    for (int i = k0 * kBlocks + tid; i < min((k0 + n) * kBlocks, p_max / BS + 1); i += kThreads)
-        bad |= table[i] < 0 || table[i] >= p.num_blocks;
-    P pipe;
-    pipe.sbase = smem_addr(smem);
-    pipe.bar0 = smem_addr(bars);
-    pipe.err = p.err;
-    if (tid == 0) P::init(pipe.bar0);
-    if (warp == kMmaWarp) {
-        tc::alloc(smem_addr(&tmem_slot), kTmemCols);
-        tc::relinquish_alloc_permit();
-    }
-    if (warp < 8) {                                        // half a row: to shared memory and the workspace
-        const int r = r0 + (tid & 127), c0 = (tid >> 7) * (D / 16);
-        const bool valid = r < nr;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + ((size_t)(ch.q_first + (valid ? r / p.G : 0)) * p.num_heads + hk * p.G + (valid ? r % p.G : 0)) * D);
-        const int at = ((tid & 127) >> 3) * P::kGroup + (tid & 7) * 16;
-        unsigned char* const to = p.q_tiles + ((size_t)item * p.row_tiles + rt) * P::kTileBytes + at;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const int c = c0 + i;
-            uint4 v = valid ? src[c] : make_uint4(0, 0, 0, 0);
-            v = make_uint4(v.x ^ p.q_sign, v.y ^ p.q_sign, v.z ^ p.q_sign, v.w ^ p.q_sign);
-            *reinterpret_cast<uint4*>(smem + at + c * 128) = v;
-            if (split == 0) *reinterpret_cast<uint4*>(to + c * 128) = v;
-        }
-        fence_proxy_async_smem();                          // to the tensor cores, behind the barrier
-    }
-    tc::fence_before_sync();
-    const bool any_bad = __syncthreads_or(bad);
-    tc::fence_after_sync();
-    pipe.tmem = tmem_slot;
-    if (warp == kLoadWarp) {
-        pipe.run_load(n, lane, false, [&](int i, uint32_t dst, uint32_t bar) {
-            load_keys<D, BS>(p, b, hk, p_max + 1, k0 + i, lane, dst, bar);
-        });
-    } else if (warp == kMmaWarp) {
-        pipe.run_mma(n, lane, false, true);
     } else {
+        // ------------------------------------------------------------ exponentials
         const int group = warp >> 2, me = tid & 127;
-        const int r = r0 + me, pr = ch.L - ch.w + min(r, nr - 1) / p.G;
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
-        float m = -INFINITY, l = 0.f;                      // of the raw products; the scale is not negative
+        // Product i, 32 columns at a time: use(column, values)
+        auto take = [&](int i, auto use) {
+            if (!wait(kBarDone + group, i / kTurn)) return false;
+            tc::fence_after_sync();
+            const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * kTile;
+            uint32_t v[2][32];
+            tc::ld32(at, v[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                tc::wait_ld();
+                if (c < 3) tc::ld32(at + 32 * (c + 1), v[(c + 1) & 1]);
+                else {
+                    tc::fence_before_sync();
+                    mbar_arrive(bar(kBarRead + group));
+                }
+                use(32 * c, v[c & 1]);
+            }
+            return true;
+        };
         bool ok = true;
-        for (int i = group; i < n && ok; i += 2) {         // the groups take turns
-            const int key0 = (k0 + i) * kTile;
-            const bool masked = any_bad || key0 + kTile - 1 > p_min;
-            ok = pipe.take(i, warp, [&](int c0, uint32_t (&v)[32]) {
-                if (masked) {
-                    constexpr uint32_t kNone = 0xff800000u;   // -infinity
+        int it = 0;                                        // of the unit's first tile
+        for (int u = 0; ok && next_unit(u); it += unit.n, ++u) {
+            const int first_pos = unit.L - unit.w, skip = (group - it) & (kTurn - 1), held = unit.held + group / kTurn;
+            unsigned char* const part = smem + S::kPart + (u & 1) * kGroups * kTile * 8;
+            if constexpr (PASS == kStats) {
+                const int r0 = held * kTile, r = min(r0 + me, unit.nr - 1), pr = first_pos + row_div(r);
+                const int p_min = first_pos + row_div(min(r0, unit.nr - 1));
+                float m = -INFINITY, l = 0.f;              // of the products; the scale is not negative
+                for (int j = skip; j < unit.n && ok; j += kTurn) {
+                    const int key0 = (unit.first + j) * kTile;
+                    const bool masked = unit.bad || key0 + kTile - 1 > p_min;
+                    ok = take(it + j, [&](int c0, uint32_t (&v)[32]) {
+                        if (masked) {
+                            constexpr uint32_t kNone = 0xff800000u;   // -infinity
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = key0 + c0 + c <= pr ? v[c] : kNone;
-                    if (any_bad)
-                        for (int s = 0; s < 32 / BS; ++s) {
-                            const int blk = (key0 + c0) / BS + s;
-                            const int id = blk <= p_max / BS ? table[blk] : 0;
-                            if (id < 0 || id >= p.num_blocks)
+                            for (int c = 0; c < 32; ++c) v[c] = key0 + c0 + c <= pr ? v[c] : kNone;
+                            if (unit.bad)
+                                for (int s = 0; s < 32 / BS; ++s) {
+                                    const int blk = (key0 + c0) / BS + s;
+                                    const int id = blk < (unit.L + BS - 1) / BS ? p.block_tables[(size_t)unit.b * p.max_blocks + blk] : 0;
+                                    if (id < 0 || id >= p.num_blocks)
 #pragma unroll
-                                for (int c = 0; c < 32; ++c) v[c] = c / BS == s ? kNone : v[c];
+                                        for (int c = 0; c < 32; ++c) v[c] = c / BS == s ? kNone : v[c];
+                                }
                         }
+                        float m4[4] = {m, m, m, m};
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2)
+                            m4[(c >> 1) & 3] = max_nan(m4[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                        const float mx = max_nan(max_nan(m4[0], m4[1], m4[2]), m4[3]);
+                        const float by = mx == -INFINITY ? 0.f : mx * p.scale_log2;
+                        const uint64_t nb2 = f2(-by, -by);
+                        uint64_t s2[2] = {0ull, 0ull};
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            float a, b;
+                            f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nb2), a, b);
+                            s2[(c >> 1) & 1] = add2(s2[(c >> 1) & 1], f2(ex2(a), ex2(b)));
+                        }
+                        float a, b, c, d;
+                        f2_split(s2[0], a, b);
+                        f2_split(s2[1], c, d);
+                        l = fmaf(l, ex2(fmaf(m, p.scale_log2, -by)), (a + b) + (c + d));
+                        m = mx;
+                    });
                 }
-                float m4[4] = {m, m, m, m};
-#pragma unroll
-                for (int c = 0; c < 32; c += 2)
-                    m4[(c >> 1) & 3] = max_nan(m4[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-                const float mx = max_nan(max_nan(m4[0], m4[1], m4[2]), m4[3]);
-                const float base = mx == -INFINITY ? 0.f : mx * p.scale_log2;
-                const uint64_t nb2 = f2(-base, -base);
-                uint64_t s2[2] = {0ull, 0ull};
-#pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    float a, b;
-                    f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nb2), a, b);
-                    s2[(c >> 1) & 1] = add2(s2[(c >> 1) & 1], f2(ex2(a), ex2(b)));
-                }
-                float a, b, c, d;
-                f2_split(s2[0], a, b);
-                f2_split(s2[1], c, d);
-                l = fmaf(l, ex2(fmaf(m, p.scale_log2, -base)), (a + b) + (c + d));
-                m = mx;
-            });
-        }
-        if (!ok) flag_error(p.err, kErrTimeout);
-        m = m == -INFINITY ? m : m * p.scale_log2;
-        if (group == 1) other[me] = make_float2(m, l);
-        groups_sync();
-        if (group == 0) {
-            const float2 o = other[me];
-            const float mx = max_nan(m, o.x), base = mx == -INFINITY ? 0.f : mx;
-            p.stats[(((size_t)item * p.row_tiles + rt) * p.splits + split) * kTile + me] =
-                make_float2(mx, l * ex2(m - base) + o.y * ex2(o.x - base));
-        }
-    }
-    tc::fence_before_sync();
-    __syncthreads();
-    if (warp == kMmaWarp) {
-        tc::fence_after_sync();
-        tc::dealloc(pipe.tmem, kTmemCols);
-    }
-}
-
-// kStreamKeys: one row tile, held, and p.per key tiles; else a key tile, held, and the row
-// tiles that see it, every csize-th for each CTA of a cluster, whose gains meet in its first.
-template <int D, int BS, bool kStreamKeys>
-__global__ void __launch_bounds__(kThreads, 2) weigh_gain_kernel(const Params p) {
-    pdl_enter();
-    using P = Pipe<D>;
-    extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(8) uint64_t bars[kNumBars];
-    __shared__ uint32_t tmem_slot;
-    __shared__ __align__(16) float base[2][kTile];         // M_r of the row tile a warpgroup works on
-    __shared__ float part[2][kTile];                       // gains of the second group, of the CTA
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = kStreamKeys ? 0 : (int)cluster_rank(), csize = kStreamKeys ? 1 : (int)cluster_size();
-    // the items that the first pass read last come first: their keys may still be in L2
-    const int item = gridDim.y - 1 - blockIdx.y, b = item / p.num_kv_heads, hk = item - b * p.num_kv_heads;
-    const Chunk ch(p, b, BS, false);
-    if (ch.w == 0) return;                                 // the whole cluster
-    const int tiles = (ch.L + kTile - 1) / kTile, nr = ch.w * p.G, row_tiles = (nr + kTile - 1) / kTile;
-    const int kt0 = kStreamKeys ? blockIdx.x * p.per : blockIdx.x / csize;
-    if (kt0 >= tiles) return;
-    const int first_pos = ch.L - ch.w;                     // of the first query that counts
-    const int rt0 = kStreamKeys ? 0 : max(0, kt0 * kTile - first_pos) * p.G / kTile + rank;
-    const int n = kStreamKeys ? min(p.per, tiles - kt0) : max(0, (row_tiles - rt0 + csize - 1) / csize);
-    int to = b;
-    bool lost = false;
-    if (p.rows) {
-        to = p.rows[b];
-        lost = to < 0 || to >= p.num_rows;
-        for (int i = tid; i < b; i += kThreads) lost |= p.rows[i] == to;
-    }
-    P pipe;
-    pipe.sbase = smem_addr(smem);
-    pipe.bar0 = smem_addr(bars);
-    pipe.err = p.err;
-    if (tid == 0) P::init(pipe.bar0);
-    if (__syncthreads_or(lost)) {
-        if (tid == 0) flag_error(p.err, kErrOutOfRange);
-        return;
-    }
-    if (warp == kMmaWarp) {
-        tc::alloc(smem_addr(&tmem_slot), kTmemCols);
-        tc::relinquish_alloc_permit();
-    }
-    const unsigned char* const q_tiles = p.q_tiles + (size_t)item * p.row_tiles * P::kTileBytes;
-    auto load_rows = [&](int rt, uint32_t dst, uint32_t bar) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(bar, P::kTileBytes);
-            bulk_load(dst, q_tiles + (size_t)rt * P::kTileBytes, P::kTileBytes, bar);
-        }
-        __syncwarp();
-    };
-    if (warp == kLoadWarp) {
-        if (kStreamKeys) load_rows(0, pipe.sbase, pipe.bar(kBarHeld));
-        else load_keys<D, BS>(p, b, hk, ch.L, kt0, lane, pipe.sbase, pipe.bar(kBarHeld));
-    }
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    pipe.tmem = tmem_slot;
-    if (warp == kLoadWarp) {
-        pipe.run_load(n, lane, true, [&](int i, uint32_t dst, uint32_t bar) {
-            if (kStreamKeys) load_keys<D, BS>(p, b, hk, ch.L, kt0 + i, lane, dst, bar);
-            else load_rows(rt0 + i * csize, dst, bar);
-        });
-    } else if (warp == kMmaWarp) {
-        pipe.run_mma(n, lane, true, !kStreamKeys);
-    } else {
-        const int group = warp >> 2, me = tid & 127;
-        // Row me of tile rt: its first statistics, and M: +infinity (no gain) for rows that are not
-        // there or that see no token
-        auto stats_at = [&](int rt) { return p.stats + ((size_t)item * p.row_tiles + rt) * p.splits * kTile + me; };
-        auto first_of = [&](int rt) {
-            return rt < row_tiles && rt * kTile + me < nr ? stats_at(rt)[0] : make_float2(-INFINITY, 0.f);
-        };
-        auto base_of = [&](int rt, float2 first) {
-            float m = first.x, l = first.y;
-            if (p.splits > 1 && rt * kTile + me < nr) {
-                const int last = first_pos + (min(nr, (rt + 1) * kTile) - 1) / p.G;
-                const int tiles_r = last / kTile + 1, per = (tiles_r + p.splits - 1) / p.splits, splits = (tiles_r + per - 1) / per;
-                const float2* at = stats_at(rt);
-#pragma unroll 8
-                for (int s = 1; s < splits; ++s) m = max_nan(m, at[s * kTile].x);
-                l = 0.f;
-                const float by = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-                for (int s = 0; s < splits; ++s) l += ex2(at[s * kTile].x - by) * at[s * kTile].y;
-            }
-            return m == -INFINITY ? INFINITY : m + log2f(l);
-        };
-        const int32_t* const table = p.block_tables + (size_t)b * p.max_blocks;
-        float* const out = p.weights + ((size_t)to * p.num_kv_heads + hk) * p.max_tokens;
-        auto write = [&](int t, float gain) {              // a token of its own for every thread
-            if (t >= ch.L) return;
-            const int id = table[t / BS];
-            if (id < 0 || id >= p.num_blocks) gain = 0.f;
-            out[t] = t < ch.L - ch.C ? fmaf(p.decay, out[t], gain) : gain;
-        };
-        const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
-        float total = 0.f;
-        bool ok = true;
-        float2 first = first_of(rt0 + (kStreamKeys ? 0 : group * csize));
-        if (kStreamKeys) {
-            base[group][me] = base_of(0, first);
-            group_sync(group);
-        }
-        const float* const bs = base[group];
-        for (int i = group; i < n; i += 2) {               // to the end: a group's warps meet in group_sync
-            const int kt = kStreamKeys ? kt0 + i : kt0, rt = kStreamKeys ? 0 : rt0 + i * csize, t = kt * kTile + me;
-            if (!kStreamKeys) {
-                const float mine = base_of(rt, first);
-                group_sync(group);                         // the last tile's are read
-                base[group][me] = mine;
-                group_sync(group);
-                first = first_of(rt + 2 * csize);
-            }
-            // token t is seen by the rows from column `from` of this tile on; past the last row a
-            // product may be a NaN (zeros times an infinite key)
-            const int from = max(0, t - first_pos) * p.G - rt * kTile, until = nr - rt * kTile;
-            const bool masked = kt * kTile + kTile - 1 > first_pos + rt * kTile / p.G || until < kTile;
-            uint64_t g2[2] = {0ull, 0ull};
-            ok = ok && pipe.take(i, warp, [&](int c0, uint32_t (&v)[32]) {
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(bs + c0 + c);
-                    float x[4];
-                    f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, f2(-m.x, -m.y)), x[0], x[1]);
-                    f2_split(fma2(f2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), sc2, f2(-m.z, -m.w)), x[2], x[3]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = ex2(x[j]);
-                    if (masked) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x[j] = c0 + c + j >= from && c0 + c + j < until ? x[j] : 0.f;
-                    }
-                    g2[0] = add2(g2[0], f2(x[0], x[1]));
-                    g2[1] = add2(g2[1], f2(x[2], x[3]));
-                }
-            });
-            float x, y, z, w;
-            f2_split(g2[0], x, y);
-            f2_split(g2[1], z, w);
-            const float gain = (x + y) + (z + w);
-            if (kStreamKeys) {
-                if (ok) write(t, gain);
+                if (ok && u >= 2) ok = wait(kBarPartFree + (u & 1), (u >> 1) - 1);
+                if (!ok) break;
+                reinterpret_cast<float2*>(part)[group * kTile + me] = make_float2(m == -INFINITY ? m : m * p.scale_log2, l);
             } else {
-                total += gain;
+                constexpr bool kRows = PASS == kGainRows;
+                float total = 0.f;
+                if (!kRows) ok = wait(kBarBase + (u & 1), u >> 1);
+                for (int j = skip; j < unit.n && ok; j += kTurn) {
+                    const int i = it + j, kt = kRows ? held : unit.first + j, rt = kRows ? unit.first + j : 0;
+                    const int t = kt * kTile + me;
+                    const float* const bs = base_at + (kRows ? i & 3 : u & 1) * kTile;
+                    if (kRows) ok = wait(kBarBase + (i & 3), i >> 2);
+                    if (!ok) break;
+                    // token t is seen by the rows from column `from` of this tile on; past the last
+                    // row a product may be a NaN (zeros times an infinite key)
+                    const int from = max(0, t - first_pos) * p.G - rt * kTile, until = unit.nr - rt * kTile;
+                    const bool masked = kt * kTile + kTile - 1 > first_pos + row_div(rt * kTile) || until < kTile;
+                    uint64_t g2[2] = {0ull, 0ull};
+                    ok = take(i, [&](int c0, uint32_t (&v)[32]) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 m = *reinterpret_cast<const float4*>(bs + c0 + c);
+                            float x[4];
+                            f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, f2(-m.x, -m.y)), x[0], x[1]);
+                            f2_split(fma2(f2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), sc2, f2(-m.z, -m.w)), x[2], x[3]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
+                            if (masked) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) x[k] = c0 + c + k >= from && c0 + c + k < until ? x[k] : 0.f;
+                            }
+                            g2[0] = add2(g2[0], f2(x[0], x[1]));
+                            g2[1] = add2(g2[1], f2(x[2], x[3]));
+                        }
+                    });
+                    float x, y, z, w;
+                    f2_split(g2[0], x, y);
+                    f2_split(g2[1], z, w);
+                    float gain = (x + y) + (z + w);
+                    if (kRows) {
+                        total += gain;
+                    } else if (ok && t < unit.L) {         // a token of its own for every thread
+                        if (unit.bad) {
+                            const int id = p.block_tables[(size_t)unit.b * p.max_blocks + t / BS];
+                            if (id < 0 || id >= p.num_blocks) gain = 0.f;
+                        }
+                        float* const at = p.weights + ((size_t)unit.to * p.num_kv_heads + unit.hk) * p.max_tokens + t;
+                        *at = t < unit.L - unit.C ? fmaf(p.decay, *at, gain) : gain;
+                    }
+                }
+                if (kRows) {
+                    if (ok && u >= 2) ok = wait(kBarPartFree + (u & 1), (u >> 1) - 1);
+                    if (!ok) break;
+                    reinterpret_cast<float*>(part)[group * kTile + me] = total;
+                }
             }
+            if (ok) mbar_arrive(bar(kBarPart + (u & 1)));
         }
-        if (!ok) flag_error(p.err, kErrTimeout);
-        if (!kStreamKeys) {
-            if (group == 1) part[0][me] = total;
-            groups_sync();
-            if (group == 0) {
-                total += part[0][me];
-                if (csize == 1) write(kt0 * kTile + me, total);
-                else part[1][me] = total;
-            }
-        }
-    }
-    if (!kStreamKeys && csize > 1) {
-        __syncwarp();
-        cluster_sync();
-        if (rank == 0 && tid < kTile && kt0 * kTile + tid < ch.L) {
-            const int t = kt0 * kTile + tid, id = p.block_tables[(size_t)b * p.max_blocks + t / BS];
-            float gain = 0.f;
-            for (int r = 0; r < csize; ++r) gain += cluster_ld(&part[1][tid], r);
-            if (id < 0 || id >= p.num_blocks) gain = 0.f;
-            float* const at = p.weights + ((size_t)to * p.num_kv_heads + hk) * p.max_tokens + t;
-            *at = t < ch.L - ch.C ? fmaf(p.decay, *at, gain) : gain;
-        }
-        __syncwarp();
-        cluster_sync();                                    // the others' shared memory is read
+        if (!ok && lane == 0) flag_error(p.err, kErrTimeout);
     }
     tc::fence_before_sync();
     __syncthreads();
     if (warp == kMmaWarp) {
         tc::fence_after_sync();
-        tc::dealloc(pipe.tmem, kTmemCols);
+        tc::dealloc(tmem, kTmemCols);
     }
 }
 
-// Row tiles and splits of the stats pass
+// The splits' statistics of a row to its M_r: a thread a row
+__global__ void __launch_bounds__(kTile) weigh_merge_kernel(const Params p, int block_size) {
+    pdl_enter();
+    const int rt = blockIdx.x, item = blockIdx.y, me = threadIdx.x;
+    Chunk ch;
+    ch.read(p, item / p.num_kv_heads, block_size);
+    const int nr = ch.w * p.G;
+    if (rt * kTile >= nr) return;
+    // as the first pass split them: the tiles that it held together
+    const int last_tile = p.row_tiles == 1 ? rt : rt | 1;
+    const int seen_tiles = (ch.L - ch.w + (min(nr, (last_tile + 1) * kTile) - 1) / p.G) / kTile + 1;
+    const int tiles = (ch.L + kTile - 1) / kTile, ns = min(p.splits, (tiles + p.per - 1) / p.per);
+    const int per = (seen_tiles + ns - 1) / ns, splits = (seen_tiles + per - 1) / per;
+    const size_t tile = (size_t)item * p.row_tiles + rt;
+    const float2* const at = p.stats + tile * p.splits * kTile + me;
+    float m = -INFINITY, l = 0.f;
+    for (int s0 = 0; s0 < splits; s0 += 8) {               // eight reads in flight
+        float2 x[8];
+        float mx = m;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = s0 + k < splits ? at[(size_t)(s0 + k) * kTile] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx = max_nan(mx, x[k].x);
+        const float by = mx == -INFINITY ? 0.f : mx;
+        l *= ex2(m - by);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) l += ex2(x[k].x - by) * x[k].y;
+        m = mx;
+    }
+    p.bases[tile * kTile + me] = rt * kTile + me < nr ? row_base(m, l) : INFINITY;
+}
+
+// Tiles, and units of both passes: about kTargetUnits each
 struct Shape {
-    long long items, row_tiles, splits;
-    Shape(int num_seqs, int num_kv_heads, int G, int max_query_len, int window) {
+    long long items, row_tiles, key_tiles, per, splits, key_pairs, row_parts;
+    Shape(int num_seqs, int num_kv_heads, int G, int max_query_len, int window, int max_blocks, int block_size) {
         const long long w = window > 0 && window < max_query_len ? window : max_query_len;
         items = (long long)num_seqs * num_kv_heads;
         row_tiles = (w * G + kTile - 1) / kTile;
-        const long long ctas = items * row_tiles;
-        splits = ctas > 0 ? kTargetCtas / ctas : 1;
+        key_tiles = ((long long)max_blocks * block_size + kTile - 1) / kTile;
+        const long long held = row_tiles > 1 ? items * ((row_tiles + 1) / 2) : items;
+        per = (held * key_tiles + kTargetUnits - 1) / kTargetUnits;
+        if (per < 4) per = 4;
+        splits = (key_tiles + per - 1) / per;
+        const long long most = kTargetUnits / (held > 0 ? held : 1) + 1;
+        if (splits > most) splits = most;                  // what the workspace holds
         if (splits < 1) splits = 1;
+        key_pairs = (key_tiles + 1) / 2;
+        const long long pairs = items * key_pairs;
+        row_parts = pairs > 0 && pairs < kTargetUnits ? (kTargetUnits + pairs - 1) / pairs : 1;
+        if (row_parts > (row_tiles + 3) / 4) row_parts = (row_tiles + 3) / 4;   // four row tiles or so at least
+        if (row_parts < 1) row_parts = 1;
     }
+    // of the workspace: the next unit, the row runs' arrivals and gains, whatever the shape (pairs
+    // that have row runs are below kTargetUnits, and all their runs below twice that)
+    static constexpr size_t kCounters = 128 + (size_t)kTargetUnits * 4, kParts = 2 * (size_t)kTargetUnits * 2 * kTile * 4;
 };
 
 template <int D, int BS>
-int launch(Params p, cudaStream_t stream) {
-    using P = Pipe<D>;
-    auto stats = weigh_stats_kernel<D, BS>;
-    auto gain = p.row_tiles == 1 ? weigh_gain_kernel<D, BS, true> : weigh_gain_kernel<D, BS, false>;
+int launch(const Params& p, cudaStream_t stream) {
+    using S = Shared<D>;
+    auto stats = p.row_tiles == 1 ? weigh_kernel<kStats, 1, D, BS> : weigh_kernel<kStats, 2, D, BS>;
+    auto gain = p.row_tiles == 1 ? weigh_kernel<kGainKeys, 1, D, BS> : weigh_kernel<kGainRows, 2, D, BS>;
     int occ = 0;
-    int st = kernel_setup(reinterpret_cast<const void*>(stats), P::kSmem, kThreads, &occ);
+    int st = kernel_setup(reinterpret_cast<const void*>(stats), S::kBytes, kThreads, &occ);
     if (st != PKV_OK) return st;
-    st = kernel_setup(reinterpret_cast<const void*>(gain), P::kSmem, kThreads, &occ);
+    st = kernel_setup(reinterpret_cast<const void*>(gain), S::kBytes, kThreads, &occ);
     if (st != PKV_OK) return st;
-    const int items = p.num_seqs * p.num_kv_heads;
+    // no more CTAs than there can be units
+    const long long all = (long long)p.num_seqs * p.num_kv_heads * p.row_tiles * p.splits;
+    const int sms = num_sms();
     note_launch();
-    cudaError_t e = launch_pdl(stats, dim3((unsigned)p.splits, (unsigned)p.row_tiles, (unsigned)items), dim3(kThreads),
-                               P::kSmem, stream, p);
+    cudaError_t e = launch_pdl(stats, dim3((unsigned)(all < sms ? all : sms)), dim3(kThreads), S::kBytes, stream, p);
     if (e != cudaSuccess) return cuda_fail("weigh_prefill_tokens: statistics launch", e);
-    // key tiles a CTA streams: enough CTAs for two waves, no more than 16
-    p.per = 1;
-    if (p.row_tiles == 1) {
-        const long long all = (long long)items * p.key_tiles;
-        p.per = (int)(all / kTargetCtas);
-        p.per = p.per < 1 ? 1 : p.per > 16 ? 16 : p.per;
+    if (p.splits > 1) {
+        note_launch();
+        e = launch_pdl(weigh_merge_kernel, dim3((unsigned)p.row_tiles, (unsigned)(p.num_seqs * p.num_kv_heads)), dim3(kTile), 0,
+                       stream, p, BS);
+        if (e != cudaSuccess) return cuda_fail("weigh_prefill_tokens: merge launch", e);
     }
-    // CTAs that share a key tile's rows: a few row tiles each, seven waves or so
-    const long long key_ctas = ((long long)p.key_tiles + p.per - 1) / p.per;
-    int size = 1;
-    if (p.row_tiles > 1)
-        while (size < 8 && key_ctas * items * size < 2048 && p.row_tiles / size > 4) size *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(key_ctas * size), (unsigned)items);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = P::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = size;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
     note_launch();
-    e = cudaLaunchKernelEx(&cfg, gain, p);
+    e = launch_pdl(gain, dim3((unsigned)sms), dim3(kThreads), S::kBytes, stream, p);
     return e == cudaSuccess ? PKV_OK : cuda_fail("weigh_prefill_tokens: weights launch", e);
 }
 
@@ -612,11 +855,11 @@ int launch(Params p, cudaStream_t stream) {
 extern "C" size_t weigh_prefill_workspace_size(int num_seqs, int num_heads, int max_query_len, int window) {
     using namespace pkv::weigh;
     if (num_seqs <= 0 || num_heads <= 0 || max_query_len <= 0 || window < 0) return 0;
-    // at most (sequences x heads) x (queries + 127) rows: 256 bytes and one pair of statistics
-    // each, and the pairs of the splits
+    // at most (sequences x heads) x (queries + 127) rows, 256 bytes, M_r and a pair of statistics each,
+    // and the pairs of the splits; what Shape counts
     const long long w = window > 0 && window < max_query_len ? window : max_query_len;
     const size_t rows = (size_t)num_seqs * num_heads * (size_t)(w + kTile - 1);
-    return rows * (256 + 8) + (size_t)kTargetCtas * kTile * 8;
+    return Shape::kCounters + Shape::kParts + rows * (256 + 4 + 8) + 2 * (size_t)kTargetUnits * kTile * 8;
 }
 
 extern "C" int weigh_prefill_tokens(float* token_weights, const int32_t* weight_rows, const void* q, const void* k_pool,
@@ -638,9 +881,10 @@ extern "C" int weigh_prefill_tokens(float* token_weights, const int32_t* weight_
     if (q_dtype != PKV_BF16 || kv_dtype != PKV_BF16 || (head_dim != 64 && head_dim != 128) ||
         (block_size != 16 && block_size != 32) || G > weigh::kMaxGroup)
         return PKV_ERR_UNSUPPORTED;
-    const weigh::Shape shape(num_seqs, num_kv_heads, G, max_query_len, window);
-    // the launches' grids; rows and positions times a group in 32 bits
-    if (shape.items > 65535 || shape.row_tiles > 65535 ||
+    const weigh::Shape shape(num_seqs, num_kv_heads, G, max_query_len, window, max_blocks_per_seq, block_size);
+    // units, rows and positions times a group in 32 bits
+    if (shape.items > 65535 || shape.row_tiles > 65535 || shape.items * shape.row_tiles * shape.splits > 0x3fffffff ||
+        shape.items * shape.key_tiles > 0x3fffffff ||
         (long long)max_blocks_per_seq * block_size > 0x7fffffffLL / weigh::kMaxGroup)
         return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || max_query_len == 0) return PKV_OK;
@@ -670,13 +914,21 @@ extern "C" int weigh_prefill_tokens(float* token_weights, const int32_t* weight_
     p.G = G;
     p.row_tiles = (int)shape.row_tiles;
     p.splits = (int)shape.splits;
-    p.key_tiles = (max_blocks_per_seq * block_size + weigh::kTile - 1) / weigh::kTile;
+    p.per = (int)shape.per;
+    p.g_magic = (uint32_t)(0x100000000ull / (unsigned)G) + 1u;
     // never 0: hidden logits are -infinity times it
     p.scale_log2 = scale == 0.f ? 1.17549435e-38f : std::fabs(scale) * 1.4426950408889634f;
-    p.q_sign = scale < 0.f ? 0x80008000u : 0u;
+    p.sign = scale < 0.f ? 0x80008000u : 0u;
     p.decay = decay;
-    p.q_tiles = static_cast<unsigned char*>(workspace);
-    p.stats = reinterpret_cast<float2*>(p.q_tiles + (size_t)(shape.items * shape.row_tiles) * weigh::kTile * head_dim * 2);
+    p.key_pairs = (int)shape.key_pairs;
+    p.row_parts = (int)shape.row_parts;
+    p.next = static_cast<int*>(workspace);
+    p.arrived = p.next + 32;
+    p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + weigh::Shape::kCounters);
+    p.q_tiles = reinterpret_cast<unsigned char*>(p.parts) + weigh::Shape::kParts;
+    const size_t row_count = (size_t)(shape.items * shape.row_tiles) * weigh::kTile;
+    p.bases = reinterpret_cast<float*>(p.q_tiles + row_count * head_dim * 2);
+    p.stats = reinterpret_cast<float2*>(p.bases + row_count);
     p.err = error_word();
     if (!p.err) return PKV_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
