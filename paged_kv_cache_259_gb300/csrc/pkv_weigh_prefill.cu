@@ -19,11 +19,11 @@
 // and streams others past them: stats, H row tiles and a run of their key tiles; gain, with one
 // row tile a kv head (a short window), the row tile and a run of key tiles, else two key tiles
 // and a run of the row tiles that see them. H is 2 wherever there are two to hold: what is
-// streamed comes from L2 at 6.5 TB/s, which bounds a unit that holds one. Warps 0-15: four groups
-// with a product (128 columns of tensor memory) and a thread a lane each; tile i of the stream
-// is, for held tile h, group h 4/H + i % (4/H)'s. Warp 16 issues the products, 17 copies keys, 18
-// rows, 19 picks the units and joins the groups' results of each. Row runs of the same key
-// tiles leave their gains in the workspace; the last of them adds all up, in order.
+// streamed comes from L2 at 6.5 TB/s, which bounds a unit that holds one. Warps 0-7: two groups
+// with a thread a lane of tensor memory, which holds four products; with two held tiles a group
+// has one of them, else every other tile of the stream. Warp 8 issues the products, 9 copies
+// keys, 10 rows, 11 picks the units and joins the groups' results of each. Row runs of the same
+// key tiles leave their gains in the workspace; the last of them adds all up, in order.
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -36,9 +36,10 @@ namespace pkv {
 namespace weigh {
 
 constexpr int kTile = 128;             // rows, keys of a tile
-constexpr int kGroups = 4;             // of 128 threads; products and streamed tiles in flight
-constexpr int kMmaWarp = 16, kKeyWarp = 17, kRowWarp = 18, kPickWarp = 19;
-constexpr int kThreads = 20 * 32;
+constexpr int kBufs = 4;               // products (128 columns of tensor memory) and streamed tiles in flight
+constexpr int kGroups = 2;             // of 128 threads
+constexpr int kMmaWarp = 8, kKeyWarp = 9, kRowWarp = 10, kPickWarp = 11;
+constexpr int kThreads = 12 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kTile, kTile);
 constexpr int kTargetUnits = 1216;     // of the stats pass: eight an SM
@@ -57,7 +58,7 @@ struct Params {
     const int32_t* query_start;
     unsigned char* q_tiles;            // [items][row_tiles] tiles of 128 rows, core matrices
     float2* stats;                     // [items][row_tiles][splits][128] maximum, sum
-    float* bases;                      // [items][row_tiles][128] M_r
+    float* bases;                      // [items][row_tiles][128] -M_r
     int* next;                         // the gain pass's next unit,
     int* arrived;                      // and the row runs of each pair of key tiles that are through
     float* parts;                      // their gains [pairs][row_parts][2][128]
@@ -126,8 +127,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
 }
 
-// M_r from a row's maximum and sum: +infinity (no gain) for a row that sees no token
-__device__ __forceinline__ float row_base(float m, float l) { return m == -INFINITY ? INFINITY : m + log2f(l); }
+// -M_r from a row's maximum and sum: -infinity (no gain) for a row that sees no token
+__device__ __forceinline__ float row_base(float m, float l) { return m == -INFINITY ? -INFINITY : -(m + log2f(l)); }
 
 // One unit: `n` stream tiles from `first` on, past the held tiles from `held` on; -1: no more
 struct Unit {
@@ -142,12 +143,12 @@ enum : int {
     kBarHeldFree = 2,                  // [2] their products are done
     kBarFull = 4,                      // [4] a streamed tile is there
     kBarFree = 8,                      // [4] its products are done
-    kBarDone = 12,                     // [4] a group's product is
+    kBarDone = 12,                     // [4] a product is done
     kBarRead = 16,                     // [4] and is read (128 threads)
-    kBarPart = 20,                     // [2] a unit's results are there (512)
+    kBarPart = 20,                     // [2] a unit's results are there (256)
     kBarPartFree = 22,                 // [2] they are joined
     kBarUnit = 24,                     // [kRing] a unit is picked
-    kBarUnitFree = 28,                 // [kRing] everybody has seen it (19 warps)
+    kBarUnitFree = 28,                 // [kRing] everybody has seen it (11 warps)
     kBarBase = 32,                     // [4] a row tile's M_r
     kBarDrain = 36,
     kNumBars
@@ -157,7 +158,7 @@ template <int D>
 struct Shared {
     static constexpr int kTileBytes = kTile * D * 2, kGroupBytes = D / 8 * 128;   // 8 rows
     static constexpr int kHeld = 0, kStream = 2 * kTileBytes;
-    static constexpr int kPart = kStream + kGroups * kTileBytes;                  // [2][4][128] of 8 bytes
+    static constexpr int kPart = kStream + kBufs * kTileBytes;                    // [2][kGroups][128] of 8 bytes
     static constexpr int kBase = kPart + 2 * kGroups * kTile * 8;                 // [4][128] float
     static constexpr int kUnits = kBase + 4 * kTile * 4;
     static constexpr int kBars = kUnits + (kRing * (int)sizeof(Unit) + 15) / 16 * 16;
@@ -186,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
     pdl_enter();
     using S = Shared<D>;
     static_assert(H == 1 || H == 2, "held tiles");
-    constexpr int kBlocks = kTile / BS, kTurn = kGroups / H;    // groups that share a held tile
+    constexpr int kBlocks = kTile / BS, kTurn = kBufs / H;      // products of a held tile
+    constexpr int kShare = kGroups / H;                         // groups that share a held tile
     // place and use of what unit u holds: two places in turn, or one of two tiles
     auto held_at = [](int u) { return H == 1 ? u & 1 : 0; };
     auto held_use = [](int u) { return H == 1 ? u >> 1 : u; };
@@ -385,19 +387,19 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
 #pragma unroll
                 for (int k = 0; k < 4 * H; ++k) {
                     const int me = lane + 32 * (k & 3), h = k >> 2, rt = unit.held + h;
-                    float2 x[kTurn];
+                    float2 x[kShare];
                     float m = -INFINITY, l = 0.f;
 #pragma unroll
-                    for (int g = 0; g < kTurn; ++g) x[g] = reinterpret_cast<const float2*>(part)[(h * kTurn + g) * kTile + me];
+                    for (int g = 0; g < kShare; ++g) x[g] = reinterpret_cast<const float2*>(part)[(h * kShare + g) * kTile + me];
 #pragma unroll
-                    for (int g = 0; g < kTurn; ++g) m = max_nan(m, x[g].x);
+                    for (int g = 0; g < kShare; ++g) m = max_nan(m, x[g].x);
                     const float by = m == -INFINITY ? 0.f : m;
 #pragma unroll
-                    for (int g = 0; g < kTurn; ++g) l += ex2(x[g].x - by) * x[g].y;
+                    for (int g = 0; g < kShare; ++g) l += ex2(x[g].x - by) * x[g].y;
                     if (rt * kTile >= unit.nr) continue;
                     const size_t tile = (size_t)unit.item * p.row_tiles + rt;
                     if (p.splits > 1) p.stats[(tile * p.splits + unit.split) * kTile + me] = make_float2(m, l);
-                    else p.bases[tile * kTile + me] = rt * kTile + me < unit.nr ? row_base(m, l) : INFINITY;
+                    else p.bases[tile * kTile + me] = rt * kTile + me < unit.nr ? row_base(m, l) : -INFINITY;
                 }
             } else {
                 float gain[4 * H];
@@ -405,8 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
                 for (int k = 0; k < 4 * H; ++k) {
                     gain[k] = 0.f;
 #pragma unroll
-                    for (int g = 0; g < kTurn; ++g)
-                        gain[k] += reinterpret_cast<const float*>(part)[((k >> 2) * kTurn + g) * kTile + lane + 32 * (k & 3)];
+                    for (int g = 0; g < kShare; ++g)
+                        gain[k] += reinterpret_cast<const float*>(part)[((k >> 2) * kShare + g) * kTile + lane + 32 * (k & 3)];
                 }
                 bool write = true;
                 if (unit.splits > 1) {                     // one of several row runs: the last adds them up
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
             for (int j = 0; j < unit.n && ok; ++j, ++it) {
                 // their place was tile it - 4's, whose groups are through once they have read the product
                 // of tile it - kTurn
-                for (int g = it % kTurn; g < kGroups && ok && it >= kTurn; g += kTurn) ok = wait(kBarRead + g, it / kTurn - 1);
+                for (int g = it % kTurn; g < kBufs && ok && it >= kTurn; g += kTurn) ok = wait(kBarRead + g, it / kTurn - 1);
                 if (!ok) break;
                 load_bases(unit.first + j, it & 3);
                 based = it + 1;
@@ -630,71 +632,67 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
         // ------------------------------------------------------------ exponentials
         const int group = warp >> 2, me = tid & 127;
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
-        // Product i, 32 columns at a time: use(column, values)
-        auto take = [&](int i, auto use) {
-            if (!wait(kBarDone + group, i / kTurn)) return false;
+        // Product of stream tile i: its 128 columns
+        uint32_t v[kTile];
+        auto take = [&](int i) {
+            const int buf = (H == 2 ? group * kTurn : 0) + i % kTurn;
+            if (!wait(kBarDone + buf, i / kTurn)) return false;
             tc::fence_after_sync();
-            const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * kTile;
-            uint32_t v[2][32];
-            tc::ld32(at, v[0]);
+            const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + buf * kTile;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                tc::wait_ld();
-                if (c < 3) tc::ld32(at + 32 * (c + 1), v[(c + 1) & 1]);
-                else {
-                    tc::fence_before_sync();
-                    mbar_arrive(bar(kBarRead + group));
-                }
-                use(32 * c, v[c & 1]);
-            }
+            for (int c = 0; c < 4; ++c) tc::ld32(at + 32 * c, reinterpret_cast<uint32_t(&)[32]>(v[32 * c]));
+            tc::wait_ld();
+            tc::fence_before_sync();
+            mbar_arrive(bar(kBarRead + buf));
             return true;
         };
         bool ok = true;
         int it = 0;                                        // of the unit's first tile
         for (int u = 0; ok && next_unit(u); it += unit.n, ++u) {
-            const int first_pos = unit.L - unit.w, skip = (group - it) & (kTurn - 1), held = unit.held + group / kTurn;
+            const int first_pos = unit.L - unit.w, skip = H == 2 ? 0 : (group - it) & 1, held = unit.held + (H == 2 ? group : 0);
             unsigned char* const part = smem + S::kPart + (u & 1) * kGroups * kTile * 8;
             if constexpr (PASS == kStats) {
                 const int r0 = held * kTile, r = min(r0 + me, unit.nr - 1), pr = first_pos + row_div(r);
                 const int p_min = first_pos + row_div(min(r0, unit.nr - 1));
                 float m = -INFINITY, l = 0.f;              // of the products; the scale is not negative
-                for (int j = skip; j < unit.n && ok; j += kTurn) {
+                for (int j = skip; j < unit.n && ok; j += kShare) {
                     const int key0 = (unit.first + j) * kTile;
                     const bool masked = unit.bad || key0 + kTile - 1 > p_min;
-                    ok = take(it + j, [&](int c0, uint32_t (&v)[32]) {
-                        if (masked) {
-                            constexpr uint32_t kNone = 0xff800000u;   // -infinity
+                    ok = take(it + j);
+                    if (!ok) break;
+                    if (masked) {
+                        constexpr uint32_t kNone = 0xff800000u;   // -infinity
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) v[c] = key0 + c0 + c <= pr ? v[c] : kNone;
-                            if (unit.bad)
-                                for (int s = 0; s < 32 / BS; ++s) {
-                                    const int blk = (key0 + c0) / BS + s;
-                                    const int id = blk < (unit.L + BS - 1) / BS ? p.block_tables[(size_t)unit.b * p.max_blocks + blk] : 0;
-                                    if (id < 0 || id >= p.num_blocks)
+                        for (int c = 0; c < kTile; ++c) v[c] = key0 + c <= pr ? v[c] : kNone;
+                        if (unit.bad)
+                            for (int s = 0; s < kBlocks; ++s) {
+                                const int blk = key0 / BS + s;
+                                const int id = blk < (unit.L + BS - 1) / BS ? p.block_tables[(size_t)unit.b * p.max_blocks + blk] : 0;
+                                if (id < 0 || id >= p.num_blocks)
 #pragma unroll
-                                        for (int c = 0; c < 32; ++c) v[c] = c / BS == s ? kNone : v[c];
-                                }
-                        }
-                        float m4[4] = {m, m, m, m};
+                                    for (int c = 0; c < kTile; ++c) v[c] = c / BS == s ? kNone : v[c];
+                            }
+                    }
+                    float m8[8];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2)
-                            m4[(c >> 1) & 3] = max_nan(m4[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-                        const float mx = max_nan(max_nan(m4[0], m4[1], m4[2]), m4[3]);
-                        const float by = mx == -INFINITY ? 0.f : mx * p.scale_log2;
-                        const uint64_t nb2 = f2(-by, -by);
-                        uint64_t s2[2] = {0ull, 0ull};
+                    for (int c = 0; c < 8; ++c) m8[c] = max_nan(m, __uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            float a, b;
-                            f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nb2), a, b);
-                            s2[(c >> 1) & 1] = add2(s2[(c >> 1) & 1], f2(ex2(a), ex2(b)));
-                        }
-                        float a, b, c, d;
-                        f2_split(s2[0], a, b);
-                        f2_split(s2[1], c, d);
-                        l = fmaf(l, ex2(fmaf(m, p.scale_log2, -by)), (a + b) + (c + d));
-                        m = mx;
-                    });
+                    for (int c = 8; c < kTile / 2; ++c)
+                        m8[c & 7] = max_nan(m8[c & 7], __uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+                    const float mx = max_nan(max_nan(max_nan(m8[0], m8[1], m8[2]), m8[3], m8[4]), m8[5], max_nan(m8[6], m8[7]));
+                    const float by = mx == -INFINITY ? 0.f : mx * p.scale_log2;
+                    const uint64_t nb2 = f2(-by, -by);
+                    uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 2) {
+                        float a, b;
+                        f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nb2), a, b);
+                        s2[(c >> 1) & 3] = add2(s2[(c >> 1) & 3], f2(ex2(a), ex2(b)));
+                    }
+                    float a, b;
+                    f2_split(add2(add2(s2[0], s2[1]), add2(s2[2], s2[3])), a, b);
+                    l = fmaf(l, ex2(fmaf(m, p.scale_log2, -by)), a + b);
+                    m = mx;
                 }
                 if (ok && u >= 2) ok = wait(kBarPartFree + (u & 1), (u >> 1) - 1);
                 if (!ok) break;
@@ -703,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
                 constexpr bool kRows = PASS == kGainRows;
                 float total = 0.f;
                 if (!kRows) ok = wait(kBarBase + (u & 1), u >> 1);
-                for (int j = skip; j < unit.n && ok; j += kTurn) {
+                for (int j = skip; j < unit.n && ok; j += kShare) {
                     const int i = it + j, kt = kRows ? held : unit.first + j, rt = kRows ? unit.first + j : 0;
                     const int t = kt * kTile + me;
                     const float* const bs = base_at + (kRows ? i & 3 : u & 1) * kTile;
@@ -713,28 +711,25 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
                     // row a product may be a NaN (zeros times an infinite key)
                     const int from = max(0, t - first_pos) * p.G - rt * kTile, until = unit.nr - rt * kTile;
                     const bool masked = kt * kTile + kTile - 1 > first_pos + row_div(rt * kTile) || until < kTile;
-                    uint64_t g2[2] = {0ull, 0ull};
-                    ok = take(i, [&](int c0, uint32_t (&v)[32]) {
+                    ok = take(i);
+                    if (!ok) break;
+                    uint64_t g2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const float4 m = *reinterpret_cast<const float4*>(bs + c0 + c);
-                            float x[4];
-                            f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, f2(-m.x, -m.y)), x[0], x[1]);
-                            f2_split(fma2(f2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), sc2, f2(-m.z, -m.w)), x[2], x[3]);
+                    for (int c = 0; c < kTile; c += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(bs + c);
+                        float x[4];
+                        f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, f2(m.x, m.y)), x[0], x[1]);
+                        f2_split(fma2(f2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), sc2, f2(m.z, m.w)), x[2], x[3]);
+                        if (masked) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) x[k] = ex2(x[k]);
-                            if (masked) {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) x[k] = c0 + c + k >= from && c0 + c + k < until ? x[k] : 0.f;
-                            }
-                            g2[0] = add2(g2[0], f2(x[0], x[1]));
-                            g2[1] = add2(g2[1], f2(x[2], x[3]));
+                            for (int k = 0; k < 4; ++k) x[k] = c + k >= from && c + k < until ? x[k] : -INFINITY;
                         }
-                    });
-                    float x, y, z, w;
-                    f2_split(g2[0], x, y);
-                    f2_split(g2[1], z, w);
-                    float gain = (x + y) + (z + w);
+                        g2[(c >> 1) & 3] = add2(g2[(c >> 1) & 3], f2(ex2(x[0]), ex2(x[1])));
+                        g2[((c >> 1) & 3) + 1] = add2(g2[((c >> 1) & 3) + 1], f2(ex2(x[2]), ex2(x[3])));
+                    }
+                    float a, b2;
+                    f2_split(add2(add2(g2[0], g2[1]), add2(g2[2], g2[3])), a, b2);
+                    float gain = a + b2;
                     if (kRows) {
                         total += gain;
                     } else if (ok && t < unit.L) {         // a token of its own for every thread
@@ -793,7 +788,7 @@ __global__ void __launch_bounds__(kTile) weigh_merge_kernel(const Params p, int 
         for (int k = 0; k < 8; ++k) l += ex2(x[k].x - by) * x[k].y;
         m = mx;
     }
-    p.bases[tile * kTile + me] = rt * kTile + me < nr ? row_base(m, l) : INFINITY;
+    p.bases[tile * kTile + me] = rt * kTile + me < nr ? row_base(m, l) : -INFINITY;
 }
 
 // Tiles, and units of both passes: about kTargetUnits each
