@@ -681,7 +681,7 @@ PKV_API size_t weighed_decode_workspace_size(int num_seqs, int num_heads, int he
  *                 no clearing; calls that overlap on the GPU need one each
  *   the rest      as paged_attention_prefill
  * Supported: BF16 / BF16, head_dim in {64,128}, block_size in {16,32}, any num_heads /
- * num_kv_heads up to 128. A sequence with C > L, L beyond its table or rows outside q, or a
+ * num_kv_heads up to 128, a scale of 0 or a magnitude from 2^-100. A sequence with C > L, L beyond its table or rows outside q, or a
  * table entry outside the pool, sets PKV_ERR_OUT_OF_RANGE (the sequence's weights are left as
  * they were, or the entry's tokens are given no weight). Chunk queries past max_query_len,
  * counted from the chunk's first, are an error of the caller: such a sequence is left as it

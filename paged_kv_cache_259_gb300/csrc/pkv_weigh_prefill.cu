@@ -42,6 +42,7 @@ constexpr int kMmaWarp = 8, kKeyWarp = 9, kRowWarp = 10, kPickWarp = 11;
 constexpr int kThreads = 12 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kTile, kTile);
+constexpr int kExt = kTile * 32;       // bytes of the 16 dims that carry -M_r / scale behind a row tile
 constexpr int kTargetUnits = 1216;     // of the stats pass: eight an SM
 constexpr int kMaxGroup = 128;
 constexpr int kRing = 4;               // units picked ahead
@@ -56,9 +57,8 @@ struct Params {
     const int32_t* block_tables;
     const int32_t* seq_lens;
     const int32_t* query_start;
-    unsigned char* q_tiles;            // [items][row_tiles] tiles of 128 rows, core matrices
+    unsigned char* q_tiles;            // [items][row_tiles] tiles of 128 rows and their 16 more dims, core matrices
     float2* stats;                     // [items][row_tiles][splits][128] maximum, sum
-    float* bases;                      // [items][row_tiles][128] -M_r
     int* next;                         // the gain pass's next unit,
     int* arrived;                      // and the row runs of each pair of key tiles that are through
     float* parts;                      // their gains [pairs][row_parts][2][128]
@@ -69,6 +69,7 @@ struct Params {
     uint32_t g_magic;                  // floor(2^32 / G) + 1: r / G for r < 2^32 / G
     float scale_log2, decay;           // the scale's magnitude,
     uint32_t sign;                     // and what turns the sign of two query elements
+    int no_scale;                      // a scale of 0: rows of zeros instead
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -100,6 +101,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -127,8 +133,22 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
 }
 
-// -M_r from a row's maximum and sum: -infinity (no gain) for a row that sees no token
-__device__ __forceinline__ float row_base(float m, float l) { return m == -INFINITY ? -INFINITY : -(m + log2f(l)); }
+// -M_r of row `me` of a tile, in units of the products, as three bf16 numbers (24 bits) in the first of
+// the 16 dims behind it, whose partners in the keys' tile are 1: the products come out less M_r, and
+// the second pass neither reads nor subtracts it (128 shared-memory reads a tile and thread group
+// less: 160 us against 116 for 4 chunks of 2048). -infinity (no gain): a row that is not there or
+// sees no token.
+__device__ __forceinline__ void write_base(unsigned char* ext, int me, float m, float l, bool there, float scale_log2) {
+    const float x = !there || m == -INFINITY ? -INFINITY : -(m + log2f(l)) / scale_log2;
+    const __nv_bfloat16 a = __float2bfloat16_rn(x);
+    float rest = x - __bfloat162float(a);
+    if (!(fabsf(x) < INFINITY)) rest = 0.f;                // infinite and NaN: one number says it
+    const __nv_bfloat16 b = __float2bfloat16_rn(rest), c = __float2bfloat16_rn(rest - __bfloat162float(b));
+    const uint32_t ab = (uint32_t)__bfloat16_as_ushort(a) | ((uint32_t)__bfloat16_as_ushort(b) << 16);
+    uint4* const at = reinterpret_cast<uint4*>(ext + (me >> 3) * 256 + (me & 7) * 16);
+    at[0] = make_uint4(ab, (uint32_t)__bfloat16_as_ushort(c), 0u, 0u);
+    at[8] = make_uint4(0u, 0u, 0u, 0u);
+}
 
 // One unit: `n` stream tiles from `first` on, past the held tiles from `held` on; -1: no more
 struct Unit {
@@ -149,18 +169,18 @@ enum : int {
     kBarPartFree = 22,                 // [2] they are joined
     kBarUnit = 24,                     // [kRing] a unit is picked
     kBarUnitFree = 28,                 // [kRing] everybody has seen it (11 warps)
-    kBarBase = 32,                     // [4] a row tile's M_r
-    kBarDrain = 36,
+    kBarDrain = 32,
     kNumBars
 };
 
 template <int D>
 struct Shared {
     static constexpr int kTileBytes = kTile * D * 2, kGroupBytes = D / 8 * 128;   // 8 rows
-    static constexpr int kHeld = 0, kStream = 2 * kTileBytes;
-    static constexpr int kPart = kStream + kBufs * kTileBytes;                    // [2][kGroups][128] of 8 bytes
-    static constexpr int kBase = kPart + 2 * kGroups * kTile * 8;                 // [4][128] float
-    static constexpr int kUnits = kBase + 4 * kTile * 4;
+    static constexpr int kSlot = kTileBytes + kExt;                               // of a row tile; a key tile takes less
+    static constexpr int kHeld = 0, kStream = 2 * kSlot;
+    static constexpr int kOnes = kStream + kBufs * kSlot;                         // the keys' 16 more dims
+    static constexpr int kPart = kOnes + kExt;                                    // [2][kGroups][128] of 8 bytes
+    static constexpr int kUnits = kPart + 2 * kGroups * kTile * 8;
     static constexpr int kBars = kUnits + (kRing * (int)sizeof(Unit) + 15) / 16 * 16;
     static constexpr int kBytes = kBars + kNumBars * 8;
     static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
@@ -200,7 +220,6 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
     auto wait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar(i), parity & 1, p.err)) != 0; };
     auto row_div = [&](int r) { return p.G == 1 ? r : (int)__umulhi((uint32_t)r, p.g_magic); };
     Unit* const units = reinterpret_cast<Unit*>(smem + S::kUnits);
-    float* const base_at = reinterpret_cast<float*>(smem + S::kBase);
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kBarHeldFull + i), 1);
@@ -212,7 +231,6 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
             mbar_init(bar(kBarFull + i), 1);
             mbar_init(bar(kBarFree + i), 1);
             mbar_init(bar(kBarDone + i), 1);
-            mbar_init(bar(kBarBase + i), 1);
             mbar_init(bar(kBarRead + i), 128);
             mbar_init(bar(kBarUnit + i), 1);
             mbar_init(bar(kBarUnitFree + i), kPickWarp);
@@ -227,6 +245,12 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
     if (warp == kMmaWarp) {
         tc::alloc(smem_addr(&tmem_slot), kTmemCols);
         tc::relinquish_alloc_permit();
+    }
+    if (PASS != kStats && tid < kTile) {
+        uint4* const at = reinterpret_cast<uint4*>(smem + S::kOnes + (tid >> 3) * 256 + (tid & 7) * 16);
+        at[0] = make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);
+        at[8] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -399,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
                     if (rt * kTile >= unit.nr) continue;
                     const size_t tile = (size_t)unit.item * p.row_tiles + rt;
                     if (p.splits > 1) p.stats[(tile * p.splits + unit.split) * kTile + me] = make_float2(m, l);
-                    else p.bases[tile * kTile + me] = rt * kTile + me < unit.nr ? row_base(m, l) : -INFINITY;
+                    else write_base(p.q_tiles + tile * S::kSlot + S::kTileBytes, me, m, l, rt * kTile + me < unit.nr, p.scale_log2);
                 }
             } else {
                 float gain[4 * H];
@@ -449,11 +473,17 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
         // ------------------------------------------------------------ keys
         // Block ids, 32 a lane each, the next 32 read ahead. Blocks that are not in the pool are
         // read from block 0 (what comes of them is left out by those who use them).
-        int ids = 0, next_ids = 0, first_block = 0, window = 0;
-        auto read_ids = [&](int k) {
+        long long ids = 0, next_ids = 0;                   // as places in the pool
+        int first_block = 0, window = 0;
+        auto read_ids = [&](int k) -> long long {
             const int blk = first_block + 32 * k + lane;
             if (blk >= (unit.L + BS - 1) / BS) return 0;
-            return p.block_tables[(size_t)unit.b * p.max_blocks + blk];
+            int id = p.block_tables[(size_t)unit.b * p.max_blocks + blk];
+            if (id < 0 || id >= p.num_blocks) {
+                flag_error(p.err, kErrOutOfRange);
+                id = 0;
+            }
+            return ((long long)id * p.num_kv_heads + unit.hk) * (BS * D);
         };
         auto begin_ids = [&](int tile) {
             first_block = tile * kBlocks;
@@ -468,17 +498,15 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
                 ids = next_ids;
                 next_ids = read_ids(window + 1);
             }
-            const int n = min(kBlocks, blocks_left(j));
+            const int n = blocks_left(j);
+            if (n >= kBlocks) {
 #pragma unroll
-            for (int k = 0; k < kBlocks; ++k) {
-                int id = __shfl_sync(0xffffffffu, ids, j * kBlocks % 32 + k);
-                if (k >= n) break;                         // the whole warp
-                if (id < 0 || id >= p.num_blocks) {
-                    if (lane == 0) flag_error(p.err, kErrOutOfRange);
-                    __syncwarp();
-                    id = 0;
-                }
-                bulk_load_elect(dst + k * BS * D * 2, p.k_pool + ((size_t)id * p.num_kv_heads + unit.hk) * (BS * D), BS * D * 2, full);
+                for (int k = 0; k < kBlocks; ++k)
+                    bulk_load_elect(dst + k * BS * D * 2, p.k_pool + __shfl_sync(0xffffffffu, ids, j * kBlocks % 32 + k), BS * D * 2, full);
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < n; ++k)
+                    bulk_load_elect(dst + k * BS * D * 2, p.k_pool + __shfl_sync(0xffffffffu, ids, j * kBlocks % 32 + k), BS * D * 2, full);
             }
         };
         int it = 0, sent = 0;
@@ -489,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
                 if (held_use(u) > 0 && !wait(kBarHeldFree + held_at(u), held_use(u) - 1)) break;
                 const int there = min(H, (unit.L + kTile - 1) / kTile - unit.held);
                 mbar_arrive_expect_tx_elect(full, (uint32_t)(min(there * kBlocks, blocks_left(0)) * BS * D * 2));
-                for (int h = 0; h < there; ++h) load_keys(h, sbase + S::kHeld + (held_at(u) + h) * S::kTileBytes, full);
+                for (int h = 0; h < there; ++h) load_keys(h, sbase + S::kHeld + (held_at(u) + h) * S::kSlot, full);
                 sent = u + 1;
             } else {
                 bool ok = true;
@@ -498,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
                     if (it >= 4) ok = wait(kBarFree + s, (it >> 2) - 1);
                     if (!ok) break;
                     mbar_arrive_expect_tx_elect(bar(kBarFull + s), (uint32_t)(min(kBlocks, blocks_left(j)) * BS * D * 2));
-                    load_keys(j, sbase + S::kStream + s * S::kTileBytes, bar(kBarFull + s));
+                    load_keys(j, sbase + S::kStream + s * S::kSlot, bar(kBarFull + s));
                     sent = it + 1;
                 }
                 if (!ok) break;
@@ -514,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
 #pragma unroll 4
             for (int g = 0; g < kTile / 8; ++g) {
                 const int r = rt * kTile + g * 8 + (lane & 7);
-                const bool some = r < unit.nr;
+                const bool some = r < unit.nr && !p.no_scale;
                 const int rr = some ? r : 0;
                 const __nv_bfloat16* src = q + ((size_t)row_div(rr) * (p.num_heads - p.G) + rr) * D;
 #pragma unroll
@@ -522,29 +550,24 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto tile_of = [&](int rt) { return p.q_tiles + ((size_t)unit.item * p.row_tiles + rt) * S::kTileBytes; };
+        auto tile_of = [&](int rt) { return p.q_tiles + ((size_t)unit.item * p.row_tiles + rt) * S::kSlot; };
         auto load_rows = [&](int rt, uint32_t dst, uint32_t full) {
-            mbar_arrive_expect_tx_elect(full, S::kTileBytes);
-            bulk_load_elect(dst, tile_of(rt), S::kTileBytes, full);
+            mbar_arrive_expect_tx_elect(full, S::kSlot);
+            bulk_load_elect(dst, tile_of(rt), S::kSlot, full);
         };
-        auto load_bases = [&](int rt, int place) {         // their M_r
-            mbar_arrive_expect_tx_elect(bar(kBarBase + place), kTile * 4);
-            bulk_load_elect(smem_addr(base_at + place * kTile), p.bases + ((size_t)unit.item * p.row_tiles + rt) * kTile, kTile * 4,
-                            bar(kBarBase + place));
-        };
-        int it = 0, sent = 0, based = 0;
+        int it = 0, sent = 0;
         for (int u = 0; next_unit(u); ++u) {
-            const uint32_t held = sbase + S::kHeld + held_at(u) * S::kTileBytes, held_full = bar(kBarHeldFull + held_at(u));
+            const uint32_t held = sbase + S::kHeld + held_at(u) * S::kSlot, held_full = bar(kBarHeldFull + held_at(u));
             if (PASS != kGainRows && held_use(u) > 0 && !wait(kBarHeldFree + held_at(u), held_use(u) - 1)) break;
             if (PASS == kStats) {
                 bulk_stores_read();                        // of the unit that had the place
                 __syncwarp();
 #pragma unroll
-                for (int h = 0; h < H; ++h) send_rows(unit.held + h, held + h * S::kTileBytes);
+                for (int h = 0; h < H; ++h) send_rows(unit.held + h, held + h * S::kSlot);
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 __syncwarp();
                 if (p.sign)                                // a negative scale: the rows turn it
-                    for (int i = lane; i < H * S::kTileBytes / 16; i += 32) {
+                    for (int i = lane; i < H * S::kSlot / 16; i += 32) {
                         uint4* const at = reinterpret_cast<uint4*>(smem + (held - sbase)) + i;
                         const uint4 v = *at;
                         *at = make_uint4(v.x ^ p.sign, v.y ^ p.sign, v.z ^ p.sign, v.w ^ p.sign);
@@ -554,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
                 if (lane == 0) {
                     mbar_arrive(held_full);
                     if (unit.split == 0)                   // for the second pass
-                        bulk_store(tile_of(unit.held), held, min(H, (unit.nr + kTile - 1) / kTile - unit.held) * S::kTileBytes);
+                        for (int h = 0; h < min(H, (unit.nr + kTile - 1) / kTile - unit.held); ++h)
+                            bulk_store(tile_of(unit.held + h), held + h * S::kSlot, S::kTileBytes);
                 }
                 __syncwarp();
                 continue;
@@ -562,63 +586,49 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
             if (PASS == kGainKeys) {
                 load_rows(0, held, held_full);
                 sent = u + 1;
-                // the unit before last, which had the place, is through
-                if (u >= 2 && !wait(kBarPart + (u & 1), (u >> 1) - 1)) break;
-                load_bases(0, u & 1);
-                based = u + 1;
                 continue;
             }
-            // streamed, three tiles ahead of the one whose M_r follow
-            auto send = [&](int j, int i) {
-                if (j >= unit.n) return true;
-                if (i >= 4 && !wait(kBarFree + (i & 3), (i >> 2) - 1)) return false;
-                load_rows(unit.first + j, sbase + S::kStream + (i & 3) * S::kTileBytes, bar(kBarFull + (i & 3)));
-                sent = i + 1;
-                return true;
-            };
             bool ok = true;
-            for (int j = 0; j < 3 && ok; ++j) ok = send(j, it + j);
             for (int j = 0; j < unit.n && ok; ++j, ++it) {
-                // their place was tile it - 4's, whose groups are through once they have read the product
-                // of tile it - kTurn
-                for (int g = it % kTurn; g < kBufs && ok && it >= kTurn; g += kTurn) ok = wait(kBarRead + g, it / kTurn - 1);
+                if (it >= 4) ok = wait(kBarFree + (it & 3), (it >> 2) - 1);
                 if (!ok) break;
-                load_bases(unit.first + j, it & 3);
-                based = it + 1;
-                ok = send(j + 3, it + 3);
+                load_rows(unit.first + j, sbase + S::kStream + (it & 3) * S::kSlot, bar(kBarFull + (it & 3)));
+                sent = it + 1;
             }
             if (!ok) break;
         }
         bulk_stores_done();
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (PASS != kStats) {
-            land(PASS == kGainKeys ? kBarHeldFull : kBarFull, PASS == kGainKeys ? 2 : 4, sent);
-            land(kBarBase, PASS == kGainKeys ? 2 : 4, based);
-        }
+        if (PASS != kStats) land(PASS == kGainKeys ? kBarHeldFull : kBarFull, PASS == kGainKeys ? 2 : 4, sent);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ products
-        constexpr uint32_t hi = tc::desc_hi(S::kGroupBytes);
+        constexpr uint32_t hi = tc::desc_hi(S::kGroupBytes), hi_ext = tc::desc_hi(256);
+        const uint32_t ones = tc::desc_lo(sbase + S::kOnes, 128);
         bool ok = true;
         int it = 0;
         for (int u = 0; ok && next_unit(u); ++u) {
             ok = wait(kBarHeldFull + held_at(u), held_use(u));
             if (!ok) break;
-            const uint32_t h_lo = tc::desc_lo(sbase + S::kHeld + held_at(u) * S::kTileBytes, 128);
+            const uint32_t h_lo = tc::desc_lo(sbase + S::kHeld + held_at(u) * S::kSlot, 128);
             for (int j = 0; j < unit.n && ok; ++j, ++it) {
                 const int s = it & 3;
                 ok = wait(kBarFull + s, it >> 2);
-                const uint32_t s_lo = tc::desc_lo(sbase + S::kStream + s * S::kTileBytes, 128);
+                const uint32_t s_lo = tc::desc_lo(sbase + S::kStream + s * S::kSlot, 128);
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
                     const int g = h * kTurn + it % kTurn;
                     if (ok && it >= kTurn) ok = wait(kBarRead + g, it / kTurn - 1);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const uint32_t held = h_lo + h * (S::kTileBytes / 16);
+                    const uint32_t held = h_lo + h * (S::kSlot / 16);
                     const uint32_t a = PASS == kGainKeys ? s_lo : held, b = PASS == kGainKeys ? held : s_lo;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         tc::mma_ss2_elect(tmem + g * kTile, a + k * 16, hi, b + k * 16, hi, kIdesc, k > 0);
+                    if (PASS != kStats) {                  // less M_r
+                        const uint32_t row = (PASS == kGainKeys ? held : s_lo) + S::kTileBytes / 16;
+                        tc::mma_ss2_elect(tmem + g * kTile, ones, hi_ext, row, hi_ext, kIdesc, 1);
+                    }
                     tc::commit_elect(bar(kBarDone + g));
                 }
                 if (ok) tc::commit_elect(bar(kBarFree + s));
@@ -700,32 +710,25 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
             } else {
                 constexpr bool kRows = PASS == kGainRows;
                 float total = 0.f;
-                if (!kRows) ok = wait(kBarBase + (u & 1), u >> 1);
                 for (int j = skip; j < unit.n && ok; j += kShare) {
                     const int i = it + j, kt = kRows ? held : unit.first + j, rt = kRows ? unit.first + j : 0;
                     const int t = kt * kTile + me;
-                    const float* const bs = base_at + (kRows ? i & 3 : u & 1) * kTile;
-                    if (kRows) ok = wait(kBarBase + (i & 3), i >> 2);
-                    if (!ok) break;
                     // token t is seen by the rows from column `from` of this tile on; past the last
                     // row a product may be a NaN (zeros times an infinite key)
                     const int from = max(0, t - first_pos) * p.G - rt * kTile, until = unit.nr - rt * kTile;
                     const bool masked = kt * kTile + kTile - 1 > first_pos + row_div(rt * kTile) || until < kTile;
                     ok = take(i);
                     if (!ok) break;
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < kTile; ++c) v[c] = c >= from && c < until ? v[c] : 0xff800000u;
+                    }
                     uint64_t g2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(bs + c);
-                        float x[4];
-                        f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, f2(m.x, m.y)), x[0], x[1]);
-                        f2_split(fma2(f2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), sc2, f2(m.z, m.w)), x[2], x[3]);
-                        if (masked) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) x[k] = c + k >= from && c + k < until ? x[k] : -INFINITY;
-                        }
-                        g2[(c >> 1) & 3] = add2(g2[(c >> 1) & 3], f2(ex2(x[0]), ex2(x[1])));
-                        g2[((c >> 1) & 3) + 1] = add2(g2[((c >> 1) & 3) + 1], f2(ex2(x[2]), ex2(x[3])));
+                    for (int c = 0; c < kTile; c += 2) {
+                        float x, y;
+                        f2_split(mul2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2), x, y);
+                        g2[(c >> 1) & 3] = add2(g2[(c >> 1) & 3], f2(ex2(x), ex2(y)));
                     }
                     float a, b2;
                     f2_split(add2(add2(g2[0], g2[1]), add2(g2[2], g2[3])), a, b2);
@@ -760,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
 }
 
 // The splits' statistics of a row to its M_r: a thread a row
-__global__ void __launch_bounds__(kTile) weigh_merge_kernel(const Params p, int block_size) {
+__global__ void __launch_bounds__(kTile) weigh_merge_kernel(const Params p, int block_size, int tile_bytes) {
     pdl_enter();
     const int rt = blockIdx.x, item = blockIdx.y, me = threadIdx.x;
     Chunk ch;
@@ -788,7 +791,7 @@ __global__ void __launch_bounds__(kTile) weigh_merge_kernel(const Params p, int 
         for (int k = 0; k < 8; ++k) l += ex2(x[k].x - by) * x[k].y;
         m = mx;
     }
-    p.bases[tile * kTile + me] = rt * kTile + me < nr ? row_base(m, l) : -INFINITY;
+    write_base(p.q_tiles + tile * (tile_bytes + kExt) + tile_bytes, me, m, l, rt * kTile + me < nr, p.scale_log2);
 }
 
 // Tiles, and units of both passes: about kTargetUnits each
@@ -836,7 +839,7 @@ int launch(const Params& p, cudaStream_t stream) {
     if (p.splits > 1) {
         note_launch();
         e = launch_pdl(weigh_merge_kernel, dim3((unsigned)p.row_tiles, (unsigned)(p.num_seqs * p.num_kv_heads)), dim3(kTile), 0,
-                       stream, p, BS);
+                       stream, p, BS, S::kTileBytes);
         if (e != cudaSuccess) return cuda_fail("weigh_prefill_tokens: merge launch", e);
     }
     note_launch();
@@ -850,11 +853,11 @@ int launch(const Params& p, cudaStream_t stream) {
 extern "C" size_t weigh_prefill_workspace_size(int num_seqs, int num_heads, int max_query_len, int window) {
     using namespace pkv::weigh;
     if (num_seqs <= 0 || num_heads <= 0 || max_query_len <= 0 || window < 0) return 0;
-    // at most (sequences x heads) x (queries + 127) rows, 256 bytes, M_r and a pair of statistics each,
+    // at most (sequences x heads) x (queries + 127) rows, 288 bytes and a pair of statistics each,
     // and the pairs of the splits; what Shape counts
     const long long w = window > 0 && window < max_query_len ? window : max_query_len;
     const size_t rows = (size_t)num_seqs * num_heads * (size_t)(w + kTile - 1);
-    return Shape::kCounters + Shape::kParts + rows * (256 + 4 + 8) + 2 * (size_t)kTargetUnits * kTile * 8;
+    return Shape::kCounters + Shape::kParts + rows * (256 + 32 + 8) + 2 * (size_t)kTargetUnits * kTile * 8;
 }
 
 extern "C" int weigh_prefill_tokens(float* token_weights, const int32_t* weight_rows, const void* q, const void* k_pool,
@@ -874,7 +877,8 @@ extern "C" int weigh_prefill_tokens(float* token_weights, const int32_t* weight_
         return PKV_ERR_INVALID_ARG;
     const int G = num_heads / num_kv_heads;
     if (q_dtype != PKV_BF16 || kv_dtype != PKV_BF16 || (head_dim != 64 && head_dim != 128) ||
-        (block_size != 16 && block_size != 32) || G > weigh::kMaxGroup)
+        (block_size != 16 && block_size != 32) || G > weigh::kMaxGroup ||
+        (scale != 0.f && std::fabs(scale) < 0x1p-100f))        // M_r / scale has to be a number
         return PKV_ERR_UNSUPPORTED;
     const weigh::Shape shape(num_seqs, num_kv_heads, G, max_query_len, window, max_blocks_per_seq, block_size);
     // units, rows and positions times a group in 32 bits
@@ -911,8 +915,8 @@ extern "C" int weigh_prefill_tokens(float* token_weights, const int32_t* weight_
     p.splits = (int)shape.splits;
     p.per = (int)shape.per;
     p.g_magic = (uint32_t)(0x100000000ull / (unsigned)G) + 1u;
-    // never 0: hidden logits are -infinity times it
-    p.scale_log2 = scale == 0.f ? 1.17549435e-38f : std::fabs(scale) * 1.4426950408889634f;
+    p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * 1.4426950408889634f;
+    p.no_scale = scale == 0.f;
     p.sign = scale < 0.f ? 0x80008000u : 0u;
     p.decay = decay;
     p.key_pairs = (int)shape.key_pairs;
@@ -922,8 +926,7 @@ extern "C" int weigh_prefill_tokens(float* token_weights, const int32_t* weight_
     p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + weigh::Shape::kCounters);
     p.q_tiles = reinterpret_cast<unsigned char*>(p.parts) + weigh::Shape::kParts;
     const size_t row_count = (size_t)(shape.items * shape.row_tiles) * weigh::kTile;
-    p.bases = reinterpret_cast<float*>(p.q_tiles + row_count * head_dim * 2);
-    p.stats = reinterpret_cast<float2*>(p.bases + row_count);
+    p.stats = reinterpret_cast<float2*>(p.q_tiles + row_count * (head_dim * 2 + 32));
     p.err = error_word();
     if (!p.err) return PKV_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
