@@ -10,8 +10,13 @@
 // every fourth tile of it through a ring of their own, with the sparse decode's tile math; the
 // warps' parts (maximum, sum, unnormalised output) meet in shared memory and go to the
 // workspace, or to the output where the row has one partition. Second kernel: a CTA merges the
-// partitions' maxima and sums of its row, which gives each head's M + log2(sum), and updates
-// 1024 tokens' weights; the row's first CTA also merges the outputs.
+// partitions' maxima and sums of its row, which gives each head's maximum and sum, and updates
+// 1024 or 2048 tokens' weights; the first CTA of a row in several partitions merges the outputs.
+// Bound: HBM bytes for many tokens (32 sequences of up to 8192, 40 bf16 heads of 128: 415 us,
+// 0.99 of the copy rate; 64 of up to 4096, E4M3, 4 heads a kv head: 60.2, 0.68, the tiles' math
+// as in the sparse decode), two launches and their chains of loads for few (1 x 4096: 8.8 us).
+// Many short partitions rather than whole rows: 4096 CTAs 415 us, 2048 434, 1024 449 (E4M3: 60.2,
+// 60.8, 65.7); 4 tiles a partition instead of 8 make 1 x 4096 12.2 us, 16 no difference.
 #pragma once
 
 #include "pkv_sparse_impl.cuh"
@@ -29,7 +34,7 @@ using sparse::softmax_base;
 constexpr int kWarps = 4;
 constexpr int kMaxStages = 8;          // of a warp's ring
 constexpr int kPartStages = 8;         // tiles of a partition, at least
-constexpr int kMaxCtas = 2048;         // partitions are made until there are so many
+constexpr int kMaxCtas = 4096;         // partitions are made until there are so many
 
 struct Params {
     void* out;
@@ -262,39 +267,49 @@ __global__ void __maxnreg__(168) weighed_decode_kernel(const Params p) {
     }
 }
 
-constexpr int kFinishThreads = 256, kFinishTokens = 4 * kFinishThreads;
+constexpr int kFinishThreads = 256;
+// Pieces of four tokens a thread: what a CTA reads for its row is shared by more of them (both
+// kernels, 32 sequences of up to 8192 tokens and 40 heads: 420.6 us with one, 415.0 with two; 64 of up
+// to 4096, E4M3: 60.7 and 60.2). Eight heads' logits leave no registers for two.
+template <int G> struct Finish {
+    static constexpr int kPieces = G <= 4 ? 2 : 1, kTokens = 4 * kPieces * kFinishThreads;
+};
 
 template <typename QT, int D, int G>
 __global__ void __launch_bounds__(kFinishThreads) weighed_finish_kernel(const Params p, int stage_tokens, int max_len) {
-    pdl_enter();
     __shared__ float head_m[G], head_inv[G];               // of each head: maximum, 1 / sum
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int row = blockIdx.y, b = row / p.num_kv_heads, hk = row - b * p.num_kv_heads;
+    // Read before the first kernel is through: lengths, rows and weights, which it does not write
+    // (and it began behind everything that did). 1 sequence of 4096 tokens: 1.2 us of 9.1.
     const int L = min(max(p.seq_lens[b], 0), max_len);     // flagged by the first kernel
     const bool merges = p.parts > 1 && blockIdx.x == 0;    // the first CTA of a row in several partitions
-    const int t0 = ((int)blockIdx.x - (p.parts > 1)) * kFinishTokens, t = t0 + 4 * tid;
+    const int t0 = ((int)blockIdx.x - (p.parts > 1)) * Finish<G>::kTokens, t = t0 + 4 * tid;
     if (!merges && t0 >= L) return;                        // the whole CTA
+    int to = b;
+    bool bad = false;
+    if (!merges && p.rows) {                               // good, and no earlier sequence's
+        to = p.rows[b];
+        bad = to < 0 || to >= p.num_rows;
+        for (int i = tid; i < b; i += kFinishThreads) bad |= p.rows[i] == to;
+    }
+    constexpr int N = Finish<G>::kPieces, kStep = 4 * kFinishThreads;
+    float4 x[N][G], before[N];
+    float* const at = p.weights + ((size_t)to * p.num_kv_heads + hk) * p.max_tokens + t;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        if (!merges && t + n * kStep < L && !(to < 0 || to >= p.num_rows))
+            before[n] = *reinterpret_cast<const float4*>(at + n * kStep);
+    pdl_enter();
     const int stages = (L + stage_tokens - 1) / stage_tokens;
     const int parts = max(1, (stages + p.part_stages - 1) / p.part_stages);
     const float* const ml = p.part_ml + (size_t)row * p.parts * 2 * G;
-    // what does not wait for the heads' sums is read ahead of them
-    int to = b;
-    bool bad = false;
-    float4 x[G], before = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!merges) {
-        if (p.rows) {                                      // good, and no earlier sequence's
-            to = p.rows[b];
-            bad = to < 0 || to >= p.num_rows;
-            for (int i = tid; i < b; i += kFinishThreads) bad |= p.rows[i] == to;
-        }
-        if (t < L) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        if (!merges && t + n * kStep < L)
 #pragma unroll
             for (int g = 0; g < G; ++g)
-                x[g] = *reinterpret_cast<const float4*>(p.logits + ((size_t)row * G + g) * p.pitch + t);
-        }
-    }
-    float* const at = p.weights + ((size_t)to * p.num_kv_heads + hk) * p.max_tokens + t;
-    if (!merges && t < L && to >= 0 && to < p.num_rows) before = *reinterpret_cast<const float4*>(at);
+                x[n][g] = *reinterpret_cast<const float4*>(p.logits + ((size_t)row * G + g) * p.pitch + t + n * kStep);
     if (w < G) {
         float M = -INFINITY, sum = 0.f;
         for (int i = lane; i < parts; i += 32) M = max_nan(M, ml[i * 2 * G + w]);
@@ -314,24 +329,29 @@ __global__ void __launch_bounds__(kFinishThreads) weighed_finish_kernel(const Pa
         return;
     }
     if (!merges) {
-        if (t >= L) return;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const float m = head_m[g], by = head_inv[g] * p.lift;
-            sum[0] += ex2(x[g].x - m) * by;
-            sum[1] += ex2(x[g].y - m) * by;
-            sum[2] += ex2(x[g].z - m) * by;
-            sum[3] += ex2(x[g].w - m) * by;
-        }
-        if (t + 4 < L) {                                   // four older ones
-            *reinterpret_cast<float4*>(at) = make_float4(fmaf(p.decay, before.x, sum[0]), fmaf(p.decay, before.y, sum[1]),
-                                                         fmaf(p.decay, before.z, sum[2]), fmaf(p.decay, before.w, sum[3]));
-        } else {
-            const float old[4] = {before.x, before.y, before.z, before.w};
+        for (int n = 0; n < N; ++n) {
+            const int tn = t + n * kStep;
+            if (tn >= L) return;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (t + j < L) at[j] = t + j < L - 1 ? fmaf(p.decay, old[j], sum[j]) : sum[j];
+            for (int g = 0; g < G; ++g) {
+                const float m = head_m[g], by = head_inv[g] * p.lift;
+                sum[0] += ex2(x[n][g].x - m) * by;
+                sum[1] += ex2(x[n][g].y - m) * by;
+                sum[2] += ex2(x[n][g].z - m) * by;
+                sum[3] += ex2(x[n][g].w - m) * by;
+            }
+            float* const to_n = at + n * kStep;
+            const float old[4] = {before[n].x, before[n].y, before[n].z, before[n].w};
+            if (tn + 4 < L) {                              // four older ones
+                *reinterpret_cast<float4*>(to_n) = make_float4(fmaf(p.decay, old[0], sum[0]), fmaf(p.decay, old[1], sum[1]),
+                                                               fmaf(p.decay, old[2], sum[2]), fmaf(p.decay, old[3], sum[3]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (tn + j < L) to_n[j] = tn + j < L - 1 ? fmaf(p.decay, old[j], sum[j]) : sum[j];
+            }
         }
         return;
     }
@@ -402,7 +422,7 @@ int launch(const Args& a) {
     cudaError_t e = launch_pdl(kern, dim3((unsigned)(rows * p.parts)), dim3(kWarps * 32), S::kBytes, a.stream, p);
     if (e != cudaSuccess) return cuda_fail("weighed decode: kernel launch", e);
     note_launch();
-    const dim3 grid((unsigned)((p.max_blocks * (BS / PAIR) + kFinishTokens - 1) / kFinishTokens + (p.parts > 1)), (unsigned)rows);
+    const dim3 grid((unsigned)((p.max_blocks * (BS / PAIR) + Finish<G>::kTokens - 1) / Finish<G>::kTokens + (p.parts > 1)), (unsigned)rows);
     e = launch_pdl(weighed_finish_kernel<QT, D, G>, grid, dim3(kFinishThreads), 0, a.stream, p, (int)BS,
                    p.max_blocks * (BS / PAIR));
     return e == cudaSuccess ? PKV_OK : cuda_fail("weighed decode: weights launch", e);

@@ -129,8 +129,8 @@ def test_keep_entry_refuses_before_any_cuda_call(over, status):
 def test_workspaces():
     lib = library()
     assert lib.weighed_decode_workspace_size(0, 4, 64, 16, 5) == 0
-    # 80 tokens pad to 96; at most 2048 partitions of 8 heads and one a head
-    assert lib.weighed_decode_workspace_size(3, 4, 64, 16, 5) == 4 * (12 * 96 + (8 * 2048 + 12) * 66)
+    # 80 tokens pad to 96; at most 4096 partitions of 8 heads and one a head
+    assert lib.weighed_decode_workspace_size(3, 4, 64, 16, 5) == 4 * (12 * 96 + (8 * 4096 + 12) * 66)
     assert lib.weighed_decode_workspace_size(64, 64, 128, 16, 1 << 14) > 4 << 30     # beyond 32 bits
     assert lib.weigh_prefill_workspace_size(2, 4, 0, 0) == 0 and lib.weigh_prefill_workspace_size(2, 4, 5, -1) == 0
     assert lib.weigh_prefill_workspace_size(2, 4, 9, 0) == lib.weigh_prefill_workspace_size(2, 4, 9, 11)
