@@ -1077,6 +1077,25 @@ PKV_API int bm_swap_out(pkv_block_manager* bm, int64_t seq_id, int64_t* pairs, i
 PKV_API int bm_swap_in(pkv_block_manager* bm, int64_t seq_id, int64_t* pairs, int cap,
                        int* num_pairs);
 PKV_API int bm_is_swapped(const pkv_block_manager* bm, int64_t seq_id, int* swapped);
+
+/* Eviction of a sequence's tokens (for select_tokens and keep_tokens; the pages have no
+ * counterpart). bm_plan_keep: every listed sequence keeps num_kept of its tokens, in fresh
+ * blocks. Writes its table and length as they were (int32 [n][max_blocks], -1 padded, int32
+ * [n]) and its new table (int32 [n][max_kept_blocks], -1 padded), ceil(num_kept / block_size)
+ * blocks, all of them taken before any old one is released (as by bm_free_seq: blocks that
+ * others share stay theirs); its length becomes num_kept. The moves have to be enqueued before
+ * anything that may write a released block.
+ * All or nothing: PKV_ERR_INVALID_ARG for num_kept < 1, a table that the buffers cannot hold, a
+ * sequence that is swapped out, listed twice or not longer than num_kept; PKV_ERR_OUT_OF_RANGE
+ * for an unknown one; PKV_ERR_POOL_EXHAUSTED if the free (plus evictable) blocks are too few,
+ * before the old ones return. With prefix caching, what a sequence appends after it kept some
+ * tokens is not registered.
+ * bm_is_kept: whether a sequence, or the one it was forked from, has dropped tokens so: its
+ * length is then not its position, and it cannot be rebuilt by recomputing so many tokens. */
+PKV_API int bm_plan_keep(pkv_block_manager* bm, const int64_t* seq_ids, int n, int num_kept,
+                         int max_blocks, int max_kept_blocks, int32_t* tables, int32_t* seq_lens,
+                         int32_t* kept_tables);
+PKV_API int bm_is_kept(const pkv_block_manager* bm, int64_t seq_id, int* kept);
 PKV_API int bm_host_free_list(const pkv_block_manager* bm, int32_t* out, int cap);
 
 /* The free list, front first, into out[0..cap); returns its length. */

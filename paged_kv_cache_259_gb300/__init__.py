@@ -189,6 +189,8 @@ def load_library():
         "bm_swap_in": (c_int, [vp, ctypes.c_int64, i64p, c_int, ip]),
         "bm_is_swapped": (c_int, [vp, ctypes.c_int64, ip]),
         "bm_host_free_list": (c_int, [vp, i32p, c_int]),
+        "bm_plan_keep": (c_int, [vp, i64p, c_int, c_int, c_int, c_int, i32p, i32p, i32p]),
+        "bm_is_kept": (c_int, [vp, ctypes.c_int64, ip]),
         "swap_blocks": (c_int, [vp, vp, vp, vp, vp, c_int, c_int, c_int, c_size, vp]),
         "bm_add_seq_prompt": (c_int, [vp, ctypes.c_int64, i32p, c_int, ip]),
         "bm_append_tokens": (c_int, [vp, ctypes.c_int64, i32p, c_int, i64p, i64p, c_int, ip]),
@@ -1541,6 +1543,29 @@ class BlockManager:
     def is_swapped(self, sid):
         f = ctypes.c_int(0)
         _check(self._lib.bm_is_swapped(self._h, sid, ctypes.byref(f)), "bm_is_swapped")
+        return bool(f.value)
+
+    # ---- eviction of a sequence's tokens
+    def plan_keep(self, seq_ids, num_kept, max_blocks=None):
+        """Every listed sequence keeps ``num_kept`` of its tokens in fresh blocks, and its
+        other blocks are released (``bm_plan_keep``): returns its tables int32 ``[n,
+        max_blocks]`` and lengths int32 ``[n]`` as they were, and its new tables int32 ``[n,
+        ceil(num_kept / block_size)]``, for ``keep_tokens``. All or nothing."""
+        ids = np.ascontiguousarray(np.asarray(seq_ids, dtype=np.int64).reshape(-1))
+        if max_blocks is None:
+            max_blocks = max((-(-self.seq_len(int(s)) // self.block_size) for s in ids), default=1)
+        width = max(1, -(-int(num_kept) // self.block_size))
+        tables = np.full((len(ids), max(1, max_blocks)), -1, dtype=np.int32)
+        lens = np.zeros(len(ids), dtype=np.int32)
+        kept = np.full((len(ids), width), -1, dtype=np.int32)
+        _check(self._lib.bm_plan_keep(self._h, _i64p(ids), len(ids), int(num_kept), tables.shape[1], width,
+                                      _i32p(tables), _i32p(lens), _i32p(kept)), "bm_plan_keep")
+        return tables, lens, kept
+
+    def is_kept(self, sid):
+        """Whether the sequence has dropped tokens (``plan_keep``)."""
+        f = ctypes.c_int(0)
+        _check(self._lib.bm_is_kept(self._h, sid, ctypes.byref(f)), "bm_is_kept")
         return bool(f.value)
 
     def host_free_list(self):

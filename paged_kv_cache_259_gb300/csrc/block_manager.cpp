@@ -86,6 +86,7 @@ struct pkv_block_manager {
         std::vector<int64_t> tokens;     // token ids (prefix caching only)
         std::vector<uint64_t> hashes;    // prefix hash after each full block
         bool swapped = false;            // table holds host blocks
+        bool kept = false;               // has dropped tokens (bm_plan_keep)
         uint64_t demand_epoch = 0;       // Demand scratch: length within a batch count
         int64_t demand_len = 0;
     };
@@ -723,6 +724,68 @@ int bm_is_swapped(const pkv_block_manager* bm, int64_t seq_id, int* swapped) {
     auto it = bm->seqs.find(seq_id);
     if (it == bm->seqs.end()) return PKV_ERR_OUT_OF_RANGE;
     *swapped = it->second.swapped ? 1 : 0;
+    return PKV_OK;
+}
+
+// Every fresh block is taken before an old one is released, so that no block is both a
+// source and a target of the moves that follow, whichever sequences they belong to.
+int bm_plan_keep(pkv_block_manager* bm, const int64_t* seq_ids, int n, int num_kept, int max_blocks,
+                 int max_kept_blocks, int32_t* tables, int32_t* seq_lens, int32_t* kept_tables) {
+    if (!bm || n < 0 || num_kept < 1 || max_blocks < 1 || max_kept_blocks < 1 ||
+        (n > 0 && (!seq_ids || !tables || !seq_lens || !kept_tables)))
+        return PKV_ERR_INVALID_ARG;
+    const int64_t fresh = ((int64_t)num_kept + bm->block_size - 1) / bm->block_size;
+    if (fresh > max_kept_blocks) return PKV_ERR_INVALID_ARG;
+    std::vector<pkv_block_manager::Seq*> seqs;
+    std::vector<std::vector<int32_t>> taken;
+    std::vector<int64_t> ids;
+    try {                                              // what the host memory cannot hold changes nothing
+        seqs.reserve((size_t)n);
+        taken.resize((size_t)n);
+        ids.assign(seq_ids, seq_ids + n);
+        std::sort(ids.begin(), ids.end());
+        for (int i = 0; i < n; ++i) {
+            auto it = bm->seqs.find(seq_ids[i]);
+            if (it == bm->seqs.end()) return PKV_ERR_OUT_OF_RANGE;
+            auto& s = it->second;
+            if (s.swapped || s.len <= num_kept || s.len > INT32_MAX || (int64_t)s.table.size() > max_blocks)
+                return PKV_ERR_INVALID_ARG;
+            seqs.push_back(&s);
+            taken[i].reserve((size_t)fresh);
+        }
+        if (std::adjacent_find(ids.begin(), ids.end()) != ids.end()) return PKV_ERR_INVALID_ARG;
+        if (fresh * n > (int64_t)bm->device_available()) return PKV_ERR_POOL_EXHAUSTED;
+    } catch (const std::bad_alloc&) {
+        return PKV_ERR_POOL_EXHAUSTED;
+    }
+    for (int i = 0; i < n; ++i) {
+        auto& s = *seqs[i];
+        int32_t* row = tables + (size_t)i * max_blocks;
+        std::fill(std::copy(s.table.begin(), s.table.end(), row), row + max_blocks, -1);
+        seq_lens[i] = (int32_t)s.len;
+        for (int64_t k = 0; k < fresh; ++k) taken[i].push_back(bm->take());
+        row = kept_tables + (size_t)i * max_kept_blocks;
+        std::fill(std::copy(taken[i].begin(), taken[i].end(), row), row + max_kept_blocks, -1);
+    }
+    for (int i = 0; i < n; ++i) {
+        auto& s = *seqs[i];
+        bm->release(s.table);
+        s.table = std::move(taken[i]);
+        s.len = num_kept;
+        s.kept = true;
+        if (bm->caching) {                             // no prefix of known tokens any more
+            s.tokens.assign((size_t)num_kept, kUnknownToken);
+            s.hashes.clear();
+        }
+    }
+    return PKV_OK;
+}
+
+int bm_is_kept(const pkv_block_manager* bm, int64_t seq_id, int* kept) {
+    if (!bm || !kept) return PKV_ERR_INVALID_ARG;
+    auto it = bm->seqs.find(seq_id);
+    if (it == bm->seqs.end()) return PKV_ERR_OUT_OF_RANGE;
+    *kept = it->second.kept ? 1 : 0;
     return PKV_OK;
 }
 

@@ -24,11 +24,13 @@ import torch
 
 from . import (PKV_ERR_POOL_EXHAUSTED, BlockManager, DecodePipelineStepArgs, PagedKVError, _check,
                PackedCall, _decode_shapes, _dt, _workspace, bind_copy_blocks, bind_paged_attention_decode_sparse,
-               bind_paged_attention_prefill, bind_paged_decode_step, bind_rotary_and_cache, bind_select_blocks,
-               bind_update_key_bounds, copy_blocks, key_bounds_dtype, key_bounds_shape, paged_attention_decode,
+               bind_keep_tokens, bind_norm_rotary_and_cache, bind_paged_attention_decode_weighed,
+               bind_paged_attention_prefill, bind_paged_decode_step, bind_reshape_and_cache, bind_rotary_and_cache,
+               bind_select_blocks, bind_select_tokens, bind_update_key_bounds, bind_weigh_prefill_tokens, copy_blocks,
+               key_bounds_dtype, key_bounds_shape, paged_attention_decode,
                paged_prefill_step, paged_attention_decode_grouped, load_library, paged_attention_workspace_size,
                pool_shapes, pool_views, reshape_and_cache, select_blocks_workspace_size, swap_blocks,
-               update_key_bounds)
+               token_weights_shape, update_key_bounds, weigh_prefill_workspace_size, weighed_decode_workspace_size)
 
 
 @dataclass
@@ -109,6 +111,25 @@ class PrefillPlan:
                 for k, v in self.host_tensors(pin=non_blocking).items()}
 
 
+@dataclass
+class KeepPlan:
+    """Host-side inputs of an eviction: sequences before it, and their tables after it."""
+    seq_ids: np.ndarray      # int64 [B]
+    tables: np.ndarray       # int32 [B, max_blocks]
+    lens: np.ndarray         # int32 [B]
+    kept_tables: np.ndarray  # int32 [B, ceil(num_kept / block_size)]
+    num_kept: int
+
+    def host_tensors(self, pin=True):
+        t = {"tables": torch.from_numpy(self.tables), "lens": torch.from_numpy(self.lens),
+             "kept_tables": torch.from_numpy(self.kept_tables)}
+        return {k: v.pin_memory() for k, v in t.items()} if pin else t
+
+    def device_tensors(self, device, non_blocking=False):
+        return {k: v.to(device, non_blocking=non_blocking)
+                for k, v in self.host_tensors(pin=non_blocking).items()}
+
+
 def host_runs(host_ids):
     """Runs of consecutive host block ids in a list: (start, stop, first id)
     triples, so block ``host_ids[i]`` for ``start <= i < stop`` is ``first id +
@@ -157,6 +178,7 @@ class PagedKVCache:
                                num_host_blocks=num_host_blocks)
         self.num_host_blocks = num_host_blocks
         self.key_bounds = None                               # see enable_key_bounds
+        self.token_weights, self._weight_rows, self._free_rows = None, {}, []   # see enable_token_weights
         if num_host_blocks:
             hk, hv = pool_shapes(num_host_blocks, num_kv_heads, block_size, head_dim, kv_dtype)
             self.host_k = torch.empty(hk, dtype=kv_dtype).pin_memory()
@@ -329,7 +351,11 @@ class PagedKVCache:
         """Preempt sequences by recomputation ("KV cache paginado...", "Como
         funciona": a preempted request's blocks are recovered by swapping or by
         recomputing them later): their blocks are freed now. Returns each one's
-        token count, for ``plan_resume``."""
+        token count, for ``plan_resume``. Not for a sequence that has dropped tokens
+        (``plan_keep``), which has more tokens than it has cached: swap it out."""
+        for s in seq_ids:
+            if self.bm.is_kept(int(s)):
+                raise ValueError(f"sequence {int(s)} has dropped tokens: swap it out")
         lens = {int(s): self.bm.seq_len(int(s)) for s in seq_ids}
         for s in seq_ids:
             self.bm.free_seq(int(s))
@@ -530,9 +556,17 @@ class PagedKVCache:
         calls = []
         if dev_plan["pairs"].shape[0]:
             calls.append(bind_copy_blocks(self.k_pool, self.v_pool, dev_plan["pairs"]))
-        calls.append(bind_rotary_and_cache(q, q, k_new, v_new, self.k_pool, self.v_pool, dev_plan["slots"],
-                                           positions, rotary.cos_sin, rotary.sections, rotary.interleaved,
-                                           k_scale, v_scale))
+        if rotary is None:
+            calls.append(bind_reshape_and_cache(k_new, v_new, self.k_pool, self.v_pool, dev_plan["slots"],
+                                                k_scale, v_scale))
+        elif rotary.q_norm is not None or rotary.k_norm is not None:
+            calls.append(bind_norm_rotary_and_cache(q, q, k_new, v_new, rotary.q_norm, rotary.k_norm, self.k_pool,
+                                                    self.v_pool, dev_plan["slots"], positions, rotary.cos_sin,
+                                                    rotary.eps, rotary.sections, rotary.interleaved, k_scale, v_scale))
+        else:
+            calls.append(bind_rotary_and_cache(q, q, k_new, v_new, self.k_pool, self.v_pool, dev_plan["slots"],
+                                               positions, rotary.cos_sin, rotary.sections, rotary.interleaved,
+                                               k_scale, v_scale))
         if self.key_bounds is not None:
             calls.append(bind_update_key_bounds(self.k_pool, self.key_bounds, dev_plan["tables"],
                                                 dev_plan["lens"], first, max_new))
@@ -589,6 +623,111 @@ class PagedKVCache:
         self._run_checked(calls, stream)
         return out
 
+    def enable_token_weights(self, max_seqs, max_tokens):
+        """Keep the attention weight that every cached token draws, for up to ``max_seqs``
+        sequences of up to ``max_tokens`` cached tokens (``weighed_step`` and
+        ``weigh_prompt`` add to it, ``keep_step`` evicts by it). A sequence gets its row when
+        ``weight_rows`` first names it, and holds it until ``drop_weight_rows``. Later calls
+        return the same tensor, whatever their sizes. Not while a graph is captured."""
+        if self.token_weights is None:
+            self.token_weights = torch.zeros(token_weights_shape(max_seqs, self.num_kv_heads, max_tokens),
+                                             dtype=torch.float32, device=self.device)
+            self._free_rows = list(range(max_seqs - 1, -1, -1))
+            if self.device.type == "cuda":                   # rows may be used on any stream
+                torch.cuda.current_stream(self.device).synchronize()
+        return self.token_weights
+
+    def weight_rows(self, seq_ids, stream=None):
+        """int32 ``[B]`` on the device: the sequences' rows of ``token_weights``. A new row
+        begins with zeros, on ``stream``. All or nothing: too few free rows raise, and none
+        is given. Not while a graph is captured (the rows come from the host)."""
+        if self.token_weights is None:
+            raise RuntimeError("call enable_token_weights first")
+        ids = [int(s) for s in seq_ids]
+        new = [s for s in dict.fromkeys(ids) if s not in self._weight_rows]
+        if len(new) > len(self._free_rows):
+            raise RuntimeError(f"{len(new)} sequences without a row of token weights, {len(self._free_rows)} rows free")
+        with self._on_stream(stream):
+            for s in new:
+                self._weight_rows[s] = self._free_rows.pop()
+                self.token_weights[self._weight_rows[s]].zero_()
+            return torch.tensor([self._weight_rows[s] for s in ids], dtype=torch.int32, device=self.device)
+
+    def drop_weight_rows(self, seq_ids):
+        """Sequences that are done give their rows back (those without one are skipped)."""
+        for s in seq_ids:
+            row = self._weight_rows.pop(int(s), None)
+            if row is not None:
+                self._free_rows.append(row)
+
+    def fork_weight_row(self, parent, child, stream=None):
+        """The child of a fork begins with its parent's token weights."""
+        rows = self.weight_rows([parent, child], stream)
+        with self._on_stream(stream):
+            self.token_weights[self._weight_rows[int(child)]].copy_(self.token_weights[self._weight_rows[int(parent)]])
+        return rows[1:]
+
+    def weighed_workspace(self, batch, max_blocks):
+        """Scratch of a weighed step."""
+        n = weighed_decode_workspace_size(batch, self.num_heads, self.head_dim, self.block_size, max_blocks)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
+
+    def weighed_step(self, q, k_new, v_new, dev_plan, rows, out, scale, workspace, decay=1.0, positions=None,
+                     first=None, rotary=None, k_scale=1.0, v_scale=1.0, stream=None):
+        """Device half of a decode step that adds up the tokens' attention weights: CoW
+        copies, append (rotated, q in place, with ``rotary`` and ``positions``), key bounds
+        (when kept: ``first``, see ``first_changed``), ``paged_attention_decode_weighed``.
+        ``rows``: ``weight_rows``; ``workspace``: ``weighed_workspace``. Refused arguments leave
+        q, the cache and the weights as they were."""
+        calls = self._bind_append(q, k_new, v_new, dev_plan, positions, first, rotary, 1, k_scale, v_scale)
+        calls.append(bind_paged_attention_decode_weighed(
+            out, self.token_weights, rows, q, self.k_pool, self.v_pool, dev_plan["tables"], dev_plan["lens"], scale,
+            decay, k_scale, v_scale, workspace))
+        self._run_checked(calls, stream)
+        return out
+
+    def weigh_workspace(self, batch, max_query_len, window=0):
+        """Scratch of ``weigh_prompt``."""
+        n = weigh_prefill_workspace_size(batch, self.num_heads, max_query_len, window)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
+
+    def weigh_prompt(self, q, dev_plan, rows, scale, max_query_len, workspace, window=0, decay=1.0, stream=None):
+        """The token weights of a prefill step, after it: those that the last ``window``
+        queries of each chunk give (0: all of them). q: as the prefill attended with it
+        (rotated)."""
+        bind_weigh_prefill_tokens(self.token_weights, rows, q, self.k_pool, dev_plan["tables"], dev_plan["lens"],
+                                  dev_plan["query_start"], scale, max_query_len, window, decay, workspace)(stream)
+
+    def plan_keep(self, seq_ids, num_kept):
+        """Host half of an eviction: those of the listed sequences that have more than
+        ``num_kept`` cached tokens get fresh blocks for so many (``BlockManager.plan_keep``).
+        None if none has. Its ``keep_step`` has to be enqueued before anything else writes the
+        cache."""
+        ids = [int(s) for s in dict.fromkeys(int(s) for s in seq_ids) if self.bm.seq_len(int(s)) > num_kept]
+        if not ids:
+            return None
+        return KeepPlan(np.asarray(ids, dtype=np.int64), *self.bm.plan_keep(ids, num_kept), int(num_kept))
+
+    def keep_step(self, dev_plan, rows, num_kept, first_tokens=0, last_tokens=0, kept=None, stream=None):
+        """Device half of an eviction: the choice of the ``num_kept`` tokens of each kv head
+        (the first, the last, the heaviest) into ``kept`` (int32 ``[B, Hkv, num_kept]``), their
+        move into the fresh blocks, and the key bounds (when kept up) of those. Returns ``kept``."""
+        B = dev_plan["lens"].shape[0]
+        with self._on_stream(stream):
+            if kept is None:
+                kept = torch.empty((B, self.num_kv_heads, int(num_kept)), dtype=torch.int32, device=self.device)
+            after = torch.full_like(dev_plan["lens"], int(num_kept))
+            none = torch.zeros_like(after)
+        if tuple(kept.shape) != (B, self.num_kv_heads, int(num_kept)):
+            raise ValueError("kept must be [B, Hkv, num_kept]")
+        calls = [bind_select_tokens(kept, self.token_weights, rows, dev_plan["lens"], first_tokens, last_tokens),
+                 bind_keep_tokens(kept, self.token_weights, rows, self.k_pool, self.v_pool, dev_plan["tables"],
+                                  dev_plan["kept_tables"], dev_plan["lens"])]
+        if self.key_bounds is not None:
+            calls.append(bind_update_key_bounds(self.k_pool, self.key_bounds, dev_plan["kept_tables"], after, none, 0))
+        self._run_checked(calls, stream)
+        return kept
+
     def step(self, q, k_new, v_new, dev_plan, out, scale, k_scale=1.0, v_scale=1.0,
              workspace=None, stream=None):
         """The device half of a decode step: copies, slot writes, attention (one
@@ -600,10 +739,13 @@ class PagedKVCache:
 @dataclass
 class Rotary:
     """How a model turns its heads: the table (``rotary_table``), the pairs each
-    position axis turns (None: one axis) and which dims form a pair."""
+    position axis turns (None: one axis), which dims form a pair, and the norm before."""
     cos_sin: torch.Tensor
     sections: list = None
     interleaved: bool = False
+    q_norm: torch.Tensor = None      # weights of the norm of each query and key head (both or
+    k_norm: torch.Tensor = None      # neither: ``norm_rotary_and_cache``)
+    eps: float = 1e-6
 
 
 def first_changed(plan):
