@@ -74,14 +74,6 @@ __device__ __forceinline__ uint2 cluster_ld2(uint32_t at) {
     asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
     return v;
 }
-__device__ __forceinline__ uint4 cluster_ld4(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(at)
-                 : "memory");
-    return v;
-}
 
 // A weight as an unsigned number of the same order; -0 as 0; what is not finite above the rest.
 // Below all of them the key of no token, above them that of a token which is always kept.
@@ -111,10 +103,10 @@ struct SelectParams {
 // at token 4 (j NT + i)); kLong: slices may be longer, further rounds are read from memory in
 // every pass.
 template <int NT, int V, bool kLong>
-__global__ void __launch_bounds__(NT, 2048 / NT >= 8 ? 4 : 2) select_tokens_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(NT, 1024 / NT) select_tokens_kernel(const SelectParams p) {
     pdl_enter();
-    constexpr int kWarps = NT / 32, kRound = NT * 4 * V, kQuads = kBins / 4 / NT;
-    static_assert(kBins % (4 * NT) == 0, "bins a thread");
+    constexpr int kWarps = NT / 32, kRound = NT * 4 * V, kPairs = kBins / 2 / NT;
+    static_assert(kBins % (2 * NT) == 0, "bins a thread");
     __shared__ __align__(16) uint32_t hist[kPasses][kBins];
     __shared__ uint32_t warp_sum[kWarps], warp_min[kWarps], warp_max[kWarps];
     __shared__ uint32_t found[3];                          // digit, keys above it, keys of it
@@ -223,29 +215,27 @@ __global__ void __launch_bounds__(NT, 2048 / NT >= 8 ? 4 : 2) select_tokens_kern
                     for (int e = 0; e < 4; ++e) count_key(at, key[j][e] - base, span, shift);
             });
             sync();
-            // this thread's bins, from the top down, and how many are above them
-            uint4 c[kQuads];
+            // this thread's bins, two and two from the top down, and how many are above them
+            uint2 c[kPairs];
             uint32_t sum = 0;
-            const int top = kBins - 4 - 4 * kQuads * tid;
+            const int top = kBins - 2 - 2 * kPairs * tid;
 #pragma unroll
-            for (int q = 0; q < kQuads; ++q) {
-                c[q] = make_uint4(0, 0, 0, 0);
+            for (int q = 0; q < kPairs; ++q) {
                 if (alone) {
-                    c[q] = *reinterpret_cast<const uint4*>(&bins[top - 4 * q]);
+                    c[q] = *reinterpret_cast<const uint2*>(&bins[top - 2 * q]);
                 } else {
-                    uint4 x[kMaxCluster];
+                    uint2 x[kMaxCluster];
 #pragma unroll
                     for (int r = 0; r < kMaxCluster; ++r)
-                        x[r] = r < csize ? cluster_ld4(cluster_addr(&bins[top - 4 * q], r)) : make_uint4(0, 0, 0, 0);
+                        x[r] = r < csize ? cluster_ld2(cluster_addr(&bins[top - 2 * q], r)) : make_uint2(0, 0);
+                    c[q] = make_uint2(0, 0);
 #pragma unroll
                     for (int r = 0; r < kMaxCluster; ++r) {
                         c[q].x += x[r].x;
                         c[q].y += x[r].y;
-                        c[q].z += x[r].z;
-                        c[q].w += x[r].w;
                     }
                 }
-                sum += c[q].x + c[q].y + c[q].z + c[q].w;
+                sum += c[q].x + c[q].y;
             }
             uint32_t before = sum;                         // inclusive scan over the block
 #pragma unroll
@@ -259,16 +249,16 @@ __global__ void __launch_bounds__(NT, 2048 / NT >= 8 ? 4 : 2) select_tokens_kern
             before += __reduce_add_sync(kFull, others) - sum;
             if (before < need && need <= before + sum) {   // one thread
 #pragma unroll
-                for (int q = 0; q < kQuads; ++q) {
-                    const uint32_t four[4] = {c[q].w, c[q].z, c[q].y, c[q].x};
+                for (int q = 0; q < kPairs; ++q) {
+                    const uint32_t two[2] = {c[q].y, c[q].x};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (before < need && need <= before + four[j]) {
-                            found[0] = (uint32_t)(top - 4 * q + 3 - j);
+                    for (int j = 0; j < 2; ++j) {
+                        if (before < need && need <= before + two[j]) {
+                            found[0] = (uint32_t)(top - 2 * q + 1 - j);
                             found[1] = before;
-                            found[2] = four[j];
+                            found[2] = two[j];
                         }
-                        before += four[j];
+                        before += two[j];
                     }
                 }
             }
@@ -573,20 +563,21 @@ int select_tokens(int32_t* kept, const float* token_weights, const int32_t* weig
     p.k = num_kept;
     p.first = first_tokens;
     p.last = last_tokens;
-    // the smallest slices that one CTA, then a cluster of up to 8, holds in registers
-    void (*kern)(SelectParams) = select_tokens_kernel<512, 8, true>;
-    int size = 1, threads = 512;
-    auto choose = [&](void (*k)(SelectParams), int nt, int v) {
-        kern = k;
-        threads = nt;
-        while (size < kMaxCluster && nt * 4 * v * size < max_tokens) size *= 2;
-    };
-    if (max_tokens <= 1024) choose(select_tokens_kernel<256, 1, false>, 256, 1);
-    else if (max_tokens <= 2048) choose(select_tokens_kernel<256, 2, false>, 256, 2);
-    else if (max_tokens <= 4096) choose(select_tokens_kernel<256, 4, false>, 256, 4);
-    else if (max_tokens <= 8192 * kMaxCluster) choose(select_tokens_kernel<256, 8, false>, 256, 8);
-    else if (max_tokens <= 16384 * kMaxCluster) choose(select_tokens_kernel<512, 8, false>, 512, 8);
-    else choose(select_tokens_kernel<512, 8, true>, 512, 8);
+    // the smallest CTA that holds a row in its registers, then clusters of up to 8 of the largest: a
+    // trip through the cluster costs about 1 us, and there are six (128 rows of 30000 tokens take
+    // 13.7 us as CTAs of 32768 and 31 us as 2 of 16384; 8 of 65536, 18 us and 20 us)
+    void (*kern)(SelectParams);
+    int size = 1, threads = 256;
+    if (max_tokens <= 1024) kern = select_tokens_kernel<256, 1, false>;
+    else if (max_tokens <= 2048) kern = select_tokens_kernel<256, 2, false>;
+    else if (max_tokens <= 4096) kern = select_tokens_kernel<256, 4, false>;
+    else if (max_tokens <= 8192) kern = select_tokens_kernel<256, 8, false>;
+    else if (max_tokens <= 16384) kern = select_tokens_kernel<512, 8, false>, threads = 512;
+    else {
+        threads = 1024;
+        while (size < kMaxCluster && 32768LL * size < max_tokens) size *= 2;
+        kern = 32768LL * size >= max_tokens ? select_tokens_kernel<1024, 8, false> : select_tokens_kernel<1024, 8, true>;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items * size));
     cfg.blockDim = dim3(threads);

@@ -659,6 +659,21 @@ def test_select_long_rows():
     check_select(W, None, [n - 3], 5000, 4, 100)
 
 
+@pytest.mark.parametrize("cap,lens", [
+    (32768, [32768, 16385, 20001, 700]), (32772, [32772, 32769, 32768, 5]), (65540, [65537, 65540, 32769, 32768]),
+    (131076, [131073, 65000, 40000]), (262148, [262145, 131077, 32768]), (600_000, [262_149, 599_999, 262_144]),
+])
+def test_select_by_several_ctas(cap, lens):
+    """Each size of CTA and cluster, and rows of it that need fewer than it has; equal weights on
+    both sides of the CTAs' borders."""
+    rng = rng_of(cap, len(lens))
+    W = weights_of(rng, len(lens), 2, cap)
+    W[:, 1] = np.floor(4 * W[:, 1]) / 4
+    W[0, 1] = 1.0
+    for K, first, last in ((500, 4, 30), (4000, 0, 0)):
+        check_select(W, None, lens, K, first, last)
+
+
 def test_select_one_value_and_extremes():
     n = 3000
     W = np.zeros((4, 2, n), dtype=np.float32)
