@@ -326,7 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
             x.n = -1;
             more = at < seen + total;
             if (more) {
-                const int k = at - seen, src = __ffs(__ballot_sync(0xffffffffu, k >= begin && k < begin + mine)) - 1;
+                const int k = PASS == kGainKeys ? seen + total - 1 - at : at - seen;
+                const int src = __ffs(__ballot_sync(0xffffffffu, k >= begin && k < begin + mine)) - 1;
                 auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
                 const int local = k - of(begin);
                 x.b = b0 + src;
