@@ -727,6 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
                     uint64_t g2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                     for (int c = 0; c < kTile; c += 2) {
+                        if (!kRows && c % 32 == 0 && c >= until) break;   // no more rows
                         float x, y;
                         f2_split(mul2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2), x, y);
                         g2[(c >> 1) & 3] = add2(g2[(c >> 1) & 3], f2(ex2(x), ex2(y)));
