@@ -15,11 +15,14 @@
 // for many rows, the chain of passes and barriers for few.
 //
 // keep_tokens. K: 16-byte pieces, one per (token, X dims), to their new place: eight
-// neighbouring threads write a whole 128-byte core matrix. V is stored transposed: a thread
-// gathers the X tokens of one dim and writes them as one 16-byte row. Source and target blocks
-// are disjoint, so nothing waits. The weights move within their row: kept[i] >= i, so one CTA
-// a row that reads a chunk of the list's weights, waits for all its threads, and writes them,
-// overwrites nothing that a later chunk reads. Bound: HBM bytes.
+// neighbouring threads write a whole 128-byte core matrix. V is stored transposed: 16 bytes are X
+// tokens of one dim, so a thread reads such a piece of each group that its X tokens come from and
+// puts their bytes together. Source and target blocks are disjoint, so nothing waits. The weights
+// move within their row: kept[i] >= i, so one CTA a row that reads a chunk of the list's weights,
+// waits for all its threads, and writes them, overwrites nothing that a later chunk reads. Bound:
+// HBM bytes, of K in sectors of 32 that two tokens share: 4096 of 8192 random tokens of 64
+// sequences (bf16, 8 heads of 128) move 2.2 GB in 410 us, 5.3 TB/s; with the neighbours' halves of
+// the sectors 3.0 GB, 7.3 TB/s. Workgroups of their own for K and V took 480 us where one took 430.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -420,24 +423,46 @@ __device__ void keep_weights(const KeepParams& p, int item) {
     }
 }
 
+// What a piece of 16 bytes gives to a word: bytes of its lower and of its upper half
+struct __align__(16) Piece {
+    uint32_t lo, lo_mask, hi, hi_mask;
+};
+
 template <int ES>                                          // bytes of an element
 __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const KeepParams p) {
     pdl_enter();
     constexpr int X = 16 / ES;
+    // V's elements are read one by one, not the pieces that they lie in: a row of 4 tokens saves few
+    // reads (16 sequences of 16384, D 64: 198 us and 205 us; bf16 135 and 123, E4M3 137 and 93)
+    constexpr bool kElements = ES == 4;
     if ((int)blockIdx.x < p.weight_ctas) {
         keep_weights(p, blockIdx.x);
         return;
     }
-    // of each token: its first 16-byte piece of K, its element of V's first dim; -1: skipped
-    __shared__ long long src_k[kKeepTokens], dst_k[kKeepTokens], src_v[kKeepTokens], dst_v[kKeepTokens];
+    // of each token: its first 16-byte piece of K; -1: skipped
+    __shared__ long long src_k[kKeepTokens], dst_k[kKeepTokens];
+    // of each row of X tokens of V: the groups of X tokens (their pieces of 16 bytes of the first dim)
+    // that it comes from, and what each of them gives to each word of a piece; kElements: its tokens'
+    // elements of the first dim
+    constexpr int kRows = kKeepTokens / X;
+    __shared__ long long dst_v[kRows], src_v[kRows][X];
+    __shared__ int num_src[kRows];
+    __shared__ uint32_t has[kRows];                        // bit e: token e is there
+    __shared__ Piece give[kElements ? 1 : kRows][X][4];
     const long long unit = (long long)blockIdx.x - p.weight_ctas;
     const int item = (int)(unit / p.chunks), b = item / p.num_kv_heads, h = item - b * p.num_kv_heads;
     const int i0 = (int)(unit - (long long)item * p.chunks) * kKeepTokens;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    if (tid < kKeepTokens) {
+    if constexpr (!kElements) {
+        static_assert(kRows * X * 4 == kKeepThreads, "an entry a thread");
+        (&give[0][0][0])[tid] = Piece{0, 0, 0, 0};
+        __syncthreads();
+    }
+    if (tid < kKeepTokens) {                               // whole warps
         const long long tile = (long long)p.d * p.bs * ES;
-        long long sk = -1, dk = -1, sv = -1, dv = -1;
-        const int i = i0 + tid;
+        long long sk = -1, dk = -1, sv = -1;
+        const int i = i0 + tid, row = tid / X, e = tid % X;
+        int at = 0;                                        // of the token in its group, in bytes
         if (i < p.k) {
             int n = p.seq_lens[b];
             if (n < 0 || n > p.max_blocks * p.bs) {
@@ -454,8 +479,9 @@ __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const KeepPar
                     const long long ot = ((long long)to * p.num_kv_heads + h) * tile;
                     sk = st + (long long)(s >> 3) * p.d * 8 * ES + (s & 7) * 16;
                     dk = ot + (long long)(o >> 3) * p.d * 8 * ES + (o & 7) * 16;
-                    sv = st + (long long)(s / X) * p.d * 16 + s % X * ES;
-                    dv = ot + (long long)(o / X) * p.d * 16 + o % X * ES;
+                    sv = st + (long long)(s / X) * p.d * 16;
+                    at = s % X * ES;
+                    dst_v[row] = ot + (long long)(o / X) * p.d * 16;   // the row's tokens agree
                 } else {
                     flag_error(p.err, kErrOutOfRange);
                 }
@@ -465,8 +491,29 @@ __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const KeepPar
         }
         src_k[tid] = sk;
         dst_k[tid] = dk;
-        src_v[tid] = sv;
-        dst_v[tid] = dv;
+        const int shift = lane & ~(X - 1);
+        constexpr uint32_t kAll = (1u << X) - 1u;
+        const uint32_t there = __ballot_sync(kFull, sv >= 0) >> shift;
+        if (e == 0) has[row] = there & kAll;
+        if constexpr (kElements) {
+            src_v[row][e] = sv + at;
+        } else {
+            const long long before = __shfl_up_sync(kFull, sv, 1);
+            const bool next = sv >= 0 && (e == 0 || before != sv); // the first of its group
+            const uint32_t firsts = __ballot_sync(kFull, next) >> shift;
+            const int r = __popc(firsts & ((2u << e) - 1u)) - 1;
+            if (next) src_v[row][r] = sv;
+            if (e == 0) num_src[row] = __popc(firsts & kAll);
+            if (sv >= 0) {
+                Piece& g = give[row][r][e * ES / 4];
+#pragma unroll
+                for (int k = 0; k < ES; ++k) {
+                    const int to = (e * ES + k) & 3;
+                    atomicOr(at < 8 ? &g.lo : &g.hi, (uint32_t)((at & 7) + k) << (4 * to));
+                    atomicOr(at < 8 ? &g.lo_mask : &g.hi_mask, 0xffu << (8 * to));
+                }
+            }
+        }
     }
     __syncthreads();
     // ---- K: a warp's 8 tokens, 4 pieces of each at a time
@@ -487,44 +534,60 @@ __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const KeepPar
             }
         }
     }
-    // ---- V: rows of X tokens of one dim (chunks begin at multiples of X, blocks hold whole ones),
-    // an element at a time: neighbouring tokens' are in the same 16 bytes, which the first brings in.
-    // A warp takes rows of 32 dims; the groups of X tokens are shared by kSame warps, or it takes several
+    // ---- V: rows of X tokens of one dim (chunks begin at multiples of X, blocks hold whole ones). A
+    // piece of 16 bytes of each group that the row comes from is read once, and its bytes put in place:
+    // two or three reads for 16 tokens when half of them stay, where elements take 16.
+    // A warp takes rows of 32 dims; the rows of X tokens are shared by kSame warps, or it takes several
     using E = typename std::conditional<ES == 4, uint32_t, typename std::conditional<ES == 2, uint16_t, uint8_t>::type>::type;
-    constexpr int kGroups = kKeepTokens / X, kWarps = kKeepThreads / 32, kSame = kGroups < kWarps ? kWarps / kGroups : 1;
-    constexpr int kU = X >= 16 ? 1 : 2;                    // rows in flight
-    for (int g = w / kSame; g < kGroups; g += kWarps / kSame) {
-        const char* from[X];
-        bool all = true;
-#pragma unroll
-        for (int e = 0; e < X; ++e) {
-            const long long at = src_v[g * X + e];
-            all &= at >= 0;
-            from[e] = p.v_pool + at;
-        }
-        const long long first = dst_v[g * X];
+    constexpr int kWarps = kKeepThreads / 32, kSame = kRows < kWarps ? kWarps / kRows : 1;
+    constexpr int kU = 2, kJ = 2;                          // dims and groups in flight
+    for (int row = w / kSame; row < kRows; row += kWarps / kSame) {
+        const uint32_t mine = has[row];
+        if (mine == 0) continue;
+        const int groups = kElements ? 0 : num_src[row];
         for (int d0 = (w % kSame) * 32 * kU + lane; d0 < p.d; d0 += kSame * 32 * kU) {
-            E v[kU][X];
+            uint32_t word[kU][4] = {};
+            if constexpr (kElements) {
 #pragma unroll
-            for (int u = 0; u < kU; ++u)
+                for (int u = 0; u < kU; ++u)
 #pragma unroll
-                for (int e = 0; e < X; ++e) {
-                    const bool has = (all || src_v[g * X + e] >= 0) && d0 + 32 * u < p.d;
-                    v[u][e] = has ? *reinterpret_cast<const E*>(from[e] + (d0 + 32 * u) * 16) : (E)0;
+                    for (int e = 0; e < X; ++e)
+                        if ((mine >> e & 1u) && d0 + 32 * u < p.d)
+                            word[u][e] = *reinterpret_cast<const uint32_t*>(p.v_pool + src_v[row][e] + (d0 + 32 * u) * 16);
+            }
+            for (int j0 = 0; !kElements && j0 < groups; j0 += kJ) {
+                uint4 v[kJ][kU];
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                    for (int u = 0; u < kU; ++u)
+                        if (j0 + j < groups && d0 + 32 * u < p.d)
+                            v[j][u] = *reinterpret_cast<const uint4*>(p.v_pool + src_v[row][j0 + j] + (d0 + 32 * u) * 16);
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    if (j0 + j >= groups) break;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const Piece g = give[row][j0 + j][q];
+#pragma unroll
+                        for (int u = 0; u < kU; ++u) {
+                            word[u][q] |= __byte_perm(v[j][u].x, v[j][u].y, g.lo) & g.lo_mask;
+                            word[u][q] |= __byte_perm(v[j][u].z, v[j][u].w, g.hi) & g.hi_mask;
+                        }
+                    }
                 }
+            }
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
                 const int d = d0 + 32 * u;
                 if (d >= p.d) break;
-                if (all) {
-                    uint32_t word[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int e = 0; e < X; ++e) word[e * ES / 4] |= (uint32_t)v[u][e] << (8 * (e * ES & 3));
-                    *reinterpret_cast<uint4*>(p.v_pool + first + d * 16) = make_uint4(word[0], word[1], word[2], word[3]);
-                } else {
+                char* const to = p.v_pool + dst_v[row] + d * 16;
+                if (mine == (1u << X) - 1u) {
+                    *reinterpret_cast<uint4*>(to) = make_uint4(word[u][0], word[u][1], word[u][2], word[u][3]);
+                } else {                                   // the others keep what they have
 #pragma unroll
                     for (int e = 0; e < X; ++e)
-                        if (dst_v[g * X + e] >= 0) *reinterpret_cast<E*>(p.v_pool + dst_v[g * X + e] + d * 16) = v[u][e];
+                        if (mine >> e & 1u) reinterpret_cast<E*>(to)[e] = (E)(word[u][e * ES / 4] >> (8 * (e * ES & 3)));
                 }
             }
         }
