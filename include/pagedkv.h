@@ -2,9 +2,10 @@
  * pagedkv.h -- C ABI of libpagedkv: decode-step and chunked-prefill attention
  * over a paged KV cache, decode attention over selected blocks of it (with the
  * score that selects them), the cache writes of a step (slot write, with or
- * without the position rotation, copy-on-write copy, swap copy to and from host
- * memory), and the host-side block manager
- * (with prefix caching, beam-search reshuffles and swapping).
+ * without the position rotation and the norm before it, copy-on-write copy, swap
+ * copy to and from host memory), caches of bounded size (the attention weight that
+ * each cached token draws, the choice of the heaviest, their move), and the host-side
+ * block manager (with prefix caching, beam-search reshuffles, swapping and eviction).
  *
  * Sources, by page title and section:
  *   "PagedAttention" (Ultralytics glossary)
@@ -595,7 +596,8 @@ PKV_API int paged_attention_decode_sparse(void* out, const void* q, const void* 
  *   token_weights device float32 [num_rows][num_kv_heads][max_tokens], 16-byte aligned,
  *                 max_tokens a multiple of 4: place t of a row is the weight of cached
  *                 token t. Never needs clearing: a token's weight begins with the call that
- *                 has it among its new tokens
+ *                 has it among its new tokens (a token appended by a step that no such call
+ *                 follows has the weight that its place held)
  *   weight_rows   device int32 [num_seqs]: the row of each sequence; NULL: sequence b has
  *                 row b (num_rows >= num_seqs). A row outside [0, num_rows), or one that an
  *                 earlier sequence of the call has, sets PKV_ERR_OUT_OF_RANGE, and that
@@ -681,11 +683,10 @@ PKV_API size_t weighed_decode_workspace_size(int num_seqs, int num_heads, int he
  *                 no clearing; calls that overlap on the GPU need one each
  *   the rest      as paged_attention_prefill
  * Supported: BF16 / BF16, head_dim in {64,128}, block_size in {16,32}, any num_heads /
- * num_kv_heads up to 128, a scale of 0 or a magnitude from 2^-100. A sequence with C > L, L beyond its table or rows outside q, or a
- * table entry outside the pool, sets PKV_ERR_OUT_OF_RANGE (the sequence's weights are left as
- * they were, or the entry's tokens are given no weight). Chunk queries past max_query_len,
- * counted from the chunk's first, are an error of the caller: such a sequence is left as it
- * was and sets PKV_ERR_OUT_OF_RANGE.
+ * num_kv_heads up to 128, a scale of 0 or of a magnitude from 2^-100. A sequence with C > L,
+ * C > max_query_len, L beyond its table or rows outside q sets PKV_ERR_OUT_OF_RANGE and is
+ * left as it was; a table entry outside the pool sets it too, and its tokens are given no
+ * weight.
  * ---------------------------------------------------------------------- */
 PKV_API int weigh_prefill_tokens(float* token_weights, const int32_t* weight_rows, const void* q,
                                  const void* k_pool, const int32_t* block_tables,
@@ -726,8 +727,9 @@ PKV_API int select_tokens(int32_t* kept, const float* token_weights, const int32
  *   kept          device int32 [num_seqs][num_kv_heads][num_kept]: tokens of the sequence,
  *                 strictly ascending, the rest -1 (select_tokens' output or the caller's
  *                 own choice). An entry that is not below seq_lens[b] or not above the entry
- *                 before it, one directly behind padding, one below its own index, or one
- *                 whose blocks are not in the pool, sets PKV_ERR_OUT_OF_RANGE and is skipped
+ *                 before it, one directly behind padding or one below its own index sets
+ *                 PKV_ERR_OUT_OF_RANGE and is skipped; so are K and V of one whose blocks
+ *                 are not in the pool (its weight moves)
  *   token_weights may be NULL (then weight_rows, num_rows and max_tokens are not looked at);
  *                 max_tokens at least max_blocks_per_seq * block_size
  *   block_tables, seq_lens  the sequences before the move

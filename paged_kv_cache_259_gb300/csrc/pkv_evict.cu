@@ -22,7 +22,7 @@
 // waits for all its threads, and writes them, overwrites nothing that a later chunk reads. Bound:
 // HBM bytes, of K in sectors of 32 that two tokens share: 4096 of 8192 random tokens of 64
 // sequences (bf16, 8 heads of 128) move 2.2 GB in 410 us, 5.3 TB/s; with the neighbours' halves of
-// the sectors 3.0 GB, 7.3 TB/s. Workgroups of their own for K and V took 480 us where one took 430.
+// the sectors 2.9 GB, 7.2 TB/s. CTAs of their own for K and V took 480 us where one took 430.
 #include <cuda_runtime.h>
 
 #include <type_traits>

@@ -285,7 +285,10 @@ __global__ void __launch_bounds__(kFinishThreads) weighed_finish_kernel(const Pa
     const int L = min(max(p.seq_lens[b], 0), max_len);     // flagged by the first kernel
     const bool merges = p.parts > 1 && blockIdx.x == 0;    // the first CTA of a row in several partitions
     const int t0 = ((int)blockIdx.x - (p.parts > 1)) * Finish<G>::kTokens, t = t0 + 4 * tid;
-    if (!merges && t0 >= L) return;                        // the whole CTA
+    if (!merges && t0 >= L) {                              // the whole CTA
+        if (blockIdx.x == 0) pdl_enter();                  // some CTA waits: what waits for this kernel waits for the first
+        return;
+    }
     int to = b;
     bool bad = false;
     if (!merges && p.rows) {                               // good, and no earlier sequence's
