@@ -37,9 +37,10 @@ namespace weigh {
 
 constexpr int kTile = 128;             // rows, keys of a tile
 constexpr int kBufs = 4;               // products (128 columns of tensor memory) and streamed tiles in flight
-constexpr int kGroups = 2;             // of 128 threads
-constexpr int kMmaWarp = 8, kKeyWarp = 9, kRowWarp = 10, kPickWarp = 11;
-constexpr int kThreads = 12 * 32;
+constexpr int kGroups = 4;             // of 128 threads
+constexpr int kMmaWarp = 16, kKeyWarp = 17, kRowWarp = 18, kPickWarp = 19;
+constexpr int kThreads = 20 * 32;
+constexpr int kHalf = kTile / 2;       // columns of a product that a thread has at a time
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kTile, kTile);
 constexpr int kExt = kTile * 32;       // bytes of the 16 dims that carry -M_r / scale behind a row tile
@@ -164,11 +165,11 @@ enum : int {
     kBarFull = 4,                      // [4] a streamed tile is there
     kBarFree = 8,                      // [4] its products are done
     kBarDone = 12,                     // [4] a product is done
-    kBarRead = 16,                     // [4] and is read (128 threads)
-    kBarPart = 20,                     // [2] a unit's results are there (256)
-    kBarPartFree = 22,                 // [2] they are joined
+    kBarRead = 16,                     // [4] and is read (its groups' warps)
+    kBarPart = 20,                     // a unit's results are there (16 warps)
+    kBarPartFree = 21,                 // they are joined
     kBarUnit = 24,                     // [kRing] a unit is picked
-    kBarUnitFree = 28,                 // [kRing] everybody has seen it (11 warps)
+    kBarUnitFree = 28,                 // [kRing] everybody has seen it (19 warps)
     kBarDrain = 32,
     kNumBars
 };
@@ -179,8 +180,8 @@ struct Shared {
     static constexpr int kSlot = kTileBytes + kExt;                               // of a row tile; a key tile takes less
     static constexpr int kHeld = 0, kStream = 2 * kSlot;
     static constexpr int kOnes = kStream + kBufs * kSlot;                         // the keys' 16 more dims
-    static constexpr int kPart = kOnes + kExt;                                    // [2][kGroups][128] of 8 bytes
-    static constexpr int kUnits = kPart + 2 * kGroups * kTile * 8;
+    static constexpr int kPart = kOnes + kExt;                                    // [kGroups][128] of 8 bytes
+    static constexpr int kUnits = kPart + kGroups * kTile * 8;
     static constexpr int kBars = kUnits + (kRing * (int)sizeof(Unit) + 15) / 16 * 16;
     static constexpr int kBytes = kBars + kNumBars * 8;
     static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
@@ -224,14 +225,14 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kBarHeldFull + i), 1);
             mbar_init(bar(kBarHeldFree + i), 1);
-            mbar_init(bar(kBarPart + i), kGroups * 128);
-            mbar_init(bar(kBarPartFree + i), 1);
         }
+        mbar_init(bar(kBarPart), kGroups * 4);
+        mbar_init(bar(kBarPartFree), 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(kBarFull + i), 1);
             mbar_init(bar(kBarFree + i), 1);
             mbar_init(bar(kBarDone + i), 1);
-            mbar_init(bar(kBarRead + i), 128);
+            mbar_init(bar(kBarRead + i), 4 * H);
             mbar_init(bar(kBarUnit + i), 1);
             mbar_init(bar(kBarUnitFree + i), kPickWarp);
         }
@@ -406,8 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
         // ------------------------------------------------------------ a unit's results
         for (int u = 0; PASS != kGainKeys && ok && u < picked; ++u) {
             unit = units[u % kRing];                       // this warp's own
-            if (unit.n < 0 || !wait(kBarPart + (u & 1), u >> 1)) break;
-            const unsigned char* const part = smem + S::kPart + (u & 1) * kGroups * kTile * 8;
+            if (unit.n < 0 || !wait(kBarPart, u)) break;
+            const unsigned char* const part = smem + S::kPart;
             if constexpr (PASS == kStats) {
 #pragma unroll
                 for (int k = 0; k < 4 * H; ++k) {
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarPartFree + (u & 1)));
+            if (lane == 0) mbar_arrive(bar(kBarPartFree));
             if (more) pick();
         }
     } else if (warp == kKeyWarp) {
@@ -643,116 +644,131 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
         // ------------------------------------------------------------ exponentials
         const int group = warp >> 2, me = tid & 127;
         const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
-        // Product of stream tile i: its 128 columns
-        uint32_t v[kTile];
-        auto take = [&](int i) {
-            const int buf = (H == 2 ? group * kTurn : 0) + i % kTurn;
-            if (!wait(kBarDone + buf, i / kTurn)) return false;
-            tc::fence_after_sync();
-            const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + buf * kTile;
+        // A product's columns, half of them at a time: two held tiles have two groups each, one for each
+        // half; of one the groups take every fourth product, both halves
+        const int mine = H == 2 ? group >> 1 : 0, half0 = H == 2 ? group & 1 : 0, half1 = H == 2 ? half0 : 1;
+        uint32_t v[kHalf];
+        auto take = [&](int i, int half) {                 // of the product of stream tile i
+            const int buf = (H == 2 ? mine * kTurn : 0) + i % kTurn;
+            if (half == half0) {
+                if (!wait(kBarDone + buf, i / kTurn)) return false;
+                tc::fence_after_sync();
+            }
+            const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + buf * kTile + half * kHalf;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tc::ld32(at + 32 * c, reinterpret_cast<uint32_t(&)[32]>(v[32 * c]));
+            for (int c = 0; c < 2; ++c) tc::ld32(at + 32 * c, reinterpret_cast<uint32_t(&)[32]>(v[32 * c]));
             tc::wait_ld();
-            tc::fence_before_sync();
-            mbar_arrive(bar(kBarRead + buf));
+            if (half == half1) {
+                tc::fence_before_sync();
+                __syncwarp();
+                mbar_arrive_elect(bar(kBarRead + buf));
+            }
             return true;
         };
         bool ok = true;
         int it = 0;                                        // of the unit's first tile
         for (int u = 0; ok && next_unit(u); it += unit.n, ++u) {
-            const int first_pos = unit.L - unit.w, skip = H == 2 ? 0 : (group - it) & 1, held = unit.held + (H == 2 ? group : 0);
-            unsigned char* const part = smem + S::kPart + (u & 1) * kGroups * kTile * 8;
+            const int first_pos = unit.L - unit.w, skip = H == 2 ? 0 : (group - it) & (kGroups - 1), held = unit.held + mine;
+            constexpr int kStep = H == 2 ? 1 : kGroups;
             if constexpr (PASS == kStats) {
                 const int r0 = held * kTile, r = min(r0 + me, unit.nr - 1), pr = first_pos + row_div(r);
                 const int p_min = first_pos + row_div(min(r0, unit.nr - 1));
                 float m = -INFINITY, l = 0.f;              // of the products; the scale is not negative
-                for (int j = skip; j < unit.n && ok; j += kShare) {
-                    const int key0 = (unit.first + j) * kTile;
-                    const bool masked = unit.bad || key0 + kTile - 1 > p_min;
-                    ok = take(it + j);
-                    if (!ok) break;
-                    if (masked) {
-                        constexpr uint32_t kNone = 0xff800000u;   // -infinity
+                for (int j = skip; j < unit.n && ok; j += kStep)
+#pragma unroll 1
+                    for (int half = half0; half <= half1; ++half) {
+                        const int key0 = (unit.first + j) * kTile + half * kHalf;
+                        const bool masked = unit.bad || key0 + kHalf - 1 > p_min;
+                        ok = take(it + j, half);
+                        if (!ok) break;
+                        if (masked) {
+                            constexpr uint32_t kNone = 0xff800000u;   // -infinity
 #pragma unroll
-                        for (int c = 0; c < kTile; ++c) v[c] = key0 + c <= pr ? v[c] : kNone;
-                        if (unit.bad)
-                            for (int s = 0; s < kBlocks; ++s) {
-                                const int blk = key0 / BS + s;
-                                const int id = blk < (unit.L + BS - 1) / BS ? p.block_tables[(size_t)unit.b * p.max_blocks + blk] : 0;
-                                if (id < 0 || id >= p.num_blocks)
+                            for (int c = 0; c < kHalf; ++c) v[c] = key0 + c <= pr ? v[c] : kNone;
+                            if (unit.bad)
+                                for (int s = 0; s < kHalf / BS; ++s) {
+                                    const int blk = key0 / BS + s;
+                                    const int id = blk < (unit.L + BS - 1) / BS ? p.block_tables[(size_t)unit.b * p.max_blocks + blk] : 0;
+                                    if (id < 0 || id >= p.num_blocks)
 #pragma unroll
-                                    for (int c = 0; c < kTile; ++c) v[c] = c / BS == s ? kNone : v[c];
-                            }
-                    }
-                    float m8[8];
+                                        for (int c = 0; c < kHalf; ++c) v[c] = c / BS == s ? kNone : v[c];
+                                }
+                        }
+                        float m4[4];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) m8[c] = max_nan(m, __uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+                        for (int c = 0; c < 4; ++c) m4[c] = max_nan(m, __uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
 #pragma unroll
-                    for (int c = 8; c < kTile / 2; ++c)
-                        m8[c & 7] = max_nan(m8[c & 7], __uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
-                    const float mx = max_nan(max_nan(max_nan(m8[0], m8[1], m8[2]), m8[3], m8[4]), m8[5], max_nan(m8[6], m8[7]));
-                    const float by = mx == -INFINITY ? 0.f : mx * p.scale_log2;
-                    const uint64_t nb2 = f2(-by, -by);
-                    uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
+                        for (int c = 4; c < kHalf / 2; ++c)
+                            m4[c & 3] = max_nan(m4[c & 3], __uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+                        const float mx = max_nan(max_nan(m4[0], m4[1], m4[2]), m4[3]);
+                        const float by = mx == -INFINITY ? 0.f : mx * p.scale_log2;
+                        const uint64_t nb2 = f2(-by, -by);
+                        uint64_t s2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 2) {
+                        for (int c = 0; c < kHalf; c += 2) {
+                            float a, b;
+                            f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nb2), a, b);
+                            s2[(c >> 1) & 3] = add2(s2[(c >> 1) & 3], f2(ex2(a), ex2(b)));
+                        }
                         float a, b;
-                        f2_split(fma2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2, nb2), a, b);
-                        s2[(c >> 1) & 3] = add2(s2[(c >> 1) & 3], f2(ex2(a), ex2(b)));
+                        f2_split(add2(add2(s2[0], s2[1]), add2(s2[2], s2[3])), a, b);
+                        l = fmaf(l, ex2(fmaf(m, p.scale_log2, -by)), a + b);
+                        m = mx;
                     }
-                    float a, b;
-                    f2_split(add2(add2(s2[0], s2[1]), add2(s2[2], s2[3])), a, b);
-                    l = fmaf(l, ex2(fmaf(m, p.scale_log2, -by)), a + b);
-                    m = mx;
-                }
-                if (ok && u >= 2) ok = wait(kBarPartFree + (u & 1), (u >> 1) - 1);
+                if (ok && u > 0) ok = wait(kBarPartFree, u - 1);
                 if (!ok) break;
-                reinterpret_cast<float2*>(part)[group * kTile + me] = make_float2(m == -INFINITY ? m : m * p.scale_log2, l);
+                reinterpret_cast<float2*>(smem + S::kPart)[group * kTile + me] =
+                    make_float2(m == -INFINITY ? m : m * p.scale_log2, l);
             } else {
                 constexpr bool kRows = PASS == kGainRows;
-                float total = 0.f;
-                for (int j = skip; j < unit.n && ok; j += kShare) {
-                    const int i = it + j, kt = kRows ? held : unit.first + j, rt = kRows ? unit.first + j : 0;
-                    const int t = kt * kTile + me;
-                    // token t is seen by the rows from column `from` of this tile on; past the last
-                    // row a product may be a NaN (zeros times an infinite key)
-                    const int from = max(0, t - first_pos) * p.G - rt * kTile, until = unit.nr - rt * kTile;
-                    const bool masked = kt * kTile + kTile - 1 > first_pos + row_div(rt * kTile) || until < kTile;
-                    ok = take(i);
-                    if (!ok) break;
-                    if (masked) {
+                float total = 0.f;                         // of the unit; else of the product
+                for (int j = skip; j < unit.n && ok; j += kStep) {
+                    const int kt = kRows ? held : unit.first + j, rt = kRows ? unit.first + j : 0, t = kt * kTile + me;
+#pragma unroll 1
+                    for (int half = half0; half <= half1; ++half) {
+                        // token t is seen by the rows from column `from` of this half on; past the last
+                        // row a product may be a NaN (zeros times an infinite key)
+                        const int first_row = rt * kTile + half * kHalf;
+                        const int from = max(0, t - first_pos) * p.G - first_row, until = unit.nr - first_row;
+                        const bool masked = kt * kTile + kTile - 1 > first_pos + row_div(first_row) || until < kHalf;
+                        ok = take(it + j, half);
+                        if (!ok) break;
+                        if (masked) {
 #pragma unroll
-                        for (int c = 0; c < kTile; ++c) v[c] = c >= from && c < until ? v[c] : 0xff800000u;
-                    }
-                    uint64_t g2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                    for (int c = 0; c < kTile; c += 2) {
-                        if (!kRows && c % 32 == 0 && c >= until) break;   // no more rows
-                        float x, y;
-                        f2_split(mul2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2), x, y);
-                        g2[(c >> 1) & 3] = add2(g2[(c >> 1) & 3], f2(ex2(x), ex2(y)));
-                    }
-                    float a, b2;
-                    f2_split(add2(add2(g2[0], g2[1]), add2(g2[2], g2[3])), a, b2);
-                    float gain = a + b2;
-                    if (kRows) {
-                        total += gain;
-                    } else if (ok && t < unit.L) {         // a token of its own for every thread
-                        if (unit.bad) {
-                            const int id = p.block_tables[(size_t)unit.b * p.max_blocks + t / BS];
-                            if (id < 0 || id >= p.num_blocks) gain = 0.f;
+                            for (int c = 0; c < kHalf; ++c) v[c] = c >= from && c < until ? v[c] : 0xff800000u;
                         }
-                        float* const at = p.weights + ((size_t)unit.to * p.num_kv_heads + unit.hk) * p.max_tokens + t;
-                        *at = t < unit.L - unit.C ? fmaf(p.decay, *at, gain) : gain;
+                        uint64_t g2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                        for (int c = 0; c < kHalf; c += 2) {
+                            if (!kRows && c % 32 == 0 && c >= until) break;   // no more rows
+                            float a, b;
+                            f2_split(mul2(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc2), a, b);
+                            g2[(c >> 1) & 3] = add2(g2[(c >> 1) & 3], f2(ex2(a), ex2(b)));
+                        }
+                        float a, b;
+                        f2_split(add2(add2(g2[0], g2[1]), add2(g2[2], g2[3])), a, b);
+                        total += a + b;
+                    }
+                    if (!kRows && ok) {
+                        if (t < unit.L) {                  // a token of its own for every thread
+                            if (unit.bad) {
+                                const int id = p.block_tables[(size_t)unit.b * p.max_blocks + t / BS];
+                                if (id < 0 || id >= p.num_blocks) total = 0.f;
+                            }
+                            float* const at = p.weights + ((size_t)unit.to * p.num_kv_heads + unit.hk) * p.max_tokens + t;
+                            *at = t < unit.L - unit.C ? fmaf(p.decay, *at, total) : total;
+                        }
+                        total = 0.f;
                     }
                 }
                 if (kRows) {
-                    if (ok && u >= 2) ok = wait(kBarPartFree + (u & 1), (u >> 1) - 1);
+                    if (ok && u > 0) ok = wait(kBarPartFree, u - 1);
                     if (!ok) break;
-                    reinterpret_cast<float*>(part)[group * kTile + me] = total;
+                    reinterpret_cast<float*>(smem + S::kPart)[group * kTile + me] = total;
                 }
             }
-            if (ok) mbar_arrive(bar(kBarPart + (u & 1)));
+            __syncwarp();
+            if (ok) mbar_arrive_elect(bar(kBarPart));
         }
         if (!ok && lane == 0) flag_error(p.err, kErrTimeout);
     }
