@@ -11,8 +11,9 @@
 // (at most three times; once or twice where weights differ, as the bins begin where the weights
 // do: a fixed first digit left a tenth of the keys in one bin). The taken keys are those above
 // the threshold and the first few equal to it; prefix sums over threads, warps and CTAs give
-// each its place in the list, which so comes out ascending. Bound: the reads (4 bytes a token)
-// for many rows, the chain of passes and barriers for few.
+// each its place in the list, which so comes out ascending. Bound: the chain of passes and
+// barriers, not the reads (4 bytes a token): 512 rows of up to 8192, one wave of CTAs, 14 us, where
+// 64 rows take 7.4 and the bytes 3.1; 8 rows of 131072, in clusters, 19 us.
 //
 // keep_tokens. K: 16-byte pieces, one per (token, X dims), to their new place: eight
 // neighbouring threads write a whole 128-byte core matrix. V is stored transposed: 16 bytes are X

@@ -19,11 +19,24 @@
 // and streams others past them: stats, H row tiles and a run of their key tiles; gain, with one
 // row tile a kv head (a short window), the row tile and a run of key tiles, else two key tiles
 // and a run of the row tiles that see them. H is 2 wherever there are two to hold: what is
-// streamed comes from L2 at 6.5 TB/s, which bounds a unit that holds one. Warps 0-7: two groups
-// with a thread a lane of tensor memory, which holds four products; with two held tiles a group
-// has one of them, else every other tile of the stream. Warp 8 issues the products, 9 copies
-// keys, 10 rows, 11 picks the units and joins the groups' results of each. Row runs of the same
-// key tiles leave their gains in the workspace; the last of them adds all up, in order.
+// streamed comes from L2 at 6.5 TB/s, which bounds a unit that holds one. Warps 0-15: four groups
+// with a thread a lane of tensor memory, which holds four products. With two held tiles two groups
+// share each product, half of its columns each; else the groups take every fourth tile of the
+// stream, its halves one after the other. Warp 16 issues the products, 17 copies keys, 18 rows, 19
+// picks the units and joins the groups' results of each. Row runs of the same key tiles leave their
+// gains in the workspace; the last of them adds all up, in order.
+//
+// Bound. 4 chunks of up to 2048 queries (32 bf16 heads, 4 kv heads of 128, up to 4096 tokens): 225 us
+// for two products of 101 GFLOP, 0.47 of the measured rate of a large library product. With two groups
+// instead of four it took 233, and of those 215 with an eighth of the products' work, 203 with a
+// sixteenth of the exponentials, 231 with an eighth of the copies, 131 with all three (warps waiting for
+// one another, units changing): not one resource, but two chains of like length, of products of 128 x
+// 128 from shared memory (590 cycles each) and of exponentials (1700 for a group's half of them). The
+// last 32 queries of 4 prompts of up to 32768: 82 us, of which K, read twice, is 55 at the copy rate,
+// and three launches. Small chunks: 12 to 19 us, the launches and a chain of loads in each. Measured and
+// not kept: two groups with halves read ahead (255 us); one exponential in four by a polynomial (255);
+// four held tiles (273 to 295: a unit's change weighs more); the next unit's held tiles in places that
+// the stream leaves (220, but 1 to 2 us more wherever units are few).
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -44,7 +57,7 @@ constexpr int kHalf = kTile / 2;       // columns of a product that a thread has
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kTile, kTile);
 constexpr int kExt = kTile * 32;       // bytes of the 16 dims that carry -M_r / scale behind a row tile
-constexpr int kTargetUnits = 1216;     // of the stats pass: eight an SM
+constexpr int kTargetUnits = 1216;     // of the stats pass: eight an SM (4 chunks of 2048: 231 us; 1824 237, 3648 267)
 constexpr int kMaxGroup = 128;
 constexpr int kRing = 4;               // units picked ahead
 
