@@ -8,15 +8,16 @@
 // rotation are float32, and there is one rounding, to the type of q_out or of the cache: a
 // norm written out in between would round to 16 bits (2^-9 of the value) first.
 //
-// Work split. A lane holds the 16 dims of rotary_and_cache (the two chunks of 8 that turn
-// together); the lanes of a row (8 for 128 dims) are neighbours, so the sum of squares is
+// Work split. A lane holds 16 dims: the two chunks of 8 that turn together, or, where neighbours
+// turn, two as far apart (so that the lanes' 16 bytes lie side by side either way); the lanes of a row (8 for 128 dims) are neighbours, so the sum of squares is
 // log2 of them shuffles. A warp takes 32 / lanes tokens and walks over some of the heads with
 // one set of cosines, sines and (if shared by the heads) weights in registers, the next heads on
 // their way through asynchronous copies: a lane's own 32 bytes of each, which cost no registers
 // and wait for no other lane. V goes through rotary_and_cache's own path.
 // Bound: HBM bytes for many tokens (8192 tokens of 32 + 2 x 8 bf16 heads of 128, three axes,
 // weights of each head: 41 us, 0.73 of the copy rate; the issue slots are half in use), a launch
-// and a chain of loads for few (64 tokens 3.6 us).
+// and a chain of loads for few (64 tokens 3.6 us). Of the 41 us the heads' own weights cost 5 (36.3 with
+// shared ones); pairs side by side take 43.5, and 48.8 with a lane's two chunks next to each other.
 #include "pkv_rotary_impl.cuh"
 
 namespace pkv {
@@ -87,6 +88,32 @@ __device__ __forceinline__ void load_weights(const void* w, int f32, long long a
     }
 }
 
+// Cosines and sines of the pairs i0 .. i0+3 at the token's positions
+__device__ __forceinline__ void load_four_turns(const RotaryParams& p, const Token& token, int i0, float* cs, float* sn) {
+    const int half = p.rot >> 1;
+    int a = 0;
+    while (i0 >= p.section_end[a]) ++a;
+    auto row_of = [&](int axis) {
+        int x = token.pos[0];
+#pragma unroll
+        for (int k = 1; k < kMaxAxes; ++k) x = axis == k ? token.pos[k] : x;
+        return p.cos_sin + (long long)x * p.rot;
+    };
+    if (i0 + 3 < p.section_end[a]) {                       // one axis for all 4 pairs
+        const float4 c = *reinterpret_cast<const float4*>(row_of(a) + i0), s = *reinterpret_cast<const float4*>(row_of(a) + i0 + half);
+        cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
+        sn[0] = s.x, sn[1] = s.y, sn[2] = s.z, sn[3] = s.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            while (i0 + j >= p.section_end[a]) ++a;
+            const float* row = row_of(a) + i0 + j;
+            cs[j] = row[0];
+            sn[j] = row[half];
+        }
+    }
+}
+
 // Heads h .. h_end-1 of q (KEYS false) or k of the tokens of group tg. Every lane copies its own
 // dims of the heads ahead to its own places of `ring`, so nothing but its own copies has to land.
 template <typename ST, typename CT, bool INTERLEAVED, bool KEYS>
@@ -99,7 +126,7 @@ __device__ __forceinline__ void norm_heads(const NormParams& n, long long tg, in
     const bool has = t < p.num_tokens && 16 * u < d;       // a row to read
     const bool turns = 16 * u < p.rot;
     int da, db;                                            // the unit's two chunks of 8 dims
-    if (INTERLEAVED || !turns) {
+    if (!turns) {
         da = 16 * u;
         db = da + 8;
     } else {
@@ -136,7 +163,14 @@ __device__ __forceinline__ void norm_heads(const NormParams& n, long long tg, in
     token.check(p);
     const bool live = token.slot >= 0;
     float cs[8], sn[8];
-    if (live && turns) load_turns(p, token, u, cs, sn);
+    if (live && turns) {
+        if constexpr (INTERLEAVED) {
+            load_four_turns(p, token, 4 * u, cs, sn);
+            load_four_turns(p, token, half / 2 + 4 * u, cs + 4, sn + 4);
+        } else {
+            load_turns(p, token, u, cs, sn);
+        }
+    }
     const long long tile_elems = (long long)d * p.bs;
     const long long blk = live ? token.slot / p.bs : 0;
     const int off = live ? (int)(token.slot - blk * p.bs) : 0;
@@ -192,7 +226,16 @@ __device__ __forceinline__ void norm_heads(const NormParams& n, long long tg, in
                 load_weights<ST>(weight, n.weights_f32, (long long)(h + i + 1) * step + da, wa);
                 load_weights<ST>(weight, n.weights_f32, (long long)(h + i + 1) * step + db, wb);
             }
-            if (INTERLEAVED && turns) turn16<INTERLEAVED>(x, y, cs, sn);
+            if (INTERLEAVED && turns) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x0 = x[2 * j], y0 = y[2 * j];
+                    x[2 * j] = fmaf(x0, cs[j], -(x[2 * j + 1] * sn[j]));
+                    x[2 * j + 1] = fmaf(x[2 * j + 1], cs[j], x0 * sn[j]);
+                    y[2 * j] = fmaf(y0, cs[4 + j], -(y[2 * j + 1] * sn[4 + j]));
+                    y[2 * j + 1] = fmaf(y[2 * j + 1], cs[4 + j], y0 * sn[4 + j]);
+                }
+            }
             if constexpr (KEYS) {
                 store_k8(tile, d, da, off, x, p.k_scale);
                 store_k8(tile, d, db, off, y, p.k_scale);
