@@ -101,6 +101,7 @@ struct SelectParams {
     const int32_t* seq_lens;
     int* err;
     int num_kv_heads, num_rows, max_tokens, k, first, last;
+    int least, most;                   // rows of more tokens than `least`, of at most `most`: the others are another launch's
 };
 
 // A CTA's slice of a row: NT threads, V pieces of 4 tokens each in registers (piece j of thread i
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_tokens_kernel(const Sele
         if (tid == 0) flag_error(p.err, kErrOutOfRange);
         n = n < 0 ? 0 : p.max_tokens;
     }
+    if (n <= p.least || n > p.most) return;                // the whole cluster
     const int row = weight_row(p.rows, b, p.num_rows, false, p.err);
     if (row < 0) n = 0;
     int32_t* const out = p.kept + (size_t)item * p.k;
@@ -367,6 +369,28 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_tokens_kernel(const Sele
             __syncthreads();                               // run[] is read
         }
     });
+}
+
+using SelectKernel = void (*)(SelectParams);
+constexpr int kShortRow = 8192;        // what a CTA of 256 threads holds
+
+int launch_select(SelectKernel kern, const SelectParams& p, long long clusters, int size, int threads, void* stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * size));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = size;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    note_launch();
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e == cudaSuccess ? PKV_OK : cuda_fail("select_tokens: kernel launch", e);
 }
 
 // -------------------------------------------------------------------- keep_tokens
@@ -630,34 +654,33 @@ int select_tokens(int32_t* kept, const float* token_weights, const int32_t* weig
     // the smallest CTA that holds a row in its registers, then clusters of up to 8 of the largest: a
     // trip through the cluster costs about 1 us, and there are six (128 rows of 30000 tokens take
     // 13.7 us as CTAs of 32768 and 31 us as 2 of 16384; 8 of 65536, 18 us and 20 us)
-    void (*kern)(SelectParams);
+    SelectKernel kern;
     int size = 1, threads = 256;
     if (max_tokens <= 1024) kern = select_tokens_kernel<256, 1, false>;
     else if (max_tokens <= 2048) kern = select_tokens_kernel<256, 2, false>;
     else if (max_tokens <= 4096) kern = select_tokens_kernel<256, 4, false>;
-    else if (max_tokens <= 8192) kern = select_tokens_kernel<256, 8, false>;
+    else if (max_tokens <= kShortRow) kern = select_tokens_kernel<256, 8, false>;
     else if (max_tokens <= 16384) kern = select_tokens_kernel<512, 8, false>, threads = 512;
     else {
         threads = 1024;
         while (size < kMaxCluster && 32768LL * size < max_tokens) size *= 2;
         kern = 32768LL * size >= max_tokens ? select_tokens_kernel<1024, 8, false> : select_tokens_kernel<1024, 8, true>;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * size));
-    cfg.blockDim = dim3(threads);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = size;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    note_launch();
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
-    return e == cudaSuccess ? PKV_OK : cuda_fail("select_tokens: kernel launch", e);
+    // More rows than one wave of such CTAs holds, which may all be short: short ones have a launch of
+    // their own, in CTAs of which an SM holds four (512 rows of 4096 tokens in rows of 131072: 24 us and
+    // 92 us; all of 30000: 97 us and 95 us. Clusters that walk over rows: 15 us, but rows of 100000 took
+    // 449 us where one row a cluster takes 245)
+    p.least = -1;
+    p.most = max_tokens;
+    const long long wave = (long long)num_sms() * (1024 / threads) / size;
+    if (max_tokens > kShortRow && items > wave) {
+        p.most = kShortRow;
+        const int st = launch_select(select_tokens_kernel<256, 8, false>, p, items, 1, 256, stream);
+        if (st != PKV_OK) return st;
+        p.least = kShortRow;
+        p.most = max_tokens;
+    }
+    return launch_select(kern, p, items, size, threads, stream);
 }
 
 int keep_tokens(const int32_t* kept, float* token_weights, const int32_t* weight_rows, void* k_pool, void* v_pool,

@@ -674,6 +674,32 @@ def test_select_by_several_ctas(cap, lens):
         check_select(W, None, lens, K, first, last)
 
 
+@pytest.mark.parametrize("cap", [12000, 20000, 40000])
+def test_select_many_rows_of_every_length(cap):
+    """More rows than one wave holds, short and long ones, bad lengths and rows among them: every list
+    is written, once."""
+    rng = rng_of(cap, 9)
+    B, K, first, last = 110, 300, 2, 7
+    lens = rng.integers(0, 8193, B)
+    lens[:9] = [0, 1, K, 8191, 8192, 8193, cap - 1, cap, 9000]
+    lens[9:12] = [cap + 5, -3, 8000]
+    W = np.floor(50 * rng.standard_normal((B, 3, cap))).astype(np.float32)
+    rows = rng.permutation(B).astype(np.int32)
+    rows[11] = B
+    got = select_gpu(W, rows, lens.astype(np.int32), K, first, last)
+    assert pkv.get_device_error() == OUT_OF_RANGE
+    for b in range(B):
+        n = 0 if rows[b] == B else min(max(lens[b], 0), cap)
+        for h in range(3):
+            if n <= K:
+                want = np.concatenate([np.arange(n), np.full(K - n, -1)])
+            else:
+                t = np.arange(first, n - last)
+                best = t[np.lexsort((t, -W[rows[b], h, t]))][:K - first - last]
+                want = np.sort(np.concatenate([np.arange(first), best, np.arange(n - last, n)]))
+            assert np.array_equal(got[b, h], want), (b, h, n)
+
+
 def test_select_one_value_and_extremes():
     n = 3000
     W = np.zeros((4, 2, n), dtype=np.float32)
