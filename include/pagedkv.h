@@ -591,7 +591,8 @@ PKV_API int paged_attention_decode_sparse(void* out, const void* q, const void* 
  * A kept key stays rotated by the position that it was appended at, so the sequence's
  * positions go on counting where its cached length does not. All five are asynchronous on
  * `stream`, allocate nothing and are launched with programmatic stream serialisation, as
- * paged_attention_decode is (weigh_prefill_tokens excepted).
+ * paged_attention_decode is (the weighed decode's second kernel reads the lengths, rows and
+ * weights before it waits for its first, which has waited for all earlier work).
  *
  *   token_weights device float32 [num_rows][num_kv_heads][max_tokens], 16-byte aligned,
  *                 max_tokens a multiple of 4: place t of a row is the weight of cached

@@ -218,7 +218,6 @@ struct Chunk {
 
 template <Pass PASS, int H, int D, int BS>
 __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
-    pdl_enter();
     using S = Shared<D>;
     static_assert(H == 1 || H == 2, "held tiles");
     constexpr int kBlocks = kTile / BS, kTurn = kBufs / H;      // products of a held tile
@@ -251,11 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
         }
         mbar_init(bar(kBarDrain), 1);
         fence_mbar_init();
-        if (PASS == kStats && blockIdx.x == 0) *p.next = 0;
     }
-    if (PASS == kStats && p.row_parts > 1)
-        for (int i = blockIdx.x * kThreads + tid; i < p.num_seqs * p.num_kv_heads * p.key_pairs; i += gridDim.x * kThreads)
-            p.arrived[i] = 0;
     if (warp == kMmaWarp) {
         tc::alloc(smem_addr(&tmem_slot), kTmemCols);
         tc::relinquish_alloc_permit();
@@ -270,6 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
+    pdl_enter();                                           // up to here nothing of the device's memory
+    if (PASS == kStats && tid == 0 && blockIdx.x == 0) *p.next = 0;
+    if (PASS == kStats && p.row_parts > 1)
+        for (int i = blockIdx.x * kThreads + tid; i < p.num_seqs * p.num_kv_heads * p.key_pairs; i += gridDim.x * kThreads)
+            p.arrived[i] = 0;
 
     // Before a copying warp leaves: what it sent has landed (after a wait that gave up, too)
     auto land = [&](int full, int parts, int sent) {
