@@ -69,6 +69,11 @@ inline int logits_pitch(int max_blocks, int block_size) { return (max_blocks * b
 // The warps' parts go where the rings were.
 template <class Math, int D, int BS, int G>
 struct Smem {
+    // CTAs of an SM: four where heads of 64 leave registers for them, else three (16 sequences of 8192, 4
+    // heads a kv head, with three and with four: bf16 of 64 34.4 and 31.0 us, E4M3 28.3 and 25.4; of 128
+    // 51.2 and 52.6, 38.0 and 37.4, a batch of 64 60.2 and 63.1; float32 of 64, 8 heads, 101 and 107)
+    static constexpr int kCtas = D == 64 && Math::Lay::kTile / (D * BS) < 4 ? 4 : 3;
+    static constexpr int kRegisters = 65536 / (kCtas * kWarps * 32) / 8 * 8;
     static constexpr bool kSimt = Math::kWarpSmemFloats > 0;
     static constexpr int kStage = 2 * Math::Lay::kTile;
     static constexpr int kPartFloats = G * (D + 4);        // m [G], l [G], (pad), o [G][D]
@@ -78,7 +83,7 @@ struct Smem {
     static constexpr int kScratch = kQ + (kSimt ? kWarps * G * D * 4 : 0);
     static constexpr int kRing = (kScratch + kWarps * Math::kWarpSmemFloats * 4 + 127) / 128 * 128;
     static constexpr int kMinStages = (kPartFloats * 4 + kStage - 1) / kStage;   // a part fits
-    static constexpr int kFit = (sparse::kSmemSm / 3 - 1024 - kRing) / (kWarps * kStage);
+    static constexpr int kFit = (sparse::kSmemSm / kCtas - 1024 - kRing) / (kWarps * kStage);
     static constexpr int kStages = kFit < kMinStages ? kMinStages : kFit > kMaxStages ? kMaxStages : kFit;
     static constexpr int kBytes = kRing + kWarps * kStages * kStage;
     static_assert(kBytes <= sparse::kSmemSm, "shared memory per CTA");
@@ -101,7 +106,7 @@ struct Keep {
 
 // PAIR = 2: a stage holds two blocks of BS / 2 tokens side by side; BS is then the stage's.
 template <class Math, typename QT, int D, int BS, int G, int PAIR>
-__global__ void __maxnreg__(168) weighed_decode_kernel(const Params p) {
+__global__ void __maxnreg__((Smem<Math, D, BS, G>::kRegisters)) weighed_decode_kernel(const Params p) {
     using S = Smem<Math, D, BS, G>;
     constexpr int TILE = Math::Lay::kTile, PBS = BS / PAIR, PTILE = TILE / PAIR, ST = S::kStages;
     pdl_enter();
