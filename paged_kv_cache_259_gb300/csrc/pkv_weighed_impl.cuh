@@ -104,11 +104,13 @@ struct Keep {
     }
 };
 
-// PAIR = 2: a stage holds two blocks of BS / 2 tokens side by side; BS is then the stage's.
-template <class Math, typename QT, int D, int BS, int G, int PAIR>
+// PAIR = 2: a stage holds two blocks of BS / 2 tokens side by side; BS is then the stage's. HALVES = 2:
+// it holds one half of a block (its K and its V are whole runs of the block's).
+template <class Math, typename QT, int D, int BS, int G, int PAIR, int HALVES>
 __global__ void __maxnreg__((Smem<Math, D, BS, G>::kRegisters)) weighed_decode_kernel(const Params p) {
     using S = Smem<Math, D, BS, G>;
     constexpr int TILE = Math::Lay::kTile, PBS = BS / PAIR, PTILE = TILE / PAIR, ST = S::kStages;
+    static_assert(PAIR == 1 || HALVES == 1, "one or the other");
     pdl_enter();
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
@@ -120,9 +122,9 @@ __global__ void __maxnreg__((Smem<Math, D, BS, G>::kRegisters)) weighed_decode_k
     const int row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts;
     const int b = row / p.num_kv_heads, hk = row - b * p.num_kv_heads;
     int L = p.seq_lens[b];
-    if (L < 0 || L > p.max_blocks * PBS) {
+    if (L < 0 || L > p.max_blocks * (PBS * HALVES)) {
         if (tid == 0) flag_error(p.err, kErrOutOfRange);
-        L = L < 0 ? 0 : p.max_blocks * PBS;
+        L = L < 0 ? 0 : p.max_blocks * (PBS * HALVES);
     }
     const int s0 = part * p.part_stages, s1 = min((L + BS - 1) / BS, s0 + p.part_stages);
     if (s0 >= s1 && part > 0) return;                      // the first partition writes a row without tokens
@@ -133,15 +135,15 @@ __global__ void __maxnreg__((Smem<Math, D, BS, G>::kRegisters)) weighed_decode_k
     __syncwarp();
     const uint64_t pol = l2_evict_first();
     const int32_t* const table = p.block_tables + (size_t)b * p.max_blocks;
-    // the tile of the sequence's block j (-1: none)
+    // the tile of the sequence's block (half block) j (-1: none)
     auto tile_of = [&](int j) -> int {
         if (j * PBS >= L) return -1;
-        const int id = table[j];
+        const int id = table[j / HALVES];
         if (id < 0 || id >= p.num_blocks) {
             flag_error(p.err, kErrOutOfRange);
             return -1;
         }
-        return id * p.num_kv_heads + hk;
+        return (id * p.num_kv_heads + hk) * HALVES + j % HALVES;
     };
     int id_a = -1, id_b = -1, chunk = -1;
     auto issue = [&](int kk, int s) {                      // this warp's tile kk into slot s
@@ -403,16 +405,17 @@ __global__ void __launch_bounds__(kFinishThreads) weighed_finish_kernel(const Pa
     }
 }
 
-template <class Math, typename QT, int D, int BS, int G, int PAIR>
+template <class Math, typename QT, int D, int BS, int G, int PAIR, int HALVES = 1>
 int launch(const Args& a) {
     using S = Smem<Math, D, BS, G>;
-    auto kern = weighed_decode_kernel<Math, QT, D, BS, G, PAIR>;
+    constexpr int BLOCK = BS / PAIR * HALVES;
+    auto kern = weighed_decode_kernel<Math, QT, D, BS, G, PAIR, HALVES>;
     int occ = 0;
     const int st = kernel_setup(reinterpret_cast<const void*>(kern), S::kBytes, kWarps * 32, &occ);
     if (st != PKV_OK) return st;
     Params p = a.p;
     const long long rows = (long long)a.num_seqs * p.num_kv_heads;
-    const int stages = (p.max_blocks * (BS / PAIR) + BS - 1) / BS;
+    const int stages = (p.max_blocks * BLOCK + BS - 1) / BS;
     long long parts = (kMaxCtas + rows - 1) / rows;
     const int most = stages / kPartStages;
     if (parts > most) parts = most;
@@ -430,16 +433,20 @@ int launch(const Args& a) {
     cudaError_t e = launch_pdl(kern, dim3((unsigned)(rows * p.parts)), dim3(kWarps * 32), S::kBytes, a.stream, p);
     if (e != cudaSuccess) return cuda_fail("weighed decode: kernel launch", e);
     note_launch();
-    const dim3 grid((unsigned)((p.max_blocks * (BS / PAIR) + Finish<G>::kTokens - 1) / Finish<G>::kTokens + (p.parts > 1)), (unsigned)rows);
+    const dim3 grid((unsigned)((p.max_blocks * BLOCK + Finish<G>::kTokens - 1) / Finish<G>::kTokens + (p.parts > 1)), (unsigned)rows);
     e = launch_pdl(weighed_finish_kernel<QT, D, G>, grid, dim3(kFinishThreads), 0, a.stream, p, (int)BS,
-                   p.max_blocks * (BS / PAIR));
+                   p.max_blocks * BLOCK);
     return e == cudaSuccess ? PKV_OK : cuda_fail("weighed decode: weights launch", e);
 }
 
-// as the sparse decode chooses (pkv_sparse_impl.cuh)
+// as the sparse decode chooses (pkv_sparse_impl.cuh); blocks of 32 float32 tokens of 128 dims, of which the
+// ring has room for one a warp, by halves (16 sequences of 8192 tokens, 8 kv heads of one query
+// head: 96.5 us whole, 80.8 by halves; of 4: 142 and 99.8)
 template <typename QT, typename KV, int D, int BS, int G>
 int launch_heads(const Args& a) {
-    if constexpr (std::is_same<KV, float>::value || (G == 1 && !std::is_same<KV, uint8_t>::value))
+    if constexpr (std::is_same<KV, float>::value && D == 128 && BS == 32)
+        return launch<sparse::SimtSums<QT, KV, D, BS / 2, G>, QT, D, BS / 2, G, 1, 2>(a);
+    else if constexpr (std::is_same<KV, float>::value || (G == 1 && !std::is_same<KV, uint8_t>::value))
         return launch<sparse::SimtSums<QT, KV, D, BS, G>, QT, D, BS, G, 1>(a);
     else if constexpr (BS == 16 && std::is_same<KV, uint8_t>::value)
         return launch<sparse::HeadsMath<KV, D, 2 * BS, G>, QT, D, 2 * BS, G, 2>(a);

@@ -379,6 +379,30 @@ def test_decode_bad_table_entries(kind, bs):
     check_decode(c, out, W, missing=missing, error=OUT_OF_RANGE)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 2), (8, 2), (8, 1)])
+def test_decode_wide_float32_blocks(Hq, Hkv):
+    """32 float32 tokens of 128 dims, which are read by halves: lengths that end in either half, blocks
+    outside the pool, a length that the table does not hold, slots past the sequence holding anything."""
+    c = decode_case("f32", [15, 16, 17, 31, 32, 33, 300, 100, 64], Hq, Hkv, 128, 32)
+    clean = c["kv"].clone(), c["vv"].clone()
+    for b, n in enumerate(c["lens"][:6]):
+        blk = c["tables"][b, (n - 1) // 32]
+        c["kv"][blk, :, (n - 1) % 32 + 1:] = math.nan
+        c["vv"][blk, :, (n - 1) % 32 + 1:] = math.inf
+    NB = c["kv"].shape[0]
+    missing = []
+    for b, j, bad in ((6, 0, NB), (6, 4, -1), (6, 9, 1 << 30), (7, 3, -7)):
+        c["tables"][b, j] = bad
+        missing += [(b, t) for t in range(j * 32, min(c["lens"][b], (j + 1) * 32))]
+    c["tables"][8, 2:] = c["tables"][8, 0]
+    c["lens"][8] = 5000                                    # clamped to the table's width
+    out, W = decode_gpu(c)
+    c["lens"][8] = c["tables"].shape[1] * 32
+    c["kv"], c["vv"] = clean
+    c["tables"] = np.where((c["tables"] < 0) | (c["tables"] >= NB), 0, c["tables"])
+    check_decode(c, out, W, missing=missing, error=OUT_OF_RANGE)
+
+
 def test_decode_every_block_bad():
     c = decode_case("e4m3", [40], 4, 2, 64, 16)
     c["tables"][:] = -1
