@@ -11,13 +11,16 @@
 // warps' parts (maximum, sum, unnormalised output) meet in shared memory and go to the
 // workspace, or to the output where the row has one partition. Second kernel: a CTA merges the
 // partitions' maxima and sums of its row, which gives each head's maximum and sum, and updates
-// 1024 or 2048 tokens' weights; the first CTA of a row in several partitions merges the outputs.
+// 1024 or 2048 tokens' weights; the outputs of a row in several partitions are merged by its first
+// CTA, or by one a head.
 // Bound: HBM bytes for many tokens (32 sequences of up to 8192, 40 bf16 heads of 128: 415 us,
 // 0.99 of the copy rate; 64 of up to 4096, E4M3, 4 heads a kv head: 60.2, 0.68, the tiles' math
 // as in the sparse decode), two launches and their chains of loads for few (1 x 4096: 8.8 us).
 // Many short partitions rather than whole rows: 4096 CTAs 415 us, 2048 434, 1024 449 (E4M3: 60.2,
 // 60.8, 65.7); 4 tiles a partition instead of 8 make 1 x 4096 12.2 us, 16 no difference.
 #pragma once
+
+#include <type_traits>
 
 #include "pkv_sparse_impl.cuh"
 
@@ -34,6 +37,8 @@ using sparse::softmax_base;
 constexpr int kWarps = 4;
 constexpr int kMaxStages = 8;          // of a warp's ring
 constexpr int kPartStages = 8;         // tiles of a partition, at least
+constexpr int kRowParts = 12;          // partitions of a row, at most; of few rows so many that they make
+constexpr int kWave = 456;             // one wave of CTAs (the merge is a row's last step: WAVE)
 constexpr int kMaxCtas = 4096;         // partitions are made until there are so many
 
 struct Params {
@@ -51,6 +56,7 @@ struct Params {
     int* err;
     int max_blocks, num_blocks, num_rows, max_tokens, num_heads, num_kv_heads;
     int pitch, parts, part_stages;
+    int merge_ctas;                    // of a row, in the second kernel: one, or one a head; 0: rows have one partition
     float qscale, v_scale, decay, lift;
 };
 
@@ -290,8 +296,8 @@ __global__ void __launch_bounds__(kFinishThreads) weighed_finish_kernel(const Pa
     // Read before the first kernel is through: lengths, rows and weights, which it does not write
     // (and it began behind everything that did). 1 sequence of 4096 tokens: 1.2 us of 9.1.
     const int L = min(max(p.seq_lens[b], 0), max_len);     // flagged by the first kernel
-    const bool merges = p.parts > 1 && blockIdx.x == 0;    // the first CTA of a row in several partitions
-    const int t0 = ((int)blockIdx.x - (p.parts > 1)) * Finish<G>::kTokens, t = t0 + 4 * tid;
+    const bool merges = (int)blockIdx.x < p.merge_ctas;    // the first CTAs of a row in several partitions
+    const int t0 = ((int)blockIdx.x - p.merge_ctas) * Finish<G>::kTokens, t = t0 + 4 * tid;
     if (!merges && t0 >= L) {                              // the whole CTA
         if (blockIdx.x == 0) pdl_enter();                  // some CTA waits: what waits for this kernel waits for the first
         return;
@@ -366,30 +372,29 @@ __global__ void __launch_bounds__(kFinishThreads) weighed_finish_kernel(const Pa
         return;
     }
     // ---- the partitions' outputs: J threads a piece of four dims, over every J-th partition each
-    constexpr int kQuads = G * D / 4, J = kQuads < kFinishThreads ? kFinishThreads / kQuads : 1;
-    __shared__ float4 halves[J > 1 ? kFinishThreads : 1];
-    const float4* const o = reinterpret_cast<const float4*>(p.part_o) + (size_t)row * p.parts * kQuads;
-#pragma unroll
-    for (int i0 = 0; i0 < kQuads; i0 += kFinishThreads) {
-        const int i = i0 + tid % (J > 1 ? kQuads : kFinishThreads), g = 4 * i / D;
+    __shared__ float4 sums[kFinishThreads];
+    auto merge = [&](auto heads_of_this, int first_head) {
+        constexpr int kQuads = decltype(heads_of_this)::value * (D / 4), J = kFinishThreads / kQuads;
+        const int i = first_head * (D / 4) + tid % kQuads, g = 4 * i / D;
+        const float4* const o = reinterpret_cast<const float4*>(p.part_o) + (size_t)row * p.parts * G * (D / 4) + i;
         const float m = head_m[g];
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int k = tid / (J > 1 ? kQuads : kFinishThreads); k < parts; k += J) {
+        for (int k = tid / kQuads; k < parts; k += J) {
             const float e = ex2(ml[k * 2 * G + g] - m);
-            const float4 a = o[(size_t)k * kQuads + i];
+            const float4 a = o[(size_t)k * G * (D / 4)];
             v.x += e * a.x;
             v.y += e * a.y;
             v.z += e * a.z;
             v.w += e * a.w;
         }
         if constexpr (J > 1) {
-            halves[tid] = v;
+            sums[tid] = v;
             __syncthreads();
             if (tid >= kQuads) return;
 #pragma unroll
             for (int j = 1; j < J; ++j) {
-                const float4 a = halves[tid + j * kQuads];
+                const float4 a = sums[tid + j * kQuads];
                 v.x += a.x;
                 v.y += a.y;
                 v.z += a.z;
@@ -402,7 +407,9 @@ __global__ void __launch_bounds__(kFinishThreads) weighed_finish_kernel(const Pa
         decode::store_out(dst + 1, v.y * by);
         decode::store_out(dst + 2, v.z * by);
         decode::store_out(dst + 3, v.w * by);
-    }
+    };
+    if (G > 1 && p.merge_ctas > 1) merge(std::integral_constant<int, 1>(), (int)blockIdx.x);
+    else merge(std::integral_constant<int, G>(), 0);
 }
 
 template <class Math, typename QT, int D, int BS, int G, int PAIR, int HALVES = 1>
@@ -417,11 +424,15 @@ int launch(const Args& a) {
     const long long rows = (long long)a.num_seqs * p.num_kv_heads;
     const int stages = (p.max_blocks * BLOCK + BS - 1) / BS;
     long long parts = (kMaxCtas + rows - 1) / rows;
+    const long long cap = kRowParts > kWave / rows ? kRowParts : kWave / rows;
+    if (parts > cap) parts = cap;
     const int most = stages / kPartStages;
     if (parts > most) parts = most;
     if (parts < 1) parts = 1;
     p.part_stages = (int)((stages + parts - 1) / parts);
     p.parts = (stages + p.part_stages - 1) / p.part_stages;
+    // a CTA a head while those are few, else the CTAs' number tells (MERGE)
+    p.merge_ctas = p.parts == 1 ? 0 : rows * G <= 2 * num_sms() ? G : 1;
     p.qscale = a.scale * a.k_scale * kLog2e;
     p.lift = 1.f;
     if constexpr (!S::kSimt) p.lift = Math::kLift == 0.f ? 1.f : 16384.f;
@@ -433,7 +444,7 @@ int launch(const Args& a) {
     cudaError_t e = launch_pdl(kern, dim3((unsigned)(rows * p.parts)), dim3(kWarps * 32), S::kBytes, a.stream, p);
     if (e != cudaSuccess) return cuda_fail("weighed decode: kernel launch", e);
     note_launch();
-    const dim3 grid((unsigned)((p.max_blocks * BLOCK + Finish<G>::kTokens - 1) / Finish<G>::kTokens + (p.parts > 1)), (unsigned)rows);
+    const dim3 grid((unsigned)((p.max_blocks * BLOCK + Finish<G>::kTokens - 1) / Finish<G>::kTokens + p.merge_ctas), (unsigned)rows);
     e = launch_pdl(weighed_finish_kernel<QT, D, G>, grid, dim3(kFinishThreads), 0, a.stream, p, (int)BS,
                    p.max_blocks * BLOCK);
     return e == cudaSuccess ? PKV_OK : cuda_fail("weighed decode: weights launch", e);
