@@ -15,7 +15,7 @@
 // CTA, or by one a head.
 // Bound: HBM bytes for many tokens (32 sequences of up to 8192, 40 bf16 heads of 128: 415 us,
 // 0.99 of the copy rate; 64 of up to 4096, E4M3, 4 heads a kv head: 60.2, 0.68, the tiles' math
-// as in the sparse decode), two launches and their chains of loads for few (1 x 4096: 8.8 us).
+// as in the sparse decode), two launches and their chains of loads for few (1 x 4096: 8.5 us).
 // Many short partitions rather than whole rows: 4096 CTAs 415 us, 2048 434, 1024 449 (E4M3: 60.2,
 // 60.8, 65.7); 4 tiles a partition instead of 8 make 1 x 4096 12.2 us, 16 no difference.
 #pragma once
@@ -37,8 +37,10 @@ using sparse::softmax_base;
 constexpr int kWarps = 4;
 constexpr int kMaxStages = 8;          // of a warp's ring
 constexpr int kPartStages = 8;         // tiles of a partition, at least
-constexpr int kRowParts = 12;          // partitions of a row, at most; of few rows so many that they make
-constexpr int kWave = 456;             // one wave of CTAs (the merge is a row's last step: WAVE)
+// Partitions of a row, at most, and of few rows so many that they make one wave of CTAs: merging them is
+// the row's last step. 1 x 65536 (8 heads a kv head) 54 us, 78 with 512 partitions a row; 2 x 16384 without
+// groups 23.4 and 30.1; 16 x 8192 (4 heads) 48.9 with 12 a row, 52.0 with 32, 51.6 with 16, 55.7 with 8.
+constexpr int kRowParts = 12, kWave = 456;
 constexpr int kMaxCtas = 4096;         // partitions are made until there are so many
 
 struct Params {
@@ -431,7 +433,8 @@ int launch(const Args& a) {
     if (parts < 1) parts = 1;
     p.part_stages = (int)((stages + parts - 1) / parts);
     p.parts = (stages + p.part_stages - 1) / p.part_stages;
-    // a CTA a head while those are few, else the CTAs' number tells (MERGE)
+    // a CTA a head while those are few (1 x 65536, 8 heads, 512 partitions: 78 us, one a row 97), else their
+    // number tells (64 sequences of up to 4096, E4M3, 4 heads: 65.8 and 60.2)
     p.merge_ctas = p.parts == 1 ? 0 : rows * G <= 2 * num_sms() ? G : 1;
     p.qscale = a.scale * a.k_scale * kLog2e;
     p.lift = 1.f;
