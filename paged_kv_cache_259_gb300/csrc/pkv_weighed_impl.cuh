@@ -14,7 +14,7 @@
 // 1024 or 2048 tokens' weights; the outputs of a row in several partitions are merged by its first
 // CTA, or by one a head.
 // Bound: HBM bytes for many tokens (32 sequences of up to 8192, 40 bf16 heads of 128: 415 us,
-// 0.99 of the copy rate; 64 of up to 4096, E4M3, 4 heads a kv head: 60.2, 0.68, the tiles' math
+// 0.99 of the copy rate; 64 of up to 4096, E4M3, 4 heads a kv head: 61.2, 0.67, the tiles' math
 // as in the sparse decode), two launches and their chains of loads for few (1 x 4096: 8.5 us).
 // Many short partitions rather than whole rows: 4096 CTAs 415 us, 2048 434, 1024 449 (E4M3: 60.2,
 // 60.8, 65.7); 4 tiles a partition instead of 8 make 1 x 4096 12.2 us, 16 no difference.
@@ -57,7 +57,7 @@ struct Params {
     float* part_o;                     // [B * Hkv][parts][G][D]
     int* err;
     int max_blocks, num_blocks, num_rows, max_tokens, num_heads, num_kv_heads;
-    int pitch, parts, part_stages;
+    int pitch, parts, part_stages;     // partitions of a row, at most; tiles of one, at least
     int merge_ctas;                    // of a row, in the second kernel: one, or one a head; 0: rows have one partition
     float qscale, v_scale, decay, lift;
 };
@@ -97,6 +97,12 @@ struct Smem {
     static_assert(kBytes <= sparse::kSmemSm, "shared memory per CTA");
 };
 
+// Tiles of a row's partitions: its own length tells, as the tables may be much wider (1 x 4096 in tables of
+// 131072 tokens 9.6 us; 35 with the width's partitions)
+__device__ __forceinline__ int part_stages(const Params& p, int stages) {
+    return max(p.part_stages, (stages + p.parts - 1) / p.parts);
+}
+
 // Keeps a tile's logits: at[head][token], tokens below `limit`
 struct Keep {
     float* at;
@@ -134,7 +140,8 @@ __global__ void __maxnreg__((Smem<Math, D, BS, G>::kRegisters)) weighed_decode_k
         if (tid == 0) flag_error(p.err, kErrOutOfRange);
         L = L < 0 ? 0 : p.max_blocks * (PBS * HALVES);
     }
-    const int s0 = part * p.part_stages, s1 = min((L + BS - 1) / BS, s0 + p.part_stages);
+    const int stages = (L + BS - 1) / BS, per = part_stages(p, stages);
+    const int s0 = part * per, s1 = min(stages, s0 + per);
     if (s0 >= s1 && part > 0) return;                      // the first partition writes a row without tokens
     const int nk = max(0, (s1 - s0 - w + kWarps - 1) / kWarps);    // this warp's tiles: s0 + w, + kWarps, ...
 
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(kFinishThreads) weighed_finish_kernel(const Pa
             before[n] = *reinterpret_cast<const float4*>(at + n * kStep);
     pdl_enter();
     const int stages = (L + stage_tokens - 1) / stage_tokens;
-    const int parts = max(1, (stages + p.part_stages - 1) / p.part_stages);
+    const int per = part_stages(p, stages), parts = max(1, (stages + per - 1) / per);
     const float* const ml = p.part_ml + (size_t)row * p.parts * 2 * G;
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -431,8 +438,9 @@ int launch(const Args& a) {
     const int most = stages / kPartStages;
     if (parts > most) parts = most;
     if (parts < 1) parts = 1;
-    p.part_stages = (int)((stages + parts - 1) / parts);
-    p.parts = (stages + p.part_stages - 1) / p.part_stages;
+    p.parts = (int)parts;
+    // rows enough for kMaxCtas: longer ones do (64 sequences of up to 4096, E4M3: 61.2 us, 63.5 with 8 tiles)
+    p.part_stages = rows * parts >= kMaxCtas ? 2 * kPartStages : kPartStages;
     // a CTA a head while those are few (1 x 65536, 8 heads, 512 partitions: 78 us, one a row 97), else their
     // number tells (64 sequences of up to 4096, E4M3, 4 heads: 65.8 and 60.2)
     p.merge_ctas = p.parts == 1 ? 0 : rows * G <= 2 * num_sms() ? G : 1;
