@@ -178,7 +178,8 @@ class PagedKVCache:
                                num_host_blocks=num_host_blocks)
         self.num_host_blocks = num_host_blocks
         self.key_bounds = None                               # see enable_key_bounds
-        self.token_weights, self._weight_rows, self._free_rows = None, {}, []   # see enable_token_weights
+        self.token_weights = self.weight_storage = None      # see enable_token_weights
+        self._weight_rows, self._free_rows = {}, []
         if num_host_blocks:
             hk, hv = pool_shapes(num_host_blocks, num_kv_heads, block_size, head_dim, kv_dtype)
             self.host_k = torch.empty(hk, dtype=kv_dtype).pin_memory()
@@ -628,10 +629,16 @@ class PagedKVCache:
         sequences of up to ``max_tokens`` cached tokens (``weighed_step`` and
         ``weigh_prompt`` add to it, ``keep_step`` evicts by it). A sequence gets its row when
         ``weight_rows`` first names it, and holds it until ``drop_weight_rows``. Later calls
-        return the same tensor, whatever their sizes. Not while a graph is captured."""
+        return the same tensor, whatever their sizes. Not while a graph is captured.
+
+        The tensor is the front of ``weight_storage``, whose rows are as long as the blocks of
+        ``max_tokens`` tokens: the library's calls take that one, and tables of no more blocks
+        than it has room for."""
         if self.token_weights is None:
-            self.token_weights = torch.zeros(token_weights_shape(max_seqs, self.num_kv_heads, max_tokens),
-                                             dtype=torch.float32, device=self.device)
+            whole = -(-max_tokens // self.block_size) * self.block_size
+            self.weight_storage = torch.zeros(token_weights_shape(max_seqs, self.num_kv_heads, whole),
+                                              dtype=torch.float32, device=self.device)
+            self.token_weights = self.weight_storage[:, :, :token_weights_shape(1, 1, max_tokens)[2]]
             self._free_rows = list(range(max_seqs - 1, -1, -1))
             if self.device.type == "cuda":                   # rows may be used on any stream
                 torch.cuda.current_stream(self.device).synchronize()
@@ -650,7 +657,7 @@ class PagedKVCache:
         with self._on_stream(stream):
             for s in new:
                 self._weight_rows[s] = self._free_rows.pop()
-                self.token_weights[self._weight_rows[s]].zero_()
+                self.weight_storage[self._weight_rows[s]].zero_()
             return torch.tensor([self._weight_rows[s] for s in ids], dtype=torch.int32, device=self.device)
 
     def drop_weight_rows(self, seq_ids):
@@ -664,7 +671,7 @@ class PagedKVCache:
         """The child of a fork begins with its parent's token weights."""
         rows = self.weight_rows([parent, child], stream)
         with self._on_stream(stream):
-            self.token_weights[self._weight_rows[int(child)]].copy_(self.token_weights[self._weight_rows[int(parent)]])
+            self.weight_storage[self._weight_rows[int(child)]].copy_(self.weight_storage[self._weight_rows[int(parent)]])
         return rows[1:]
 
     def weighed_workspace(self, batch, max_blocks):
@@ -681,7 +688,7 @@ class PagedKVCache:
         q, the cache and the weights as they were."""
         calls = self._bind_append(q, k_new, v_new, dev_plan, positions, first, rotary, 1, k_scale, v_scale)
         calls.append(bind_paged_attention_decode_weighed(
-            out, self.token_weights, rows, q, self.k_pool, self.v_pool, dev_plan["tables"], dev_plan["lens"], scale,
+            out, self.weight_storage, rows, q, self.k_pool, self.v_pool, dev_plan["tables"], dev_plan["lens"], scale,
             decay, k_scale, v_scale, workspace))
         self._run_checked(calls, stream)
         return out
@@ -695,7 +702,7 @@ class PagedKVCache:
         """The token weights of a prefill step, after it: those that the last ``window``
         queries of each chunk give (0: all of them). q: as the prefill attended with it
         (rotated)."""
-        bind_weigh_prefill_tokens(self.token_weights, rows, q, self.k_pool, dev_plan["tables"], dev_plan["lens"],
+        bind_weigh_prefill_tokens(self.weight_storage, rows, q, self.k_pool, dev_plan["tables"], dev_plan["lens"],
                                   dev_plan["query_start"], scale, max_query_len, window, decay, workspace)(stream)
 
     def plan_keep(self, seq_ids, num_kept):
@@ -720,8 +727,8 @@ class PagedKVCache:
             none = torch.zeros_like(after)
         if tuple(kept.shape) != (B, self.num_kv_heads, int(num_kept)):
             raise ValueError("kept must be [B, Hkv, num_kept]")
-        calls = [bind_select_tokens(kept, self.token_weights, rows, dev_plan["lens"], first_tokens, last_tokens),
-                 bind_keep_tokens(kept, self.token_weights, rows, self.k_pool, self.v_pool, dev_plan["tables"],
+        calls = [bind_select_tokens(kept, self.weight_storage, rows, dev_plan["lens"], first_tokens, last_tokens),
+                 bind_keep_tokens(kept, self.weight_storage, rows, self.k_pool, self.v_pool, dev_plan["tables"],
                                   dev_plan["kept_tables"], dev_plan["lens"])]
         if self.key_bounds is not None:
             calls.append(bind_update_key_bounds(self.k_pool, self.key_bounds, dev_plan["kept_tables"], after, none, 0))

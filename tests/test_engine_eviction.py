@@ -1,0 +1,95 @@
+"""The engine's side of caches of bounded size, on the host: what its calls are given and what it
+refuses before anything changes, with the library's calls recorded instead of run."""
+import numpy as np
+import pytest
+import torch
+
+from _lib import library
+from paged_kv_cache_259_gb300 import engine
+
+NB, HQ, HKV, D, BS = 80, 4, 2, 64, 16
+BF, I32, I64 = torch.bfloat16, torch.int32, torch.int64
+
+
+class NoStream:
+    def __init__(self, *a):
+        pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *a):
+        pass
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """(name, arguments) of the library's calls that a step binds and runs; no streams."""
+    library()
+    monkeypatch.setattr(torch.cuda, "stream", NoStream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    log = []
+    for name in ("copy_blocks", "reshape_and_cache", "rotary_and_cache", "norm_rotary_and_cache", "update_key_bounds",
+                 "paged_attention_decode_weighed", "weigh_prefill_tokens", "select_tokens", "keep_tokens",
+                 "paged_attention_prefill", "select_blocks", "paged_attention_decode_sparse"):
+        monkeypatch.setattr(engine, "bind_" + name, lambda *a, name=name: lambda s=None: log.append((name, a)))
+    return log
+
+
+def cache(head_dim=D, block_size=BS, num_blocks=NB, **kw):
+    return engine.PagedKVCache(num_blocks, HQ, HKV, head_dim, block_size, BF, range(num_blocks), device="cpu", **kw)
+
+
+def filled(c, lens):
+    for s, n in enumerate(lens):
+        c.bm.add_seq(s)
+        c.bm.append_n(s, n)
+
+
+def rows_of(n):
+    q, kv = torch.zeros(n, HQ, D, dtype=BF), torch.zeros(n, HKV, D, dtype=BF)
+    return q, kv, kv.clone()
+
+
+# ------------------------------------------------- rows of token weights of any size
+@pytest.mark.parametrize("block_size", [16, 32])
+@pytest.mark.parametrize("max_tokens", [1, 50, 1000, 1024])
+@pytest.mark.parametrize("max_seqs", [1, 3])
+def test_rows_hold_the_whole_blocks_of_the_longest_sequence(calls, max_tokens, block_size, max_seqs):
+    """The calls want a place for every slot of the table; a sequence of max_tokens has that
+    many rounded up to whole blocks."""
+    c = cache(block_size=block_size)
+    W = c.enable_token_weights(max_seqs, max_tokens)
+    assert W.shape == (max_seqs, HKV, -(-max_tokens // 4) * 4) and c.enable_token_weights(9, 9) is W
+    filled(c, [max_tokens - 1])
+    plan = c.plan_step([0], group_prefixes=False)
+    assert plan.lens.tolist() == [max_tokens]
+    dev, rows = plan.device_tensors("cpu"), c.weight_rows([0])
+    q, k, v = rows_of(1)
+    c.weighed_step(q, k, v, dev, rows, torch.empty_like(q), 0.1, None)
+    c.weigh_prompt(q, dict(dev, query_start=torch.zeros(2, dtype=I32)), rows, 0.1, 1, None)
+    given = [a[{"paged_attention_decode_weighed": 1, "weigh_prefill_tokens": 0}[name]] for name, a in calls
+             if name != "reshape_and_cache"]
+    if max_tokens > 1:
+        keep = c.plan_keep([0], 1)
+        c.keep_step(keep.device_tensors("cpu"), rows, 1)
+        given += [a[1] for name, a in calls[-2:]]
+        assert keep.tables.shape == plan.tables.shape
+    assert len(given) == (4 if max_tokens > 1 else 2)
+    for t in given:
+        assert t.is_contiguous() and t.shape[2] >= plan.tables.shape[1] * block_size
+        t[:, :, 0] = 5.0
+        assert (W[:, :, 0] == 5).all()                     # the same weights
+        t.zero_()
+
+
+def test_a_fork_copies_the_whole_row(calls):
+    c = cache()
+    c.enable_token_weights(2, 50)
+    c.weight_rows([0])
+    c.weight_storage.fill_(3.0)
+    c.fork_weight_row(0, 1)
+    assert (c.weight_storage == 3).all()
+    c.drop_weight_rows([1])
+    c.weight_rows([2])
+    assert (c.weight_storage[1] == 0).all()
