@@ -126,8 +126,11 @@ class KeepPlan:
         return {k: v.pin_memory() for k, v in t.items()} if pin else t
 
     def device_tensors(self, device, non_blocking=False):
-        return {k: v.to(device, non_blocking=non_blocking)
-                for k, v in self.host_tensors(pin=non_blocking).items()}
+        """The host tensors on the device, plus the host int ``num_kept``."""
+        d = {k: v.to(device, non_blocking=non_blocking)
+             for k, v in self.host_tensors(pin=non_blocking).items()}
+        d["num_kept"] = self.num_kept
+        return d
 
 
 def host_runs(host_ids):
@@ -718,7 +721,10 @@ class PagedKVCache:
     def keep_step(self, dev_plan, rows, num_kept, first_tokens=0, last_tokens=0, kept=None, stream=None):
         """Device half of an eviction: the choice of the ``num_kept`` tokens of each kv head
         (the first, the last, the heaviest) into ``kept`` (int32 ``[B, Hkv, num_kept]``), their
-        move into the fresh blocks, and the key bounds (when kept up) of those. Returns ``kept``."""
+        move into the fresh blocks, and the key bounds (when kept up) of those. ``num_kept`` is
+        the plan's. Returns ``kept``."""
+        if dev_plan.get("num_kept", num_kept) != num_kept:   # what the manager counts on from now on
+            raise ValueError(f"num_kept is {num_kept}, the plan keeps {dev_plan['num_kept']} tokens")
         B = dev_plan["lens"].shape[0]
         with self._on_stream(stream):
             if kept is None:

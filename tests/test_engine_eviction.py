@@ -93,3 +93,19 @@ def test_a_fork_copies_the_whole_row(calls):
     c.drop_weight_rows([1])
     c.weight_rows([2])
     assert (c.weight_storage[1] == 0).all()
+
+
+# ------------------------------------------------------------- evictions as planned
+@pytest.mark.parametrize("other", [16, 31, 33, 40, 0])
+def test_another_number_than_the_plan_has_is_refused(calls, other):
+    """The manager counts the planned tokens: fewer would leave slots that nobody filled."""
+    c = cache()
+    c.enable_token_weights(2, 128)
+    filled(c, [100, 70])
+    plan = c.plan_keep([0, 1], 32)
+    dev, rows = plan.device_tensors("cpu"), c.weight_rows([0, 1])
+    with pytest.raises(ValueError, match="num_kept"):
+        c.keep_step(dev, rows, other)
+    assert calls == []
+    kept = c.keep_step(dev, rows, 32)                      # the plan still stands
+    assert kept.shape == (2, HKV, 32) and [name for name, _ in calls] == ["select_tokens", "keep_tokens"]
