@@ -119,6 +119,8 @@ class KeepPlan:
     lens: np.ndarray         # int32 [B]
     kept_tables: np.ndarray  # int32 [B, ceil(num_kept / block_size)]
     num_kept: int
+    first_tokens: int = 0    # always among them
+    last_tokens: int = 0
 
     def host_tensors(self, pin=True):
         t = {"tables": torch.from_numpy(self.tables), "lens": torch.from_numpy(self.lens),
@@ -126,10 +128,11 @@ class KeepPlan:
         return {k: v.pin_memory() for k, v in t.items()} if pin else t
 
     def device_tensors(self, device, non_blocking=False):
-        """The host tensors on the device, plus the host int ``num_kept``."""
+        """The host tensors on the device, plus the host ints ``num_kept``, ``first_tokens``
+        and ``last_tokens``."""
         d = {k: v.to(device, non_blocking=non_blocking)
              for k, v in self.host_tensors(pin=non_blocking).items()}
-        d["num_kept"] = self.num_kept
+        d.update(num_kept=self.num_kept, first_tokens=self.first_tokens, last_tokens=self.last_tokens)
         return d
 
 
@@ -708,23 +711,38 @@ class PagedKVCache:
         bind_weigh_prefill_tokens(self.weight_storage, rows, q, self.k_pool, dev_plan["tables"], dev_plan["lens"],
                                   dev_plan["query_start"], scale, max_query_len, window, decay, workspace)(stream)
 
-    def plan_keep(self, seq_ids, num_kept):
+    def plan_keep(self, seq_ids, num_kept, first_tokens=0, last_tokens=0):
         """Host half of an eviction: those of the listed sequences that have more than
         ``num_kept`` cached tokens get fresh blocks for so many (``BlockManager.plan_keep``).
         None if none has. Its ``keep_step`` has to be enqueued before anything else writes the
-        cache."""
-        ids = [int(s) for s in dict.fromkeys(int(s) for s in seq_ids) if self.bm.seq_len(int(s)) > num_kept]
+        cache. What no ``keep_step`` could do is refused here, before anything changes: always
+        keeping more first and last tokens than ``num_kept``, block or head sizes that
+        ``keep_tokens`` does not move, sequences longer than their token weights."""
+        num_kept, first, last = int(num_kept), int(first_tokens), int(last_tokens)
+        if first < 0 or last < 0 or first + last > max(num_kept, 0):
+            raise ValueError(f"first_tokens ({first}) and last_tokens ({last}) are at least 0 and at most num_kept "
+                             f"({num_kept}) together")
+        if self.block_size % 16 or self.head_dim % 16 or self.head_dim > 512:
+            raise ValueError("keep_tokens moves blocks and heads (up to 512) of multiples of 16")
+        ids = [s for s in dict.fromkeys(int(s) for s in seq_ids) if self.bm.seq_len(s) > num_kept]
         if not ids:
             return None
-        return KeepPlan(np.asarray(ids, dtype=np.int64), *self.bm.plan_keep(ids, num_kept), int(num_kept))
+        slots = max(-(-self.bm.seq_len(s) // self.block_size) for s in ids) * self.block_size
+        if self.weight_storage is not None and slots > self.weight_storage.shape[2]:
+            raise ValueError(f"a sequence has more tokens than its token weights ({self.weight_storage.shape[2]})")
+        return KeepPlan(np.asarray(ids, dtype=np.int64), *self.bm.plan_keep(ids, num_kept), num_kept, first, last)
 
-    def keep_step(self, dev_plan, rows, num_kept, first_tokens=0, last_tokens=0, kept=None, stream=None):
+    def keep_step(self, dev_plan, rows, num_kept, first_tokens=None, last_tokens=None, kept=None, stream=None):
         """Device half of an eviction: the choice of the ``num_kept`` tokens of each kv head
         (the first, the last, the heaviest) into ``kept`` (int32 ``[B, Hkv, num_kept]``), their
         move into the fresh blocks, and the key bounds (when kept up) of those. ``num_kept`` is
-        the plan's. Returns ``kept``."""
+        the plan's; ``first_tokens`` and ``last_tokens`` are unless given here. Refused arguments
+        leave the cache and the weights as they were: the step can be called again with better
+        ones, and has to be. Returns ``kept``."""
         if dev_plan.get("num_kept", num_kept) != num_kept:   # what the manager counts on from now on
             raise ValueError(f"num_kept is {num_kept}, the plan keeps {dev_plan['num_kept']} tokens")
+        first_tokens = dev_plan.get("first_tokens", 0) if first_tokens is None else first_tokens
+        last_tokens = dev_plan.get("last_tokens", 0) if last_tokens is None else last_tokens
         B = dev_plan["lens"].shape[0]
         with self._on_stream(stream):
             if kept is None:

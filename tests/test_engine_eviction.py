@@ -109,3 +109,50 @@ def test_another_number_than_the_plan_has_is_refused(calls, other):
     assert calls == []
     kept = c.keep_step(dev, rows, 32)                      # the plan still stands
     assert kept.shape == (2, HKV, 32) and [name for name, _ in calls] == ["select_tokens", "keep_tokens"]
+
+
+def host_state(c, ids):
+    return (c.bm.free_list(), [(c.bm.block_table(s), c.bm.seq_len(s), c.bm.is_kept(s)) for s in ids])
+
+
+@pytest.mark.parametrize("first,last", [(33, 0), (0, 33), (20, 13), (-1, 5), (5, -1), (1 << 31, 1 << 31)])
+def test_ends_that_cannot_be_kept_are_refused_before_the_plan(calls, first, last):
+    c = cache()
+    c.enable_token_weights(2, 128)
+    filled(c, [100, 70])
+    before = host_state(c, [0, 1])
+    with pytest.raises(ValueError, match="first_tokens"):
+        c.plan_keep([0, 1], 32, first, last)
+    assert host_state(c, [0, 1]) == before and c.plan_keep([0, 1], 32, 20, 12) is not None
+
+
+@pytest.mark.parametrize("head_dim,block_size", [(24, 16), (528, 16), (64, 24), (64, 8)])
+def test_a_cache_that_cannot_be_moved_is_refused_before_the_plan(calls, head_dim, block_size):
+    c = cache(head_dim=head_dim, block_size=block_size)
+    filled(c, [100])
+    before = host_state(c, [0])
+    with pytest.raises(ValueError, match="multiples of 16"):
+        c.plan_keep([0], 32)
+    assert host_state(c, [0]) == before
+
+
+def test_a_sequence_longer_than_its_weights_is_refused_before_the_plan(calls):
+    c = cache()
+    c.enable_token_weights(2, 50)                          # whole blocks: 64
+    filled(c, [64, 65])
+    before = host_state(c, [0, 1])
+    with pytest.raises(ValueError, match="token weights"):
+        c.plan_keep([0, 1], 32)
+    assert host_state(c, [0, 1]) == before
+    assert c.plan_keep([0], 32).lens.tolist() == [64]
+
+
+def test_the_plans_ends_are_those_of_the_step(calls):
+    c = cache()
+    c.enable_token_weights(1, 128)
+    filled(c, [100])
+    dev, rows = c.plan_keep([0], 32, 4, 20).device_tensors("cpu"), c.weight_rows([0])
+    c.keep_step(dev, rows, 32)
+    c.keep_step(dev, rows, 32, 1, 2)
+    c.keep_step(dev, rows, 32, last_tokens=7)
+    assert [a[4:] for name, a in calls if name == "select_tokens"] == [(4, 20), (1, 2), (4, 7)]

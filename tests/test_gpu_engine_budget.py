@@ -1,9 +1,11 @@
 """The engine with caches of bounded size where its limits are: rows of token weights of any
 number of tokens, used to the last one, each step against float64 on the pool's own values."""
+import numpy as np
 import pytest
 import torch
 
 from _lib import library, pkv
+from oracle import eviction as oev
 from test_gpu_engine_eviction import Loop
 
 pytestmark = pytest.mark.gpu
@@ -40,4 +42,31 @@ def test_every_token_that_the_rows_hold(max_tokens):
         x.decode([1, 0])
     assert x.c.bm.seq_len(0) == max_tokens
     x.evict([1], 33, 0, 1)
+    assert pkv.get_device_error() == 0
+
+
+def test_refused_eviction_changes_nothing_and_can_be_repeated():
+    x = loop(128, seed=1, bounds=True)
+    x.prompts([0, 1], [100, 61], 0)
+    c = x.c
+    rows = c.weight_rows([0, 1])
+    before, weights = [x.cached(s) for s in (0, 1)], c.token_weights.cpu().numpy()
+    dev = c.plan_keep([0, 1], 32, 3, 8).device_tensors("cuda")
+    pools = [t.clone() for t in (c.k_pool, c.v_pool, c.weight_storage, c.key_bounds)]
+    for bad in (dict(num_kept=31), dict(first_tokens=30), dict(last_tokens=-1), dict(rows=rows[:1]), dict(rows=rows.long()),
+                dict(kept=torch.empty(2, 2, 31, dtype=torch.int32, device="cuda")),
+                dict(kept=torch.empty(2, 2, 32, device="cuda")), dict(dev_plan=dict(dev, kept_tables=dev["kept_tables"][:, :1].contiguous()))):
+        a = dict(dev_plan=dev, rows=rows, num_kept=32)
+        a.update(bad)
+        with pytest.raises((ValueError, TypeError, pkv.PagedKVError)):
+            c.keep_step(**a)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(pools, (c.k_pool, c.v_pool, c.weight_storage, c.key_bounds)))
+    kept = c.keep_step(dev, rows, 32).cpu().numpy()
+    for b, s in enumerate((0, 1)):
+        k, v = x.cached(s)
+        for h in range(2):
+            t = kept[b, h]
+            assert t.tolist() == oev.select(weights[c._weight_rows[s], h], len(before[b][0][h]), 32, 3, 8)
+            assert np.array_equal(k[h], before[b][0][h, t]) and np.array_equal(v[h], before[b][1][h, t])
     assert pkv.get_device_error() == 0
