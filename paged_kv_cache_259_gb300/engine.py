@@ -211,7 +211,8 @@ class PagedKVCache:
         return pool_views(self.k_pool, self.v_pool)[1]
 
     def replay(self, script):
-        """Apply block-manager operations; returns the CoW pairs raised (in order)."""
+        """Apply block-manager operations; returns the CoW pairs raised (in order). Nothing on
+        the device: token weights follow by ``fork_weight_row`` and ``beam_weight_rows``."""
         pairs = []
         for op in script:
             if op[0] == "add":
@@ -679,6 +680,36 @@ class PagedKVCache:
         with self._on_stream(stream):
             self.weight_storage[self._weight_rows[int(child)]].copy_(self.weight_storage[self._weight_rows[int(parent)]])
         return rows[1:]
+
+    def beam_weight_rows(self, old_ids, parents, new_ids, stream=None):
+        """After ``BlockManager.beam_step`` with these arguments: each new beam continues with
+        the token weights of its parent, ``old_ids[parents[i]]``, and the old beams give their
+        rows back. int32 ``[len(new_ids)]``, the new beams' rows (``weight_rows``), on the
+        device. A parent's first child takes its row over, the others copy it on ``stream``;
+        children of a parent without a row begin with zeros. All or nothing."""
+        if self.token_weights is None:
+            raise RuntimeError("call enable_token_weights first")
+        old, par, new = ([int(x) for x in xs] for xs in (old_ids, parents, new_ids))
+        if len(par) != len(new) or not all(0 <= p < len(old) for p in par) or len({*old, *new}) != len(old) + len(new):
+            raise ValueError("parents and new_ids differ in length, a parent is not in old_ids or an id is repeated")
+        heirs, copies, begun = {}, [], 0                     # parent -> its first child
+        for p, s in zip(par, new):
+            if old[p] not in self._weight_rows:
+                begun += 1
+            elif heirs.setdefault(old[p], s) != s:
+                copies.append((s, old[p]))
+        gone = [s for s in old + new if s in self._weight_rows and s not in heirs]
+        free = len(self._free_rows) + len(gone)
+        if len(copies) + begun > free:
+            raise RuntimeError(f"{len(copies) + begun} beams without a row of token weights, {free} rows free")
+        self.drop_weight_rows(gone)
+        with self._on_stream(stream):
+            for s, parent in copies:
+                self._weight_rows[s] = self._free_rows.pop()
+                self.weight_storage[self._weight_rows[s]].copy_(self.weight_storage[self._weight_rows[parent]])
+        for parent, s in heirs.items():
+            self._weight_rows[s] = self._weight_rows.pop(parent)
+        return self.weight_rows(new, stream)
 
     def weighed_workspace(self, batch, max_blocks):
         """Scratch of a weighed step."""

@@ -156,3 +156,60 @@ def test_the_plans_ends_are_those_of_the_step(calls):
     c.keep_step(dev, rows, 32, 1, 2)
     c.keep_step(dev, rows, 32, last_tokens=7)
     assert [a[4:] for name, a in calls if name == "select_tokens"] == [(4, 20), (1, 2), (4, 7)]
+
+
+# ----------------------------------------------------------------- beam search
+def beams(c, n, rows):
+    """n beams of one prompt; those in ``rows`` have token weights, all 10 + their number."""
+    c.bm.add_seq(0)
+    c.bm.append_n(0, 20)
+    for s in range(1, n):
+        c.bm.fork(0, s)
+    for s in rows:
+        c.weight_storage[c.weight_rows([s]).tolist()] = 10.0 + s
+
+
+@pytest.mark.parametrize("parents", [[0, 1, 2, 3], [3, 2, 1, 0], [1, 1, 1, 1], [2, 0, 2, 0], [0, 0, 3, 3], [2], []])
+@pytest.mark.parametrize("max_seqs", [4, 7])
+def test_new_beams_take_their_parents_weights(calls, parents, max_seqs):
+    """With no more rows than there are beams, too."""
+    c = cache()
+    W = c.enable_token_weights(max_seqs, 50)
+    beams(c, 4, range(4))
+    new = list(range(10, 10 + len(parents)))
+    c.bm.beam_step(range(4), parents, new)
+    rows = c.beam_weight_rows(range(4), parents, new)
+    assert rows.dtype == I32 and len(set(rows.tolist())) == len(new)
+    assert rows.tolist() == c.weight_rows(new).tolist()
+    for r, p in zip(rows.tolist(), parents):
+        assert (c.weight_storage[r] == 10 + p).all() and (W[r] == 10 + p).all()
+    left = c.weight_rows(range(20, 20 + max_seqs - len(new)))      # the old beams' rows are free
+    assert sorted(rows.tolist() + left.tolist()) == list(range(max_seqs))
+
+
+def test_beams_without_weights_and_ids_used_before(calls):
+    c = cache()
+    c.enable_token_weights(4, 50)
+    beams(c, 3, [1])
+    c.weight_storage[c.weight_rows([11]).tolist()] = 7.0           # of a sequence that is long gone
+    c.bm.beam_step(range(3), [1, 0, 1], [10, 11, 12])
+    rows = c.beam_weight_rows(range(3), [1, 0, 1], [10, 11, 12]).tolist()
+    assert [c.weight_storage[r].unique().tolist() for r in rows] == [[11.0], [0.0], [11.0]]
+    assert len(c.weight_rows([30])) == 1 and len(set(rows)) == 3
+
+
+def test_beams_are_handed_over_all_or_none(calls):
+    c = cache()
+    c.enable_token_weights(3, 50)
+    beams(c, 2, range(2))
+    c.weight_rows([9])
+    before = c.weight_storage.clone(), c.weight_rows([0, 1, 9]).tolist()
+    with pytest.raises(RuntimeError, match="rows free"):
+        c.beam_weight_rows([0, 1], [0, 0, 1], [10, 11, 12])
+    for old, parents, new in (([0, 1], [0], [10, 11]), ([0, 1], [2], [10]), ([0, 1], [-1], [10]), ([0, 1], [0, 1], [10, 10]),
+                              ([0, 1], [0], [1]), ([0, 0], [0], [10])):
+        with pytest.raises(ValueError):
+            c.beam_weight_rows(old, parents, new)
+    assert torch.equal(c.weight_storage, before[0]) and c.weight_rows([0, 1, 9]).tolist() == before[1]
+    with pytest.raises(RuntimeError, match="enable"):
+        cache().beam_weight_rows([0], [0], [1])

@@ -70,3 +70,31 @@ def test_refused_eviction_changes_nothing_and_can_be_repeated():
             assert t.tolist() == oev.select(weights[c._weight_rows[s], h], len(before[b][0][h]), 32, 3, 8)
             assert np.array_equal(k[h], before[b][0][h, t]) and np.array_equal(v[h], before[b][1][h, t])
     assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_beam_search_at_a_budget(side):
+    """Beams hand their token weights on; with no row more than there are beams."""
+    x = loop(96, max_seqs=3, seed=11 + side, stream=torch.cuda.Stream() if side else None)
+    x.prompts([0], [41], 4)
+    ids = [0, 1, 2]
+    for s in ids[1:]:
+        x.c.bm.fork(0, s)
+        x.c.fork_weight_row(0, s, x.stream)
+        x.pos[s], x.W[s] = x.pos[0], x.W[0].copy()
+    for step, parents in enumerate(([0, 1, 2], [2, 2, 0], [1, 0, 1], [0, 0, 0], [2, 1, 0])):
+        for _ in range(4):
+            x.decode(ids, decay=0.99)
+        new = [100 * (step + 1) + i for i in range(3)]
+        x.c.bm.beam_step(ids, parents, new)
+        rows = x.c.beam_weight_rows(ids, parents, new, x.stream)
+        torch.cuda.synchronize()
+        assert rows.tolist() == x.c.weight_rows(new).tolist()
+        for p, s in zip(parents, new):
+            x.pos[s], x.W[s] = x.pos[ids[p]], x.W[ids[p]].copy()
+            x.check_weights(s)
+        ids = new
+        if step % 2:
+            x.evict(ids, 40, 2, 6)
+    x.decode(ids)
+    assert pkv.get_device_error() == 0
