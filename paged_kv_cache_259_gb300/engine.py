@@ -560,7 +560,7 @@ class PagedKVCache:
 
     def _bind_append(self, q, k_new, v_new, dev_plan, positions, first, rotary, max_new,
                      k_scale, v_scale):
-        """The calls of a rotated append, in order, bound."""
+        """The calls of an append, in order, bound: rotated, or as the rows are (no ``rotary``)."""
         calls = []
         if dev_plan["pairs"].shape[0]:
             calls.append(bind_copy_blocks(self.k_pool, self.v_pool, dev_plan["pairs"]))
@@ -579,6 +579,11 @@ class PagedKVCache:
             calls.append(bind_update_key_bounds(self.k_pool, self.key_bounds, dev_plan["tables"],
                                                 dev_plan["lens"], first, max_new))
         return calls
+
+    @staticmethod
+    def _rotates(rotary):
+        if rotary is None:
+            raise TypeError("rotary must be a Rotary")
 
     @staticmethod
     def _run_checked(calls, stream):
@@ -603,6 +608,7 @@ class PagedKVCache:
         ``[axes, T]``; ``first``: ``first_changed(plan)`` on the device. k_new and v_new
         may be views of a fused projection, q has to be contiguous. bfloat16 caches
         (the prefill attention's). Refused arguments leave q and the cache as they were."""
+        self._rotates(rotary)
         calls = self._bind_append(q, k_new, v_new, dev_plan, positions, first, rotary, max_query_len,
                                   1.0, 1.0)
         calls.append(bind_paged_attention_prefill(out, q, self.k_pool, self.v_pool, dev_plan["tables"],
@@ -622,6 +628,7 @@ class PagedKVCache:
         last blocks alone). k_new and v_new may be views of
         a fused projection, q has to be contiguous. Refused arguments leave q and the cache
         as they were."""
+        self._rotates(rotary)
         self.enable_key_bounds(stream)
         calls = self._bind_append(q, k_new, v_new, dev_plan, positions, first, rotary, 1, k_scale, v_scale)
         calls += [bind_select_blocks(selected, q, self.key_bounds, dev_plan["tables"], dev_plan["lens"],

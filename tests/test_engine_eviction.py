@@ -213,3 +213,23 @@ def test_beams_are_handed_over_all_or_none(calls):
     assert torch.equal(c.weight_storage, before[0]) and c.weight_rows([0, 1, 9]).tolist() == before[1]
     with pytest.raises(RuntimeError, match="enable"):
         cache().beam_weight_rows([0], [0], [1])
+
+
+# ------------------------------------------------------------- steps that rotate
+def test_a_rotated_step_without_a_rotary_is_refused(calls, monkeypatch):
+    """Only a weighed step has a form without the rotation: the others would attend with
+    unrotated keys."""
+    monkeypatch.setattr(engine.PagedKVCache, "enable_key_bounds", lambda self, stream=None: None)
+    c = cache()
+    filled(c, [30])
+    plan = c.plan_step([0], group_prefixes=False).device_tensors("cpu")
+    q, k, v = rows_of(1)
+    pos = torch.zeros(1, dtype=I32)
+    with pytest.raises(TypeError, match="rotary"):
+        c.rotary_prefill_step(q, k, v, dict(plan, query_start=torch.zeros(2, dtype=I32)), pos, pos, None, q, 0.1, 1)
+    with pytest.raises(TypeError, match="rotary"):
+        c.sparse_step(q, k, v, plan, pos, pos, None, torch.zeros(1, HKV, 2, dtype=I32), q, 0.1)
+    assert calls == []
+    c.enable_token_weights(1, 64)
+    c.weighed_step(q, k, v, plan, c.weight_rows([0]), q, 0.1, None)
+    assert [name for name, _ in calls] == ["reshape_and_cache", "paged_attention_decode_weighed"]
