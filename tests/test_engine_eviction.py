@@ -233,3 +233,35 @@ def test_a_rotated_step_without_a_rotary_is_refused(calls, monkeypatch):
     c.enable_token_weights(1, 64)
     c.weighed_step(q, k, v, plan, c.weight_rows([0]), q, 0.1, None)
     assert [name for name, _ in calls] == ["reshape_and_cache", "paged_attention_decode_weighed"]
+
+
+@pytest.mark.parametrize("what", ["dtype", "aligned k", "aligned v"])
+def test_an_unrotated_step_checks_its_append_before_the_copies(calls, what):
+    c = cache()
+    filled(c, [20])
+    c.bm.fork(0, 1)
+    c.enable_token_weights(2, 64)
+    plan = c.plan_step([0, 1], group_prefixes=False)
+    assert len(plan.pairs) == 1                            # a copy of the shared block
+    q, k, v = rows_of(2)
+    odd = torch.zeros(2 * HKV * D + 1, dtype=BF)[1:].view(2, HKV, D)
+    bad = {"dtype": (k.float(), v.float()), "aligned k": (odd, v), "aligned v": (k, odd)}[what]
+    dev, rows = plan.device_tensors("cpu"), c.weight_rows([0, 1])
+    with pytest.raises((TypeError, ValueError)):
+        c.weighed_step(q, *bad, dev, rows, q, 0.1, None)
+    assert calls == []
+    c.weighed_step(q, k, v, dev, rows, q, 0.1, None)
+    assert [name for name, _ in calls] == ["copy_blocks", "reshape_and_cache", "paged_attention_decode_weighed"]
+
+
+def test_an_unrotated_step_of_an_e4m3_cache_takes_either_type(calls):
+    c = engine.PagedKVCache(NB, HQ, HKV, D, BS, torch.uint8, range(NB), device="cpu")
+    filled(c, [20])
+    c.enable_token_weights(1, 64)
+    plan, rows = c.plan_step([0], group_prefixes=False).device_tensors("cpu"), c.weight_rows([0])
+    q, k, v = rows_of(1)
+    c.weighed_step(q, k, v, plan, rows, q, 0.1, None)
+    c.weighed_step(q, k.float(), v.float(), plan, rows, q, 0.1, None)
+    with pytest.raises(TypeError):
+        c.weighed_step(q, k.half(), v.half(), plan, rows, q, 0.1, None)
+    assert len(calls) == 4
