@@ -409,7 +409,6 @@ struct KeepParams {
     int* err;
     int k, max_blocks, max_kept_blocks, num_blocks, num_rows, max_tokens, num_kv_heads, d, bs;
     int chunks;                        // of kKeepTokens tokens
-    int items;                         // (sequence, kv head)
     int weight_ctas;                   // the first ones of the launch
 };
 
@@ -728,7 +727,6 @@ int keep_tokens(const int32_t* kept, float* token_weights, const int32_t* weight
     p.num_kv_heads = num_kv_heads;
     p.d = head_dim;
     p.bs = block_size;
-    p.items = (int)items;
     p.weight_ctas = token_weights ? (int)items : 0;
     auto kern = kv_dtype == PKV_F32 ? keep_tokens_kernel<4> : kv_dtype == PKV_BF16 ? keep_tokens_kernel<2> : keep_tokens_kernel<1>;
     note_launch();

@@ -71,12 +71,12 @@ extern "C" int paged_attention_decode_weighed(
     a.p.num_blocks = num_blocks;
     a.p.num_rows = num_rows;
     a.p.max_tokens = max_tokens;
-    a.p.num_heads = num_heads;
     a.p.num_kv_heads = num_kv_heads;
     a.p.pitch = weighed::logits_pitch(max_blocks_per_seq, block_size);
     a.p.v_scale = v_scale;
     a.p.decay = decay;
     a.num_seqs = num_seqs;
+    a.num_heads = num_heads;
     a.head_dim = head_dim;
     a.block_size = block_size;
     a.scale = scale;

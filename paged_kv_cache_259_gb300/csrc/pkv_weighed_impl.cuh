@@ -56,7 +56,7 @@ struct Params {
     float* part_ml;                    // [B * Hkv][parts][2][G]
     float* part_o;                     // [B * Hkv][parts][G][D]
     int* err;
-    int max_blocks, num_blocks, num_rows, max_tokens, num_heads, num_kv_heads;
+    int max_blocks, num_blocks, num_rows, max_tokens, num_kv_heads;
     int pitch, parts, part_stages;     // partitions of a row, at most; tiles of one, at least
     int merge_ctas;                    // of a row, in the second kernel: one, or one a head; 0: rows have one partition
     float qscale, v_scale, decay, lift;
@@ -64,7 +64,7 @@ struct Params {
 
 struct Args {
     Params p;
-    int num_seqs, head_dim, block_size;
+    int num_seqs, num_heads, head_dim, block_size;
     float scale, k_scale;
     void* workspace;
     cudaStream_t stream;
@@ -477,7 +477,7 @@ int launch_heads(const Args& a) {
 
 template <typename QT, typename KV, int D, int BS>
 int dispatch_group(const Args& a) {
-    switch (a.p.num_heads / a.p.num_kv_heads) {
+    switch (a.num_heads / a.p.num_kv_heads) {
         case 1: return launch_heads<QT, KV, D, BS, 1>(a);
         case 2: return launch_heads<QT, KV, D, BS, 2>(a);
         case 4: return launch_heads<QT, KV, D, BS, 4>(a);
