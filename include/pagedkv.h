@@ -602,7 +602,9 @@ PKV_API int paged_attention_decode_sparse(void* out, const void* q, const void* 
  *   weight_rows   device int32 [num_seqs]: the row of each sequence; NULL: sequence b has
  *                 row b (num_rows >= num_seqs). A row outside [0, num_rows), or one that an
  *                 earlier sequence of the call has, sets PKV_ERR_OUT_OF_RANGE, and that
- *                 sequence's weights are left as they were (select_tokens: see there)
+ *                 sequence's weights are left as they were (select_tokens: see there). The
+ *                 weighed decode and weigh_prefill_tokens do not look at the row of a
+ *                 sequence without tokens, or without a chunk
  *
  * norm_rotary_and_cache -- rotary_and_cache of normalised heads: every head x of q and k is
  * first replaced by
@@ -647,8 +649,9 @@ PKV_API int norm_rotary_and_cache(void* q_out, const void* q, const void* k, con
  *   workspace     device scratch of weighed_decode_workspace_size bytes, 16-byte aligned
  *                 (the logits, 4 bytes per query head and cached token, and the partitions'
  *                 results). Needs no clearing; calls that overlap on the GPU need one each
- *   the rest      as paged_attention_decode (same supported sizes and types; queries of any
- *                 magnitude, as paged_attention_decode_sparse)
+ *   the rest      as paged_attention_decode (same supported sizes and types, num_seqs *
+ *                 num_kv_heads at most 65535; queries of any magnitude, as
+ *                 paged_attention_decode_sparse)
  * A table entry outside the pool sets PKV_ERR_OUT_OF_RANGE; its tokens are given no weight.
  * A length that the table cannot hold is clamped and sets PKV_ERR_OUT_OF_RANGE.
  * ---------------------------------------------------------------------- */
@@ -684,7 +687,8 @@ PKV_API size_t weighed_decode_workspace_size(int num_seqs, int num_heads, int he
  *                 no clearing; calls that overlap on the GPU need one each
  *   the rest      as paged_attention_prefill
  * Supported: BF16 / BF16, head_dim in {64,128}, block_size in {16,32}, any num_heads /
- * num_kv_heads up to 128, a scale of 0 or of a magnitude from 2^-100. A sequence with C > L,
+ * num_kv_heads up to 128, num_seqs * num_kv_heads at most 65535, tables of at most 2^24 - 1
+ * tokens, a scale of 0 or of a magnitude from 2^-100. A sequence with C > L,
  * C > max_query_len, L beyond its table or rows outside q sets PKV_ERR_OUT_OF_RANGE and is
  * left as it was; a table entry outside the pool sets it too, and its tokens are given no
  * weight.

@@ -11,9 +11,11 @@
 // (at most three times; once or twice where weights differ, as the bins begin where the weights
 // do: a fixed first digit left a tenth of the keys in one bin). The taken keys are those above
 // the threshold and the first few equal to it; prefix sums over threads, warps and CTAs give
-// each its place in the list, which so comes out ascending. Bound: the chain of passes and
-// barriers, not the reads (4 bytes a token): 512 rows of up to 8192, one wave of CTAs, 14 us, where
-// 64 rows take 7.4 and the bytes 3.1; 8 rows of 131072, in clusters, 19 us.
+// each its place in the list, which so comes out ascending. Bound, few rows: the chain of passes and
+// barriers, not the reads (4 bytes a token); many: instructions, 72 for 32 keys, which an SM with three
+// or four rows issues on 0.63 of its cycles, the busiest on 0.80 (the bins' additions are 1.8% of them and
+// take 6% of the shared memory's cycles). Rows of 8192: 64 of them 6.1 us, 152 7.0, 304 8.4, 512 12.5 (14.0
+// where lengths differ; the bytes 3.1); 8 rows of 131072, in clusters, 19 us.
 //
 // keep_tokens. K: 16-byte pieces, one per (token, X dims), to their new place: eight
 // neighbouring threads write a whole 128-byte core matrix. V is stored transposed: 16 bytes are X

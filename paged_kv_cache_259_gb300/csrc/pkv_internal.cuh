@@ -37,12 +37,25 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // Launch with programmatic stream serialisation: the kernel's CTAs may be
 // scheduled once every CTA of the previous launch in the stream has allowed it
 // (launch_dependents) or exited. Every kernel launched this way calls
-// wait_prerequisites() before it touches global memory (the merge of a split
-// decode excepted: it reads only what was written before the decode launch
-// began until it waits), and allows its own dependents only after that wait,
-// so each launch still sees all earlier work complete: the ordering of plain
-// launches, without their launch gaps. Used for the decode step's launches
-// (block copies, slot writes, decode, merge); the chunked-prefill attention
+// wait_prerequisites() before it touches global memory, and allows its own
+// dependents only after that wait, so each launch still sees all earlier work
+// complete: the ordering of plain launches, without their launch gaps. The
+// exceptions, each right for the reason given:
+//  * the second kernel of a call reads, before it waits, what the first does not
+//    write: everything that did was complete before the first let it start (the
+//    merge of a split decode; the weighed decode's lengths, rows and weights).
+//  * of the weighed decode's second kernel, CTAs without tokens leave without
+//    waiting; the first CTA of every row waits, so that the launch as a whole is
+//    not complete before the first kernel is.
+//  * attention and block choice that follow their own call's writes (`defer`,
+//    `scored`) allow their dependents first and wait where they read those writes.
+//  * weigh_kernel sets up barriers and tensor memory before it waits. It then holds
+//    tensor memory while an earlier launch may still be running: no launch that
+//    allocates some after it has let its dependents start (the prefill attention
+//    with `defer`) may fit on an SM beside it (96 KB of shared memory and 32,768
+//    registers; weigh_kernel leaves 4,096 of the registers).
+// Used for the decode step's launches (block copies, slot writes, decode, merge)
+// and those of sparse, weighed and bounded caches; the chunked-prefill attention
 // measured ~1% slower this way and keeps a plain launch.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
@@ -100,7 +113,7 @@ __device__ __forceinline__ void launch_dependents() {
 __device__ __forceinline__ void wait_prerequisites() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
-// The first statement of every kernel launched with launch_pdl (see there).
+// The first statement of kernels launched with launch_pdl (the exceptions: see there).
 __device__ __forceinline__ void pdl_enter() {
     wait_prerequisites();
     launch_dependents();

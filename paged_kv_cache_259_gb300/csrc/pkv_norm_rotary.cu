@@ -9,15 +9,19 @@
 // norm written out in between would round to 16 bits (2^-9 of the value) first.
 //
 // Work split. A lane holds 16 dims: the two chunks of 8 that turn together, or, where neighbours
-// turn, two as far apart (so that the lanes' 16 bytes lie side by side either way); the lanes of a row (8 for 128 dims) are neighbours, so the sum of squares is
-// log2 of them shuffles. A warp takes 32 / lanes tokens and walks over some of the heads with
-// one set of cosines, sines and (if shared by the heads) weights in registers, the next heads on
-// their way through asynchronous copies: a lane's own 32 bytes of each, which cost no registers
-// and wait for no other lane. V goes through rotary_and_cache's own path.
+// turn, two as far apart (so that the lanes' 16 bytes lie side by side either way); the lanes of a
+// row (8 for 128 dims) are neighbours, so the sum of squares is log2 of them shuffles. A warp takes
+// 32 / lanes tokens and walks over some of the heads with one set of cosines, sines and (if shared by
+// the heads) weights in registers, the next heads on their way through asynchronous copies: a lane's
+// own 32 bytes of each, which cost no registers and wait for no other lane. V goes through
+// rotary_and_cache's own path.
 // Bound: HBM bytes for many tokens (8192 tokens of 32 + 2 x 8 bf16 heads of 128, three axes,
 // weights of each head: 41 us, 0.73 of the copy rate; the issue slots are half in use), a launch
 // and a chain of loads for few (64 tokens 3.6 us). Of the 41 us the heads' own weights cost 5 (36.3 with
 // shared ones); pairs side by side take 43.5, and 48.8 with a lane's two chunks next to each other.
+// Into an E4M3 cache 45.0 us (shared weights 41.6), 0.61: issue slots, of which the codes take more (0.57
+// of all cycles, 0.53 into bf16). Float32 87.7 (83.7), 0.68: twice the shared-memory pieces, on which
+// and on whose copies its warps wait (issue on 0.23 of all cycles).
 #include "pkv_rotary_impl.cuh"
 
 namespace pkv {

@@ -32,11 +32,14 @@
 // sixteenth of the exponentials, 231 with an eighth of the copies, 131 with all three (warps waiting for
 // one another, units changing): not one resource, but two chains of like length, of products of 128 x
 // 128 from shared memory (590 cycles each) and of exponentials (1700 for a group's half of them). The
-// last 32 queries of 4 prompts of up to 32768: 82 us, of which K, read twice, is 55 at the copy rate,
-// and three launches. Small chunks: 12 to 19 us, the launches and a chain of loads in each. Measured and
-// not kept: two groups with halves read ahead (255 us); one exponential in four by a polynomial (255);
-// four held tiles (273 to 295: a unit's change weighs more); the next unit's held tiles in places that
-// the stream leaves (220, but 1 to 2 us more wherever units are few).
+// last 32 queries of 4 prompts of up to 32768: 82 us, of which K, read twice, is 55 at the copy rate
+// (once would do if the rows' statistics came from the prefill, which has them), and three launches.
+// Small chunks: 12 to 19 us, the launches and a chain of loads in each. Units are made by the tables' width:
+// of 8 x 4096 tokens the last 32 of 512 queries take 39.7 us, 49.2 in tables of 131072 tokens (all of
+// them 279 and 253). Measured and not kept: two groups with
+// halves read ahead (255 us); one exponential in four by a polynomial (255); four held tiles (273 to 295:
+// a unit's change weighs more); the next unit's held tiles in places that the stream leaves (220, but 1
+// to 2 us more wherever units are few).
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -57,7 +60,9 @@ constexpr int kHalf = kTile / 2;       // columns of a product that a thread has
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kTile, kTile);
 constexpr int kExt = kTile * 32;       // bytes of the 16 dims that carry -M_r / scale behind a row tile
-constexpr int kTargetUnits = 1216;     // of the stats pass: eight an SM (4 chunks of 2048: 231 us; 1824 237, 3648 267)
+// Units of the stats pass: eight on each of 152 SMs (4 chunks of 2048: 231 us; 1824 237, 3648 267). A
+// constant, as the workspace's size, which is told without a device, goes by it
+constexpr int kTargetUnits = 1216;
 constexpr int kMaxGroup = 128;
 constexpr int kRing = 4;               // units picked ahead
 
@@ -265,7 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const Params p) {
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
-    pdl_enter();                                           // up to here nothing of the device's memory
+    // Up to here nothing of the device's memory. Tensor memory held while earlier launches may still run
+    // keeps none of them from theirs: beside these registers no CTA that takes some fits (launch_pdl)
+    pdl_enter();
     if (PASS == kStats && tid == 0 && blockIdx.x == 0) *p.next = 0;
     if (PASS == kStats && p.row_parts > 1)
         for (int i = blockIdx.x * kThreads + tid; i < p.num_seqs * p.num_kv_heads * p.key_pairs; i += gridDim.x * kThreads)

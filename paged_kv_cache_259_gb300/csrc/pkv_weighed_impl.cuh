@@ -14,8 +14,11 @@
 // 1024 or 2048 tokens' weights; the outputs of a row in several partitions are merged by its first
 // CTA, or by one a head.
 // Bound: HBM bytes for many tokens (32 sequences of up to 8192, 40 bf16 heads of 128: 415 us,
-// 0.99 of the copy rate; 64 of up to 4096, E4M3, 4 heads a kv head: 61.2, 0.67, the tiles' math
-// as in the sparse decode), two launches and their chains of loads for few (1 x 4096: 8.5 us).
+// 0.99 of the copy rate); of E4M3 no unit (64 of up to 4096, 4 heads a kv head: 61.1, 0.67): three
+// warps a scheduler, each a chain of fragments, products and exponentials, issue on 0.42 of the cycles,
+// tensor pipe 0.26, HBM 0.65. Float32 heads of 64: arithmetic of the CUDA cores beside HBM (16 x 8192:
+// one head a kv head 45 us, four 53, floor 40). Few tokens: two launches and their chains of loads
+// (1 x 4096: 8.5 us).
 // Many short partitions rather than whole rows: 4096 CTAs 415 us, 2048 434, 1024 449 (E4M3: 60.2,
 // 60.8, 65.7); 4 tiles a partition instead of 8 make 1 x 4096 12.2 us, 16 no difference.
 #pragma once
@@ -37,9 +40,11 @@ using sparse::softmax_base;
 constexpr int kWarps = 4;
 constexpr int kMaxStages = 8;          // of a warp's ring
 constexpr int kPartStages = 8;         // tiles of a partition, at least
-// Partitions of a row, at most, and of few rows so many that they make one wave of CTAs: merging them is
-// the row's last step. 1 x 65536 (8 heads a kv head) 54 us, 78 with 512 partitions a row; 2 x 16384 without
-// groups 23.4 and 30.1; 16 x 8192 (4 heads) 48.9 with 12 a row, 52.0 with 32, 51.6 with 16, 55.7 with 8.
+// Partitions of a row, at most, and of few rows so many that they make kWave CTAs, three on each of 152
+// SMs: merging them is the row's last step. 1 x 65536 (8 heads a kv head) 54 us, 78 with 512 partitions a
+// row; 2 x 16384 without groups 23.4 and 30.1; 16 x 8192 (4 heads) 48.9 with 12 a row, 52.0 with 32, 51.6
+// with 16, 55.7 with 8. Heads of 64, of which an SM holds four CTAs, gain nothing from a fourth more: with
+// 608 1 x 65536 takes 33.0 us (31.0 with 456; E4M3 21.2 and 23.0), 4 x 8192 12.9 (14.1), 2 x 16384 16.2 (16.4).
 constexpr int kRowParts = 12, kWave = 456;
 constexpr int kMaxCtas = 4096;         // partitions are made until there are so many
 

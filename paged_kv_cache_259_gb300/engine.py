@@ -751,7 +751,7 @@ class PagedKVCache:
     def weigh_prompt(self, q, dev_plan, rows, scale, max_query_len, workspace, window=0, decay=1.0, stream=None):
         """The token weights of a prefill step, after it: those that the last ``window``
         queries of each chunk give (0: all of them). q: as the prefill attended with it
-        (rotated)."""
+        (rotated). bfloat16 caches (the prefill attention's)."""
         bind_weigh_prefill_tokens(self.weight_storage, rows, q, self.k_pool, dev_plan["tables"], dev_plan["lens"],
                                   dev_plan["query_start"], scale, max_query_len, window, decay, workspace)(stream)
 
