@@ -562,17 +562,17 @@ class PagedKVCache:
                      k_scale, v_scale):
         """The calls of an append, in order, bound: rotated, or as the rows are (no ``rotary``)."""
         calls = []
-        if rotary is None:                                   # what its call would refuse behind the copies
-            types = (torch.float32, torch.bfloat16) if self.k_pool.element_size() == 1 else (self.k_pool.dtype,)
-            if k_new.dtype not in types or v_new.dtype != k_new.dtype:
-                raise TypeError(f"k_new and v_new must both be {' or '.join(map(str, types))}")
-            if k_new.data_ptr() % 16 or v_new.data_ptr() % 16:
-                raise ValueError("k_new and v_new must be aligned to 16 bytes")
         if dev_plan["pairs"].shape[0]:
             calls.append(bind_copy_blocks(self.k_pool, self.v_pool, dev_plan["pairs"]))
         if rotary is None:
             calls.append(bind_reshape_and_cache(k_new, v_new, self.k_pool, self.v_pool, dev_plan["slots"],
                                                 k_scale, v_scale))
+            # what this call would refuse only when it runs, behind the copies
+            types = (torch.float32, torch.bfloat16) if self.k_pool.element_size() == 1 else (self.k_pool.dtype,)
+            if k_new.dtype not in types:
+                raise TypeError(f"k_new and v_new must be {' or '.join(map(str, types))}")
+            if k_new.data_ptr() % 16 or v_new.data_ptr() % 16:
+                raise ValueError("k_new and v_new must be aligned to 16 bytes")
         elif rotary.q_norm is not None or rotary.k_norm is not None:
             calls.append(bind_norm_rotary_and_cache(q, q, k_new, v_new, rotary.q_norm, rotary.k_norm, self.k_pool,
                                                     self.v_pool, dev_plan["slots"], positions, rotary.cos_sin,

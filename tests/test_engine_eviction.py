@@ -265,3 +265,16 @@ def test_an_unrotated_step_of_an_e4m3_cache_takes_either_type(calls):
     with pytest.raises(TypeError):
         c.weighed_step(q, k.half(), v.half(), plan, rows, q, 0.1, None)
     assert len(calls) == 4
+
+
+def test_an_unrotated_step_without_rows_is_refused_as_the_binding_does(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "stream", NoStream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    c = cache()
+    filled(c, [20])
+    c.enable_token_weights(1, 64)
+    plan, rows = c.plan_step([0], group_prefixes=False).device_tensors("cpu"), c.weight_rows([0])
+    q, k, v = rows_of(1)
+    for bad in ((None, v), (k, None)):
+        with pytest.raises(TypeError, match="must be a tensor"):
+            c.weighed_step(q, *bad, plan, rows, q, 0.1, None)
